@@ -46,6 +46,15 @@
  *   tv_eagle_expand_select    per layer: the top-k candidates to expand next
  *   tv_eagle_rerank           global top-N by survival probability -> parent lists
  *
+ * Around the verification step, the calls of plain decoding and of a cache
+ * held in 8 bits:
+ *
+ *   tv_rope_axes              rotary positions with several axes (images, video)
+ *   tv_kv_quant_append        K/V rows quantised into an 8-bit paged cache
+ *   tv_kv_quant_read          rows of that cache read back into the bf16 pools
+ *   tv_decode_attention       attention of one new token per request over a
+ *                             paged cache (bf16 or 8 bits)
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - All array arguments are DEVICE pointers owned by the caller. The library
@@ -63,6 +72,8 @@
  *    (block size 16). block_table is int32 [batch][max_blocks_per_req]:
  *    slot s of request b lives in block block_table[b][s / 16], row s % 16.
  *    n_blocks[b] is how many leading table entries request b holds.
+ *    An 8-bit pool has the same layout with one byte per element, and a
+ *    float32 scale per row in an array of its own, [num_blocks][Hkv][16].
  *  - Return value: TV_OK or a negative TV_ERR_* code from host-side argument
  *    checks (nothing is launched then). Errors in the DATA are reported per
  *    request in `status` (int32 [batch], TV_ST_* flags); a request with a
@@ -521,6 +532,170 @@ int tv_accept_commit(const tv_geom* geom, const int32_t* target_ids, const int32
                      int32_t max_blocks_per_req, void* k_cache, void* v_cache, int32_t num_blocks,
                      int32_t* new_len, int32_t* released, int32_t* released_count,
                      int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions with several axes
+ * ------------------------------------------------------------------------ */
+
+#define TV_DTYPE_BF16 0
+#define TV_DTYPE_F32 1
+#define TV_MAX_ROPE_AXES 4
+
+typedef struct tv_rope_axes_geom {
+  int32_t num_q_heads;     /* >= 1 */
+  int32_t num_kv_heads;    /* >= 0; 0: no keys (k and k_out are not used) */
+  int32_t head_dim;        /* D: 2..512 */
+  int32_t rope_style;      /* 0: pair i is columns (2i, 2i+1); 1: (i, i + R), R = all rotated pairs */
+  int32_t num_axes;        /* 1..4: time, height, width, ... */
+  int32_t section[TV_MAX_ROPE_AXES]; /* pairs that take axis a's position, >= 0; sum R in [1, D/2] */
+  int32_t section_order;   /* 0: axis 0's pairs first, then axis 1's, ...;
+                              1: the axes in turn, one used up is passed over */
+} tv_rope_axes_geom;
+
+/*
+ * Rotate the queries and keys of tokens that have a position on each of
+ * several axes (image and video tokens: time, height, width; a text token
+ * has the same position on all of them). Pair i of row t is turned by the
+ * angle positions[axis(i)][t] * inv_freq[i]:
+ *   (a, b) -> (a cos - b sin, b cos + a sin)
+ * Columns from 2R on pass through. The angle is the exact product reduced
+ * modulo one turn in 64-bit fixed point, so it does not lose digits at far
+ * positions; the rotation is float32, rounded once to the output type.
+ * tv_tree_attention_verify rotates a tree's own nodes; this call serves the
+ * prompts, and decode steps ahead of tv_kv_quant_append / tv_decode_attention.
+ *
+ *  rows           tokens (0 is a no-op)
+ *  dtype          TV_DTYPE_* of q, k and the outputs
+ *  q, k           [rows][heads][D]; the heads of a row lie back to back, rows
+ *                 are q_ld / k_ld ELEMENTS apart (>= heads * D), so slices of
+ *                 a fused projection need no copy. Element alignment suffices;
+ *                 16-byte aligned rows and heads take wider loads.
+ *  positions      int32 [num_axes][pos_ld], pos_ld >= rows; may be negative
+ *  inv_freq       float32 [R], radians per position of each pair
+ *  q_out, k_out   as q and k, row strides q_out_ld / k_out_ld; an output may be
+ *                 its own input (same pointer and stride), else no array of
+ *                 the call may overlap an output
+ */
+int tv_rope_axes(const tv_rope_axes_geom* geom, int32_t rows, int32_t dtype, const void* q,
+                 int64_t q_ld, const void* k, int64_t k_ld, const int32_t* positions,
+                 int64_t pos_ld, const float* inv_freq, void* q_out, int64_t q_out_ld, void* k_out,
+                 int64_t k_out_ld, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * The paged KV cache in 8 bits
+ * ------------------------------------------------------------------------ */
+
+#define TV_KV_BF16 0   /* bf16 pools, no scales (tv_decode_attention only) */
+#define TV_KV_E4M3 1   /* fp8 e4m3 codes, the row's scale a power of two */
+#define TV_KV_INT8 2   /* int8 codes in [-127, 127], scale = largest magnitude / 127 */
+
+/*
+ * Quantise fresh K/V rows into an 8-bit paged cache. A row is one head's D
+ * values of one token, a its largest magnitude:
+ *   e4m3  scale = the smallest 2^n, n >= -100, with a <= 448 * 2^n;
+ *         code = x / scale rounded to the nearest e4m3 value, ties to even
+ *   int8  a' = max(a, 2^-100), scale = a' / 127 (float32);
+ *         code = 127 x / a' rounded to the nearest integer, ties to even
+ * Both quotients are taken exactly, so the codes are the same on every
+ * implementation of these lines. A row with a NaN or an infinity gets codes 0
+ * and scale NaN: it reads back as NaN.
+ *
+ *  geom           num_kv_heads, head_dim and block_size are used
+ *  kv_format      TV_KV_E4M3 or TV_KV_INT8
+ *  batch          0..4096
+ *  rows           rows of k_new / v_new; rows from cu_rows[batch] on are ignored
+ *  k_new, v_new   bf16 [rows][Hkv][D], heads back to back, rows kv_ld ELEMENTS
+ *                 apart (>= Hkv * D, a multiple of 8); already rotated keys
+ *  cu_rows        int32 [batch+1] offsets of the requests' rows (as cu_nodes;
+ *                 a request may have none)
+ *  start_len      int32 [batch] row i of request b goes to slot start_len[b] + i
+ *  block_table, n_blocks, max_blocks_per_req, num_blocks
+ *                 as elsewhere; the blocks of the written slots must be held.
+ *                 No slot may be written twice in a call.
+ *  k_cache, v_cache   bytes [num_blocks][Hkv][16][D], 16-byte aligned
+ *  k_scale, v_scale   float32 [num_blocks][Hkv][16]
+ *  status         int32 [batch] in/out: requests with non-zero status are
+ *                 skipped; TV_ST_BAD_SIZE (offsets or start_len) and
+ *                 TV_ST_BAD_BLOCK are OR-ed in and nothing of that request
+ *                 is written
+ */
+int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_t batch, int32_t rows,
+                       const void* k_new, const void* v_new, int64_t kv_ld,
+                       const int32_t* cu_rows, const int32_t* start_len,
+                       const int32_t* block_table, const int32_t* n_blocks,
+                       int32_t max_blocks_per_req, void* k_cache, void* v_cache, float* k_scale,
+                       float* v_scale, int32_t num_blocks, int32_t* status, void* stream);
+
+/*
+ * Read rows of an 8-bit cache back into bf16 pools (code * scale in float32,
+ * rounded once to bf16): slots [first[b], last[b]) of request b go to the same
+ * slots of the request's pages in the destination pools, where
+ * tv_tree_attention_verify and tv_kv_commit work on them. Other slots of the
+ * destination pages are left as they are.
+ *
+ *  first          int32 [batch], or NULL for 0: rows before it are there already
+ *  last           int32 [batch]; last[b] <= first[b] copies nothing
+ *  block_table, n_blocks, max_blocks_per_req, num_blocks
+ *                 of the 8-bit cache
+ *  out_block_table, out_n_blocks, out_max_blocks_per_req, out_num_blocks
+ *                 of the bf16 pools k_out / v_out (16-byte aligned), which
+ *                 share no memory with the 8-bit cache. Two requests may read
+ *                 the same block; no two may write one.
+ *  status         as for tv_kv_quant_append (both tables are checked)
+ */
+int tv_kv_quant_read(const tv_geom* geom, int32_t kv_format, int32_t batch, const int32_t* first,
+                     const int32_t* last, const int32_t* block_table, const int32_t* n_blocks,
+                     int32_t max_blocks_per_req, const void* k_cache, const void* v_cache,
+                     const float* k_scale, const float* v_scale, int32_t num_blocks,
+                     const int32_t* out_block_table, const int32_t* out_n_blocks,
+                     int32_t out_max_blocks_per_req, void* k_out, void* v_out,
+                     int32_t out_num_blocks, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of one new token
+ * ------------------------------------------------------------------------ */
+
+/* Workspace size for tv_decode_attention on the CURRENT device (the same
+ * rules as tv_workspace_bytes: no initialisation, one call at a time). */
+int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes);
+
+/*
+ * Plain decoding's attention: one query token per request over the slots
+ * [0, seq_len[b]) of its paged cache (the token's own row among them, written
+ * before this call). For query head h, reading KV head h / (Hq / Hkv):
+ *   s_j = softmax_scale * q . k_j,  out = sum_j softmax(s)_j v_j,
+ *   lse = log sum_j exp(s_j)
+ * with k_j, v_j the cached values (code * scale for 8-bit pools). Scores, the
+ * softmax and its sums are float32. A request without keys (seq_len 0) gets
+ * out = 0 and lse = -inf. Slots from seq_len[b] on may hold anything. The
+ * result does not depend on timing: the split over the cache's length is a
+ * function of the arguments, and its parts are joined in a fixed order.
+ *
+ *  geom           rope fields are checked, not used: q comes rotated
+ *  kv_format      TV_KV_BF16, TV_KV_E4M3 or TV_KV_INT8
+ *  batch          0..4096
+ *  q              bf16 [batch][Hq][D], rows q_ld ELEMENTS apart (>= Hq * D, a
+ *                 multiple of 8)
+ *  seq_len        int32 [batch], <= 16 * max_blocks_per_req
+ *  block_table, n_blocks, max_blocks_per_req, num_blocks
+ *                 as elsewhere; requests may share blocks
+ *  k_cache, v_cache   pools of the given format, 16-byte aligned
+ *  k_scale, v_scale   float32 [num_blocks][Hkv][16], 16-byte aligned; NULL for
+ *                 TV_KV_BF16
+ *  out            bf16 [batch][Hq][D] out
+ *  lse            float32 [batch][Hq] out, or NULL
+ *  workspace      device scratch of tv_decode_workspace_bytes() bytes
+ *                 (256-byte aligned)
+ *  status         int32 [batch] in/out: requests with non-zero status are
+ *                 skipped; TV_ST_BAD_SIZE (seq_len < 0) and TV_ST_BAD_BLOCK
+ *                 are OR-ed in (outputs untouched)
+ */
+int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32_t batch, const void* q,
+                        int64_t q_ld, const int32_t* seq_len, const int32_t* block_table,
+                        const int32_t* n_blocks, int32_t max_blocks_per_req, const void* k_cache,
+                        const void* v_cache, const float* k_scale, const float* v_scale,
+                        int32_t num_blocks, void* out, float* lse, void* workspace,
+                        size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Name of a TV_ERR_* code or of a single TV_ST_* flag. */
 const char* tv_status_string(int code);

@@ -45,6 +45,9 @@ from .sample_ref import sample_tokens_ref, sampled_walk_ref
 from .ddtree_ref import ddtree_build_ref, ddtree_from_logits_ref, topk_logprobs_ref
 from .eagle_ref import eagle_expand_select_ref, eagle_rerank_ref, eagle_scores_ref
 from .rejection_ref import chosen_path_ref, rejection_walk_ref
+from .decode_ref import (
+    axis_of_pair_ref, decode_attention_ref, kv_quant_ref, rope_axes_ref, round_e4m3_ref,
+)
 
 __all__ = [
     "bf16_bits_to_f64", "f64_to_bf16_bits", "round_to_bf16",
@@ -58,4 +61,5 @@ __all__ = [
     "topk_logprobs_ref", "ddtree_build_ref", "ddtree_from_logits_ref",
     "eagle_scores_ref", "eagle_expand_select_ref", "eagle_rerank_ref",
     "chosen_path_ref", "rejection_walk_ref",
+    "axis_of_pair_ref", "decode_attention_ref", "kv_quant_ref", "rope_axes_ref", "round_e4m3_ref",
 ]
