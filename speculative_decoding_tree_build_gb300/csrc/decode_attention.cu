@@ -3,11 +3,62 @@
 //
 //   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = log sum_j exp(s_j)
 //
-// One warp per query head; a lane holds D / 32 columns and the warp walks the
-// cache with the running maximum and sum of the softmax.
+// What bounds it: the cache is read once and a byte of it takes 2 G / size
+// multiply-adds (G query heads to a cached head), far below the tensor
+// cores' rate per byte, so the floor is the cache's bytes at HBM bandwidth.
+// The design follows from that:
+//  - The G <= 16 query heads that share a cached head go together, so every
+//    cached row is read once. They are the N side of mma.sync m16n8k16 and the
+//    cached rows the M side: S^T = K Q^T (16 keys x 8 queries), O^T = V^T P^T
+//    (16 columns of D x 8 queries). At this intensity a tcgen05 tile of 128
+//    rows would be 7/8 empty, and the register path needs no staging:
+//  - Cached rows go from global memory straight to registers in the layout
+//    that the MMA wants. The contraction may run over D and over the keys in
+//    any order, so each thread takes whole 16-byte pieces: of K the pieces
+//    t, t + 4, ... of rows g and g + 8, of V the piece g of rows 2t, 2t + 1,
+//    2t + 8, 2t + 9 (g = lane / 4, t = lane % 4). V's two rows are interleaved
+//    by byte permutes on the way into the MMA. No shared memory, no barriers
+//    in the loop: 12 to 16 warps an SM with a page each of K and V in flight.
+//  - 8-bit codes become f16 exactly (e4m3 by the hardware's conversion, int8
+//    through the 1024 + u trick). Queries are scaled to f16 by a power of two
+//    per head, which is exact but for elements 2^-14 below the head's largest.
+//  - The softmax's reference is not the exact running maximum: it moves only
+//    when a score exceeds it by 2^8, so the common page takes one warp vote
+//    and no reduction; weights stay below 2^8. A value row's scale joins the
+//    exponent: w_j = 2^(s_j + log2 vscale_j - M), with its own reference M, so
+//    the largest contribution is near 1 in f16 whatever the scales are. The
+//    sum of the softmax is float32 of unrounded terms.
+//
+// Work plan: a unit is (request, KV head), its tiles are 64 keys (a page for
+// each of the CTA's four warps). All units' tiles are laid end to end and
+// every CTA takes a contiguous share, whatever the mix of lengths; the share
+// is computed by each CTA from seq_len, so no host round trip. A unit cut
+// between CTAs leaves one partial result a CTA in the workspace and a second
+// grid joins them in order. Where the block table holds at most
+// kNoSplitPages pages a request, units are never cut and there is one launch.
+#include <cuda_fp16.h>
+
 #include "tv_kv8.cuh"
 
 namespace tv {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecTileKeys = TV_BLOCK_SIZE * kDecWarps;
+constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
+constexpr int kDecMinShare = 4;        // least cost worth a CTA of its own
+constexpr int kNoSplitPages = 16;
+constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
+constexpr int kMergeThreads = 512;
+constexpr float kLowest = -3.4028234663852886e38f;
+
+// What a CTA tells the joining grid.
+struct DecTask {
+  int b, h, last;      // the unit it begins and does not finish (its partial is slot 1), and the
+                       // last CTA that works on it; last < 0: none
+  int mid_b, mid_h;    // the unit whose partial is in slot 0; mid_b < 0: none
+  int pad[3];
+};
 
 struct DecodeParams {
   const __nv_bfloat16* q;
@@ -15,90 +66,620 @@ struct DecodeParams {
   const int32_t* seq_len;
   const int32_t* block_table;
   const int32_t* n_blocks;
-  const void* k_cache;
-  const void* v_cache;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;
   const float* k_scale;
   const float* v_scale;
   __nv_bfloat16* out;
   float* lse;
+  DecTask* tasks;
+  float* partials;     // two slots a CTA: [group][D] sums, then [group] x (m, M, l, -)
   int32_t* status;
-  int batch, hq, hkv, group, max_blocks, num_blocks;
+  int batch, hq, hkv, group, max_blocks, num_blocks, split;
   float scale_log2;
 };
 
-template <int kFmt, int N>
-__device__ __forceinline__ void decode_load(const void* cache, size_t elem, float (&x)[N]) {
-  if constexpr (kFmt == TV_KV_BF16) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = __bfloat162float(static_cast<const __nv_bfloat16*>(cache)[elem + i]);
+__host__ __device__ constexpr size_t dec_slot_floats(int group, int d) { return static_cast<size_t>(group) * (d + 4); }
+
+// ------------------------------------------------------------------ pieces
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ uint2 ldg_stream8(const void* p) {
+  uint2 r;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ float ldg_float(const float* p) {
+  float r;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r) : "l"(p));
+  return r;
+}
+
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 2) {
-      const uint32_t w = *reinterpret_cast<const uint16_t*>(static_cast<const uint8_t*>(cache) + elem + i);
-      const float2 f = kv_decode2<kFmt>(w);
-      x[i] = f.x;
-      x[i + 1] = f.y;
-    }
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   }
 }
 
-template <int kFmt, int D>
-__global__ void __launch_bounds__(512) decode_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int N = D / 32;
+// Transpose of an 8 x 8 matrix of 16-bit elements held one row per four lanes.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Four codes of a word to two f16x2: (byte 0, byte 1) and (byte 2, byte 3).
+template <int kFmt>
+__device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (kFmt == TV_KV_E4M3) {
+    const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w & 0xffffu), __NV_E4M3);
+    const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(w >> 16), __NV_E4M3);
+    lo = *reinterpret_cast<const uint32_t*>(&a);
+    hi = *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    // code + 128 = u in the last bits of f16 1024 + u, then minus 1152: exact
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 off = __half2half2(__ushort_as_half(0x6480));
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), off);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// Tiles of a request; a request without keys, or one that will be flagged, is
+// one tile that computes nothing.
+__device__ __forceinline__ int dec_tiles(int n, int max_blocks) {
+  if (n <= 0 || n > static_cast<long long>(max_blocks) * TV_BLOCK_SIZE) return 1;
+  return (n + kDecTileKeys - 1) / kDecTileKeys;
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int kFmt, int D, int NT>
+struct DecTraits {
+  static constexpr bool kHalf = kFmt != TV_KV_BF16;
+  static constexpr int kElem = kHalf ? 1 : 2;
+  static constexpr int kRowBytes = D * kElem;
+  static constexpr int kKPieces = kRowBytes / 64;              // 16-byte pieces of a K row a thread holds
+  static constexpr int kSteps = D / 16;                        // MMA steps over D (QK), tiles of D (PV)
+  // registers: K and V of a page, the queries and the output accumulators
+  static constexpr int kPerSm = kHalf ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+};
+
+template <int kFmt, int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, (DecTraits<kFmt, D, NT>::kPerSm))
+decode_kernel(const __grid_constant__ DecodeParams p) {
+  using Tr = DecTraits<kFmt, D, NT>;
+  constexpr bool kHalf = Tr::kHalf;
+  constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kSteps = Tr::kSteps;
+  constexpr int kRowPad = D + 4;
+  extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
+  __shared__ float s_m[kDecWarps][16], s_ref[kDecWarps][16], s_l[kDecWarps][16];
+  __shared__ long long s_sum[kDecWarps];
+  __shared__ long long s_prefix;
+  __shared__ int s_first;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int b = blockIdx.x / p.hkv, kvh = blockIdx.x % p.hkv;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int st = p.status[b], n = p.seq_len[b], held = min(p.n_blocks[b], p.max_blocks);
-  if (st != 0) return;
-  const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-  int bad = n < 0 ? TV_ST_BAD_SIZE : 0;
-  const int pages = n > 0 ? (n - 1) / TV_BLOCK_SIZE + 1 : 0;
-  if (!bad && pages > held) bad = TV_ST_BAD_BLOCK;
-  if (!bad) {
-    for (int e = threadIdx.x; e < pages; e += blockDim.x) {
-      const int blk = row[e];
-      if (blk < 0 || blk >= p.num_blocks) bad = TV_ST_BAD_BLOCK;
-    }
+
+  // ---- this CTA's share of the tiles
+  // every thread sums the costs of a run of requests; the scan gives the total
+  // and the thread whose run holds the share's start
+  const int per = (p.batch + kDecThreads - 1) / kDecThreads;
+  const int r0 = min(p.batch, static_cast<int>(threadIdx.x) * per), r1 = min(p.batch, r0 + per);
+  long long mine = 0;
+  for (int b = r0; b < r1; ++b)
+    mine += static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
+  long long upto = mine;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) {
+    const long long o = __shfl_up_sync(0xffffffffu, upto, s);
+    if (lane >= s) upto += o;
   }
-  if (__syncthreads_or(bad)) {
-    if (bad) atomicOr(p.status + b, bad);
+  if (lane == 31) s_sum[warp] = upto;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecWarps; ++w) {
+    if (w < warp) upto += s_sum[w];
+    total += s_sum[w];
+  }
+  const long long before = upto - mine;
+  const long long most = (total + kDecMinShare - 1) / kDecMinShare;
+  const int grid = static_cast<int>(most < static_cast<long long>(gridDim.x) ? most : gridDim.x);
+  const int cta = blockIdx.x;
+  const long long lo = cta < grid ? total * cta / grid : total, hi = cta < grid ? total * (cta + 1) / grid : total;
+  DecTask task = {0, 0, -1, -1, 0, {0, 0, 0}};
+  if (lo >= hi) {
+    if (p.split && threadIdx.x == 0) p.tasks[cta] = task;
     return;
   }
-  const int h = kvh * p.group + warp;
-  float q[N], o[N], m = -INFINITY, l = 0.0f;
-  decode_load<TV_KV_BF16, N>(p.q, static_cast<size_t>(b) * p.q_ld + static_cast<size_t>(h) * D + lane * N, q);
-#pragma unroll
-  for (int i = 0; i < N; ++i) o[i] = 0.0f;
-  for (int j = 0; j < n; ++j) {
-    const size_t r = (static_cast<size_t>(row[j / TV_BLOCK_SIZE]) * p.hkv + kvh) * TV_BLOCK_SIZE + j % TV_BLOCK_SIZE;
-    float k[N], v[N], s = 0.0f;
-    decode_load<kFmt, N>(p.k_cache, r * D + lane * N, k);
-    decode_load<kFmt, N>(p.v_cache, r * D + lane * N, v);
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += q[i] * k[i];
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    float vs = 1.0f;
-    if (kFmt != TV_KV_BF16) {
-      s *= p.k_scale[r];
-      vs = p.v_scale[r];
+  if (mine > 0 && lo >= before && lo < upto) {
+    long long at = before;
+    int b = r0;
+    for (;; ++b) {
+      const long long c = static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
+      if (lo < at + c || b + 1 >= r1) break;
+      at += c;
     }
-    const float mn = fmaxf(m, s), ref = mn == -INFINITY ? 0.0f : mn;
-    const float down = exp2f(m - ref), e = exp2f(s - ref);
-    l = l * down + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) o[i] = o[i] * down + e * vs * v[i];
-    m = mn;
+    s_first = b;
+    s_prefix = at;
   }
-  const float inv = n == 0 ? 0.0f : 1.0f / l;
-  __nv_bfloat16* out = p.out + (static_cast<size_t>(b) * p.hq + h) * D + lane * N;
+  __syncthreads();
+  int b = s_first;
+  int n = p.seq_len[b], nt = dec_tiles(n, p.max_blocks);
+  long long unit;                      // where the unit starts in the sequence of costs
+  int h, tile0;
+  {
+    const long long cost = kDecUnitCost + nt, rel = lo - s_prefix;
+    h = static_cast<int>(rel / cost);
+    const long long off = rel - h * cost;
+    unit = s_prefix + h * cost;
+    // tile 0 starts at 0, tile k at kDecUnitCost + k
+    tile0 = off == 0 ? 0 : off <= kDecUnitCost + 1 ? 1 : static_cast<int>(off - kDecUnitCost);
+    if (!p.split && off != 0) tile0 = nt;              // the unit belongs to the CTA of its start
+  }
+
+  for (;;) {
+    // ---- the next unit, or part of one
+    if (tile0 >= nt) {
+      unit += kDecUnitCost + nt;
+      tile0 = 0;
+      if (++h == p.hkv) {
+        h = 0;
+        if (++b == p.batch) break;
+        n = p.seq_len[b];
+        nt = dec_tiles(n, p.max_blocks);
+      }
+      continue;
+    }
+    if (tile0 == 0 ? unit >= hi : unit + kDecUnitCost + tile0 >= hi) break;
+    int tile1 = nt;
+    if (p.split && hi - unit - kDecUnitCost < nt) tile1 = max(tile0 + 1, static_cast<int>(hi - unit - kDecUnitCost));
+
+    const int st = p.status[b], held = min(p.n_blocks[b], p.max_blocks);
+    const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
+    const int pages = fits ? (n + TV_BLOCK_SIZE - 1) / TV_BLOCK_SIZE : 0;
+    int bad = n < 0 ? TV_ST_BAD_SIZE : (!fits || pages > held) ? TV_ST_BAD_BLOCK : 0;
+    if (st != 0 || bad) {
+      // (pages > held is a fact of the request: every CTA that meets it finds the same)
+      if (st == 0 && threadIdx.x == 0) atomicOr(p.status + b, bad);
+      if (tile0 > 0) { task.mid_b = b; task.mid_h = h; }
+      tile0 = nt;
+      if (st != 0 || bad) continue;
+    }
+    const int page_end = min(pages, tile1 * kDecWarps);
+    const int first = tile0 * kDecWarps + warp;
+    const int iters = page_end > first ? (page_end - first + kDecWarps - 1) / kDecWarps : 0;
+    const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+
+    // ---- queries: the thread's columns of query g (and g + 8), as MMA operands
+    uint32_t qf[NT][kSteps][2];
+    float fac[NT][2];                  // score factor of queries 2t and 2t + 1
 #pragma unroll
-  for (int i = 0; i < N; ++i) out[i] = __float2bfloat16_rn(o[i] * inv);
-  if (p.lse != nullptr && lane == 0)
-    p.lse[static_cast<size_t>(b) * p.hq + h] = n == 0 ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+    for (int x = 0; x < NT; ++x) {
+      const int qi = x * 8 + g;
+      const bool live = qi < p.group;
+      const __nv_bfloat16* src = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + (live ? qi : 0)) * D;
+      if constexpr (!kHalf) {
+#pragma unroll
+        for (int c = 0; c < kKPieces; ++c) {
+          uint4 w = *reinterpret_cast<const uint4*>(src + (t + 4 * c) * 8);
+          if (!live) w = make_uint4(0u, 0u, 0u, 0u);
+          qf[x][2 * c][0] = w.x; qf[x][2 * c][1] = w.y;
+          qf[x][2 * c + 1][0] = w.z; qf[x][2 * c + 1][1] = w.w;
+        }
+        fac[x][0] = fac[x][1] = p.scale_log2;
+      } else {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < kKPieces; ++c) {
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint4 w = *reinterpret_cast<const uint4*>(src + (t + 4 * c) * 16 + 8 * u);
+            if (!live) w = make_uint4(0u, 0u, 0u, 0u);
+            qf[x][4 * c + 2 * u][0] = w.x; qf[x][4 * c + 2 * u][1] = w.y;
+            qf[x][4 * c + 2 * u + 1][0] = w.z; qf[x][4 * c + 2 * u + 1][1] = w.w;
+          }
+        }
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) top = max(top, max(qf[x][s][e] & 0x7fffu, (qf[x][s][e] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // 2^e <= largest magnitude < 2^(e+1); queries are held as q / 2^e
+        const int e = min(max(static_cast<int>(top >> 7) - 127, -126), 126);
+        const float down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        const float mine_fac = __uint_as_float(static_cast<uint32_t>(127 + e) << 23) * p.scale_log2;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            qf[x][s][u] = pack_half2(bf16_lo(qf[x][s][u]) * down, bf16_hi(qf[x][s][u]) * down);
+        fac[x][0] = __shfl_sync(0xffffffffu, mine_fac, 8 * t);
+        fac[x][1] = __shfl_sync(0xffffffffu, mine_fac, 8 * t + 4);
+      }
+    }
+
+    float o[NT][kSteps][4];
+    float m[NT][2], ref[NT][2], l[NT][2];
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[x][s][e] = 0.0f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) { m[x][e] = ref[x][e] = kLowest; l[x][e] = 0.0f; }
+    }
+
+    // ---- pages: block ids a warp-load at a time, rows a page ahead
+    int ids = 0, ids_next = 0;
+    auto load_ids = [&](int base) {
+      const int i = base + lane;
+      int blk = i < iters ? row[first + i * kDecWarps] : 0;
+      if (blk < 0 || blk >= p.num_blocks) { bad = TV_ST_BAD_BLOCK; blk = 0; }
+      return blk;
+    };
+    uint4 kf[2][kKPieces];
+    uint4 vf[4][kRowBytes >= 128 ? kRowBytes / 128 : 1];
+    float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
+    auto head_row = [&](int it) {      // the page's first row of this head, as a row number of the pool
+      const int blk = __shfl_sync(0xffffffffu, ids, it % 32);
+      return (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE;
+    };
+    auto load_k = [&](size_t r) {
+      const uint8_t* base = p.k_cache + r * kRowBytes + t * 16;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < kKPieces; ++c) kf[u][c] = ldg_stream(base + (g + 8 * u) * kRowBytes + c * 64);
+      if constexpr (kHalf) {
+        ks[0] = ldg_float(p.k_scale + r + g);
+        ks[1] = ldg_float(p.k_scale + r + g + 8);
+      }
+    };
+    auto load_v = [&](size_t r) {
+      const uint8_t* base = p.v_cache + r * kRowBytes;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const uint8_t* src = base + (2 * t + (u & 1) + (u >> 1) * 8) * kRowBytes;
+        if constexpr (kRowBytes >= 128) {
+#pragma unroll
+          for (int c = 0; c < kRowBytes / 128; ++c) vf[u][c] = ldg_stream(src + g * 16 + c * 128);
+        } else {
+          const uint2 w = ldg_stream8(src + g * 8);
+          vf[u][0] = make_uint4(w.x, w.y, 0u, 0u);
+        }
+      }
+      if constexpr (kHalf) {
+        vs[0] = ldg_float(p.v_scale + r + g);
+        vs[1] = ldg_float(p.v_scale + r + g + 8);
+      }
+    };
+    size_t r_now = 0;
+    if (iters > 0) {
+      ids = load_ids(0);
+      r_now = head_row(0);
+      load_k(r_now);
+      load_v(r_now);
+      ids_next = iters > 32 ? load_ids(32) : 0;
+    }
+    for (int it = 0; it < iters; ++it) {
+      const int key0 = (first + it * kDecWarps) * TV_BLOCK_SIZE;
+      const bool tail = key0 + TV_BLOCK_SIZE > n;
+      // scores of 16 keys: thread holds keys g, g + 8 of queries 2t, 2t + 1
+      float s[NT][4];
+#pragma unroll
+      for (int x = 0; x < NT; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[x][e] = 0.0f;
+#pragma unroll
+      for (int c = 0; c < kKPieces; ++c) {
+        const uint32_t a[4] = {kf[0][c].x, kf[0][c].y, kf[0][c].z, kf[0][c].w};
+        const uint32_t e[4] = {kf[1][c].x, kf[1][c].y, kf[1][c].z, kf[1][c].w};
+        if constexpr (kHalf) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t a0, a1, a2, a3;
+            codes_to_half<kFmt>(a[j], a0, a2);
+            codes_to_half<kFmt>(e[j], a1, a3);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) mma16816<true>(s[x], a0, a1, a2, a3, qf[x][4 * c + j][0], qf[x][4 * c + j][1]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+              mma16816<false>(s[x], a[2 * j], e[2 * j], a[2 * j + 1], e[2 * j + 1], qf[x][2 * c + j][0], qf[x][2 * c + j][1]);
+        }
+      }
+      const float k0 = ks[0], k1 = ks[1];
+      if (it + 1 < iters) {
+        if ((it + 1) % 32 == 0) {
+          ids = ids_next;
+          ids_next = it + 33 < iters ? load_ids(it + 33) : 0;
+        }
+        r_now = head_row(it + 1);
+        load_k(r_now);
+      }
+      const bool live0 = !tail || key0 + g < n, live1 = !tail || key0 + g + 8 < n;
+      float lv0 = 0.0f, lv1 = 0.0f;
+      if constexpr (kHalf) { lv0 = __log2f(vs[0]); lv1 = __log2f(vs[1]); }
+      bool over = false;
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = kHalf ? fac[x][e & 1] * (e < 2 ? k0 : k1) : fac[x][e & 1];
+          s[x][e] = (e < 2 ? live0 : live1) ? s[x][e] * f : -INFINITY;
+          over |= s[x][e] > m[x][e & 1] + 8.0f;
+          if (kHalf) over |= s[x][e] + (e < 2 ? lv0 : lv1) > ref[x][e & 1] + 8.0f;
+        }
+      }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float a = fmaxf(s[x][e], s[x][e + 2]);
+            float c = a;
+            if (kHalf) c = fmaxf(s[x][e] + (live0 ? lv0 : 0.0f), s[x][e + 2] + (live1 ? lv1 : 0.0f));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+              if (kHalf) c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
+            }
+            a = fmaxf(a, m[x][e]);
+            l[x][e] *= fast_exp2(m[x][e] - a);
+            m[x][e] = a;
+            c = kHalf ? fmaxf(c, ref[x][e]) : a;
+            const float down = fast_exp2(ref[x][e] - c);
+            ref[x][e] = c;
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) { o[x][i][e] *= down; o[x][i][e + 2] *= down; }
+          }
+        }
+      }
+      // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8)
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int x = 0; x < NT; ++x) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          w[e] = fast_exp2(s[x][e] - m[x][e & 1]);
+          l[x][e & 1] += w[e];
+          if (kHalf) {
+            w[e] = fast_exp2(s[x][e] + (e < 2 ? lv0 : lv1) - ref[x][e & 1]);
+            if (tail && !(e < 2 ? live0 : live1)) w[e] = 0.0f;
+          }
+        }
+        pf[x][0] = transpose8x8(kHalf ? pack_half2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+        pf[x][1] = transpose8x8(kHalf ? pack_half2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+      }
+      if (tail) {                      // rows past the end may hold anything, NaN among it
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (key0 + 2 * t + (u & 1) + (u >> 1) * 8 < n) continue;
+#pragma unroll
+          for (int c = 0; c < (kRowBytes >= 128 ? kRowBytes / 128 : 1); ++c) vf[u][c] = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < (kRowBytes >= 128 ? kRowBytes / 128 : 1); ++c) {
+        const uint32_t v0[4] = {vf[0][c].x, vf[0][c].y, vf[0][c].z, vf[0][c].w};
+        const uint32_t v1[4] = {vf[1][c].x, vf[1][c].y, vf[1][c].z, vf[1][c].w};
+        const uint32_t v2[4] = {vf[2][c].x, vf[2][c].y, vf[2][c].z, vf[2][c].w};
+        const uint32_t v3[4] = {vf[3][c].x, vf[3][c].y, vf[3][c].z, vf[3][c].w};
+        constexpr int kWords = kRowBytes >= 128 ? 4 : 2;
+#pragma unroll
+        for (int j = 0; j < kWords; ++j) {
+          if constexpr (kHalf) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {        // two columns of two rows, by bytes
+              const uint32_t sel = i ? 0x7362 : 0x5140;
+              uint32_t a0, a1, a2, a3;
+              codes_to_half<kFmt>(__byte_perm(v0[j], v1[j], sel), a0, a1);
+              codes_to_half<kFmt>(__byte_perm(v2[j], v3[j], sel), a2, a3);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16816<true>(o[x][2 * j + i], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+            }
+          } else {
+            const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+            const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+#pragma unroll
+            for (int x = 0; x < NT; ++x) mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+          }
+        }
+      }
+      if (it + 1 < iters) load_v(r_now);
+    }
+
+    // ---- join the warps
+    const bool any_bad = __syncthreads_or(bad);
+    if (any_bad && bad) atomicOr(p.status + b, bad);
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
+        if (g == 0) {
+          s_m[warp][8 * x + 2 * t + e] = m[x][e];
+          s_ref[warp][8 * x + 2 * t + e] = ref[x][e];
+          s_l[warp][8 * x + 2 * t + e] = l[x][e];
+        }
+      }
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int qi = 8 * x + 2 * t + e;
+        float top = s_ref[0][qi];
+#pragma unroll
+        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_ref[w][qi]);
+        const float f = fast_exp2(ref[x][e] - top);
+        float* dst = s_o + (static_cast<size_t>(warp) * 8 * NT + qi) * kRowPad;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+          // the column of tile i's row g (and the next one in its row g + 8)
+          const int d = kRowBytes == 256 ? 8 * g + 64 * (i / 4) + 2 * (i % 4) : kRowBytes == 128 && kHalf ? 16 * g + 2 * i : 8 * g + 2 * i;
+          *reinterpret_cast<float2*>(dst + d) = make_float2(o[x][i][e] * f, o[x][i][e + 2] * f);
+        }
+      }
+    __syncthreads();
+    const bool whole = tile0 == 0 && tile1 == nt;
+    float* slot = p.partials + (static_cast<size_t>(cta) * 2 + (tile0 == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
+    if (!any_bad || !whole) {
+      for (int i = threadIdx.x; i < p.group * (D / 2); i += kDecThreads) {
+        const int qi = i / (D / 2), d = i % (D / 2) * 2;
+        float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          const float2 v = *reinterpret_cast<const float2*>(s_o + (static_cast<size_t>(w) * 8 * NT + qi) * kRowPad + d);
+          acc.x += v.x;
+          acc.y += v.y;
+        }
+        float mm = s_m[0][qi], mr = s_ref[0][qi], ll = 0.0f;
+#pragma unroll
+        for (int w = 1; w < kDecWarps; ++w) { mm = fmaxf(mm, s_m[w][qi]); mr = fmaxf(mr, s_ref[w][qi]); }
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) ll += s_l[w][qi] * fast_exp2(s_m[w][qi] - mm);
+        if (whole) {
+          const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
+          const float f = n == 0 ? 0.0f : fast_exp2(mr - mm) / ll;
+          *reinterpret_cast<uint32_t*>(p.out + at * D + d) = pack_bf16x2(acc.x * f, acc.y * f);
+          if (p.lse != nullptr && d == 0) p.lse[at] = n == 0 ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float2*>(slot + static_cast<size_t>(qi) * D + d) = acc;
+          if (d == 0) *reinterpret_cast<float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi) = make_float4(mm, mr, ll, 0.0f);
+        }
+      }
+    }
+    if (!whole) {
+      if (tile0 > 0) {
+        task.mid_b = b;
+        task.mid_h = h;
+      } else {
+        task.b = b;
+        task.h = h;
+        // the CTA of the unit's last tile: the largest c with total * c / grid <= its start
+        const long long e = unit + kDecUnitCost + nt;
+        task.last = static_cast<int>((e * grid + total - 1) / total - 1);
+      }
+    }
+    __syncthreads();                   // the shared sums are read before the next unit writes them
+    if (tile1 < nt) break;
+    tile0 = nt;
+  }
+  if (p.split && threadIdx.x == 0) p.tasks[cta] = task;
 }
+
+// Join the partials of the unit that CTA blockIdx.x began: slot 1 of that
+// CTA, then slot 0 of the CTAs after it that worked on the unit. A warp takes
+// a query head and every (warps per head)-th partial.
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kVec = D / 32;
+  constexpr int kWarps = kMergeThreads / 32;
+  __shared__ float s_acc[kWarps][D];
+  __shared__ float s_stat[kWarps][3];
+  grid_dependency_wait();
+  const DecTask task = p.tasks[blockIdx.x];
+  if (task.last < 0) return;
+  if (p.status[task.b] != 0) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int parts = kWarps / p.group;            // group <= 16
+  const int qi = warp % p.group, part = warp / p.group;
+  float acc[kVec], mm = kLowest, mr = kLowest, ll = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+  if (part < parts) {
+#pragma unroll 4
+    for (int c = static_cast<int>(blockIdx.x) + part; c <= task.last; c += parts) {
+      const bool own = c == static_cast<int>(blockIdx.x);
+      const bool has = own || (p.tasks[c].mid_b == task.b && p.tasks[c].mid_h == task.h);
+      const float* slot = p.partials + (static_cast<size_t>(c) * 2 + (own ? 1 : 0)) * dec_slot_floats(p.group, D);
+      if (!has) continue;
+      const float4 st = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi);
+      const float nm = fmaxf(mm, st.x), nr = fmaxf(mr, st.y);
+      ll = ll * fast_exp2(mm - nm) + st.z * fast_exp2(st.x - nm);
+      const float a = fast_exp2(mr - nr), c2 = fast_exp2(st.y - nr);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] = acc[i] * a + slot[static_cast<size_t>(qi) * D + i * 32 + lane] * c2;
+      mm = nm;
+      mr = nr;
+    }
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) s_acc[warp][i * 32 + lane] = acc[i];
+    if (lane == 0) { s_stat[warp][0] = mm; s_stat[warp][1] = mr; s_stat[warp][2] = ll; }
+  }
+  __syncthreads();
+  if (part != 0 || warp >= p.group) return;
+  for (int w = 1; w < parts; ++w) {
+    const int o = w * p.group + qi;
+    const float om = s_stat[o][0], orf = s_stat[o][1];
+    const float nm = fmaxf(mm, om), nr = fmaxf(mr, orf);
+    ll = ll * fast_exp2(mm - nm) + s_stat[o][2] * fast_exp2(om - nm);
+    const float a = fast_exp2(mr - nr), c2 = fast_exp2(orf - nr);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] = acc[i] * a + s_acc[o][i * 32 + lane] * c2;
+    mm = nm;
+    mr = nr;
+  }
+  const size_t at = static_cast<size_t>(task.b) * p.hq + static_cast<size_t>(task.h) * p.group + qi;
+  const float f = fast_exp2(mr - mm) / ll;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) p.out[at * D + i * 32 + lane] = __float2bfloat16_rn(acc[i] * f);
+  if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
+}
+
+template <int kFmt, int D, int NT>
+static int launch_decode(const DecodeParams& p, int sms, int dev, cudaStream_t stream) {
+  using Tr = DecTraits<kFmt, D, NT>;
+  constexpr size_t smem = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
+  static size_t smem_set[kMaxDevices] = {0};
+  auto* kernel = decode_kernel<kFmt, D, NT>;
+  if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+  const int grid = sms * Tr::kPerSm;
+  if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), smem, stream, p) != cudaSuccess) return TV_ERR_CUDA;
+  if (p.split && launch_pdl(decode_merge_kernel<D>, dim3(grid), dim3(kMergeThreads), 0, stream, p) != cudaSuccess)
+    return TV_ERR_CUDA;
+  return TV_OK;
+}
+
+template <int kFmt>
+static int launch_decode_fmt(const DecodeParams& p, int d, int sms, int dev, cudaStream_t stream) {
+  if (d == 64)
+    return p.group <= 8 ? launch_decode<kFmt, 64, 1>(p, sms, dev, stream) : launch_decode<kFmt, 64, 2>(p, sms, dev, stream);
+  return p.group <= 8 ? launch_decode<kFmt, 128, 1>(p, sms, dev, stream) : launch_decode<kFmt, 128, 2>(p, sms, dev, stream);
+}
+
+static size_t dec_task_bytes(int ctas) { return (sizeof(DecTask) * ctas + 255) / 256 * 256; }
 
 }  // namespace tv
 
@@ -107,7 +688,13 @@ extern "C" int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, siz
   if (rc != TV_OK) return rc;
   if (bytes == nullptr) return TV_ERR_NULL_POINTER;
   if (batch < 0 || batch > tv::kKvMaxBatch) return TV_ERR_BAD_SIZE;
-  *bytes = 256;
+  const int dev = tv::current_device();
+  if (dev < 0) return TV_ERR_CUDA;
+  const int sms = tv::device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
+  const int ctas = sms * tv::kDecMaxPerSm;
+  *bytes = tv::dec_task_bytes(ctas) +
+           sizeof(float) * 2 * ctas * tv::dec_slot_floats(geom->num_q_heads / geom->num_kv_heads, geom->head_dim);
   return TV_OK;
 }
 
@@ -138,22 +725,27 @@ extern "C" int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32
   rc = tv_decode_workspace_bytes(geom, batch, &need);
   if (rc != TV_OK) return rc;
   if (workspace_bytes < need) return TV_ERR_WORKSPACE;
+  const int dev = tv::current_device();
+  if (dev < 0) return TV_ERR_CUDA;
+  const int sms = tv::device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
   tv::DecodeParams p = {};
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.q_ld = q_ld;
   p.seq_len = seq_len; p.block_table = block_table; p.n_blocks = n_blocks;
-  p.k_cache = k_cache; p.v_cache = v_cache; p.k_scale = k_scale; p.v_scale = v_scale;
+  p.k_cache = static_cast<const uint8_t*>(k_cache); p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.k_scale = k_scale; p.v_scale = v_scale;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse; p.status = status;
+  p.tasks = static_cast<tv::DecTask*>(workspace);
+  p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tv::dec_task_bytes(sms * tv::kDecMaxPerSm));
   p.batch = batch; p.hq = geom->num_q_heads; p.hkv = geom->num_kv_heads;
   p.group = geom->num_q_heads / geom->num_kv_heads;
   p.max_blocks = max_blocks_per_req; p.num_blocks = num_blocks;
+  p.split = max_blocks_per_req > tv::kNoSplitPages ? 1 : 0;
   const float scale = geom->softmax_scale > 0.0f ? geom->softmax_scale : 1.0f / sqrtf(static_cast<float>(geom->head_dim));
   p.scale_log2 = scale * 1.4426950408889634f;
-  void (*kernel)(tv::DecodeParams) = nullptr;
-  const bool d64 = geom->head_dim == 64;
-  if (kv_format == TV_KV_BF16) kernel = d64 ? tv::decode_kernel<TV_KV_BF16, 64> : tv::decode_kernel<TV_KV_BF16, 128>;
-  else if (kv_format == TV_KV_E4M3) kernel = d64 ? tv::decode_kernel<TV_KV_E4M3, 64> : tv::decode_kernel<TV_KV_E4M3, 128>;
-  else kernel = d64 ? tv::decode_kernel<TV_KV_INT8, 64> : tv::decode_kernel<TV_KV_INT8, 128>;
-  const cudaError_t err = tv::launch_pdl(kernel, dim3(batch * p.hkv), dim3(32 * p.group), 0, tv::as_stream(stream), p);
-  return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+  const cudaStream_t s = tv::as_stream(stream);
+  if (kv_format == TV_KV_BF16) return tv::launch_decode_fmt<TV_KV_BF16>(p, geom->head_dim, sms, dev, s);
+  if (kv_format == TV_KV_E4M3) return tv::launch_decode_fmt<TV_KV_E4M3>(p, geom->head_dim, sms, dev, s);
+  return tv::launch_decode_fmt<TV_KV_INT8>(p, geom->head_dim, sms, dev, s);
 }

@@ -180,6 +180,12 @@ class Cache:
             out.append(x.cpu().numpy())
         return out
 
+    def value_scales(self, b, n):
+        if self.vs is None:
+            return None
+        page, at = self.at(b, range(n))
+        return f64(self.vs[page, :, at])
+
 
 def fresh(seed, rows, hkv, d, pad=0):
     """Two bf16 row sets, slices of one matrix; a few rows are made difficult."""
@@ -346,8 +352,9 @@ def test_read_back_skips_and_flags():
 # ---------------------------------------------------------------- one-token attention
 
 
-def decode_tolerance(q, k, v, scale, held):
-    """Element-wise bounds of the output and of lse from the kernel's roundings."""
+def decode_tolerance(q, k, v, scale, held, vs=None):
+    """Element-wise bounds of the output and of lse from the kernel's roundings
+    (vs: the value rows' scales [n][Hkv])."""
     out, lse, absv, big = decode_attention_ref(q, k, v, scale)
     d, n = q.shape[1], k.shape[0]
     # a score: D products and sums in float32, the scale factors, 2^-24 each; exp2: 2^-22; the
@@ -357,6 +364,15 @@ def decode_tolerance(q, k, v, scale, held):
     weight = HALF[BF16] if held == "bf16" else 2.0 ** -11           # weights as tensor-core operands
     rel = weight + 2 * score + 2 * sums
     tol = absv * rel[:, None] + HALF[BF16] * np.abs(out) + 1e-30
+    if held != "bf16" and n:
+        # The weights p_j vs_j are f16 numbers over a common power 2^M <= max_j p_j vs_j, and f16's
+        # smallest step is 2^-24: each is off by up to 2^-25 2^M besides its relative 2^-11, and
+        # multiplies the code |v_j| / vs_j. Where the heaviest row's code is 0, all that a column
+        # holds can lie below that step.
+        for h in range(q.shape[0]):
+            g = h // (q.shape[0] // k.shape[1])
+            p = np.exp(scale * (k[:, g] @ q[h]) - lse[h])
+            tol[h] += 2.0 ** -25 * (p * vs[:, g]).max() * (np.abs(v[:, g]) / vs[:, g][:, None]).sum(0)
     return out, lse, tol, score + sums + 2.0 ** -22 * np.abs(np.where(np.isfinite(lse), lse, 0))
 
 
@@ -376,7 +392,7 @@ def check_decode(c, q, lens, out, lse, scale=0.0, which=None):
     scale = scale or q.shape[2] ** -0.5
     for b in (range(len(lens)) if which is None else which):
         k, v = c.rows(b, lens[b])
-        want, wl, tol, ltol = decode_tolerance(f64(q[b]), k, v, scale, c.held)
+        want, wl, tol, ltol = decode_tolerance(f64(q[b]), k, v, scale, c.held, c.value_scales(b, lens[b]))
         err = np.abs(f64(out[b]) - want)
         assert np.all(err <= tol), (b, lens[b], float((err - tol).max()))
         if lse is not None:
@@ -540,7 +556,7 @@ def test_offsets_past_32_bits():
     assert np.array_equal(ks[page, :, slots % 16].cpu().numpy(), sc)
     vcode, vsc = kv_quant_ref(f64(v), "int8")
     rows = [code * sc.astype(np.float64)[..., None], vcode * vsc.astype(np.float64)[..., None]]
-    want, wl, tol, ltol = decode_tolerance(f64(q[0]), *rows, d ** -0.5, "int8")
+    want, wl, tol, ltol = decode_tolerance(f64(q[0]), *rows, d ** -0.5, "int8", vsc.astype(np.float64))
     assert np.all(np.abs(f64(got[0][0][0]) - want) <= tol) and np.all(np.abs(f64(got[0][1][0]) - wl) <= ltol)
     rows = [f64(x[page, :, slots % 16]) for x in (ko, vo)]
     want, wl, tol, ltol = decode_tolerance(f64(q[0]), *rows, d ** -0.5, "bf16")
