@@ -600,10 +600,11 @@ int tv_rope_axes(const tv_rope_axes_geom* geom, int32_t rows, int32_t dtype, con
  * implementation of these lines. A row with a NaN or an infinity gets codes 0
  * and scale NaN: it reads back as NaN.
  *
- *  geom           num_kv_heads, head_dim and block_size are used
+ *  geom           num_kv_heads (<= 4096), head_dim and block_size are used
  *  kv_format      TV_KV_E4M3 or TV_KV_INT8
  *  batch          0..4096
- *  rows           rows of k_new / v_new; rows from cu_rows[batch] on are ignored
+ *  rows           rows of k_new / v_new (0 is a no-op); rows from cu_rows[batch]
+ *                 on are ignored
  *  k_new, v_new   bf16 [rows][Hkv][D], heads back to back, rows kv_ld ELEMENTS
  *                 apart (>= Hkv * D, a multiple of 8); already rotated keys
  *  cu_rows        int32 [batch+1] offsets of the requests' rows (as cu_nodes;

@@ -39,6 +39,7 @@
 #include <cuda_fp16.h>
 
 #include "tv_kv8.cuh"
+#include "tv_share.cuh"
 
 namespace tv {
 
@@ -175,66 +176,30 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kRowPad = D + 4;
   extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
   __shared__ float s_m[kDecWarps][16], s_ref[kDecWarps][16], s_l[kDecWarps][16];
-  __shared__ long long s_sum[kDecWarps];
-  __shared__ long long s_prefix;
-  __shared__ int s_first;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_dependency_wait();
   grid_launch_dependents();
 
   // ---- this CTA's share of the tiles
-  // every thread sums the costs of a run of requests; the scan gives the total
-  // and the thread whose run holds the share's start
-  const int per = (p.batch + kDecThreads - 1) / kDecThreads;
-  const int r0 = min(p.batch, static_cast<int>(threadIdx.x) * per), r1 = min(p.batch, r0 + per);
-  long long mine = 0;
-  for (int b = r0; b < r1; ++b)
-    mine += static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
-  long long upto = mine;
-#pragma unroll
-  for (int s = 1; s < 32; s <<= 1) {
-    const long long o = __shfl_up_sync(0xffffffffu, upto, s);
-    if (lane >= s) upto += o;
-  }
-  if (lane == 31) s_sum[warp] = upto;
-  __syncthreads();
-  long long total = 0;
-#pragma unroll
-  for (int w = 0; w < kDecWarps; ++w) {
-    if (w < warp) upto += s_sum[w];
-    total += s_sum[w];
-  }
-  const long long before = upto - mine;
-  const long long most = (total + kDecMinShare - 1) / kDecMinShare;
-  const int grid = static_cast<int>(most < static_cast<long long>(gridDim.x) ? most : gridDim.x);
-  const int cta = blockIdx.x;
-  const long long lo = cta < grid ? total * cta / grid : total, hi = cta < grid ? total * (cta + 1) / grid : total;
+  const Share sh = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int b) {
+    return static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
+  });
+  const int cta = blockIdx.x, grid = sh.ctas;
+  const long long hi = sh.hi, total = sh.total;
   DecTask task = {0, 0, -1, -1, 0, {0, 0, 0}};
-  if (lo >= hi) {
+  if (sh.lo >= sh.hi) {
     if (p.split && threadIdx.x == 0) p.tasks[cta] = task;
     return;
   }
-  if (mine > 0 && lo >= before && lo < upto) {
-    long long at = before;
-    int b = r0;
-    for (;; ++b) {
-      const long long c = static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
-      if (lo < at + c || b + 1 >= r1) break;
-      at += c;
-    }
-    s_first = b;
-    s_prefix = at;
-  }
-  __syncthreads();
-  int b = s_first;
+  int b = sh.b;
   int n = p.seq_len[b], nt = dec_tiles(n, p.max_blocks);
   long long unit;                      // where the unit starts in the sequence of costs
   int h, tile0;
   {
-    const long long cost = kDecUnitCost + nt, rel = lo - s_prefix;
+    const long long cost = kDecUnitCost + nt, rel = sh.lo - sh.start;
     h = static_cast<int>(rel / cost);
     const long long off = rel - h * cost;
-    unit = s_prefix + h * cost;
+    unit = sh.start + h * cost;
     // tile 0 starts at 0, tile k at kDecUnitCost + k
     tile0 = off == 0 ? 0 : off <= kDecUnitCost + 1 ? 1 : static_cast<int>(off - kDecUnitCost);
     if (!p.split && off != 0) tile0 = nt;              // the unit belongs to the CTA of its start

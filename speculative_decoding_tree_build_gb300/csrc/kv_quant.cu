@@ -5,13 +5,17 @@
 // magnitude, scale, codes (tv_kv8.cuh). Both calls are bound by memory: the
 // append reads 2 D bytes a row and writes D + 4, the read the other way round.
 // A row is held by D / 8 neighbouring lanes, 16 bytes of bf16 each; its
-// largest magnitude takes log2(D / 8) shuffles of an integer maximum.
+// largest magnitude takes log2(D / 8) shuffles of a paired integer maximum.
+// The append's rows are loaded before their slots are known, so the chain of
+// small loads (offsets, lengths, block ids) overlaps the one large one.
 #include "tv_kv8.cuh"
+#include "tv_share.cuh"
 
 namespace tv {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendRows = 4;       // rows of k_new / v_new per CTA
+constexpr int kAppendBatch = 4;      // 16-byte loads a thread has in flight
+constexpr int kAppendMaxRows = 64;   // rows of k_new / v_new per CTA at most
 
 struct AppendParams {
   const __nv_bfloat16* k_new;
@@ -26,7 +30,8 @@ struct AppendParams {
   float* k_scale;
   float* v_scale;
   int32_t* status;
-  int batch, rows, hkv, max_blocks, num_blocks;
+  int batch, rows, hkv, max_blocks, num_blocks, cta_rows;
+  uint32_t heads_magic;              // ceil(2^32 / (2 hkv))
 };
 
 // The request that owns row t: the largest b with cu[b] <= t (requests without
@@ -44,98 +49,135 @@ __device__ __forceinline__ int request_of_row(const int32_t* cu, int batch, int 
 template <int kFmt, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;        // lanes that hold one row
-  __shared__ int s_cu[kKvMaxBatch + 1];
-  __shared__ int s_req[kAppendRows], s_slot[kAppendRows], s_blk[kAppendRows], s_bad[kAppendRows];
+  constexpr int kItems = kAppendThreads / kLanes;                      // rows of heads a sweep takes
+  extern __shared__ int s_cu[];        // [batch + 1]
+  __shared__ int s_req[kAppendMaxRows], s_slot[kAppendMaxRows], s_blk[kAppendMaxRows], s_bad[kAppendMaxRows];
+  __shared__ int s_first[kAppendMaxRows], s_pages[kAppendMaxRows];     // of a run's request: its span
   grid_dependency_wait();
   grid_launch_dependents();
-  const int t0 = blockIdx.x * kAppendRows;
-  const int nrows = min(kAppendRows, p.rows - t0);
-  for (int i = threadIdx.x; i <= p.batch; i += blockDim.x) s_cu[i] = p.cu_rows[i];
+  const int t0 = blockIdx.x * p.cta_rows;
+  const int nrows = min(p.cta_rows, p.rows - t0);
+  const int per_row = 2 * p.hkv;                                       // K heads, then V heads
+  const int total = nrows * per_row, lane = threadIdx.x % kLanes;
+  uint4 x[kAppendBatch];
+  auto place = [&](int it, int& r, int& kvh) {
+    r = static_cast<int>(__umulhi(static_cast<uint32_t>(it), p.heads_magic));
+    kvh = it - r * per_row;
+  };
+  auto load = [&](int base) {
+#pragma unroll
+    for (int e = 0; e < kAppendBatch; ++e) {
+      const int it = base + e * kItems;
+      x[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (it < total) {
+        int r, kvh;
+        place(it, r, kvh);
+        const bool isv = kvh >= p.hkv;
+        const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + (t0 + r) * p.kv_ld;
+        x[e] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(isv ? kvh - p.hkv : kvh) * D + lane * 8);
+      }
+    }
+  };
+  load(threadIdx.x / kLanes);          // on their way while the rows' slots are found
+
+  for (int i = threadIdx.x; i <= p.batch; i += kAppendThreads) s_cu[i] = p.cu_rows[i];
   __syncthreads();
-  if (threadIdx.x < kAppendRows) {
-    const int r = threadIdx.x;
-    const int b = r < nrows ? request_of_row(s_cu, p.batch, t0 + r) : -1;
+  if (blockIdx.x == 0) {               // requests whose rows lie past the array, in part or altogether
+    for (int b = threadIdx.x; b < p.batch; b += kAppendThreads)
+      if (s_cu[b + 1] > p.rows && s_cu[b + 1] > s_cu[b] && p.status[b] == 0) atomicOr(p.status + b, TV_ST_BAD_SIZE);
+  }
+  if (threadIdx.x < nrows) {
+    const int r = threadIdx.x, t = t0 + r;
+    const int b = request_of_row(s_cu, p.batch, t);
+    int bad = -1, blk = -1;            // -1: not this call's to write, nothing to report
     s_req[r] = b;
-    s_bad[r] = 0;
-    s_blk[r] = -1;
+    s_pages[r] = 0;
     if (b >= 0) {
-      const int start = p.start_len[b];
-      const long long slot = static_cast<long long>(start) + (t0 + r - s_cu[b]);
-      if (p.status[b] != 0) {
-        s_bad[r] = -1;                                       // skipped, nothing to report
-      } else if (start < 0 || s_cu[b] < 0 || s_cu[b + 1] > p.rows || slot > 0x7fffffffll) {
-        s_bad[r] = TV_ST_BAD_SIZE;
+      const int st = p.status[b], start = p.start_len[b], held = min(p.n_blocks[b], p.max_blocks);
+      const long long slot = static_cast<long long>(start) + (t - s_cu[b]);
+      const long long end = static_cast<long long>(start) + (s_cu[b + 1] - s_cu[b]);
+      if (st == 0) {
+        bad = 0;
+        if (start < 0 || s_cu[b] < 0 || end > 0x7fffffffll) bad = TV_ST_BAD_SIZE;
+        else if (s_cu[b + 1] > p.rows) bad = -1;                       // CTA 0 reports it
+        else if ((end - 1) / TV_BLOCK_SIZE >= held) bad = TV_ST_BAD_BLOCK;
+      }
+      if (bad == 0) {
+        blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + slot / TV_BLOCK_SIZE];
+        if (blk < 0 || blk >= p.num_blocks) bad = TV_ST_BAD_BLOCK;
+        // the request's first row here checks the blocks of rows that lie in other CTAs
+        if (bad == 0 && (r == 0 || t - 1 < s_cu[b]) && (s_cu[b] < t0 || s_cu[b + 1] > t0 + nrows)) {
+          s_first[r] = start / TV_BLOCK_SIZE;
+          s_pages[r] = static_cast<int>((end - 1) / TV_BLOCK_SIZE) - s_first[r] + 1;
+        }
       }
       s_slot[r] = static_cast<int>(slot);
     }
+    s_bad[r] = bad;
+    s_blk[r] = blk;
   }
   __syncthreads();
-  // every block of a request's written slots has to be held and in range
+  // at most two requests reach beyond this CTA's rows: the first and the last one
   for (int r = 0; r < nrows; ++r) {
-    const int b = s_req[r];
-    if (b < 0 || s_bad[r] != 0) continue;
-    if (r > 0 && s_req[r - 1] == b) continue;
-    const long long first = p.start_len[b];
-    const long long last = first + (s_cu[b + 1] - s_cu[b]) - 1;
-    const int held = min(p.n_blocks[b], p.max_blocks);
-    int bad = last / TV_BLOCK_SIZE >= held ? 1 : 0;
-    if (!bad) {
-      const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-      for (int e = static_cast<int>(first / TV_BLOCK_SIZE) + threadIdx.x; e <= last / TV_BLOCK_SIZE; e += blockDim.x) {
-        const int blk = row[e];
-        bad |= (blk < 0 || blk >= p.num_blocks) ? 1 : 0;
-      }
+    const int pages = s_pages[r];
+    if (pages == 0) continue;
+    const int32_t* row = p.block_table + static_cast<size_t>(s_req[r]) * p.max_blocks + s_first[r];
+    bool bad = false;
+    for (int e = threadIdx.x; e < pages; e += kAppendThreads) {
+      const int blk = row[e];
+      bad |= blk < 0 || blk >= p.num_blocks;
     }
     if (bad) s_bad[r] = TV_ST_BAD_BLOCK;
   }
   __syncthreads();
-  if (threadIdx.x < nrows) {
+  if (threadIdx.x < nrows && s_req[threadIdx.x] >= 0) {
+    // one bad row of a request holds all of its rows back
     const int r = threadIdx.x, b = s_req[r];
-    if (b >= 0) {
-      int head = r;                                          // the run's first row holds the verdict
-      while (head > 0 && s_req[head - 1] == b) --head;
-      const int bad = s_bad[head];
-      if (bad > 0 && head == r) atomicOr(p.status + b, bad);
-      if (bad == 0) s_blk[r] = p.block_table[static_cast<size_t>(b) * p.max_blocks + s_slot[r] / TV_BLOCK_SIZE];
-    }
+    int bad = s_bad[r];
+    const int own = bad;
+    for (int o = r - 1; o >= 0 && s_req[o] == b; --o) bad = max(bad, s_bad[o]);
+    for (int o = r + 1; o < nrows && s_req[o] == b; ++o) bad = max(bad, s_bad[o]);
+    if (bad != 0) s_blk[r] = -1;
+    if (own > 0) atomicOr(p.status + b, own);
   }
   __syncthreads();
-  const int per_row = 2 * p.hkv;                             // K heads, then V heads
-  const int lane = threadIdx.x % kLanes;
-  const int total = nrows * per_row;
   // whole groups of kLanes threads take an item, so the shuffles have all of their lanes
-  for (int it = threadIdx.x / kLanes; it < (total + 32 / kLanes - 1) / (32 / kLanes) * (32 / kLanes);
-       it += blockDim.x / kLanes) {
-    const bool live = it < total;
-    const int r = live ? it / per_row : 0, kvh = live ? it % per_row : 0;
-    const bool isv = kvh >= p.hkv;
-    const int h = isv ? kvh - p.hkv : kvh;
-    const int blk = live ? s_blk[r] : -1;
-    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-    if (blk >= 0)
-      x = *reinterpret_cast<const uint4*>((isv ? p.v_new : p.k_new) + (t0 + r) * p.kv_ld +
-                                          static_cast<long long>(h) * D + lane * 8);
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-    uint32_t top = 0;
+  for (int base = threadIdx.x / kLanes; base - threadIdx.x / kLanes < total; base += kAppendBatch * kItems) {
+    if (base != static_cast<int>(threadIdx.x / kLanes)) load(base);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) top = max(top, max(w[e] & 0x7fffu, (w[e] >> 16) & 0x7fffu));
+    for (int e = 0; e < kAppendBatch; ++e) {
+      const int it = base + e * kItems;
+      int r = 0, kvh = 0;
+      if (it < total) place(it, r, kvh);
+      const int blk = it < total ? s_blk[r] : -1;
+      const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
+      // bits 14..0 of both halves order as integers: halves are compared apart
+      uint32_t top = 0;
 #pragma unroll
-    for (int s = kLanes / 2; s > 0; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
-    if (blk < 0) continue;
-    const KvRowScale sc = kv_row_scale<kFmt>(top);
-    uint32_t c[4];
+      for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] = kv_encode2<kFmt>(bf16_lo(w[e]), bf16_hi(w[e]), sc);
-    const size_t row = (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE + s_slot[r] % TV_BLOCK_SIZE;
-    *reinterpret_cast<uint2*>((isv ? p.v_cache : p.k_cache) + row * D + lane * 8) =
-        make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-    if (lane == 0) (isv ? p.v_scale : p.k_scale)[row] = sc.scale;
+      for (int s = kLanes / 2; s > 0; s >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
+      top = max(top & 0xffffu, top >> 16);
+      if (blk < 0) continue;
+      const KvRowScale sc = kv_row_scale<kFmt>(top);
+      uint2 c = make_uint2(0u, 0u);
+      if (sc.mul != 0.0f) {
+        c.x = kv_encode2<kFmt>(bf16_lo(w[0]), bf16_hi(w[0]), sc) | (kv_encode2<kFmt>(bf16_lo(w[1]), bf16_hi(w[1]), sc) << 16);
+        c.y = kv_encode2<kFmt>(bf16_lo(w[2]), bf16_hi(w[2]), sc) | (kv_encode2<kFmt>(bf16_lo(w[3]), bf16_hi(w[3]), sc) << 16);
+      }
+      const bool isv = kvh >= p.hkv;
+      const int h = isv ? kvh - p.hkv : kvh;
+      const size_t row = (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE + s_slot[r] % TV_BLOCK_SIZE;
+      *reinterpret_cast<uint2*>((isv ? p.v_cache : p.k_cache) + row * D + lane * 8) = c;
+      if (lane == 0) (isv ? p.v_scale : p.k_scale)[row] = sc.scale;
+    }
   }
 }
 
 // ------------------------------------------------------------------ read back
 
 constexpr int kReadThreads = 256;
+constexpr int kReadBatch = 4;          // items a thread has in flight
 
 struct ReadParams {
   const int32_t* first;
@@ -154,64 +196,108 @@ struct ReadParams {
   int batch, hkv, max_blocks, num_blocks, out_max_blocks, out_num_blocks;
 };
 
+// Pages that a request's range touches; a negative end is one page, so that
+// some CTA meets the request and flags it.
+__device__ __forceinline__ int read_pages(int first, int last) {
+  if (first < 0 || last < 0) return 1;
+  return last <= first ? 0 : (last - 1) / TV_BLOCK_SIZE - first / TV_BLOCK_SIZE + 1;
+}
+
+// An item is one head of one page, K and V: 32 D bytes of codes to 64 D bytes
+// of bf16. All items are laid end to end and a CTA takes a contiguous range.
+// A thread turns 8 codes (8 bytes) into one 16-byte store, so that a warp's
+// stores cover whole 32-byte sectors (16 codes a thread and two stores a
+// stride apart: 118 us for the 692 MB of the largest measured case).
 template <int kFmt, int D>
 __global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kVecs = TV_BLOCK_SIZE * D / 8;               // 8-code vectors of K (or V) in an item
+  constexpr int kPer = 2 * kVecs / kReadThreads;             // a thread's vectors in an item: 2 or 1
   grid_dependency_wait();
   grid_launch_dependents();
-  const int b = blockIdx.y;
-  const int st = p.status[b];
-  const int first = p.first ? p.first[b] : 0, last = p.last[b];
-  if (st != 0) return;
-  if (first < 0 || last < 0) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status + b, TV_ST_BAD_SIZE);
-    return;
-  }
-  if (last <= first) return;
-  const int page0 = first / TV_BLOCK_SIZE, page1 = (last - 1) / TV_BLOCK_SIZE;
-  if (static_cast<long long>(page0) + blockIdx.x > page1 && blockIdx.x != 0) return;
-  const int32_t* from = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-  const int32_t* to = p.out_table + static_cast<size_t>(b) * p.out_max_blocks;
-  int bad = page1 >= min(p.n_blocks[b], p.max_blocks) || page1 >= min(p.out_n_blocks[b], p.out_max_blocks);
-  if (!bad) {
-    for (int e = page0 + threadIdx.x; e <= page1; e += blockDim.x) {
-      const int s = from[e], d = to[e];
-      bad |= s < 0 || s >= p.num_blocks || d < 0 || d >= p.out_num_blocks;
-    }
-  }
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(p.status + b, TV_ST_BAD_BLOCK);
-    return;
-  }
-  constexpr int kVecs = TV_BLOCK_SIZE * D / 16;              // 16-byte vectors of codes of a page's head
-  for (int page = page0 + blockIdx.x; page <= page1; page += gridDim.x) {
-    const size_t sblk = from[page], dblk = to[page];
-    for (int i = threadIdx.x; i < 2 * p.hkv * kVecs; i += blockDim.x) {
-      const bool isv = i >= p.hkv * kVecs;
-      const int e = isv ? i - p.hkv * kVecs : i;
-      const int h = e / kVecs, row = e % kVecs / (D / 16), vec = e % (D / 16);
-      const int slot = page * TV_BLOCK_SIZE + row;
-      if (slot < first || slot >= last) continue;
-      const size_t srow = (sblk * p.hkv + h) * TV_BLOCK_SIZE + row;
-      const uint4 c = *reinterpret_cast<const uint4*>((isv ? p.v_cache : p.k_cache) + srow * D + vec * 16);
-      const float sc = (isv ? p.v_scale : p.k_scale)[srow];
-      const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 lo = kv_decode2<kFmt>(w[j] & 0xffffu), hi = kv_decode2<kFmt>(w[j] >> 16);
-        o[2 * j] = pack_bf16x2(lo.x * sc, lo.y * sc);
-        o[2 * j + 1] = pack_bf16x2(hi.x * sc, hi.y * sc);
+  const Share sh = find_share<kReadThreads>(p.batch, 1, [&](int b) {
+    return static_cast<long long>(read_pages(p.first ? p.first[b] : 0, p.last[b])) * p.hkv;
+  });
+  long long at = sh.start;
+  long long pos = sh.lo;
+  for (int b = sh.b; b < p.batch && pos < sh.hi; ++b) {
+    const int first = p.first ? p.first[b] : 0, last = p.last[b], st = p.status[b];
+    const int pages = read_pages(first, last);
+    const long long end = at + static_cast<long long>(pages) * p.hkv;
+    if (pos >= end) { at = end; continue; }
+    const long long stop = end < sh.hi ? end : sh.hi;
+    const int page0 = max(first, 0) / TV_BLOCK_SIZE, page1 = page0 + pages - 1;
+    const int32_t* from = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+    const int32_t* to = p.out_table + static_cast<size_t>(b) * p.out_max_blocks;
+    int bad = 0;
+    if (first < 0 || last < 0) {
+      bad = TV_ST_BAD_SIZE;
+    } else if (page1 >= min(p.n_blocks[b], p.max_blocks) || page1 >= min(p.out_n_blocks[b], p.out_max_blocks)) {
+      bad = TV_ST_BAD_BLOCK;
+    } else {
+      for (int e = page0 + threadIdx.x; e <= page1; e += kReadThreads) {
+        const int s = from[e], d = to[e];
+        if (s < 0 || s >= p.num_blocks || d < 0 || d >= p.out_num_blocks) bad = TV_ST_BAD_BLOCK;
       }
-      uint4* dst = reinterpret_cast<uint4*>((isv ? p.v_out : p.k_out) +
-                                            ((dblk * p.hkv + h) * TV_BLOCK_SIZE + row) * D + vec * 16);
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
     }
+    // status is only OR-ed into after this point of some CTA, by a CTA that found the same fault
+    if (__syncthreads_or(bad | st)) {
+      if (bad && st == 0) atomicOr(p.status + b, bad);
+    } else {
+      const int i0 = static_cast<int>((pos - at) % p.hkv);
+      const int p0 = page0 + static_cast<int>((pos - at) / p.hkv);
+      const int count = static_cast<int>(stop - pos);
+      for (int base = 0; base < count; base += kReadBatch) {
+        uint2 c[kReadBatch][kPer];
+        float sc[kReadBatch][kPer];
+        size_t dst[kReadBatch];
+        bool live[kReadBatch][kPer];
+#pragma unroll
+        for (int e = 0; e < kReadBatch; ++e) {
+          const int i = i0 + base + e;
+          const int page = p0 + i / p.hkv, h = i % p.hkv;
+          const bool there = base + e < count;
+          const size_t src = there ? (static_cast<size_t>(from[page]) * p.hkv + h) * TV_BLOCK_SIZE : 0;
+          dst[e] = there ? (static_cast<size_t>(to[page]) * p.hkv + h) * TV_BLOCK_SIZE : 0;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            const int idx = threadIdx.x + j * kReadThreads;
+            const bool isv = idx >= kVecs;
+            const int v = isv ? idx - kVecs : idx, row = v / (D / 8), slot = page * TV_BLOCK_SIZE + row;
+            live[e][j] = there && slot >= first && slot < last;
+            c[e][j] = make_uint2(0u, 0u);
+            sc[e][j] = 0.0f;
+            if (live[e][j]) {
+              c[e][j] = __ldcs(reinterpret_cast<const uint2*>((isv ? p.v_cache : p.k_cache) + src * D) + v);
+              sc[e][j] = __ldg((isv ? p.v_scale : p.k_scale) + src + row);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < kReadBatch; ++e) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            if (!live[e][j]) continue;
+            const int idx = threadIdx.x + j * kReadThreads;
+            const bool isv = idx >= kVecs;
+            const int v = isv ? idx - kVecs : idx;
+            const float s = sc[e][j];
+            const float2 f0 = kv_decode2<kFmt>(c[e][j].x & 0xffffu), f1 = kv_decode2<kFmt>(c[e][j].x >> 16);
+            const float2 f2 = kv_decode2<kFmt>(c[e][j].y & 0xffffu), f3 = kv_decode2<kFmt>(c[e][j].y >> 16);
+            reinterpret_cast<uint4*>((isv ? p.v_out : p.k_out) + dst[e] * D)[v] =
+                make_uint4(pack_bf16x2(f0.x * s, f0.y * s), pack_bf16x2(f1.x * s, f1.y * s),
+                           pack_bf16x2(f2.x * s, f2.y * s), pack_bf16x2(f3.x * s, f3.y * s));
+          }
+        }
+      }
+    }
+    pos = stop;
+    at = end;
   }
 }
 
-static int check_kv_format(int fmt) {
-  return fmt == TV_KV_E4M3 || fmt == TV_KV_INT8 ? TV_OK : TV_ERR_BAD_GEOMETRY;
+static int check_kv_format(const tv_geom* geom, int fmt) {
+  // row and head numbers within a CTA are divided by multiplication: exact up to 4096 heads
+  return (fmt == TV_KV_E4M3 || fmt == TV_KV_INT8) && geom->num_kv_heads <= 4096 ? TV_OK : TV_ERR_BAD_GEOMETRY;
 }
 
 }  // namespace tv
@@ -225,7 +311,7 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
                                   int32_t* status, void* stream) {
   int rc = tv::check_geom(geom);
   if (rc != TV_OK) return rc;
-  rc = tv::check_kv_format(kv_format);
+  rc = tv::check_kv_format(geom, kv_format);
   if (rc != TV_OK) return rc;
   if (batch < 0 || batch > tv::kKvMaxBatch || rows < 0 || max_blocks_per_req < 1 || num_blocks < 1 ||
       kv_ld < static_cast<long long>(geom->num_kv_heads) * geom->head_dim)
@@ -250,8 +336,19 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   auto* kernel = kv_format == TV_KV_E4M3
       ? (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_E4M3, 64> : tv::kv_quant_append_kernel<TV_KV_E4M3, 128>)
       : (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_INT8, 64> : tv::kv_quant_append_kernel<TV_KV_INT8, 128>);
-  const dim3 grid((rows + tv::kAppendRows - 1) / tv::kAppendRows);
-  const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), 0, tv::as_stream(stream), p);
+  // Rows of a CTA: four loads a thread where that fills the SMs eight times
+  // over, fewer when there are few rows.
+  const int lanes = geom->head_dim / 8, per_row = 2 * p.hkv;
+  long long cta_rows = 4ll * tv::kAppendThreads / (static_cast<long long>(per_row) * lanes);
+  const long long spread = (rows + 152 * 8 - 1) / (152 * 8);
+  if (cta_rows > spread) cta_rows = spread;
+  if (cta_rows < 1) cta_rows = 1;
+  if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
+  p.cta_rows = static_cast<int>(cta_rows);
+  p.heads_magic = static_cast<uint32_t>(((1ull << 32) + per_row - 1) / per_row);
+  const size_t smem = sizeof(int) * (static_cast<size_t>(batch) + 1);
+  const dim3 grid(static_cast<unsigned>((rows + cta_rows - 1) / cta_rows));
+  const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), smem, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
@@ -266,7 +363,7 @@ extern "C" int tv_kv_quant_read(const tv_geom* geom, int32_t kv_format, int32_t 
                                 void* stream) {
   int rc = tv::check_geom(geom);
   if (rc != TV_OK) return rc;
-  rc = tv::check_kv_format(kv_format);
+  rc = tv::check_kv_format(geom, kv_format);
   if (rc != TV_OK) return rc;
   if (batch < 0 || batch > tv::kKvMaxBatch || max_blocks_per_req < 1 || num_blocks < 1 ||
       out_max_blocks_per_req < 1 || out_num_blocks < 1)
@@ -278,6 +375,8 @@ extern "C" int tv_kv_quant_read(const tv_geom* geom, int32_t kv_format, int32_t 
   if (!tv::aligned(k_cache, 16) || !tv::aligned(v_cache, 16) || !tv::aligned(k_out, 16) ||
       !tv::aligned(v_out, 16) || !tv::aligned(k_scale, 4) || !tv::aligned(v_scale, 4))
     return TV_ERR_MISALIGNED;
+  const int dev = tv::current_device();
+  if (dev < 0) return TV_ERR_CUDA;
   tv::ReadParams p = {};
   p.first = first; p.last = last; p.block_table = block_table; p.n_blocks = n_blocks;
   p.k_cache = static_cast<const uint8_t*>(k_cache); p.v_cache = static_cast<const uint8_t*>(v_cache);
@@ -290,8 +389,12 @@ extern "C" int tv_kv_quant_read(const tv_geom* geom, int32_t kv_format, int32_t 
   auto* kernel = kv_format == TV_KV_E4M3
       ? (geom->head_dim == 64 ? tv::kv_quant_read_kernel<TV_KV_E4M3, 64> : tv::kv_quant_read_kernel<TV_KV_E4M3, 128>)
       : (geom->head_dim == 64 ? tv::kv_quant_read_kernel<TV_KV_INT8, 64> : tv::kv_quant_read_kernel<TV_KV_INT8, 128>);
-  const int pages = max_blocks_per_req < out_max_blocks_per_req ? max_blocks_per_req : out_max_blocks_per_req;
-  const dim3 grid(pages < 256 ? pages : 256, batch);
+  // as many CTAs as are resident, or as there can be items
+  const int sms = tv::device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
+  const long long pages = max_blocks_per_req < out_max_blocks_per_req ? max_blocks_per_req : out_max_blocks_per_req;
+  const long long items = pages * batch * p.hkv, most = static_cast<long long>(sms) * 6;
+  const dim3 grid(static_cast<unsigned>(items < most ? items : most));
   const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kReadThreads), 0, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }

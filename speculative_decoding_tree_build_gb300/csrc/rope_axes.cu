@@ -10,15 +10,17 @@
 // sincospif.
 //
 // Memory bound: every value is read and written once, 6 float operations a
-// pair. One CTA rotates a few rows; the sines and cosines of a row are
-// computed once in shared memory and used by all of its heads.
+// pair. One CTA rotates a few rows (or some heads of one row); the sines and
+// cosines of a row are computed once in shared memory and used by all of its
+// heads, and each thread's first vectors are in flight meanwhile.
 #include "tv_common.cuh"
 
 namespace tv {
 
 constexpr int kRopeAxThreads = 256;
 constexpr int kRopeAxMaxPairs = 256;
-constexpr int kRopeAxRows = 4;         // rows per CTA
+constexpr int kRopeAxMaxRows = 8;      // rows per CTA at most
+constexpr int kRopeAxBatch = 4;        // items a thread has in flight
 
 struct RopeAxParams {
   const void* q;
@@ -28,64 +30,174 @@ struct RopeAxParams {
   void* q_out;
   void* k_out;
   long long q_ld, k_ld, q_out_ld, k_out_ld, pos_ld;
-  int rows, hq, hkv, d, pairs, style;
+  int rows, hq, heads, d, pairs;
+  int cta_rows, cta_heads, groups;     // a CTA's rows and heads; head groups per row block
+  int units, rot_units;                // items of a head; those of them that rotate
+  uint32_t units_magic, heads_magic;   // ceil(2^32 / units), ceil(2^32 / cta_heads)
   uint8_t axis[kRopeAxMaxPairs];
 };
 
-__device__ __forceinline__ float rope_load(const float* p) { return *p; }
-__device__ __forceinline__ float rope_load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void rope_store(float* p, float x) { *p = x; }
-__device__ __forceinline__ void rope_store(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+template <typename T, int N>
+struct alignas(sizeof(T) * N) RopeVec {
+  T x[N];
+};
 
-// cos and sin of position * inv_freq
-__device__ __forceinline__ float2 rope_cos_sin(int position, float inv_freq) {
-  double turns = static_cast<double>(inv_freq) * 0.15915494309189533577;   // 1 / (2 pi)
-  turns -= floor(turns);
-  const unsigned long long f = __double2ull_rn(turns * 18446744073709551616.0);
-  const unsigned long long a = static_cast<unsigned long long>(static_cast<long long>(position)) * f;
-  // the fraction of a turn in [-1/2, 1/2), in half turns for sincospif
-  const float half_turns = static_cast<float>(static_cast<int>(a >> 32)) * (1.0f / 2147483648.0f);
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(c, s);
+__device__ __forceinline__ float rope_float(float x) { return x; }
+__device__ __forceinline__ float rope_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void rope_round(float& y, float x) { y = x; }
+__device__ __forceinline__ void rope_round(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
+
+// i / n for i * n < 2^32
+__device__ __forceinline__ int rope_div(int i, int n, uint32_t magic) {
+  return n == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
 }
 
-template <typename T>
+// T: element, N: elements of a vector, kHalves: rotary style 1 (a pair's two
+// columns lie in two vectors; else N = 1 or both are in one vector).
+template <typename T, int N, bool kHalves>
 __global__ void __launch_bounds__(kRopeAxThreads) rope_axes_kernel(const __grid_constant__ RopeAxParams p) {
-  __shared__ float2 s_cs[kRopeAxRows * kRopeAxMaxPairs];
+  // pairs of an item, and whether it holds a second vector
+  constexpr int P = kHalves ? N : (N == 1 ? 1 : N / 2);
+  constexpr bool kTwo = kHalves || N == 1;
+  using Vec = RopeVec<T, N>;
+  __shared__ unsigned long long s_f[kRopeAxMaxPairs];
+  __shared__ __align__(16) float s_cos[kRopeAxMaxRows * kRopeAxMaxPairs];
+  __shared__ __align__(16) float s_sin[kRopeAxMaxRows * kRopeAxMaxPairs];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int row0 = blockIdx.x * kRopeAxRows;
-  const int nrows = min(kRopeAxRows, p.rows - row0);
-  for (int i = threadIdx.x; i < nrows * p.pairs; i += blockDim.x) {
-    const int r = i / p.pairs, pr = i % p.pairs;
-    s_cs[i] = rope_cos_sin(p.positions[p.axis[pr] * p.pos_ld + row0 + r], p.inv_freq[pr]);
+  const int block = blockIdx.x / p.groups, group = blockIdx.x - block * p.groups;
+  const int row0 = block * p.cta_rows, nrows = min(p.cta_rows, p.rows - row0);
+  const int head0 = group * p.cta_heads;
+  const int total = nrows * p.cta_heads * p.units;
+
+  Vec va[kRopeAxBatch], vb[kRopeAxBatch];
+  auto place = [&](int i, int& u, int& r, int& h) {
+    const int rh = rope_div(i, p.units, p.units_magic);
+    u = i - rh * p.units;
+    r = rope_div(rh, p.cta_heads, p.heads_magic);
+    h = head0 + rh - r * p.cta_heads;
+  };
+  // the columns of an item's two vectors
+  auto columns = [&](int u, int& ca, int& cb) {
+    if (u < p.rot_units) {
+      ca = kHalves ? u * N : u * (N == 1 ? 2 : N);
+      cb = kHalves ? ca + p.pairs : ca + 1;
+    } else {
+      ca = 2 * p.pairs + (u - p.rot_units) * N;
+      cb = -1;
+    }
+  };
+  auto load = [&](int base) {
+#pragma unroll
+    for (int e = 0; e < kRopeAxBatch; ++e) {
+      const int i = base + e * kRopeAxThreads;
+      if (i >= total) break;
+      int u, r, h, ca, cb;
+      place(i, u, r, h);
+      if (h >= p.heads) continue;
+      columns(u, ca, cb);
+      const long long row = row0 + r;
+      const T* src = h < p.hq ? static_cast<const T*>(p.q) + row * p.q_ld + static_cast<long long>(h) * p.d
+                              : static_cast<const T*>(p.k) + row * p.k_ld + static_cast<long long>(h - p.hq) * p.d;
+      va[e] = *reinterpret_cast<const Vec*>(src + ca);
+      if (kTwo && cb >= 0) vb[e] = *reinterpret_cast<const Vec*>(src + cb);
+    }
+  };
+  load(threadIdx.x);                   // the first items are on their way while the angles are made
+
+  // inv_freq as a 64-bit fraction of a turn
+  for (int i = threadIdx.x; i < p.pairs; i += kRopeAxThreads) {
+    double turns = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;   // 1 / (2 pi)
+    turns -= floor(turns);
+    s_f[i] = __double2ull_rn(turns * 18446744073709551616.0);
   }
   __syncthreads();
-  // one thread per pair (or pair of passed-through columns) of one head
-  const int half = p.d / 2, rest = p.d - 2 * p.pairs, units = p.pairs + (rest + 1) / 2;
-  (void)half;
-  const int heads = p.hq + p.hkv;
-  for (int i = threadIdx.x; i < nrows * heads * units; i += blockDim.x) {
-    const int r = i / (heads * units), h = i / units % heads, u = i % units;
-    const long long row = row0 + r;
-    const bool isq = h < p.hq;
-    const T* src = isq ? static_cast<const T*>(p.q) + row * p.q_ld + static_cast<long long>(h) * p.d
-                       : static_cast<const T*>(p.k) + row * p.k_ld + static_cast<long long>(h - p.hq) * p.d;
-    T* dst = isq ? static_cast<T*>(p.q_out) + row * p.q_out_ld + static_cast<long long>(h) * p.d
-                 : static_cast<T*>(p.k_out) + row * p.k_out_ld + static_cast<long long>(h - p.hq) * p.d;
-    if (u < p.pairs) {
-      const int ca = p.style ? u : 2 * u, cb = p.style ? u + p.pairs : 2 * u + 1;
-      const float2 cs = s_cs[r * p.pairs + u];
-      const float a = rope_load(src + ca), b = rope_load(src + cb);
-      rope_store(dst + ca, a * cs.x - b * cs.y);
-      rope_store(dst + cb, b * cs.x + a * cs.y);
-    } else {
-      const int c = 2 * u;
-      dst[c] = src[c];
-      if (c + 1 < p.d) dst[c + 1] = src[c + 1];
+  for (int i = threadIdx.x; i < nrows * p.pairs; i += kRopeAxThreads) {
+    const int r = i / p.pairs, pr = i - r * p.pairs;
+    const long long position = p.positions[p.axis[pr] * p.pos_ld + row0 + r];
+    const unsigned long long a = static_cast<unsigned long long>(position) * s_f[pr];
+    // the fraction of a turn in [-1/2, 1/2), in half turns for sincospif
+    const float half_turns = static_cast<float>(static_cast<int>(a >> 32)) * (1.0f / 2147483648.0f);
+    sincospif(half_turns, &s_sin[i], &s_cos[i]);
+  }
+  __syncthreads();
+
+  for (int base = threadIdx.x; base < total; base += kRopeAxBatch * kRopeAxThreads) {
+    if (base != static_cast<int>(threadIdx.x)) load(base);
+#pragma unroll
+    for (int e = 0; e < kRopeAxBatch; ++e) {
+      const int i = base + e * kRopeAxThreads;
+      if (i >= total) break;
+      int u, r, h, ca, cb;
+      place(i, u, r, h);
+      if (h >= p.heads) continue;
+      columns(u, ca, cb);
+      const long long row = row0 + r;
+      T* dst = h < p.hq ? static_cast<T*>(p.q_out) + row * p.q_out_ld + static_cast<long long>(h) * p.d
+                        : static_cast<T*>(p.k_out) + row * p.k_out_ld + static_cast<long long>(h - p.hq) * p.d;
+      if (u < p.rot_units) {
+        const float* cs = s_cos + r * p.pairs + u * P;
+        const float* sn = s_sin + r * p.pairs + u * P;
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          T& xa = kTwo ? va[e].x[j] : va[e].x[2 * j];
+          T& xb = kTwo ? vb[e].x[j] : va[e].x[2 * j + (N > 1 ? 1 : 0)];
+          const float a = rope_float(xa), b = rope_float(xb);
+          rope_round(xa, a * cs[j] - b * sn[j]);
+          rope_round(xb, b * cs[j] + a * sn[j]);
+        }
+        if (kTwo) *reinterpret_cast<Vec*>(dst + cb) = vb[e];
+      }
+      *reinterpret_cast<Vec*>(dst + ca) = va[e];
     }
   }
+}
+
+template <typename T, int N>
+static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t stream) {
+  const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
+  p.rot_units = p.pairs / per_unit;
+  p.units = p.rot_units + (p.d - 2 * p.pairs) / N;
+  // Rows and heads of a CTA: four to ten items a thread when there is work
+  // for every SM, down to one item a thread (a head group of one row) when
+  // there is little, so that few rows still spread over the chip.
+  const long long row_items = static_cast<long long>(p.heads) * p.units;
+  long long per = row_items * p.rows / (152 * 8);
+  per = per < kRopeAxThreads ? kRopeAxThreads : per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per;
+  if (per >= row_items) {
+    p.cta_rows = static_cast<int>(per / row_items);
+    if (p.cta_rows > kRopeAxMaxRows) p.cta_rows = kRopeAxMaxRows;
+    p.cta_heads = p.heads;
+    p.groups = 1;
+  } else {
+    p.cta_rows = 1;
+    const long long groups = (row_items + per - 1) / per;
+    p.cta_heads = static_cast<int>((p.heads + groups - 1) / groups);
+    p.groups = (p.heads + p.cta_heads - 1) / p.cta_heads;
+  }
+  p.units_magic = static_cast<uint32_t>(((1ull << 32) + p.units - 1) / p.units);
+  p.heads_magic = static_cast<uint32_t>(((1ull << 32) + p.cta_heads - 1) / p.cta_heads);
+  const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  auto* kernel = halves ? rope_axes_kernel<T, N, true> : rope_axes_kernel<T, N, false>;
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRopeAxThreads), 0, stream, p);
+}
+
+// The widest vector (16 or 8 bytes, else single elements) that the addresses,
+// strides, head dimension and pairs allow.
+template <typename T>
+static cudaError_t launch_rope_axes_any(const RopeAxParams& p, bool halves, bool keys, cudaStream_t stream) {
+  auto fits = [&](int n) {
+    const uintptr_t bytes = n * sizeof(T);
+    const int cols = halves ? p.pairs : 2 * p.pairs;
+    return p.d % n == 0 && cols % n == 0 && p.q_ld % n == 0 && p.q_out_ld % n == 0 && aligned(p.q, bytes) &&
+           aligned(p.q_out, bytes) &&
+           (!keys || (p.k_ld % n == 0 && p.k_out_ld % n == 0 && aligned(p.k, bytes) && aligned(p.k_out, bytes)));
+  };
+  constexpr int kFull = 16 / sizeof(T);
+  if (fits(kFull)) return launch_rope_axes<T, kFull>(p, halves, stream);
+  if (fits(kFull / 2)) return launch_rope_axes<T, kFull / 2>(p, halves, stream);
+  return launch_rope_axes<T, 1>(p, halves, stream);
 }
 
 }  // namespace tv
@@ -120,8 +232,7 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
   tv::RopeAxParams p = {};
   p.q = q; p.k = k; p.positions = positions; p.inv_freq = inv_freq; p.q_out = q_out; p.k_out = k_out;
   p.q_ld = q_ld; p.k_ld = k_ld; p.q_out_ld = q_out_ld; p.k_out_ld = k_out_ld; p.pos_ld = pos_ld;
-  p.rows = rows; p.hq = g->num_q_heads; p.hkv = g->num_kv_heads; p.d = g->head_dim; p.pairs = pairs;
-  p.style = g->rope_style;
+  p.rows = rows; p.hq = g->num_q_heads; p.heads = g->num_q_heads + g->num_kv_heads; p.d = g->head_dim; p.pairs = pairs;
   int left[TV_MAX_ROPE_AXES] = {0};
   for (int a = 0; a < g->num_axes; ++a) left[a] = g->section[a];
   for (int i = 0, a = 0; i < pairs;) {
@@ -133,9 +244,9 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
       a = (a + 1) % g->num_axes;
     }
   }
-  const dim3 grid((rows + tv::kRopeAxRows - 1) / tv::kRopeAxRows);
+  const bool halves = g->rope_style == 1;
   const cudaError_t err = dtype == TV_DTYPE_BF16
-      ? tv::launch_pdl(tv::rope_axes_kernel<__nv_bfloat16>, grid, dim3(tv::kRopeAxThreads), 0, tv::as_stream(stream), p)
-      : tv::launch_pdl(tv::rope_axes_kernel<float>, grid, dim3(tv::kRopeAxThreads), 0, tv::as_stream(stream), p);
+      ? tv::launch_rope_axes_any<__nv_bfloat16>(p, halves, keys, tv::as_stream(stream))
+      : tv::launch_rope_axes_any<float>(p, halves, keys, tv::as_stream(stream));
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }

@@ -9,11 +9,11 @@ namespace tv {
 
 constexpr int kKvMaxBatch = 4096;
 
-// What a row's codes are made from: its scale and the factors of its values.
+// What a row's codes are made from: its scale and the factor of its values.
 struct KvRowScale {
   float scale;   // stored beside the codes; NaN when the row is not finite
-  float mul;     // e4m3: 1 / scale, a power of two, so x * mul is x / scale exactly
-  float div;     // int8: code = rint(x * mul / div)
+  float mul;     // e4m3: 1 / scale; int8: 127 / largest magnitude; 0: all codes are 0
+  float pre;     // int8: a power of two that keeps mul in range, applied first
 };
 
 // `top` = largest magnitude of the row's bf16 values as bits 14..0 of bf16.
@@ -22,46 +22,49 @@ struct KvRowScale {
 template <int kFmt>
 __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
   KvRowScale r;
-  const bool finite = top < 0x7f80u;
   const float a = __uint_as_float(top << 16);
+  r.pre = 1.0f;
   if constexpr (kFmt == TV_KV_E4M3) {
     // a = 2^E * m, 1 <= m < 2: 448 = 1.75 * 2^8, so n = E - 8, one more when
     // m > 1.75 (bf16 significand bits above 0x60), and not below -100
     int n = static_cast<int>(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
     n = max(n, -100);
     r.scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
-    r.mul = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);   // n <= 120
-    r.div = 1.0f;
+    r.mul = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);   // n <= 120: exact, as is x * mul
   } else {
     const float b = fmaxf(a, 7.888609052210118e-31f);                // 2^-100
     r.scale = __fdiv_rn(b, 127.0f);
-    // 127 x must not overflow: large rows are scaled down, exactly
-    const float down = b > 1e30f ? 9.5367431640625e-07f : 1.0f;      // 2^-20
-    r.mul = 127.0f * down;
-    r.div = b * down;
+    if (b > 1e30f) r.pre = 9.5367431640625e-07f;                     // 2^-20: keeps mul a normal number
+    r.mul = __fdiv_rn(127.0f, b * r.pre);
   }
-  if (!finite) {
+  if (top >= 0x7f80u) {
     r.scale = __uint_as_float(0x7fc00000u);
     r.mul = 0.0f;
-    r.div = 1.0f;
   }
   return r;
 }
 
-// Two values to two codes (first in the low byte). bf16 x 127 and the float32
-// quotient: 127 x has 15 significant bits and the divisor 8, so a quotient
-// that is not a tie lies at least 2^-9 of an integer step away from one and
-// the quotient's own rounding cannot reach it; exact ties come out exact.
+// The int8 code of x in the low byte. The exact quotient Q = 127 x / a of two
+// bf16 numbers is 127 X / (A 2^k) with X, A < 2^8, so unless it is a tie (an
+// integer and a half) it lies at least |Q| / (254 X) > 2^-16 |Q| away from
+// one. x * fl(127 / a) is within 2^-22 |Q| of it. So a product within
+// 2^-18 |Q| of half an integer IS that number, and is set to it before it is
+// rounded to even; every other one rounds as Q does.
+__device__ __forceinline__ uint32_t kv_int8_code(float x, const KvRowScale& r) {
+  const float magic = 12582912.0f;                                   // 1.5 * 2^23: rounds to an integer
+  const float y = x * r.pre * r.mul;
+  const float twice = __fadd_rn(__fadd_rn(2.0f * y, magic), -magic); // nearest half integer, doubled
+  const float snapped = fabsf(2.0f * y - twice) <= 7.62939453125e-06f * fabsf(y) ? 0.5f * twice : y;
+  return __float_as_uint(__fadd_rn(snapped, magic)) & 0xffu;
+}
+
+// Two values to two codes (first in the low byte).
 template <int kFmt>
 __device__ __forceinline__ uint32_t kv_encode2(float x, float y, const KvRowScale& r) {
   if constexpr (kFmt == TV_KV_E4M3) {
-    if (r.mul == 0.0f) return 0u;                                    // 0 * infinity is NaN
     return __nv_cvt_float2_to_fp8x2(make_float2(x * r.mul, y * r.mul), __NV_SATFINITE, __NV_E4M3);
   } else {
-    if (r.mul == 0.0f) return 0u;
-    const int a = __float2int_rn(__fdiv_rn(x * r.mul, r.div));
-    const int b = __float2int_rn(__fdiv_rn(y * r.mul, r.div));
-    return (static_cast<uint32_t>(a) & 0xffu) | ((static_cast<uint32_t>(b) & 0xffu) << 8);
+    return kv_int8_code(x, r) | (kv_int8_code(y, r) << 8);
   }
 }
 

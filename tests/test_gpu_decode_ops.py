@@ -292,6 +292,26 @@ def test_append_offsets_past_the_rows_are_flagged():
     before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
     assert run_append(c, k, v, [0, 4, 9], [0, 0]) == [0, 1]    # rows 4..8 of 6
     check_append(c, before, k, v, [0, 4, 9], [0, 0], [0])
+    assert run_append(c, k, v, [0, 4, 4], [0, -1]) == [0, 0]   # no rows, nothing to object to
+    c = Cache(26, [32, 32, 32], 1, 64, "e4m3")
+    assert run_append(c, k, v, [0, 6, 6, 9], [0, 0, 0]) == [0, 0, 1]    # rows 6..8 of 6
+
+
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+def test_append_every_pair_of_significands(held):
+    """Every bf16 significand under every largest one, at eight binary distances: all exact ties
+    of the quotient, and the quotients nearest to one."""
+    top = torch.arange(128, 256).float().repeat_interleave(8)
+    x = torch.arange(128, 256).float()[None] * torch.exp2(-torch.arange(1, 9).float()).repeat(128)[:, None]
+    x[:, 127] = top                                   # 255 gives way to the largest
+    y = torch.arange(128, 256).float()[None] * torch.exp2(-torch.arange(1, 9).float()).repeat(128)[:, None]
+    y[:, 0] = -top
+    k, v = x.to(BF16).cuda()[:, None], y.to(BF16).cuda()[:, None]
+    assert bool((k.float().cpu()[:, 0] == x).all())
+    c = Cache(28, [1024], 1, 128, held)
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    assert run_append(c, k, v, [0, 1024], [0]) == [0]
+    check_append(c, before, k, v, [0, 1024], [0], [0])
 
 
 @pytest.mark.parametrize("held", ["e4m3", "int8"])
