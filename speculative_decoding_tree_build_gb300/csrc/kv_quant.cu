@@ -14,7 +14,7 @@
 namespace tv {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendBatch = 4;      // 16-byte loads a thread has in flight
+constexpr int kAppendBatch = 4;      // rows whose loads a thread has in flight
 constexpr int kAppendMaxRows = 64;   // rows of k_new / v_new per CTA at most
 
 struct AppendParams {
@@ -31,7 +31,8 @@ struct AppendParams {
   float* v_scale;
   int32_t* status;
   int batch, rows, hkv, max_blocks, num_blocks, cta_rows;
-  uint32_t heads_magic;              // ceil(2^32 / (2 hkv))
+  int cta_heads;                     // of the 2 hkv heads of a row (K's, then V's), taken at a time
+  int slots;                         // rows taken at a time
 };
 
 // The request that owns row t: the largest b with cu[b] <= t (requests without
@@ -49,7 +50,6 @@ __device__ __forceinline__ int request_of_row(const int32_t* cu, int batch, int 
 template <int kFmt, int D>
 __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 8;        // lanes that hold one row
-  constexpr int kItems = kAppendThreads / kLanes;                      // rows of heads a sweep takes
   extern __shared__ int s_cu[];        // [batch + 1]
   __shared__ int s_req[kAppendMaxRows], s_slot[kAppendMaxRows], s_blk[kAppendMaxRows], s_bad[kAppendMaxRows];
   __shared__ int s_first[kAppendMaxRows], s_pages[kAppendMaxRows];     // of a run's request: its span
@@ -57,32 +57,26 @@ __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const _
   grid_launch_dependents();
   const int t0 = blockIdx.x * p.cta_rows;
   const int nrows = min(p.cta_rows, p.rows - t0);
-  const int per_row = 2 * p.hkv;                                       // K heads, then V heads
-  const int total = nrows * per_row, lane = threadIdx.x % kLanes;
+  // kLanes threads keep one head and step through the CTA's rows
+  const int part = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int slot0 = part / p.cta_heads, head = blockIdx.y * p.cta_heads + part - slot0 * p.cta_heads;
+  const bool mine = slot0 < p.slots && head < 2 * p.hkv;
+  const bool isv = head >= p.hkv;
+  const int h = isv ? head - p.hkv : head;
+  const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + static_cast<long long>(h) * D + lane * 8;
   uint4 x[kAppendBatch];
-  auto place = [&](int it, int& r, int& kvh) {
-    r = static_cast<int>(__umulhi(static_cast<uint32_t>(it), p.heads_magic));
-    kvh = it - r * per_row;
-  };
-  auto load = [&](int base) {
+  auto load = [&](int r0) {
 #pragma unroll
     for (int e = 0; e < kAppendBatch; ++e) {
-      const int it = base + e * kItems;
-      x[e] = make_uint4(0u, 0u, 0u, 0u);
-      if (it < total) {
-        int r, kvh;
-        place(it, r, kvh);
-        const bool isv = kvh >= p.hkv;
-        const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + (t0 + r) * p.kv_ld;
-        x[e] = *reinterpret_cast<const uint4*>(src + static_cast<long long>(isv ? kvh - p.hkv : kvh) * D + lane * 8);
-      }
+      const int r = r0 + e * p.slots;
+      x[e] = mine && r < nrows ? *reinterpret_cast<const uint4*>(src + (t0 + r) * p.kv_ld) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  load(threadIdx.x / kLanes);          // on their way while the rows' slots are found
+  load(slot0);                         // on their way while the rows' slots are found
 
   for (int i = threadIdx.x; i <= p.batch; i += kAppendThreads) s_cu[i] = p.cu_rows[i];
   __syncthreads();
-  if (blockIdx.x == 0) {               // requests whose rows lie past the array, in part or altogether
+  if (blockIdx.x == 0 && blockIdx.y == 0) {    // requests whose rows lie past the array, in part or altogether
     for (int b = threadIdx.x; b < p.batch; b += kAppendThreads)
       if (s_cu[b + 1] > p.rows && s_cu[b + 1] > s_cu[b] && p.status[b] == 0) atomicOr(p.status + b, TV_ST_BAD_SIZE);
   }
@@ -141,20 +135,19 @@ __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const _
     if (own > 0) atomicOr(p.status + b, own);
   }
   __syncthreads();
-  // whole groups of kLanes threads take an item, so the shuffles have all of their lanes
-  for (int base = threadIdx.x / kLanes; base - threadIdx.x / kLanes < total; base += kAppendBatch * kItems) {
-    if (base != static_cast<int>(threadIdx.x / kLanes)) load(base);
+  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + lane * 8;
+  float* scales = isv ? p.v_scale : p.k_scale;
+  for (int r0 = 0; r0 < nrows; r0 += kAppendBatch * p.slots) {
+    if (r0 > 0) load(r0 + slot0);
 #pragma unroll
     for (int e = 0; e < kAppendBatch; ++e) {
-      const int it = base + e * kItems;
-      int r = 0, kvh = 0;
-      if (it < total) place(it, r, kvh);
-      const int blk = it < total ? s_blk[r] : -1;
+      if (r0 + e * p.slots >= nrows) break;                  // the same for all threads: the shuffles are whole
+      const int r = r0 + slot0 + e * p.slots;
+      const int blk = mine && r < nrows ? s_blk[r] : -1;
       const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
       // bits 14..0 of both halves order as integers: halves are compared apart
-      uint32_t top = 0;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) top = __vmaxu2(top, w[j] & 0x7fff7fffu);
+      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                              __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
 #pragma unroll
       for (int s = kLanes / 2; s > 0; s >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
       top = max(top & 0xffffu, top >> 16);
@@ -165,11 +158,9 @@ __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const _
         c.x = kv_encode2<kFmt>(bf16_lo(w[0]), bf16_hi(w[0]), sc) | (kv_encode2<kFmt>(bf16_lo(w[1]), bf16_hi(w[1]), sc) << 16);
         c.y = kv_encode2<kFmt>(bf16_lo(w[2]), bf16_hi(w[2]), sc) | (kv_encode2<kFmt>(bf16_lo(w[3]), bf16_hi(w[3]), sc) << 16);
       }
-      const bool isv = kvh >= p.hkv;
-      const int h = isv ? kvh - p.hkv : kvh;
       const size_t row = (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE + s_slot[r] % TV_BLOCK_SIZE;
-      *reinterpret_cast<uint2*>((isv ? p.v_cache : p.k_cache) + row * D + lane * 8) = c;
-      if (lane == 0) (isv ? p.v_scale : p.k_scale)[row] = sc.scale;
+      *reinterpret_cast<uint2*>(codes + row * D) = c;
+      if (lane == 0) scales[row] = sc.scale;
     }
   }
 }
@@ -296,7 +287,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __gri
 }
 
 static int check_kv_format(const tv_geom* geom, int fmt) {
-  // row and head numbers within a CTA are divided by multiplication: exact up to 4096 heads
+  // heads go to grid.y in blocks of 16 or 32
   return (fmt == TV_KV_E4M3 || fmt == TV_KV_INT8) && geom->num_kv_heads <= 4096 ? TV_OK : TV_ERR_BAD_GEOMETRY;
 }
 
@@ -336,18 +327,22 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   auto* kernel = kv_format == TV_KV_E4M3
       ? (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_E4M3, 64> : tv::kv_quant_append_kernel<TV_KV_E4M3, 128>)
       : (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_INT8, 64> : tv::kv_quant_append_kernel<TV_KV_INT8, 128>);
-  // Rows of a CTA: four loads a thread where that fills the SMs eight times
-  // over, fewer when there are few rows.
-  const int lanes = geom->head_dim / 8, per_row = 2 * p.hkv;
-  long long cta_rows = 4ll * tv::kAppendThreads / (static_cast<long long>(per_row) * lanes);
-  const long long spread = (rows + 152 * 8 - 1) / (152 * 8);
-  if (cta_rows > spread) cta_rows = spread;
-  if (cta_rows < 1) cta_rows = 1;
+  // A CTA takes up to 256 / (D / 8) heads of a row at a time, several rows at
+  // a time when a row has fewer, and two batches of loads a thread where that
+  // still gives every SM eight CTAs (fewer rows than that: down to one sweep).
+  const int parts = tv::kAppendThreads / (geom->head_dim / 8), heads = 2 * p.hkv;
+  p.cta_heads = heads < parts ? heads : parts;
+  p.slots = parts / p.cta_heads;
+  const int head_blocks = (heads + p.cta_heads - 1) / p.cta_heads;
+  const long long ctas = 152 * 8 / head_blocks + 1;
+  long long cta_rows = (rows + ctas - 1) / ctas;
+  const long long most = 2ll * tv::kAppendBatch * p.slots;
+  if (cta_rows > most) cta_rows = most;
   if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
+  cta_rows = (cta_rows + p.slots - 1) / p.slots * p.slots;
   p.cta_rows = static_cast<int>(cta_rows);
-  p.heads_magic = static_cast<uint32_t>(((1ull << 32) + per_row - 1) / per_row);
   const size_t smem = sizeof(int) * (static_cast<size_t>(batch) + 1);
-  const dim3 grid(static_cast<unsigned>((rows + cta_rows - 1) / cta_rows));
+  const dim3 grid(static_cast<unsigned>((rows + cta_rows - 1) / cta_rows), head_blocks);
   const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), smem, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }

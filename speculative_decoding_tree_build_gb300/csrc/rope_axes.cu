@@ -3,24 +3,30 @@
 // Pair i of row t turns by positions[axis(i)][t] * inv_freq[i]. The angle is
 // wanted modulo one turn, and float32 has no digits left for that at far
 // positions (at position 10^6 its last bit is 0.06 rad). So inv_freq is held
-// as a 64-bit fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64, and the
-// integer product position * F modulo 2^64 IS the angle's fraction of a turn,
-// with an error of |position| * 2^-64 turns from F's own rounding (and of
-// 2^-53 of the angle from inv_freq / 2 pi in float64). Its top 32 bits go to
-// sincospif.
+// as a 64-bit fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64, made from
+// the float's significand and a 64-bit 1 / 2 pi by integer arithmetic, and
+// the integer product position * F modulo 2^64 IS the angle's fraction of a
+// turn, within |position| * 2^-63 turns. Its top 32 bits give the quadrant and
+// a remainder of at most an eighth of a turn, for which the Taylor series of
+// sine and cosine end below float32's last bit after five and six terms.
 //
 // Memory bound: every value is read and written once, 6 float operations a
 // pair. One CTA rotates a few rows (or some heads of one row); the sines and
-// cosines of a row are computed once in shared memory and used by all of its
-// heads, and each thread's first vectors are in flight meanwhile.
+// cosines of a row are computed once in shared memory. A thread keeps the same
+// columns and the same (at most four) heads of every row it takes, so it
+// reads a row's sines once into registers and steps its pointers by a fixed
+// stride; its first vectors are in flight while the angles are made.
+// (Items numbered across rows, heads and columns, with divisions for each,
+// float64 for F and sincospif took 175 instructions a vector and were bound
+// by issue: 93 us for 332 MB.)
 #include "tv_common.cuh"
 
 namespace tv {
 
 constexpr int kRopeAxThreads = 256;
 constexpr int kRopeAxMaxPairs = 256;
-constexpr int kRopeAxMaxRows = 8;      // rows per CTA at most
-constexpr int kRopeAxBatch = 4;        // items a thread has in flight
+constexpr int kRopeAxAngles = 2048;    // rows x pairs of a CTA at most
+constexpr int kRopeAxBatch = 4;        // heads of a row that a thread takes at most
 
 struct RopeAxParams {
   const void* q;
@@ -30,10 +36,11 @@ struct RopeAxParams {
   void* q_out;
   void* k_out;
   long long q_ld, k_ld, q_out_ld, k_out_ld, pos_ld;
+  long long q_step, k_step, q_out_step, k_out_step;   // row_slots rows on
   int rows, hq, heads, d, pairs;
   int cta_rows, cta_heads, groups;     // a CTA's rows and heads; head groups per row block
-  int units, rot_units;                // items of a head; those of them that rotate
-  uint32_t units_magic, heads_magic;   // ceil(2^32 / units), ceil(2^32 / cta_heads)
+  int units, rot_units;                // column units of a head; those of them that rotate
+  int head_slots, row_slots;           // heads and rows that the CTA's threads take at a time
   uint8_t axis[kRopeAxMaxPairs];
 };
 
@@ -47,108 +54,185 @@ __device__ __forceinline__ float rope_float(__nv_bfloat16 x) { return __bfloat16
 __device__ __forceinline__ void rope_round(float& y, float x) { y = x; }
 __device__ __forceinline__ void rope_round(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
-// i / n for i * n < 2^32
-__device__ __forceinline__ int rope_div(int i, int n, uint32_t magic) {
-  return n == 1 ? i : static_cast<int>(__umulhi(static_cast<uint32_t>(i), magic));
+// inv_freq as a 64-bit fraction of a turn: |inv_freq| = m 2^(e - 150) with an
+// integer m < 2^24, and 1 / 2 pi = C 2^-66, so F = m C 2^(e - 152) modulo 2^64.
+__device__ __forceinline__ unsigned long long rope_turns(float inv_freq) {
+  constexpr unsigned long long kC = 11743562013128004906ull;         // 2^66 / 2 pi
+  const uint32_t bits = __float_as_uint(inv_freq);
+  const uint32_t field = (bits >> 23) & 0xffu;
+  const unsigned long long m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
+  const int shift = 152 - static_cast<int>(field ? field : 1u);
+  const unsigned long long lo = m * kC, hi = __umul64hi(m, kC);
+  unsigned long long f;
+  if (shift <= 0) f = shift > -64 ? lo << -shift : 0ull;
+  else if (shift < 64) f = (lo >> shift) | (hi << (64 - shift));
+  else f = shift < 128 ? hi >> (shift - 64) : 0ull;
+  return bits >> 31 ? 0ull - f : f;
+}
+
+// (cos, sin) of position * F / 2^64 turns.
+__device__ __forceinline__ float2 rope_cos_sin(int position, unsigned long long f) {
+  const uint32_t lo = static_cast<uint32_t>(f), hi = static_cast<uint32_t>(f >> 32), pos = static_cast<uint32_t>(position);
+  // bits 63..32 of the product: the angle in 2^-32 turns
+  const uint32_t a = __umulhi(pos, lo) + pos * hi - (position < 0 ? lo : 0u);
+  const uint32_t quarter = (a + 0x20000000u) >> 30;                  // nearest quarter turn
+  const float x = static_cast<float>(static_cast<int>(a - (quarter << 30))) * 1.46291807926715968e-9f;   // 2 pi 2^-32
+  const float z = x * x;
+  // Taylor: |x| <= pi / 4, the first term left out is below 2^-29
+  float s = fmaf(z, 1.0f / 362880.0f, -1.0f / 5040.0f);
+  s = fmaf(z, s, 1.0f / 120.0f);
+  s = fmaf(z, s, -1.0f / 6.0f);
+  s = fmaf(z * x, s, x);
+  float c = fmaf(z, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+  c = fmaf(z, c, -1.0f / 720.0f);
+  c = fmaf(z, c, 1.0f / 24.0f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  const bool swap = quarter & 1u;
+  const float cs = swap ? s : c, sn = swap ? c : s;
+  return make_float2(quarter == 1u || quarter == 2u ? -cs : cs, quarter & 2u ? -sn : sn);
+}
+
+// Turn the N values of a vector of a pair-interleaved head (N / 2 pairs), or
+// the pairs of two vectors.
+template <typename T, int N, int P, bool kTwo>
+__device__ __forceinline__ void rope_turn(RopeVec<T, N>& va, RopeVec<T, N>& vb, const float2 (&cs)[P]) {
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    T& xa = kTwo ? va.x[j] : va.x[2 * j];
+    T& xb = kTwo ? vb.x[j] : va.x[2 * j + (N > 1 ? 1 : 0)];
+    const float a = rope_float(xa), b = rope_float(xb);
+    const float ra = a * cs[j].x - b * cs[j].y, rb = b * cs[j].x + a * cs[j].y;
+    rope_round(xa, ra);
+    rope_round(xb, rb);
+  }
+}
+
+// The same for bf16 vectors, two values a conversion.
+template <int N, int P, bool kTwo>
+__device__ __forceinline__ void rope_turn_bf16(RopeVec<__nv_bfloat16, N>& va, RopeVec<__nv_bfloat16, N>& vb, const float2 (&cs)[P]) {
+  uint32_t* wa = reinterpret_cast<uint32_t*>(&va);
+  uint32_t* wb = reinterpret_cast<uint32_t*>(&vb);
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    if constexpr (kTwo) {
+      const float a0 = bf16_lo(wa[j]), a1 = bf16_hi(wa[j]), b0 = bf16_lo(wb[j]), b1 = bf16_hi(wb[j]);
+      const float2 c0 = cs[2 * j], c1 = cs[2 * j + 1];
+      wa[j] = pack_bf16x2(a0 * c0.x - b0 * c0.y, a1 * c1.x - b1 * c1.y);
+      wb[j] = pack_bf16x2(b0 * c0.x + a0 * c0.y, b1 * c1.x + a1 * c1.y);
+    } else {
+      const float a = bf16_lo(wa[j]), b = bf16_hi(wa[j]);
+      wa[j] = pack_bf16x2(a * cs[j].x - b * cs[j].y, b * cs[j].x + a * cs[j].y);
+    }
+  }
 }
 
 // T: element, N: elements of a vector, kHalves: rotary style 1 (a pair's two
 // columns lie in two vectors; else N = 1 or both are in one vector).
 template <typename T, int N, bool kHalves>
-__global__ void __launch_bounds__(kRopeAxThreads) rope_axes_kernel(const __grid_constant__ RopeAxParams p) {
-  // pairs of an item, and whether it holds a second vector
+__global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_kernel(const __grid_constant__ RopeAxParams p) {
+  // pairs of a unit, and whether it holds a second vector
   constexpr int P = kHalves ? N : (N == 1 ? 1 : N / 2);
   constexpr bool kTwo = kHalves || N == 1;
+  constexpr bool kPacked = sizeof(T) == 2 && N > 1;
   using Vec = RopeVec<T, N>;
-  __shared__ unsigned long long s_f[kRopeAxMaxPairs];
-  __shared__ __align__(16) float s_cos[kRopeAxMaxRows * kRopeAxMaxPairs];
-  __shared__ __align__(16) float s_sin[kRopeAxMaxRows * kRopeAxMaxPairs];
+  __shared__ __align__(16) float2 s_cs[kRopeAxAngles];
   grid_dependency_wait();
   grid_launch_dependents();
   const int block = blockIdx.x / p.groups, group = blockIdx.x - block * p.groups;
   const int row0 = block * p.cta_rows, nrows = min(p.cta_rows, p.rows - row0);
-  const int head0 = group * p.cta_heads;
-  const int total = nrows * p.cta_heads * p.units;
+  const int head_end = min(p.heads, (group + 1) * p.cta_heads);
+  // a thread's first column unit, row and heads (more units than threads: one row and head)
+  const int span = min(p.units, kRopeAxThreads);
+  const int slot = threadIdx.x / span, u0 = threadIdx.x - slot * span;
+  const int first_row = slot / p.head_slots;
+  const int head0 = first_row < p.row_slots ? group * p.cta_heads + slot - first_row * p.head_slots : head_end;
+  const bool at_work = first_row < nrows && head0 < head_end;
 
-  Vec va[kRopeAxBatch], vb[kRopeAxBatch];
-  auto place = [&](int i, int& u, int& r, int& h) {
-    const int rh = rope_div(i, p.units, p.units_magic);
-    u = i - rh * p.units;
-    r = rope_div(rh, p.cta_heads, p.heads_magic);
-    h = head0 + rh - r * p.cta_heads;
-  };
-  // the columns of an item's two vectors
+  // the columns of a unit's two vectors
   auto columns = [&](int u, int& ca, int& cb) {
     if (u < p.rot_units) {
       ca = kHalves ? u * N : u * (N == 1 ? 2 : N);
       cb = kHalves ? ca + p.pairs : ca + 1;
     } else {
       ca = 2 * p.pairs + (u - p.rot_units) * N;
-      cb = -1;
+      cb = ca;
     }
   };
-  auto load = [&](int base) {
+  Vec va[kRopeAxBatch], vb[kRopeAxBatch];
+  // the row's heads of q and of k, and the thread's heads in them
+  const T *qs, *ks;
+  T *qd, *kd;
+  int off[kRopeAxBatch];
+#pragma unroll
+  for (int e = 0; e < kRopeAxBatch; ++e) {
+    const int h = head0 + e * p.head_slots;
+    off[e] = (h < p.hq ? h : h - p.hq) * p.d;
+  }
+  int ca, cb;
+  columns(u0, ca, cb);
+  auto is_q = [&](int e) { return head0 + e * p.head_slots < p.hq; };
+  auto point = [&]() {
+    const long long row = row0 + first_row;
+    qs = static_cast<const T*>(p.q) + row * p.q_ld;
+    ks = static_cast<const T*>(p.k) + row * p.k_ld;
+    qd = static_cast<T*>(p.q_out) + row * p.q_out_ld;
+    kd = static_cast<T*>(p.k_out) + row * p.k_out_ld;
+  };
+  auto load = [&]() {
 #pragma unroll
     for (int e = 0; e < kRopeAxBatch; ++e) {
-      const int i = base + e * kRopeAxThreads;
-      if (i >= total) break;
-      int u, r, h, ca, cb;
-      place(i, u, r, h);
-      if (h >= p.heads) continue;
-      columns(u, ca, cb);
-      const long long row = row0 + r;
-      const T* src = h < p.hq ? static_cast<const T*>(p.q) + row * p.q_ld + static_cast<long long>(h) * p.d
-                              : static_cast<const T*>(p.k) + row * p.k_ld + static_cast<long long>(h - p.hq) * p.d;
+      if (head0 + e * p.head_slots >= head_end) break;
+      const T* src = (is_q(e) ? qs : ks) + off[e];
       va[e] = *reinterpret_cast<const Vec*>(src + ca);
-      if (kTwo && cb >= 0) vb[e] = *reinterpret_cast<const Vec*>(src + cb);
+      if (kTwo) vb[e] = *reinterpret_cast<const Vec*>(src + cb);
     }
   };
-  load(threadIdx.x);                   // the first items are on their way while the angles are made
+  if (at_work) {                       // the first row is on its way while the angles are made
+    point();
+    load();
+  }
 
-  // inv_freq as a 64-bit fraction of a turn
-  for (int i = threadIdx.x; i < p.pairs; i += kRopeAxThreads) {
-    double turns = static_cast<double>(p.inv_freq[i]) * 0.15915494309189533577;   // 1 / (2 pi)
-    turns -= floor(turns);
-    s_f[i] = __double2ull_rn(turns * 18446744073709551616.0);
+  {
+    const int step = kRopeAxThreads / p.pairs;               // rows taken at a time, a thread keeps its pair
+    const int r0 = threadIdx.x / p.pairs, pr = threadIdx.x - r0 * p.pairs;
+    if (r0 < step && r0 < nrows) {
+      const unsigned long long f = rope_turns(p.inv_freq[pr]);
+      const int32_t* position = p.positions + p.axis[pr] * p.pos_ld + row0;
+      for (int r = r0; r < nrows; r += step) s_cs[r * p.pairs + pr] = rope_cos_sin(position[r], f);
+    }
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < nrows * p.pairs; i += kRopeAxThreads) {
-    const int r = i / p.pairs, pr = i - r * p.pairs;
-    const long long position = p.positions[p.axis[pr] * p.pos_ld + row0 + r];
-    const unsigned long long a = static_cast<unsigned long long>(position) * s_f[pr];
-    // the fraction of a turn in [-1/2, 1/2), in half turns for sincospif
-    const float half_turns = static_cast<float>(static_cast<int>(a >> 32)) * (1.0f / 2147483648.0f);
-    sincospif(half_turns, &s_sin[i], &s_cos[i]);
-  }
-  __syncthreads();
+  if (!at_work) return;
 
-  for (int base = threadIdx.x; base < total; base += kRopeAxBatch * kRopeAxThreads) {
-    if (base != static_cast<int>(threadIdx.x)) load(base);
-#pragma unroll
-    for (int e = 0; e < kRopeAxBatch; ++e) {
-      const int i = base + e * kRopeAxThreads;
-      if (i >= total) break;
-      int u, r, h, ca, cb;
-      place(i, u, r, h);
-      if (h >= p.heads) continue;
+  for (int u = u0; u < p.units; u += kRopeAxThreads) {
+    if (u != u0) {
       columns(u, ca, cb);
-      const long long row = row0 + r;
-      T* dst = h < p.hq ? static_cast<T*>(p.q_out) + row * p.q_out_ld + static_cast<long long>(h) * p.d
-                        : static_cast<T*>(p.k_out) + row * p.k_out_ld + static_cast<long long>(h - p.hq) * p.d;
-      if (u < p.rot_units) {
-        const float* cs = s_cos + r * p.pairs + u * P;
-        const float* sn = s_sin + r * p.pairs + u * P;
+      point();
+    }
+    const bool turns = u < p.rot_units;
+    for (int r = first_row; r < nrows; r += p.row_slots) {
+      if (u != u0 || r != first_row) load();
+      float2 cs[P];
+      if (turns) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
-          T& xa = kTwo ? va[e].x[j] : va[e].x[2 * j];
-          T& xb = kTwo ? vb[e].x[j] : va[e].x[2 * j + (N > 1 ? 1 : 0)];
-          const float a = rope_float(xa), b = rope_float(xb);
-          rope_round(xa, a * cs[j] - b * sn[j]);
-          rope_round(xb, b * cs[j] + a * sn[j]);
-        }
-        if (kTwo) *reinterpret_cast<Vec*>(dst + cb) = vb[e];
+        for (int j = 0; j < P; ++j) cs[j] = s_cs[r * p.pairs + u * P + j];
       }
-      *reinterpret_cast<Vec*>(dst + ca) = va[e];
+#pragma unroll
+      for (int e = 0; e < kRopeAxBatch; ++e) {
+        if (head0 + e * p.head_slots >= head_end) break;
+        if (turns) {
+          if constexpr (kPacked) rope_turn_bf16<N, P, kTwo>(va[e], vb[e], cs);
+          else rope_turn<T, N, P, kTwo>(va[e], vb[e], cs);
+        }
+        T* dst = (is_q(e) ? qd : kd) + off[e];
+        *reinterpret_cast<Vec*>(dst + ca) = va[e];
+        if (kTwo && turns) *reinterpret_cast<Vec*>(dst + cb) = vb[e];
+      }
+      qs += p.q_step;
+      ks += p.k_step;
+      qd += p.q_out_step;
+      kd += p.k_out_step;
     }
   }
 }
@@ -158,25 +242,42 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
   const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
   p.rot_units = p.pairs / per_unit;
   p.units = p.rot_units + (p.d - 2 * p.pairs) / N;
-  // Rows and heads of a CTA: four to ten items a thread when there is work
-  // for every SM, down to one item a thread (a head group of one row) when
-  // there is little, so that few rows still spread over the chip.
+  const int slots = p.units < kRopeAxThreads ? kRopeAxThreads / p.units : 1;
+  // Little work (less than a vector a thread for eight CTAs an SM): a CTA takes
+  // one sweep of one row, so that few rows still spread over the chip. Else
+  // about ten vectors a thread: all heads of some rows, in the 1 to 4 sweeps
+  // over a row's heads that leave the fewest threads idle (40 heads of 8
+  // units: 32 + 8 heads would idle 3 threads in 8; 4 x 10 heads of 3 rows 1 in 16).
   const long long row_items = static_cast<long long>(p.heads) * p.units;
-  long long per = row_items * p.rows / (152 * 8);
-  per = per < kRopeAxThreads ? kRopeAxThreads : per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per;
-  if (per >= row_items) {
-    p.cta_rows = static_cast<int>(per / row_items);
-    if (p.cta_rows > kRopeAxMaxRows) p.cta_rows = kRopeAxMaxRows;
-    p.cta_heads = p.heads;
-    p.groups = 1;
-  } else {
-    p.cta_rows = 1;
-    const long long groups = (row_items + per - 1) / per;
-    p.cta_heads = static_cast<int>((p.heads + groups - 1) / groups);
-    p.groups = (p.heads + p.cta_heads - 1) / p.cta_heads;
+  const long long per = row_items * p.rows / (152 * 8);
+  p.cta_rows = 1;
+  p.row_slots = 1;
+  p.head_slots = p.heads < slots ? p.heads : slots;
+  p.cta_heads = p.head_slots;
+  if (per >= kRopeAxThreads) {
+    p.cta_heads = p.heads < kRopeAxBatch * slots ? p.heads : kRopeAxBatch * slots;
+    int best = 0;
+    for (int k = 1; k <= kRopeAxBatch; ++k) {
+      const int hs = (p.cta_heads + k - 1) / k;
+      if (hs > slots) continue;
+      const int busy = slots / hs * p.cta_heads * 16 / k;      // threads at work, in sixteenths of a slot
+      if (busy >= best) {
+        best = busy;
+        p.head_slots = hs;
+        p.row_slots = slots / hs;
+      }
+    }
+    const long long items = static_cast<long long>(p.cta_heads) * p.units;
+    long long rows = (per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per) / items;
+    rows = (rows + p.row_slots - 1) / p.row_slots * p.row_slots;
+    if (rows > kRopeAxAngles / p.pairs) rows = kRopeAxAngles / p.pairs;
+    p.cta_rows = rows < 1 ? 1 : static_cast<int>(rows);
   }
-  p.units_magic = static_cast<uint32_t>(((1ull << 32) + p.units - 1) / p.units);
-  p.heads_magic = static_cast<uint32_t>(((1ull << 32) + p.cta_heads - 1) / p.cta_heads);
+  p.q_step = p.row_slots * p.q_ld;
+  p.k_step = p.row_slots * p.k_ld;
+  p.q_out_step = p.row_slots * p.q_out_ld;
+  p.k_out_step = p.row_slots * p.k_out_ld;
+  p.groups = (p.heads + p.cta_heads - 1) / p.cta_heads;
   const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   auto* kernel = halves ? rope_axes_kernel<T, N, true> : rope_axes_kernel<T, N, false>;
