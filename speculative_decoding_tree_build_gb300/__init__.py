@@ -11,6 +11,7 @@ not been built, ``load()`` raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -381,10 +382,29 @@ def accept_commit(g: TvGeom, target_ids, draft_tokens, cu_nodes, next_token, nex
 
 
 # ---------------------------------------------------------------- plain decoding, 8-bit cache
+#
+# These calls come once a layer in a decode step, so their tensors are checked
+# and passed on by the extension module of csrc/binding.cpp (the same library
+# underneath). Its functions raise ValueError for a tensor that does not fit.
 
-DTYPE_BF16, DTYPE_F32 = 0, 1
 KV_BF16, KV_E4M3, KV_INT8 = 0, 1, 2
-_KV_FORMATS = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3, torch.int8: KV_INT8}
+ext_path = os.path.join(_PKG, "_treeverify_torch.so")
+_ext = None
+
+
+def _native():
+    global _ext
+    if _ext is None:
+        load()
+        if not os.path.exists(ext_path):
+            raise FileNotFoundError(
+                f"{ext_path} is missing: build it with `python -m "
+                "speculative_decoding_tree_build_gb300.build` (or __graft_entry__.build()); there is "
+                "no fallback implementation")
+        spec = importlib.util.spec_from_file_location("_treeverify_torch", ext_path)
+        _ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_ext)
+    return _ext
 
 
 def rope_axes_geom(num_q_heads, num_kv_heads, head_dim, sections, rope_style=1,
@@ -396,66 +416,13 @@ def rope_axes_geom(num_q_heads, num_kv_heads, head_dim, sections, rope_style=1,
                       (ctypes.c_int32 * 4)(*sections), section_order)
 
 
-def _heads(t, heads, head_dim, name, dtype=None):
-    """(pointer, row stride) of a CUDA tensor [rows][heads][head_dim] whose
-    rows are contiguous (the row stride may exceed heads * head_dim)."""
-    if (not t.is_cuda or t.dim() != 3 or t.shape[1] != heads or t.shape[2] != head_dim or
-            (t.numel() and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != head_dim)))):
-        raise ValueError(f"{name} must be a CUDA tensor [rows][{heads}][{head_dim}] with "
-                         "contiguous rows")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    # the stride of a single row is free: any legal value does
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else heads * head_dim
-
-
 def rope_axes(g: TvRopeAxes, q, k, positions, inv_freq, q_out, k_out, stream=None):
     """Rotary positions with several axes: ``q``/``k`` [rows][heads][D]
     (bf16 or float32; slices of a fused projection are fine), ``positions``
     int32 [axes][rows], ``inv_freq`` float32 [pairs]. ``k``/``k_out`` are None
     when the geometry has no KV heads; an output may be its own input."""
-    if q.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"q must be bfloat16 or float32, got {q.dtype}")
-    rows = q.shape[0]
-    if (not positions.is_cuda or positions.dtype != I32 or
-            tuple(positions.shape) != (g.num_axes, rows) or (rows > 1 and positions.stride(1) != 1)):
-        raise ValueError("positions must be an int32 CUDA matrix [axes][rows] with contiguous rows")
-    if inv_freq.numel() != sum(g.section[:g.num_axes]):
-        raise ValueError("inv_freq must hold one frequency per rotated pair")
-    qp, qld = _heads(q, g.num_q_heads, g.head_dim, "q")
-    qo, qold = _heads(q_out, g.num_q_heads, g.head_dim, "q_out", q.dtype)
-    kp, kld, ko, kold = None, 0, None, 0
-    if g.num_kv_heads:
-        kp, kld = _heads(k, g.num_kv_heads, g.head_dim, "k", q.dtype)
-        ko, kold = _heads(k_out, g.num_kv_heads, g.head_dim, "k_out", q.dtype)
-        if k.shape[0] != rows or k_out.shape[0] != rows:
-            raise ValueError("k and k_out must have as many rows as q")
-    if q_out.shape[0] != rows:
-        raise ValueError("q_out must have as many rows as q")
-    return _check("tv_rope_axes", load().tv_rope_axes(
-        ctypes.byref(g), rows, DTYPE_BF16 if q.dtype == BF16 else DTYPE_F32, qp, qld, kp, kld,
-        positions.data_ptr(), positions.stride(0) if g.num_axes > 1 else rows,
-        _ptr(inv_freq, torch.float32, "inv_freq"), qo, qold, ko, kold, _stream(stream)))
-
-
-def _kv_pools(g, k_cache, v_cache, k_scale, v_scale):
-    """(format, pointers of the two pools and the two scale arrays)."""
-    fmt = _KV_FORMATS.get(k_cache.dtype)
-    if fmt is None:
-        raise ValueError(f"k_cache must be bfloat16, float8_e4m3fn or int8, got {k_cache.dtype}")
-    shape = (k_cache.shape[0], g.num_kv_heads, 16, g.head_dim)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if tuple(t.shape) != shape:
-            raise ValueError(f"{name} must be [num_blocks][{g.num_kv_heads}][16][{g.head_dim}]")
-    ptrs = [_ptr(k_cache, k_cache.dtype, "k_cache"), _ptr(v_cache, k_cache.dtype, "v_cache")]
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if fmt == KV_BF16:
-            ptrs.append(None)
-            continue
-        if t is None or tuple(t.shape) != shape[:3]:
-            raise ValueError(f"{name} must be float32 [num_blocks][{g.num_kv_heads}][16]")
-        ptrs.append(_ptr(t, torch.float32, name))
-    return fmt, ptrs
+    rc = (_ext or _native()).rope_axes(g, q, k, positions, inv_freq, q_out, k_out, stream)
+    return rc and _check("tv_rope_axes", rc)
 
 
 def kv_quant_append(g: TvGeom, k_new, v_new, cu_rows, start_len, block_table, n_blocks, k_cache,
@@ -463,33 +430,19 @@ def kv_quant_append(g: TvGeom, k_new, v_new, cu_rows, start_len, block_table, n_
     """Quantise fresh rows [rows][Hkv][D] (bf16) into an 8-bit paged cache
     (pools of float8_e4m3fn or int8 with float32 scales [num_blocks][Hkv][16]):
     row i of request b goes to slot ``start_len[b] + i``."""
-    fmt, (kc, vc, ks, vs) = _kv_pools(g, k_cache, v_cache, k_scale, v_scale)
-    kp, kld = _heads(k_new, g.num_kv_heads, g.head_dim, "k_new", BF16)
-    vp, vld = _heads(v_new, g.num_kv_heads, g.head_dim, "v_new", BF16)
-    if kld != vld or k_new.shape[0] != v_new.shape[0]:
-        raise ValueError("k_new and v_new must have the same rows and row stride")
-    batch = cu_rows.numel() - 1
-    return _check("tv_kv_quant_append", load().tv_kv_quant_append(
-        ctypes.byref(g), fmt, batch, k_new.shape[0], kp, vp, kld, _ptr(cu_rows, I32, "cu_rows"),
-        _ptr(start_len, I32, "start_len"), _ptr(block_table, I32, "block_table"),
-        _ptr(n_blocks, I32, "n_blocks"), block_table.shape[1], kc, vc, ks, vs, k_cache.shape[0],
-        _ptr(status, I32, "status"), _stream(stream)))
+    rc = (_ext or _native()).kv_quant_append(g, k_new, v_new, cu_rows, start_len, block_table, n_blocks,
+                                             k_cache, v_cache, k_scale, v_scale, status, stream)
+    return rc and _check("tv_kv_quant_append", rc)
 
 
 def kv_quant_read(g: TvGeom, first, last, block_table, n_blocks, k_cache, v_cache, k_scale, v_scale,
                   out_block_table, out_n_blocks, k_out, v_out, status, stream=None):
     """Read slots [first[b], last[b]) of an 8-bit paged cache back into bf16
     pools with their own block table (``first`` None: from slot 0)."""
-    fmt, (kc, vc, ks, vs) = _kv_pools(g, k_cache, v_cache, k_scale, v_scale)
-    ofmt, (ko, vo, _, _) = _kv_pools(g, k_out, v_out, None, None) if k_out.dtype == BF16 else (-1, [None] * 4)
-    if ofmt != KV_BF16:
-        raise ValueError("k_out and v_out must be bfloat16 pools")
-    return _check("tv_kv_quant_read", load().tv_kv_quant_read(
-        ctypes.byref(g), fmt, last.numel(), _ptr(first, I32, "first"), _ptr(last, I32, "last"),
-        _ptr(block_table, I32, "block_table"), _ptr(n_blocks, I32, "n_blocks"), block_table.shape[1],
-        kc, vc, ks, vs, k_cache.shape[0], _ptr(out_block_table, I32, "out_block_table"),
-        _ptr(out_n_blocks, I32, "out_n_blocks"), out_block_table.shape[1], ko, vo, k_out.shape[0],
-        _ptr(status, I32, "status"), _stream(stream)))
+    rc = (_ext or _native()).kv_quant_read(g, first, last, block_table, n_blocks, k_cache, v_cache,
+                                           k_scale, v_scale, out_block_table, out_n_blocks, k_out,
+                                           v_out, status, stream)
+    return rc and _check("tv_kv_quant_read", rc)
 
 
 def decode_workspace_bytes(g: TvGeom, batch: int) -> int:
@@ -504,15 +457,6 @@ def decode_attention(g: TvGeom, q, seq_len, block_table, n_blocks, k_cache, v_ca
     """Attention of one new token per request (``q`` [batch][Hq][D] bf16) over
     slots [0, seq_len[b]) of a paged cache: bf16 pools (scales None) or 8-bit
     pools with their scales. ``lse`` float32 [batch][Hq] or None."""
-    fmt, (kc, vc, ks, vs) = _kv_pools(g, k_cache, v_cache, k_scale, v_scale)
-    qp, qld = _heads(q, g.num_q_heads, g.head_dim, "q", BF16)
-    batch = seq_len.numel()
-    if q.shape[0] != batch or out.numel() != batch * g.num_q_heads * g.head_dim:
-        raise ValueError("q and out must have one row per request")
-    return _check("tv_decode_attention", load().tv_decode_attention(
-        ctypes.byref(g), fmt, batch, qp, qld, _ptr(seq_len, I32, "seq_len"),
-        _ptr(block_table, I32, "block_table"), _ptr(n_blocks, I32, "n_blocks"),
-        block_table.shape[1], kc, vc, ks, vs, k_cache.shape[0], _ptr(out, BF16, "out"),
-        _ptr(lse, torch.float32, "lse"), _ptr(workspace, None, "workspace"),
-        workspace.numel() * workspace.element_size(), _ptr(status, I32, "status"),
-        _stream(stream)))
+    rc = (_ext or _native()).decode_attention(g, q, seq_len, block_table, n_blocks, k_cache, v_cache,
+                                              k_scale, v_scale, out, lse, workspace, status, stream)
+    return rc and _check("tv_decode_attention", rc)

@@ -1,8 +1,10 @@
 """Build libtreeverify.so in-tree for sm_103a with nvcc.
 
 Each translation unit under csrc/ is compiled in parallel, then linked into
-``speculative_decoding_tree_build_gb300/libtreeverify.so``. A stamp of the
-sources and flags skips the build when nothing changed.
+``speculative_decoding_tree_build_gb300/libtreeverify.so``. csrc/binding.cpp is
+compiled with the host compiler against torch's headers and linked to it as
+the extension module ``_treeverify_torch.so``. A stamp of the sources, flags
+and torch's version skips the build when nothing changed.
 
     python -m speculative_decoding_tree_build_gb300.build [--force] [--verbose-ptxas]
 """
@@ -16,12 +18,16 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtreeverify.so")
+EXT = os.path.join(PKG, "_treeverify_torch.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
               "--expt-relaxed-constexpr", "-I", os.path.join(ROOT, "include")]
@@ -43,12 +49,46 @@ def _stamp(extra):
     files = _sources() + sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC)
                                 if f.endswith((".cuh", ".h")))
     files.append(os.path.join(ROOT, "include", "treeverify.h"))
+    files.append(os.path.join(CSRC, "binding.cpp"))
     for f in files:
         h.update(f.encode())
         with open(f, "rb") as fh:
             h.update(fh.read())
-    h.update(" ".join(ARCH + NVCC_FLAGS + extra).encode())
+    h.update(" ".join(ARCH + NVCC_FLAGS + extra + [torch.__version__, sys.version]).encode())
     return h.hexdigest()
+
+
+def _torch_dirs():
+    root = os.path.dirname(torch.__file__)
+    return os.path.join(root, "include"), os.path.join(root, "lib")
+
+
+def _compile_binding(nvcc):
+    """csrc/binding.cpp -> object file."""
+    include, _ = _torch_dirs()
+    obj = os.path.join(BUILD, "binding.o")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda,
+           "-c", os.path.join(CSRC, "binding.cpp"), "-o", obj]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding does not compile:\n{res.stdout}\n{res.stderr}")
+    return obj
+
+
+def _link_binding(obj):
+    _, lib = _torch_dirs()
+    tmp = EXT + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", PKG, "-ltreeverify",
+           "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"the binding does not link:\n{res.stdout}\n{res.stderr}")
+    os.replace(tmp, EXT)
 
 
 def build(force=False, verbose_ptxas=False, quiet=True):
@@ -57,7 +97,7 @@ def build(force=False, verbose_ptxas=False, quiet=True):
     os.makedirs(BUILD, exist_ok=True)
     stamp_path = os.path.join(BUILD, "stamp")
     stamp = _stamp(extra)
-    if not force and os.path.exists(LIB) and os.path.exists(stamp_path):
+    if not force and os.path.exists(LIB) and os.path.exists(EXT) and os.path.exists(stamp_path):
         with open(stamp_path) as fh:
             if fh.read() == stamp:
                 return LIB
@@ -74,14 +114,17 @@ def build(force=False, verbose_ptxas=False, quiet=True):
             sys.stderr.write(res.stdout + res.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(16, os.cpu_count() or 4)) as ex:
+        binding = ex.submit(_compile_binding, nvcc)
         objs = list(ex.map(compile_one, _sources()))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     with open(stamp_path, "w") as fh:
         fh.write(stamp)
     return LIB

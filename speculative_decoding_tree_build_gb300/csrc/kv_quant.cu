@@ -4,8 +4,8 @@
 // A row (one head's D values of one token) is quantised on its own: largest
 // magnitude, scale, codes (tv_kv8.cuh). Both calls are bound by memory: the
 // append reads 2 D bytes a row and writes D + 4, the read the other way round.
-// A row is held by D / 8 neighbouring lanes, 16 bytes of bf16 each; its
-// largest magnitude takes log2(D / 8) shuffles of a paired integer maximum.
+// A row is held by D / 16 neighbouring lanes, 32 bytes of bf16 each; its
+// largest magnitude takes log2(D / 16) shuffles of a paired integer maximum.
 // The append's rows are loaded before their slots are known, so the chain of
 // small loads (offsets, lengths, block ids) overlaps the one large one.
 #include "tv_kv8.cuh"
@@ -14,6 +14,7 @@
 namespace tv {
 
 constexpr int kAppendThreads = 256;
+constexpr int kAppendPerSm = 3;      // CTAs an SM: 2 / 3 / 4 took 46.6 / 41.8 / 42.1 us for 201 MB (4 spills)
 constexpr int kAppendBatch = 4;      // rows whose loads a thread has in flight
 constexpr int kAppendMaxRows = 64;   // rows of k_new / v_new per CTA at most
 
@@ -35,28 +36,25 @@ struct AppendParams {
   int slots;                         // rows taken at a time
 };
 
-// The request that owns row t: the largest b with cu[b] <= t (requests without
-// rows are passed over), -1 when t is outside [cu[0], cu[batch]).
-__device__ __forceinline__ int request_of_row(const int32_t* cu, int batch, int t) {
-  if (t < cu[0] || t >= cu[batch]) return -1;
-  int lo = 0, hi = batch;              // cu[lo] <= t < cu[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (cu[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
+// What the CTA knows of the row of K/V it handles.
+struct AppendRow {
+  int req;       // the request that owns it, -1: none (or one that is skipped)
+  int head;      // the CTA's first row of that request: its verdict counts for all of them
+  int slot;
+  int blk;       // the slot's block
+};
 
 template <int kFmt, int D>
-__global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const __grid_constant__ AppendParams p) {
-  constexpr int kLanes = D / 8;        // lanes that hold one row
-  extern __shared__ int s_cu[];        // [batch + 1]
-  __shared__ int s_req[kAppendMaxRows], s_slot[kAppendMaxRows], s_blk[kAppendMaxRows], s_bad[kAppendMaxRows];
-  __shared__ int s_first[kAppendMaxRows], s_pages[kAppendMaxRows];     // of a run's request: its span
+__global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int kLanes = D / 16;       // lanes that hold one row, two pieces of 8 values each
+  __shared__ AppendRow s_row[kAppendMaxRows];
+  __shared__ int s_bad[kAppendMaxRows];                      // by head row
+  __shared__ int s_cross[2][4];        // requests that reach past the CTA's rows, before and behind:
+                                       // request, first page, pages, head row
   grid_dependency_wait();
   grid_launch_dependents();
   const int t0 = blockIdx.x * p.cta_rows;
-  const int nrows = min(p.cta_rows, p.rows - t0);
+  const int nrows = min(p.cta_rows, p.rows - t0), t1 = t0 + nrows;
   // kLanes threads keep one head and step through the CTA's rows
   const int part = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int slot0 = part / p.cta_heads, head = blockIdx.y * p.cta_heads + part - slot0 * p.cta_heads;
@@ -64,103 +62,131 @@ __global__ void __launch_bounds__(kAppendThreads) kv_quant_append_kernel(const _
   const bool isv = head >= p.hkv;
   const int h = isv ? head - p.hkv : head;
   const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + static_cast<long long>(h) * D + lane * 8;
-  uint4 x[kAppendBatch];
+  uint4 x[kAppendBatch][2];            // a warp's loads cover whole sectors: piece lane, piece lane + kLanes
   auto load = [&](int r0) {
 #pragma unroll
     for (int e = 0; e < kAppendBatch; ++e) {
       const int r = r0 + e * p.slots;
-      x[e] = mine && r < nrows ? *reinterpret_cast<const uint4*>(src + (t0 + r) * p.kv_ld) : make_uint4(0u, 0u, 0u, 0u);
+      x[e][0] = x[e][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (mine && r < nrows) {
+        const __nv_bfloat16* from = src + (t0 + r) * p.kv_ld;
+        x[e][0] = *reinterpret_cast<const uint4*>(from);
+        x[e][1] = *reinterpret_cast<const uint4*>(from + kLanes * 8);
+      }
     }
   };
   load(slot0);                         // on their way while the rows' slots are found
 
-  for (int i = threadIdx.x; i <= p.batch; i += kAppendThreads) s_cu[i] = p.cu_rows[i];
-  __syncthreads();
-  if (blockIdx.x == 0 && blockIdx.y == 0) {    // requests whose rows lie past the array, in part or altogether
-    for (int b = threadIdx.x; b < p.batch; b += kAppendThreads)
-      if (s_cu[b + 1] > p.rows && s_cu[b + 1] > s_cu[b] && p.status[b] == 0) atomicOr(p.status + b, TV_ST_BAD_SIZE);
+  // A thread looks at request i with all that it needs of it in one round
+  // trip, and describes those of the CTA's rows that the request owns.
+  if (threadIdx.x < kAppendMaxRows) {
+    s_row[threadIdx.x].req = -1;
+    s_bad[threadIdx.x] = 0;
   }
-  if (threadIdx.x < nrows) {
-    const int r = threadIdx.x, t = t0 + r;
-    const int b = request_of_row(s_cu, p.batch, t);
-    int bad = -1, blk = -1;            // -1: not this call's to write, nothing to report
-    s_req[r] = b;
-    s_pages[r] = 0;
-    if (b >= 0) {
-      const int st = p.status[b], start = p.start_len[b], held = min(p.n_blocks[b], p.max_blocks);
-      const long long slot = static_cast<long long>(start) + (t - s_cu[b]);
-      const long long end = static_cast<long long>(start) + (s_cu[b + 1] - s_cu[b]);
-      if (st == 0) {
-        bad = 0;
-        if (start < 0 || s_cu[b] < 0 || end > 0x7fffffffll) bad = TV_ST_BAD_SIZE;
-        else if (s_cu[b + 1] > p.rows) bad = -1;                       // CTA 0 reports it
-        else if ((end - 1) / TV_BLOCK_SIZE >= held) bad = TV_ST_BAD_BLOCK;
-      }
-      if (bad == 0) {
-        blk = p.block_table[static_cast<size_t>(b) * p.max_blocks + slot / TV_BLOCK_SIZE];
-        if (blk < 0 || blk >= p.num_blocks) bad = TV_ST_BAD_BLOCK;
-        // the request's first row here checks the blocks of rows that lie in other CTAs
-        if (bad == 0 && (r == 0 || t - 1 < s_cu[b]) && (s_cu[b] < t0 || s_cu[b + 1] > t0 + nrows)) {
-          s_first[r] = start / TV_BLOCK_SIZE;
-          s_pages[r] = static_cast<int>((end - 1) / TV_BLOCK_SIZE) - s_first[r] + 1;
-        }
-      }
-      s_slot[r] = static_cast<int>(slot);
+  if (threadIdx.x < 2) s_cross[threadIdx.x][2] = 0;
+  __syncthreads();
+#pragma unroll 2
+  for (int i = threadIdx.x; i < p.batch; i += kAppendThreads) {
+    const int c0 = p.cu_rows[i], c1 = p.cu_rows[i + 1], st = p.status[i], start = p.start_len[i];
+    const int held = min(p.n_blocks[i], p.max_blocks);
+    if (c1 <= c0 || st != 0) continue;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && (c1 > p.rows || c0 < 0 || start < 0)) atomicOr(p.status + i, TV_ST_BAD_SIZE);
+    if (c0 < 0 || c1 > p.rows || start < 0 || c0 >= t1 || c1 <= t0) continue;
+    const int first = max(c0, t0) - t0, last = min(c1, t1) - t0;
+    const long long end = static_cast<long long>(start) + (c1 - c0);
+    const bool fits = (end - 1) / TV_BLOCK_SIZE < held;      // (which also keeps slots below 2^31)
+    if (!fits) s_bad[first] = TV_ST_BAD_BLOCK;
+    for (int r = first; r < last; ++r) {
+      AppendRow a;
+      a.req = i;
+      a.head = first;
+      a.slot = fits ? start + (t0 + r - c0) : 0;
+      a.blk = -1;
+      s_row[r] = a;
     }
-    s_bad[r] = bad;
-    s_blk[r] = blk;
+    if (fits && (c0 < t0 || c1 > t1)) {
+      int* cross = s_cross[c0 < t0 ? 0 : 1];
+      cross[0] = i;
+      cross[1] = start / TV_BLOCK_SIZE;
+      cross[3] = first;
+      cross[2] = static_cast<int>((end - 1) / TV_BLOCK_SIZE) - cross[1] + 1;
+    }
   }
   __syncthreads();
-  // at most two requests reach beyond this CTA's rows: the first and the last one
-  for (int r = 0; r < nrows; ++r) {
-    const int pages = s_pages[r];
-    if (pages == 0) continue;
-    const int32_t* row = p.block_table + static_cast<size_t>(s_req[r]) * p.max_blocks + s_first[r];
+  // the rows' blocks, and all other blocks of a request that other CTAs have rows of
+  if (threadIdx.x < nrows && s_row[threadIdx.x].req >= 0) {
+    AppendRow& a = s_row[threadIdx.x];
+    if (s_bad[a.head] == 0) {
+      const int blk = p.block_table[static_cast<size_t>(a.req) * p.max_blocks + a.slot / TV_BLOCK_SIZE];
+      a.blk = blk;
+      if (blk < 0 || blk >= p.num_blocks) s_bad[a.head] = TV_ST_BAD_BLOCK;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const int pages = s_cross[c][2];
+    const int32_t* row = p.block_table + static_cast<size_t>(s_cross[c][0]) * p.max_blocks + s_cross[c][1];
     bool bad = false;
     for (int e = threadIdx.x; e < pages; e += kAppendThreads) {
       const int blk = row[e];
       bad |= blk < 0 || blk >= p.num_blocks;
     }
-    if (bad) s_bad[r] = TV_ST_BAD_BLOCK;
+    if (bad) s_bad[s_cross[c][3]] = TV_ST_BAD_BLOCK;
   }
-  __syncthreads();
-  if (threadIdx.x < nrows && s_req[threadIdx.x] >= 0) {
-    // one bad row of a request holds all of its rows back
-    const int r = threadIdx.x, b = s_req[r];
-    int bad = s_bad[r];
-    const int own = bad;
-    for (int o = r - 1; o >= 0 && s_req[o] == b; --o) bad = max(bad, s_bad[o]);
-    for (int o = r + 1; o < nrows && s_req[o] == b; ++o) bad = max(bad, s_bad[o]);
-    if (bad != 0) s_blk[r] = -1;
-    if (own > 0) atomicOr(p.status + b, own);
-  }
-  __syncthreads();
-  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + lane * 8;
-  float* scales = isv ? p.v_scale : p.k_scale;
-  for (int r0 = 0; r0 < nrows; r0 += kAppendBatch * p.slots) {
-    if (r0 > 0) load(r0 + slot0);
+
+  uint2 code[kAppendBatch][2];
+  float scale[kAppendBatch];
+  auto encode = [&](int r0) {
 #pragma unroll
     for (int e = 0; e < kAppendBatch; ++e) {
       if (r0 + e * p.slots >= nrows) break;                  // the same for all threads: the shuffles are whole
-      const int r = r0 + slot0 + e * p.slots;
-      const int blk = mine && r < nrows ? s_blk[r] : -1;
-      const uint32_t w[4] = {x[e].x, x[e].y, x[e].z, x[e].w};
       // bits 14..0 of both halves order as integers: halves are compared apart
-      uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                              __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+      uint32_t top = 0;
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        top = __vmaxu2(top, __vmaxu2(__vmaxu2(x[e][u].x & 0x7fff7fffu, x[e][u].y & 0x7fff7fffu),
+                                     __vmaxu2(x[e][u].z & 0x7fff7fffu, x[e][u].w & 0x7fff7fffu)));
 #pragma unroll
       for (int s = kLanes / 2; s > 0; s >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
       top = max(top & 0xffffu, top >> 16);
-      if (blk < 0) continue;
       const KvRowScale sc = kv_row_scale<kFmt>(top);
-      uint2 c = make_uint2(0u, 0u);
-      if (sc.mul != 0.0f) {
-        c.x = kv_encode2<kFmt>(bf16_lo(w[0]), bf16_hi(w[0]), sc) | (kv_encode2<kFmt>(bf16_lo(w[1]), bf16_hi(w[1]), sc) << 16);
-        c.y = kv_encode2<kFmt>(bf16_lo(w[2]), bf16_hi(w[2]), sc) | (kv_encode2<kFmt>(bf16_lo(w[3]), bf16_hi(w[3]), sc) << 16);
+      scale[e] = sc.scale;
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        uint2 c = make_uint2(0u, 0u);
+        if (sc.mul != 0.0f) {
+          c.x = kv_encode2<kFmt>(bf16_lo(x[e][u].x), bf16_hi(x[e][u].x), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].y), bf16_hi(x[e][u].y), sc) << 16);
+          c.y = kv_encode2<kFmt>(bf16_lo(x[e][u].z), bf16_hi(x[e][u].z), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].w), bf16_hi(x[e][u].w), sc) << 16);
+        }
+        code[e][u] = c;
       }
-      const size_t row = (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE + s_slot[r] % TV_BLOCK_SIZE;
-      *reinterpret_cast<uint2*>(codes + row * D) = c;
-      if (lane == 0) scales[row] = sc.scale;
+    }
+  };
+  encode(0);                           // while the block ids are on their way
+  __syncthreads();
+  if (threadIdx.x < nrows && blockIdx.y == 0) {
+    const AppendRow a = s_row[threadIdx.x];
+    if (a.req >= 0 && a.head == static_cast<int>(threadIdx.x) && s_bad[a.head] != 0) atomicOr(p.status + a.req, s_bad[a.head]);
+  }
+
+  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + lane * 8;
+  float* scales = isv ? p.v_scale : p.k_scale;
+  for (int r0 = 0; r0 < nrows; r0 += kAppendBatch * p.slots) {
+    if (r0 > 0) {
+      load(r0 + slot0);
+      encode(r0);
+    }
+#pragma unroll
+    for (int e = 0; e < kAppendBatch; ++e) {
+      const int r = r0 + slot0 + e * p.slots;
+      if (!mine || r >= nrows) break;
+      const AppendRow a = s_row[r];
+      if (a.req < 0 || s_bad[a.head] != 0) continue;
+      const size_t row = (static_cast<size_t>(a.blk) * p.hkv + h) * TV_BLOCK_SIZE + a.slot % TV_BLOCK_SIZE;
+      uint8_t* to = codes + row * D;
+      *reinterpret_cast<uint2*>(to) = code[e][0];
+      *reinterpret_cast<uint2*>(to + kLanes * 8) = code[e][1];
+      if (lane == 0) scales[row] = scale[e];
     }
   }
 }
@@ -287,7 +313,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __gri
 }
 
 static int check_kv_format(const tv_geom* geom, int fmt) {
-  // heads go to grid.y in blocks of 16 or 32
+  // heads go to grid.y in blocks of 32 or 64
   return (fmt == TV_KV_E4M3 || fmt == TV_KV_INT8) && geom->num_kv_heads <= 4096 ? TV_OK : TV_ERR_BAD_GEOMETRY;
 }
 
@@ -327,10 +353,10 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   auto* kernel = kv_format == TV_KV_E4M3
       ? (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_E4M3, 64> : tv::kv_quant_append_kernel<TV_KV_E4M3, 128>)
       : (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_INT8, 64> : tv::kv_quant_append_kernel<TV_KV_INT8, 128>);
-  // A CTA takes up to 256 / (D / 8) heads of a row at a time, several rows at
+  // A CTA takes up to 256 / (D / 16) heads of a row at a time, several rows at
   // a time when a row has fewer, and two batches of loads a thread where that
   // still gives every SM eight CTAs (fewer rows than that: down to one sweep).
-  const int parts = tv::kAppendThreads / (geom->head_dim / 8), heads = 2 * p.hkv;
+  const int parts = tv::kAppendThreads / (geom->head_dim / 16), heads = 2 * p.hkv;
   p.cta_heads = heads < parts ? heads : parts;
   p.slots = parts / p.cta_heads;
   const int head_blocks = (heads + p.cta_heads - 1) / p.cta_heads;
@@ -341,9 +367,8 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
   cta_rows = (cta_rows + p.slots - 1) / p.slots * p.slots;
   p.cta_rows = static_cast<int>(cta_rows);
-  const size_t smem = sizeof(int) * (static_cast<size_t>(batch) + 1);
   const dim3 grid(static_cast<unsigned>((rows + cta_rows - 1) / cta_rows), head_blocks);
-  const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), smem, tv::as_stream(stream), p);
+  const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), 0, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
