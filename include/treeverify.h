@@ -672,7 +672,8 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  * result does not depend on timing: the split over the cache's length is a
  * function of the arguments, and its parts are joined in a fixed order.
  *
- *  geom           rope fields are checked, not used: q comes rotated
+ *  geom           num_kv_heads <= 4096; rope fields are checked, not used: q
+ *                 comes rotated
  *  kv_format      TV_KV_BF16, TV_KV_E4M3 or TV_KV_INT8
  *  batch          0..4096
  *  q              bf16 [batch][Hq][D], rows q_ld ELEMENTS apart (>= Hq * D, a

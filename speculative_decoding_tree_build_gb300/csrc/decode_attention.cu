@@ -50,15 +50,16 @@ constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
 constexpr int kDecMinShare = 4;        // least cost worth a CTA of its own
 constexpr int kNoSplitPages = 16;
 constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
-constexpr int kMergeThreads = 512;
+constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay below 2^24
+constexpr int kMergeThreads = 128;
+constexpr int kMergeBatch = 8;         // partials a warp has in flight
 constexpr float kLowest = -3.4028234663852886e38f;
 
-// What a CTA tells the joining grid.
-struct DecTask {
-  int b, h, last;      // the unit it begins and does not finish (its partial is slot 1), and the
-                       // last CTA that works on it; last < 0: none
-  int mid_b, mid_h;    // the unit whose partial is in slot 0; mid_b < 0: none
-  int pad[3];
+// What the CTA that begins a unit tells the joining grid: the CTAs that work
+// on the unit (its own partial is its slot 1, the others' their slot 0).
+// last < 0: nothing to join.
+struct DecBegin {
+  int unit, first, last, pad;
 };
 
 struct DecodeParams {
@@ -73,10 +74,12 @@ struct DecodeParams {
   const float* v_scale;
   __nv_bfloat16* out;
   float* lse;
-  DecTask* tasks;
+  DecBegin* begins;    // by unit, or by CTA where there are more units than CTAs
+  int* mids;           // [CTAs] the unit whose partial is in slot 0, -1: none
   float* partials;     // two slots a CTA: [group][D] sums, then [group] x (m, M, l, -)
   int32_t* status;
   int batch, hq, hkv, group, max_blocks, num_blocks, split;
+  int by_unit;         // how begins is indexed
   float scale_log2;
 };
 
@@ -84,22 +87,31 @@ __host__ __device__ constexpr size_t dec_slot_floats(int group, int d) { return 
 
 // ------------------------------------------------------------------ pieces
 
+// Loads that stay where they are written, ahead of the branches that follow.
+// (Not .nc: the grid may be resident while the one before it still writes.)
+
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
   return r;
 }
 
 __device__ __forceinline__ uint2 ldg_stream8(const void* p) {
   uint2 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+  return r;
+}
+
+__device__ __forceinline__ int ldg_int(const int32_t* p) {
+  int r;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(r) : "l"(p));
   return r;
 }
 
 __device__ __forceinline__ float ldg_float(const float* p) {
   float r;
-  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(r) : "l"(p));
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(r) : "l"(p));
   return r;
 }
 
@@ -175,7 +187,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kSteps = Tr::kSteps;
   constexpr int kRowPad = D + 4;
   extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
-  __shared__ float s_m[kDecWarps][16], s_ref[kDecWarps][16], s_l[kDecWarps][16];
+  __shared__ float4 s_stat[kDecWarps][16];                     // (m, M, l, -)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_dependency_wait();
   grid_launch_dependents();
@@ -186,9 +198,13 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   });
   const int cta = blockIdx.x, grid = sh.ctas;
   const long long hi = sh.hi, total = sh.total;
-  DecTask task = {0, 0, -1, -1, 0, {0, 0, 0}};
+  int mid = -1;                        // the unit whose partial this CTA leaves in slot 0
+  DecBegin begun = {0, 0, -1, 0};      // the unit that it begins and does not finish
   if (sh.lo >= sh.hi) {
-    if (p.split && threadIdx.x == 0) p.tasks[cta] = task;
+    if (p.split && threadIdx.x == 0) {
+      p.mids[cta] = -1;
+      if (!p.by_unit) p.begins[cta] = begun;
+    }
     return;
   }
   int b = sh.b;
@@ -222,21 +238,16 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     int tile1 = nt;
     if (p.split && hi - unit - kDecUnitCost < nt) tile1 = max(tile0 + 1, static_cast<int>(hi - unit - kDecUnitCost));
 
-    const int st = p.status[b], held = min(p.n_blocks[b], p.max_blocks);
+    // the loads that need nothing but (b, h): status, held blocks, the first block ids, the queries
     const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
     const int pages = fits ? (n + TV_BLOCK_SIZE - 1) / TV_BLOCK_SIZE : 0;
-    int bad = n < 0 ? TV_ST_BAD_SIZE : (!fits || pages > held) ? TV_ST_BAD_BLOCK : 0;
-    if (st != 0 || bad) {
-      // (pages > held is a fact of the request: every CTA that meets it finds the same)
-      if (st == 0 && threadIdx.x == 0) atomicOr(p.status + b, bad);
-      if (tile0 > 0) { task.mid_b = b; task.mid_h = h; }
-      tile0 = nt;
-      if (st != 0 || bad) continue;
-    }
     const int page_end = min(pages, tile1 * kDecWarps);
     const int first = tile0 * kDecWarps + warp;
     const int iters = page_end > first ? (page_end - first + kDecWarps - 1) / kDecWarps : 0;
     const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+    auto fetch_ids = [&](int base) { return base + lane < iters ? ldg_int(row + first + (base + lane) * kDecWarps) : 0; };
+    const int ids_first = fetch_ids(0);
+    const int st = *const_cast<volatile int32_t*>(p.status + b), held = min(ldg_int(p.n_blocks + b), p.max_blocks);
 
     // ---- queries: the thread's columns of query g (and g + 8), as MMA operands
     uint32_t qf[NT][kSteps][2];
@@ -244,29 +255,34 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
       const int qi = x * 8 + g;
-      const bool live = qi < p.group;
-      const __nv_bfloat16* src = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + (live ? qi : 0)) * D;
-      if constexpr (!kHalf) {
+      const __nv_bfloat16* src = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + min(qi, p.group - 1)) * D;
 #pragma unroll
-        for (int c = 0; c < kKPieces; ++c) {
-          uint4 w = *reinterpret_cast<const uint4*>(src + (t + 4 * c) * 8);
-          if (!live) w = make_uint4(0u, 0u, 0u, 0u);
-          qf[x][2 * c][0] = w.x; qf[x][2 * c][1] = w.y;
-          qf[x][2 * c + 1][0] = w.z; qf[x][2 * c + 1][1] = w.w;
-        }
+      for (int s = 0; s < kSteps; s += 2) {
+        // 8 values: bf16 pieces t + 4 c of the row, or half a 16-value piece
+        const uint4 w = ldg_stream(kHalf ? src + (t + 4 * (s / 4)) * 16 + 4 * (s % 4) : src + (t + 2 * s) * 8);
+        qf[x][s][0] = w.x; qf[x][s][1] = w.y;
+        qf[x][s + 1][0] = w.z; qf[x][s + 1][1] = w.w;
+      }
+    }
+    int bad = n < 0 ? TV_ST_BAD_SIZE : (!fits || pages > held) ? TV_ST_BAD_BLOCK : 0;
+    // another CTA may flag the request while this one's threads read its status: they decide
+    // together. (The barrier also keeps the last unit's shared sums until they are read.)
+    if (__syncthreads_or(st | bad)) {
+      if (st == 0 && threadIdx.x == 0) atomicOr(p.status + b, bad);
+      if (tile0 == 0 && p.split && p.by_unit && threadIdx.x == 0) p.begins[b * p.hkv + h] = DecBegin{0, 0, -1, 0};
+      tile0 = nt;
+      continue;
+    }
+#pragma unroll
+    for (int x = 0; x < NT; ++x) {
+      if (x * 8 + g >= p.group) {
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) qf[x][s][0] = qf[x][s][1] = 0u;
+      }
+      if constexpr (!kHalf) {
         fac[x][0] = fac[x][1] = p.scale_log2;
       } else {
         uint32_t top = 0;
-#pragma unroll
-        for (int c = 0; c < kKPieces; ++c) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            uint4 w = *reinterpret_cast<const uint4*>(src + (t + 4 * c) * 16 + 8 * u);
-            if (!live) w = make_uint4(0u, 0u, 0u, 0u);
-            qf[x][4 * c + 2 * u][0] = w.x; qf[x][4 * c + 2 * u][1] = w.y;
-            qf[x][4 * c + 2 * u + 1][0] = w.z; qf[x][4 * c + 2 * u + 1][1] = w.w;
-          }
-        }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s)
 #pragma unroll
@@ -301,9 +317,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 
     // ---- pages: block ids a warp-load at a time, rows a page ahead
     int ids = 0, ids_next = 0;
-    auto load_ids = [&](int base) {
-      const int i = base + lane;
-      int blk = i < iters ? row[first + i * kDecWarps] : 0;
+    auto valid = [&](int blk) {
       if (blk < 0 || blk >= p.num_blocks) { bad = TV_ST_BAD_BLOCK; blk = 0; }
       return blk;
     };
@@ -345,11 +359,11 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     };
     size_t r_now = 0;
     if (iters > 0) {
-      ids = load_ids(0);
+      ids = valid(ids_first);
       r_now = head_row(0);
       load_k(r_now);
       load_v(r_now);
-      ids_next = iters > 32 ? load_ids(32) : 0;
+      ids_next = fetch_ids(32);
     }
     for (int it = 0; it < iters; ++it) {
       const int key0 = (first + it * kDecWarps) * TV_BLOCK_SIZE;
@@ -384,8 +398,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       const float k0 = ks[0], k1 = ks[1];
       if (it + 1 < iters) {
         if ((it + 1) % 32 == 0) {
-          ids = ids_next;
-          ids_next = it + 33 < iters ? load_ids(it + 33) : 0;
+          ids = valid(ids_next);
+          ids_next = fetch_ids(it + 33);
         }
         r_now = head_row(it + 1);
         load_k(r_now);
@@ -484,56 +498,45 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     }
 
     // ---- join the warps
-    const bool any_bad = __syncthreads_or(bad);
-    if (any_bad && bad) atomicOr(p.status + b, bad);
 #pragma unroll
     for (int x = 0; x < NT; ++x)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) l[x][e] += __shfl_xor_sync(0xffffffffu, l[x][e], d);
-        if (g == 0) {
-          s_m[warp][8 * x + 2 * t + e] = m[x][e];
-          s_ref[warp][8 * x + 2 * t + e] = ref[x][e];
-          s_l[warp][8 * x + 2 * t + e] = l[x][e];
-        }
-      }
-    __syncthreads();
-#pragma unroll
-    for (int x = 0; x < NT; ++x)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
         const int qi = 8 * x + 2 * t + e;
-        float top = s_ref[0][qi];
-#pragma unroll
-        for (int w = 1; w < kDecWarps; ++w) top = fmaxf(top, s_ref[w][qi]);
-        const float f = fast_exp2(ref[x][e] - top);
+        if (g == 0) s_stat[warp][qi] = make_float4(m[x][e], ref[x][e], l[x][e], 0.0f);
         float* dst = s_o + (static_cast<size_t>(warp) * 8 * NT + qi) * kRowPad;
 #pragma unroll
         for (int i = 0; i < kSteps; ++i) {
           // the column of tile i's row g (and the next one in its row g + 8)
           const int d = kRowBytes == 256 ? 8 * g + 64 * (i / 4) + 2 * (i % 4) : kRowBytes == 128 && kHalf ? 16 * g + 2 * i : 8 * g + 2 * i;
-          *reinterpret_cast<float2*>(dst + d) = make_float2(o[x][i][e] * f, o[x][i][e + 2] * f);
+          *reinterpret_cast<float2*>(dst + d) = make_float2(o[x][i][e], o[x][i][e + 2]);
         }
       }
-    __syncthreads();
+    const bool any_bad = __syncthreads_or(bad);
+    if (bad) atomicOr(p.status + b, bad);
     const bool whole = tile0 == 0 && tile1 == nt;
     float* slot = p.partials + (static_cast<size_t>(cta) * 2 + (tile0 == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
     if (!any_bad || !whole) {
       for (int i = threadIdx.x; i < p.group * (D / 2); i += kDecThreads) {
         const int qi = i / (D / 2), d = i % (D / 2) * 2;
+        float mm = kLowest, mr = kLowest, ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+          mm = fmaxf(mm, s_stat[w][qi].x);
+          mr = fmaxf(mr, s_stat[w][qi].y);
+        }
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
         for (int w = 0; w < kDecWarps; ++w) {
+          const float4 s4 = s_stat[w][qi];
+          const float f = fast_exp2(s4.y - mr);
           const float2 v = *reinterpret_cast<const float2*>(s_o + (static_cast<size_t>(w) * 8 * NT + qi) * kRowPad + d);
-          acc.x += v.x;
-          acc.y += v.y;
+          acc.x += v.x * f;
+          acc.y += v.y * f;
+          ll += s4.z * fast_exp2(s4.x - mm);
         }
-        float mm = s_m[0][qi], mr = s_ref[0][qi], ll = 0.0f;
-#pragma unroll
-        for (int w = 1; w < kDecWarps; ++w) { mm = fmaxf(mm, s_m[w][qi]); mr = fmaxf(mr, s_ref[w][qi]); }
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) ll += s_l[w][qi] * fast_exp2(s_m[w][qi] - mm);
         if (whole) {
           const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
           const float f = n == 0 ? 0.0f : fast_exp2(mr - mm) / ll;
@@ -545,94 +548,124 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         }
       }
     }
-    if (!whole) {
-      if (tile0 > 0) {
-        task.mid_b = b;
-        task.mid_h = h;
-      } else {
-        task.b = b;
-        task.h = h;
+    if (tile0 > 0) {
+      mid = b * p.hkv + h;
+    } else if (p.split) {
+      DecBegin d = {b * p.hkv + h, cta, -1, 0};
+      if (!whole) {
         // the CTA of the unit's last tile: the largest c with total * c / grid <= its start
         const long long e = unit + kDecUnitCost + nt;
-        task.last = static_cast<int>((e * grid + total - 1) / total - 1);
+        d.last = static_cast<int>((e * grid + total - 1) / total - 1);
+        begun = d;
       }
+      if (p.by_unit && threadIdx.x == 0) p.begins[d.unit] = d;
     }
-    __syncthreads();                   // the shared sums are read before the next unit writes them
     if (tile1 < nt) break;
     tile0 = nt;
   }
-  if (p.split && threadIdx.x == 0) p.tasks[cta] = task;
+  if (p.split && threadIdx.x == 0) {
+    p.mids[cta] = mid;
+    if (!p.by_unit) p.begins[cta] = begun;
+  }
 }
 
-// Join the partials of the unit that CTA blockIdx.x began: slot 1 of that
-// CTA, then slot 0 of the CTAs after it that worked on the unit. A warp takes
-// a query head and every (warps per head)-th partial.
+// Join the partials of one unit (blockIdx.x) for one query head (blockIdx.y).
+// D / 4 lanes hold a partial; a warp takes every (warps)-th one, kMergeBatch
+// of them in flight: which partials exist, their references and their sums
+// come in one round trip.
 template <int D>
 __global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kVec = D / 32;
-  constexpr int kWarps = kMergeThreads / 32;
-  __shared__ float s_acc[kWarps][D];
-  __shared__ float s_stat[kWarps][3];
+  constexpr int kLanes = D / 4, kSub = 32 / kLanes, kWarps = kMergeThreads / 32, kParts = kWarps * kSub;
+  __shared__ float4 s_acc[kParts][kLanes];
+  __shared__ float s_stat[kParts][3];
   grid_dependency_wait();
-  const DecTask task = p.tasks[blockIdx.x];
+  grid_launch_dependents();
+  const DecBegin task = p.begins[blockIdx.x];
   if (task.last < 0) return;
-  if (p.status[task.b] != 0) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int parts = kWarps / p.group;            // group <= 16
-  const int qi = warp % p.group, part = warp / p.group;
-  float acc[kVec], mm = kLowest, mr = kLowest, ll = 0.0f;
+  const int b = task.unit / p.hkv, h = task.unit - b * p.hkv, qi = blockIdx.y;
+  const int lane = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+  const int st = p.status[b], count = task.last - task.first + 1;
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float mm = kLowest, mr = kLowest, ll = 0.0f;
+  for (int base = part; base < count; base += kMergeBatch * kParts) {
+    float4 v[kMergeBatch], s[kMergeBatch];
+    bool has[kMergeBatch];
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
-  if (part < parts) {
-#pragma unroll 4
-    for (int c = static_cast<int>(blockIdx.x) + part; c <= task.last; c += parts) {
-      const bool own = c == static_cast<int>(blockIdx.x);
-      const bool has = own || (p.tasks[c].mid_b == task.b && p.tasks[c].mid_h == task.h);
-      const float* slot = p.partials + (static_cast<size_t>(c) * 2 + (own ? 1 : 0)) * dec_slot_floats(p.group, D);
-      if (!has) continue;
-      const float4 st = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi);
-      const float nm = fmaxf(mm, st.x), nr = fmaxf(mr, st.y);
-      ll = ll * fast_exp2(mm - nm) + st.z * fast_exp2(st.x - nm);
-      const float a = fast_exp2(mr - nr), c2 = fast_exp2(st.y - nr);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) acc[i] = acc[i] * a + slot[static_cast<size_t>(qi) * D + i * 32 + lane] * c2;
-      mm = nm;
-      mr = nr;
+    for (int u = 0; u < kMergeBatch; ++u) {
+      const int i = base + u * kParts, c = min(task.first + i, task.last);
+      const float* slot = p.partials + (static_cast<size_t>(c) * 2 + (i == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
+      has[u] = i < count && (i == 0 || p.mids[c] == task.unit);
+      s[u] = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi);
+      v[u] = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(qi) * D + 4 * lane);
     }
+    float nm = mm, nr = mr;
 #pragma unroll
-    for (int i = 0; i < kVec; ++i) s_acc[warp][i * 32 + lane] = acc[i];
-    if (lane == 0) { s_stat[warp][0] = mm; s_stat[warp][1] = mr; s_stat[warp][2] = ll; }
-  }
-  __syncthreads();
-  if (part != 0 || warp >= p.group) return;
-  for (int w = 1; w < parts; ++w) {
-    const int o = w * p.group + qi;
-    const float om = s_stat[o][0], orf = s_stat[o][1];
-    const float nm = fmaxf(mm, om), nr = fmaxf(mr, orf);
-    ll = ll * fast_exp2(mm - nm) + s_stat[o][2] * fast_exp2(om - nm);
-    const float a = fast_exp2(mr - nr), c2 = fast_exp2(orf - nr);
-#pragma unroll
-    for (int i = 0; i < kVec; ++i) acc[i] = acc[i] * a + s_acc[o][i * 32 + lane] * c2;
+    for (int u = 0; u < kMergeBatch; ++u) {
+      if (has[u]) {
+        nm = fmaxf(nm, s[u].x);
+        nr = fmaxf(nr, s[u].y);
+      }
+    }
+    ll *= fast_exp2(mm - nm);
+    const float down = fast_exp2(mr - nr);
+    acc = make_float4(acc.x * down, acc.y * down, acc.z * down, acc.w * down);
     mm = nm;
     mr = nr;
-  }
-  const size_t at = static_cast<size_t>(task.b) * p.hq + static_cast<size_t>(task.h) * p.group + qi;
-  const float f = fast_exp2(mr - mm) / ll;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) p.out[at * D + i * 32 + lane] = __float2bfloat16_rn(acc[i] * f);
-  if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
+    for (int u = 0; u < kMergeBatch; ++u) {
+      if (has[u]) {
+        const float f = fast_exp2(s[u].y - mr);
+        ll += s[u].z * fast_exp2(s[u].x - mm);
+        acc.x += v[u].x * f;
+        acc.y += v[u].y * f;
+        acc.z += v[u].z * f;
+        acc.w += v[u].w * f;
+      }
+    }
+  }
+  s_acc[part][lane] = acc;
+  if (lane == 0) {
+    s_stat[part][0] = mm;
+    s_stat[part][1] = mr;
+    s_stat[part][2] = ll;
+  }
+  __syncthreads();
+  if (part != 0 || st != 0) return;
+  float nm = mm, nr = mr;
+#pragma unroll
+  for (int w = 1; w < kParts; ++w) {
+    nm = fmaxf(nm, s_stat[w][0]);
+    nr = fmaxf(nr, s_stat[w][1]);
+  }
+  ll = 0.0f;
+  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+  for (int w = 0; w < kParts; ++w) {
+    const float f = fast_exp2(s_stat[w][1] - nr);
+    const float4 v = s_acc[w][lane];
+    ll += s_stat[w][2] * fast_exp2(s_stat[w][0] - nm);
+    acc.x += v.x * f;
+    acc.y += v.y * f;
+    acc.z += v.z * f;
+    acc.w += v.w * f;
+  }
+  const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
+  const float f = fast_exp2(nr - nm) / ll;
+  *reinterpret_cast<uint2*>(p.out + at * D + 4 * lane) = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
+  if (p.lse != nullptr && lane == 0) p.lse[at] = (nm + log2f(ll)) * 0.69314718055994531f;
 }
 
 template <int kFmt, int D, int NT>
-static int launch_decode(const DecodeParams& p, int sms, int dev, cudaStream_t stream) {
+static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) {
   using Tr = DecTraits<kFmt, D, NT>;
   constexpr size_t smem = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
   static size_t smem_set[kMaxDevices] = {0};
   auto* kernel = decode_kernel<kFmt, D, NT>;
   if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
-  const int grid = sms * Tr::kPerSm;
+  const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
+  p.by_unit = units <= grid ? 1 : 0;
   if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), smem, stream, p) != cudaSuccess) return TV_ERR_CUDA;
-  if (p.split && launch_pdl(decode_merge_kernel<D>, dim3(grid), dim3(kMergeThreads), 0, stream, p) != cudaSuccess)
+  if (p.split && launch_pdl(decode_merge_kernel<D>, dim3(p.by_unit ? units : grid, p.group), dim3(kMergeThreads), 0, stream, p) != cudaSuccess)
     return TV_ERR_CUDA;
   return TV_OK;
 }
@@ -644,7 +677,7 @@ static int launch_decode_fmt(const DecodeParams& p, int d, int sms, int dev, cud
   return p.group <= 8 ? launch_decode<kFmt, 128, 1>(p, sms, dev, stream) : launch_decode<kFmt, 128, 2>(p, sms, dev, stream);
 }
 
-static size_t dec_task_bytes(int ctas) { return (sizeof(DecTask) * ctas + 255) / 256 * 256; }
+static size_t dec_task_bytes(int ctas) { return ((sizeof(DecBegin) + sizeof(int)) * ctas + 255) / 256 * 256; }
 
 }  // namespace tv
 
@@ -673,7 +706,8 @@ extern "C" int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32
                                    void* stream) {
   int rc = tv::check_geom(geom);
   if (rc != TV_OK) return rc;
-  if (kv_format != TV_KV_BF16 && kv_format != TV_KV_E4M3 && kv_format != TV_KV_INT8) return TV_ERR_BAD_GEOMETRY;
+  if ((kv_format != TV_KV_BF16 && kv_format != TV_KV_E4M3 && kv_format != TV_KV_INT8) || geom->num_kv_heads > tv::kDecMaxHeads)
+    return TV_ERR_BAD_GEOMETRY;
   if (batch < 0 || batch > tv::kKvMaxBatch || max_blocks_per_req < 1 || num_blocks < 1 ||
       q_ld < static_cast<long long>(geom->num_q_heads) * geom->head_dim)
     return TV_ERR_BAD_SIZE;
@@ -701,7 +735,8 @@ extern "C" int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32
   p.k_cache = static_cast<const uint8_t*>(k_cache); p.v_cache = static_cast<const uint8_t*>(v_cache);
   p.k_scale = k_scale; p.v_scale = v_scale;
   p.out = static_cast<__nv_bfloat16*>(out); p.lse = lse; p.status = status;
-  p.tasks = static_cast<tv::DecTask*>(workspace);
+  p.begins = static_cast<tv::DecBegin*>(workspace);
+  p.mids = reinterpret_cast<int*>(p.begins + sms * tv::kDecMaxPerSm);
   p.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + tv::dec_task_bytes(sms * tv::kDecMaxPerSm));
   p.batch = batch; p.hq = geom->num_q_heads; p.hkv = geom->num_kv_heads;
   p.group = geom->num_q_heads / geom->num_kv_heads;

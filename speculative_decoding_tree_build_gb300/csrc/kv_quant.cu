@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __gri
             sc[e][j] = 0.0f;
             if (live[e][j]) {
               c[e][j] = __ldcs(reinterpret_cast<const uint2*>((isv ? p.v_cache : p.k_cache) + src * D) + v);
-              sc[e][j] = __ldg((isv ? p.v_scale : p.k_scale) + src + row);
+              sc[e][j] = (isv ? p.v_scale : p.k_scale)[src + row];
             }
           }
         }
