@@ -38,6 +38,8 @@
 // kNoSplitPages pages a request, units are never cut and there is one launch.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "tv_kv8.cuh"
 #include "tv_share.cuh"
 
@@ -47,12 +49,13 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecTileKeys = TV_BLOCK_SIZE * kDecWarps;
 constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
-constexpr int kDecMinShare = 4;        // least cost worth a CTA of its own
+constexpr int kDecMinShare = 3;        // least cost worth a CTA of its own: a unit of one tile
 constexpr int kNoSplitPages = 16;
 constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
 constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay below 2^24
-constexpr int kMergeThreads = 128;
-constexpr int kMergeBatch = 8;         // partials a warp has in flight
+constexpr int kMergeWarps = 4;         // warps of a joining CTA at least
+constexpr int kMergeMaxParts = 8;      // warps that share a query head's partials at most
+constexpr int kMergeBatch = 8;         // partials whose sums a warp has in flight
 constexpr float kLowest = -3.4028234663852886e38f;
 
 // What the CTA that begins a unit tells the joining grid: the CTAs that work
@@ -80,6 +83,7 @@ struct DecodeParams {
   int32_t* status;
   int batch, hq, hkv, group, max_blocks, num_blocks, split;
   int by_unit;         // how begins is indexed
+  int parts;           // warps that share a query head's partials
   float scale_log2;
 };
 
@@ -569,90 +573,110 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   }
 }
 
-// Join the partials of one unit (blockIdx.x) for one query head (blockIdx.y).
-// D / 4 lanes hold a partial; a warp takes every (warps)-th one, kMergeBatch
-// of them in flight: which partials exist, their references and their sums
-// come in one round trip.
+// Join the partials of unit blockIdx.x. A warp takes a query head, or one of
+// p.parts interleaved parts of its partials where a unit is cut into many. A
+// lane looks up one of up to 32 partials (does that CTA's slot hold this unit,
+// its references and sum), while the first sums are already on their way.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) decode_merge_kernel(const __grid_constant__ DecodeParams p) {
-  constexpr int kLanes = D / 4, kSub = 32 / kLanes, kWarps = kMergeThreads / 32, kParts = kWarps * kSub;
-  __shared__ float4 s_acc[kParts][kLanes];
-  __shared__ float s_stat[kParts][3];
+__global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const __grid_constant__ DecodeParams p) {
+  constexpr int kVec = D / 32;         // columns of a lane
+  using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
+  __shared__ float s_acc[kMergeMaxParts][D];
+  __shared__ float4 s_stat[kMergeMaxParts];
   grid_dependency_wait();
   grid_launch_dependents();
   const DecBegin task = p.begins[blockIdx.x];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
+  const int part = warp % p.parts, qi = blockIdx.y * (warps / p.parts) + warp / p.parts;
   if (task.last < 0) return;
-  const int b = task.unit / p.hkv, h = task.unit - b * p.hkv, qi = blockIdx.y;
-  const int lane = threadIdx.x % kLanes, part = threadIdx.x / kLanes;
+  const int b = task.unit / p.hkv, h = task.unit - b * p.hkv;
+  const bool live = qi < p.group;
+  float acc[kVec], mm = kLowest, mr = kLowest, ll = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
   const int st = p.status[b], count = task.last - task.first + 1;
-  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  float mm = kLowest, mr = kLowest, ll = 0.0f;
-  for (int base = part; base < count; base += kMergeBatch * kParts) {
-    float4 v[kMergeBatch], s[kMergeBatch];
-    bool has[kMergeBatch];
+  const int mine = live && part < count ? (count - part - 1) / p.parts + 1 : 0;     // this warp's partials
+  auto slot_of = [&](int i) {
+    const int k = part + i * p.parts;
+    return p.partials + (static_cast<size_t>(task.first + k) * 2 + (k == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
+  };
+  for (int base = 0; base < mine; base += 32) {
+    const int here = min(32, mine - base);
+    Vec v[kMergeBatch];
+    auto load = [&](int from) {
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
-      const int i = base + u * kParts, c = min(task.first + i, task.last);
-      const float* slot = p.partials + (static_cast<size_t>(c) * 2 + (i == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
-      has[u] = i < count && (i == 0 || p.mids[c] == task.unit);
-      s[u] = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi);
-      v[u] = *reinterpret_cast<const float4*>(slot + static_cast<size_t>(qi) * D + 4 * lane);
+      for (int u = 0; u < kMergeBatch; ++u)
+        v[u] = *reinterpret_cast<const Vec*>(slot_of(base + min(from + u, here - 1)) + static_cast<size_t>(qi) * D + kVec * lane);
+    };
+    load(0);
+    float4 s = make_float4(kLowest, kLowest, 0.0f, 0.0f);
+    bool has = false;
+    if (lane < here) {
+      const int k = part + (base + lane) * p.parts;
+      has = k == 0 || p.mids[task.first + k] == task.unit;
+      s = *reinterpret_cast<const float4*>(slot_of(base + lane) + static_cast<size_t>(p.group) * D + 4 * qi);
     }
-    float nm = mm, nr = mr;
+    float nm = has ? fmaxf(mm, s.x) : mm, nr = has ? fmaxf(mr, s.y) : mr;
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
-      if (has[u]) {
-        nm = fmaxf(nm, s[u].x);
-        nr = fmaxf(nr, s[u].y);
-      }
+    for (int d = 16; d > 0; d >>= 1) {
+      nm = fmaxf(nm, __shfl_xor_sync(0xffffffffu, nm, d));
+      nr = fmaxf(nr, __shfl_xor_sync(0xffffffffu, nr, d));
     }
-    ll *= fast_exp2(mm - nm);
+    float sum = has ? s.z * fast_exp2(s.x - nm) : 0.0f;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    ll = ll * fast_exp2(mm - nm) + sum;
     const float down = fast_exp2(mr - nr);
-    acc = make_float4(acc.x * down, acc.y * down, acc.z * down, acc.w * down);
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) acc[i] *= down;
     mm = nm;
     mr = nr;
+    const float f = fast_exp2(s.y - nr);
+    const unsigned hold = __ballot_sync(0xffffffffu, has);
+    for (int from = 0; from < here; from += kMergeBatch) {
+      if (from > 0) load(from);
 #pragma unroll
-    for (int u = 0; u < kMergeBatch; ++u) {
-      if (has[u]) {
-        const float f = fast_exp2(s[u].y - mr);
-        ll += s[u].z * fast_exp2(s[u].x - mm);
-        acc.x += v[u].x * f;
-        acc.y += v[u].y * f;
-        acc.z += v[u].z * f;
-        acc.w += v[u].w * f;
+      for (int u = 0; u < kMergeBatch; ++u) {
+        const float w = __shfl_sync(0xffffffffu, f, (from + u) % 32);
+        if (from + u < here && (hold >> (from + u) & 1u)) {
+          const float* x = reinterpret_cast<const float*>(&v[u]);
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) acc[i] += x[i] * w;
+        }
       }
     }
   }
-  s_acc[part][lane] = acc;
-  if (lane == 0) {
-    s_stat[part][0] = mm;
-    s_stat[part][1] = mr;
-    s_stat[part][2] = ll;
-  }
-  __syncthreads();
-  if (part != 0 || st != 0) return;
-  float nm = mm, nr = mr;
+  if (p.parts > 1) {
 #pragma unroll
-  for (int w = 1; w < kParts; ++w) {
-    nm = fmaxf(nm, s_stat[w][0]);
-    nr = fmaxf(nr, s_stat[w][1]);
-  }
-  ll = 0.0f;
-  acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = 0; i < kVec; ++i) s_acc[warp][kVec * lane + i] = acc[i];
+    if (lane == 0) s_stat[warp] = make_float4(mm, mr, ll, 0.0f);
+    __syncthreads();
+    if (part != 0) return;
+    float nm = mm, nr = mr;
+    for (int w = 1; w < p.parts; ++w) {
+      nm = fmaxf(nm, s_stat[warp + w].x);
+      nr = fmaxf(nr, s_stat[warp + w].y);
+    }
+    ll = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kParts; ++w) {
-    const float f = fast_exp2(s_stat[w][1] - nr);
-    const float4 v = s_acc[w][lane];
-    ll += s_stat[w][2] * fast_exp2(s_stat[w][0] - nm);
-    acc.x += v.x * f;
-    acc.y += v.y * f;
-    acc.z += v.z * f;
-    acc.w += v.w * f;
+    for (int i = 0; i < kVec; ++i) acc[i] = 0.0f;
+    for (int w = 0; w < p.parts; ++w) {
+      const float4 s4 = s_stat[warp + w];
+      const float f = fast_exp2(s4.y - nr);
+      ll += s4.z * fast_exp2(s4.x - nm);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) acc[i] += s_acc[warp + w][kVec * lane + i] * f;
+    }
+    mm = nm;
+    mr = nr;
   }
+  if (!live || st != 0) return;
   const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
-  const float f = fast_exp2(nr - nm) / ll;
-  *reinterpret_cast<uint2*>(p.out + at * D + 4 * lane) = make_uint2(pack_bf16x2(acc.x * f, acc.y * f), pack_bf16x2(acc.z * f, acc.w * f));
-  if (p.lse != nullptr && lane == 0) p.lse[at] = (nm + log2f(ll)) * 0.69314718055994531f;
+  const float f = fast_exp2(mr - mm) / ll;
+  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + at * D + kVec * lane);
+#pragma unroll
+  for (int i = 0; i < kVec; i += 2) out[i / 2] = pack_bf16x2(acc[i] * f, acc[i + 1] * f);
+  if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
 template <int kFmt, int D, int NT>
@@ -664,8 +688,14 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
   if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
   const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
   p.by_unit = units <= grid ? 1 : 0;
+  p.parts = 1;
   if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), smem, stream, p) != cudaSuccess) return TV_ERR_CUDA;
-  if (p.split && launch_pdl(decode_merge_kernel<D>, dim3(p.by_unit ? units : grid, p.group), dim3(kMergeThreads), 0, stream, p) != cudaSuccess)
+  if (!p.split) return TV_OK;
+  // a unit's partials: about grid / units and both ends; eight of them a warp
+  const int partials = grid / units + 2;
+  while (p.parts < kMergeMaxParts && p.parts * kMergeBatch < partials) p.parts *= 2;
+  const int warps = p.parts > kMergeWarps ? p.parts : kMergeWarps, heads = warps / p.parts;
+  if (launch_pdl(decode_merge_kernel<D>, dim3(p.by_unit ? units : grid, (p.group + heads - 1) / heads), dim3(32 * warps), 0, stream, p) != cudaSuccess)
     return TV_ERR_CUDA;
   return TV_OK;
 }
