@@ -14,9 +14,9 @@
 namespace tv {
 
 constexpr int kAppendThreads = 256;
-constexpr int kAppendPerSm = 3;      // CTAs an SM: 2 / 3 / 4 took 46.6 / 41.8 / 42.1 us for 201 MB (4 spills)
-constexpr int kAppendBatch = 4;      // rows whose loads a thread has in flight
-constexpr int kAppendMaxRows = 64;   // rows of k_new / v_new per CTA at most
+constexpr int kAppendPerSm = 3;      // CTAs an SM
+constexpr int kAppendAhead = 4;      // rows whose loads a thread has in flight
+constexpr int kAppendMaxRows = 128;  // rows of k_new / v_new per CTA at most
 
 struct AppendParams {
   const __nv_bfloat16* k_new;
@@ -36,54 +36,58 @@ struct AppendParams {
   int slots;                         // rows taken at a time
 };
 
-// What the CTA knows of the row of K/V it handles.
-struct AppendRow {
-  int req;       // the request that owns it, -1: none (or one that is skipped)
-  int head;      // the CTA's first row of that request: its verdict counts for all of them
-  int slot;
-  int blk;       // the slot's block
+// A request's rows among the CTA's rows.
+struct AppendRun {
+  int req;
+  int c0;        // the request's first row
+  int start;     // that row's slot
+  int last;      // one past the run, counted from the CTA's first row
 };
 
+// A CTA quantises a contiguous range of rows (all of them in one wave of CTAs
+// where they fit), kLanes threads a row and head. Each thread keeps its head
+// and steps through the rows with kAppendAhead of them in flight: a row's
+// registers are loaded again as soon as it is encoded. (Loading a batch of
+// four, then encoding and storing it, left the memory idle while the CTAs of
+// an SM computed in step: 41.8 us for 201 MB.)
 template <int kFmt, int D>
 __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int kLanes = D / 16;       // lanes that hold one row, two pieces of 8 values each
-  __shared__ AppendRow s_row[kAppendMaxRows];
-  __shared__ int s_bad[kAppendMaxRows];                      // by head row
+  __shared__ AppendRun s_run[kAppendMaxRows];                // by the run's first row
+  __shared__ int s_bad[kAppendMaxRows];                      // by the run's first row
+  __shared__ uint32_t s_heads[kAppendMaxRows / 32];          // bit r: a run begins at row r
+  __shared__ long long s_row[kAppendMaxRows];                // the row's place in the pool (head 0), -1: none
+  __shared__ int s_head[kAppendMaxRows];
   __shared__ int s_cross[2][4];        // requests that reach past the CTA's rows, before and behind:
-                                       // request, first page, pages, head row
+                                       // request, first page, pages, first row of the run
   grid_dependency_wait();
   grid_launch_dependents();
   const int t0 = blockIdx.x * p.cta_rows;
   const int nrows = min(p.cta_rows, p.rows - t0), t1 = t0 + nrows;
-  // kLanes threads keep one head and step through the CTA's rows
   const int part = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
   const int slot0 = part / p.cta_heads, head = blockIdx.y * p.cta_heads + part - slot0 * p.cta_heads;
   const bool mine = slot0 < p.slots && head < 2 * p.hkv;
   const bool isv = head >= p.hkv;
   const int h = isv ? head - p.hkv : head;
-  const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + static_cast<long long>(h) * D + lane * 8;
-  uint4 x[kAppendBatch][2];            // a warp's loads cover whole sectors: piece lane, piece lane + kLanes
-  auto load = [&](int r0) {
-#pragma unroll
-    for (int e = 0; e < kAppendBatch; ++e) {
-      const int r = r0 + e * p.slots;
-      x[e][0] = x[e][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (mine && r < nrows) {
-        const __nv_bfloat16* from = src + (t0 + r) * p.kv_ld;
-        x[e][0] = *reinterpret_cast<const uint4*>(from);
-        x[e][1] = *reinterpret_cast<const uint4*>(from + kLanes * 8);
-      }
+  const long long step = p.slots * p.kv_ld;
+  const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + (t0 + slot0) * p.kv_ld + static_cast<long long>(h) * D + lane * 8;
+  uint4 x[kAppendAhead][2];            // a warp's loads cover whole sectors: piece lane, piece lane + kLanes
+  auto load = [&](uint4 (&to)[2], int r) {
+    to[0] = to[1] = make_uint4(0u, 0u, 0u, 0u);
+    if (mine && r < nrows) {
+      to[0] = *reinterpret_cast<const uint4*>(src);
+      to[1] = *reinterpret_cast<const uint4*>(src + kLanes * 8);
     }
+    src += step;
   };
-  load(slot0);                         // on their way while the rows' slots are found
+#pragma unroll
+  for (int e = 0; e < kAppendAhead; ++e) load(x[e], slot0 + e * p.slots);    // on their way while slots are found
 
   // A thread looks at request i with all that it needs of it in one round
   // trip, and describes those of the CTA's rows that the request owns.
-  if (threadIdx.x < kAppendMaxRows) {
-    s_row[threadIdx.x].req = -1;
-    s_bad[threadIdx.x] = 0;
-  }
-  if (threadIdx.x < 2) s_cross[threadIdx.x][2] = 0;
+  if (threadIdx.x < kAppendMaxRows) s_bad[threadIdx.x] = 0;
+  if (threadIdx.x < kAppendMaxRows / 32) s_heads[threadIdx.x] = 0u;
+  if (threadIdx.x < 8) s_cross[threadIdx.x / 4][threadIdx.x % 4] = 0;
   __syncthreads();
 #pragma unroll 2
   for (int i = threadIdx.x; i < p.batch; i += kAppendThreads) {
@@ -92,18 +96,12 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
     if (c1 <= c0 || st != 0) continue;
     if (blockIdx.x == 0 && blockIdx.y == 0 && (c1 > p.rows || c0 < 0 || start < 0)) atomicOr(p.status + i, TV_ST_BAD_SIZE);
     if (c0 < 0 || c1 > p.rows || start < 0 || c0 >= t1 || c1 <= t0) continue;
-    const int first = max(c0, t0) - t0, last = min(c1, t1) - t0;
+    const int first = max(c0, t0) - t0;
     const long long end = static_cast<long long>(start) + (c1 - c0);
     const bool fits = (end - 1) / TV_BLOCK_SIZE < held;      // (which also keeps slots below 2^31)
     if (!fits) s_bad[first] = TV_ST_BAD_BLOCK;
-    for (int r = first; r < last; ++r) {
-      AppendRow a;
-      a.req = i;
-      a.head = first;
-      a.slot = fits ? start + (t0 + r - c0) : 0;
-      a.blk = -1;
-      s_row[r] = a;
-    }
+    s_run[first] = AppendRun{i, c0, start, min(c1, t1) - t0};
+    atomicOr(&s_heads[first / 32], 1u << (first % 32));
     if (fits && (c0 < t0 || c1 > t1)) {
       int* cross = s_cross[c0 < t0 ? 0 : 1];
       cross[0] = i;
@@ -114,32 +112,53 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
   }
   __syncthreads();
   // the rows' blocks, and all other blocks of a request that other CTAs have rows of
-  if (threadIdx.x < nrows && s_row[threadIdx.x].req >= 0) {
-    AppendRow& a = s_row[threadIdx.x];
-    if (s_bad[a.head] == 0) {
-      const int blk = p.block_table[static_cast<size_t>(a.req) * p.max_blocks + a.slot / TV_BLOCK_SIZE];
-      a.blk = blk;
-      if (blk < 0 || blk >= p.num_blocks) s_bad[a.head] = TV_ST_BAD_BLOCK;
+  if (threadIdx.x < nrows) {
+    const int r = threadIdx.x;
+    int w = r / 32, first = -1;
+    uint32_t bits = s_heads[w] & (0xffffffffu >> (31 - r % 32));
+    while (bits == 0u && w > 0) bits = s_heads[--w];
+    if (bits != 0u) first = 32 * w + 31 - __clz(bits);
+    s_row[r] = -1;
+    s_head[r] = 0;
+    if (first >= 0 && r < s_run[first].last && s_bad[first] == 0) {
+      const AppendRun run = s_run[first];
+      // (offsets that overlap let two requests describe one run: the index stays inside the table)
+      const int slot = run.start + (t0 + r - run.c0);
+      const int page = slot / TV_BLOCK_SIZE;
+      const int blk = slot >= 0 && page < p.max_blocks ? p.block_table[static_cast<size_t>(run.req) * p.max_blocks + page] : -1;
+      s_row[r] = static_cast<long long>(blk) * p.hkv * TV_BLOCK_SIZE + slot % TV_BLOCK_SIZE;
+      s_head[r] = first;
+      if (blk < 0 || blk >= p.num_blocks) s_bad[first] = TV_ST_BAD_BLOCK;
     }
   }
 #pragma unroll
   for (int c = 0; c < 2; ++c) {
-    const int pages = s_cross[c][2];
+    const int pages = min(s_cross[c][2], p.max_blocks - s_cross[c][1]);
     const int32_t* row = p.block_table + static_cast<size_t>(s_cross[c][0]) * p.max_blocks + s_cross[c][1];
     bool bad = false;
+#pragma unroll 4
     for (int e = threadIdx.x; e < pages; e += kAppendThreads) {
       const int blk = row[e];
       bad |= blk < 0 || blk >= p.num_blocks;
     }
     if (bad) s_bad[s_cross[c][3]] = TV_ST_BAD_BLOCK;
   }
+  __syncthreads();
+  // one bad block holds all rows of its request back
+  if (threadIdx.x < nrows) {
+    const int r = threadIdx.x;
+    if (s_bad[s_head[r]] != 0) s_row[r] = -1;
+    if (s_bad[r] != 0 && blockIdx.y == 0) atomicOr(p.status + s_run[r].req, s_bad[r]);
+  }
+  __syncthreads();
 
-  uint2 code[kAppendBatch][2];
-  float scale[kAppendBatch];
-  auto encode = [&](int r0) {
+  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + lane * 8;
+  float* scales = isv ? p.v_scale : p.k_scale;
+  for (int r0 = 0; r0 < nrows; r0 += kAppendAhead * p.slots) {
 #pragma unroll
-    for (int e = 0; e < kAppendBatch; ++e) {
+    for (int e = 0; e < kAppendAhead; ++e) {
       if (r0 + e * p.slots >= nrows) break;                  // the same for all threads: the shuffles are whole
+      const int r = r0 + slot0 + e * p.slots;
       // bits 14..0 of both halves order as integers: halves are compared apart
       uint32_t top = 0;
 #pragma unroll
@@ -150,43 +169,22 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
       for (int s = kLanes / 2; s > 0; s >>= 1) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, s));
       top = max(top & 0xffffu, top >> 16);
       const KvRowScale sc = kv_row_scale<kFmt>(top);
-      scale[e] = sc.scale;
+      uint2 code[2] = {make_uint2(0u, 0u), make_uint2(0u, 0u)};
+      if (sc.mul != 0.0f) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        uint2 c = make_uint2(0u, 0u);
-        if (sc.mul != 0.0f) {
-          c.x = kv_encode2<kFmt>(bf16_lo(x[e][u].x), bf16_hi(x[e][u].x), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].y), bf16_hi(x[e][u].y), sc) << 16);
-          c.y = kv_encode2<kFmt>(bf16_lo(x[e][u].z), bf16_hi(x[e][u].z), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].w), bf16_hi(x[e][u].w), sc) << 16);
+        for (int u = 0; u < 2; ++u) {
+          code[u].x = kv_encode2<kFmt>(bf16_lo(x[e][u].x), bf16_hi(x[e][u].x), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].y), bf16_hi(x[e][u].y), sc) << 16);
+          code[u].y = kv_encode2<kFmt>(bf16_lo(x[e][u].z), bf16_hi(x[e][u].z), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].w), bf16_hi(x[e][u].w), sc) << 16);
         }
-        code[e][u] = c;
       }
-    }
-  };
-  encode(0);                           // while the block ids are on their way
-  __syncthreads();
-  if (threadIdx.x < nrows && blockIdx.y == 0) {
-    const AppendRow a = s_row[threadIdx.x];
-    if (a.req >= 0 && a.head == static_cast<int>(threadIdx.x) && s_bad[a.head] != 0) atomicOr(p.status + a.req, s_bad[a.head]);
-  }
-
-  uint8_t* codes = (isv ? p.v_cache : p.k_cache) + lane * 8;
-  float* scales = isv ? p.v_scale : p.k_scale;
-  for (int r0 = 0; r0 < nrows; r0 += kAppendBatch * p.slots) {
-    if (r0 > 0) {
-      load(r0 + slot0);
-      encode(r0);
-    }
-#pragma unroll
-    for (int e = 0; e < kAppendBatch; ++e) {
-      const int r = r0 + slot0 + e * p.slots;
-      if (!mine || r >= nrows) break;
-      const AppendRow a = s_row[r];
-      if (a.req < 0 || s_bad[a.head] != 0) continue;
-      const size_t row = (static_cast<size_t>(a.blk) * p.hkv + h) * TV_BLOCK_SIZE + a.slot % TV_BLOCK_SIZE;
+      load(x[e], r + kAppendAhead * p.slots);
+      const long long place = mine && r < nrows ? s_row[r] : -1;
+      if (place < 0) continue;
+      const long long row = place + h * TV_BLOCK_SIZE;
       uint8_t* to = codes + row * D;
-      *reinterpret_cast<uint2*>(to) = code[e][0];
-      *reinterpret_cast<uint2*>(to + kLanes * 8) = code[e][1];
-      if (lane == 0) scales[row] = scale[e];
+      *reinterpret_cast<uint2*>(to) = code[0];
+      *reinterpret_cast<uint2*>(to + kLanes * 8) = code[1];
+      if (lane == 0) scales[row] = sc.scale;
     }
   }
 }
@@ -194,8 +192,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
 // ------------------------------------------------------------------ read back
 
 constexpr int kReadThreads = 256;
-constexpr int kReadBatch = 4;          // items a thread has in flight
-
+constexpr int kReadPerSm = 4;          // CTAs an SM: 3 to 6 all take 117 to 119 us for 692 MB, small calls least with 4
 struct ReadParams {
   const int32_t* first;
   const int32_t* last;
@@ -220,26 +217,30 @@ __device__ __forceinline__ int read_pages(int first, int last) {
   return last <= first ? 0 : (last - 1) / TV_BLOCK_SIZE - first / TV_BLOCK_SIZE + 1;
 }
 
-// An item is one head of one page, K and V: 32 D bytes of codes to 64 D bytes
-// of bf16. All items are laid end to end and a CTA takes a contiguous range.
-// A thread turns 8 codes (8 bytes) into one 16-byte store, so that a warp's
-// stores cover whole 32-byte sectors (16 codes a thread and two stores a
-// stride apart: 118 us for the 692 MB of the largest measured case).
+// An item is the K or V rows of one head of one page: 16 D bytes of codes to
+// 32 D bytes of bf16. All items are laid end to end, a CTA takes a contiguous
+// range of them and its warps every eighth item. A lane turns 8 codes (8
+// bytes) into one 16-byte store, so that a warp's stores cover whole 32-byte
+// sectors, and a warp's loads of an item are all in flight together. The
+// page's 16 scales come in one load and go round by shuffles.
 template <int kFmt, int D>
-__global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __grid_constant__ ReadParams p) {
-  constexpr int kVecs = TV_BLOCK_SIZE * D / 8;               // 8-code vectors of K (or V) in an item
-  constexpr int kPer = 2 * kVecs / kReadThreads;             // a thread's vectors in an item: 2 or 1
+__global__ void __launch_bounds__(kReadThreads, kReadPerSm) kv_quant_read_kernel(const __grid_constant__ ReadParams p) {
+  constexpr int kWarps = kReadThreads / 32;
+  constexpr int kPerRow = D / 8;                             // 8-code vectors of a row
+  constexpr int kPer = TV_BLOCK_SIZE * kPerRow / 32;         // a lane's vectors: 8 or 4
   grid_dependency_wait();
   grid_launch_dependents();
   const Share sh = find_share<kReadThreads>(p.batch, 1, [&](int b) {
-    return static_cast<long long>(read_pages(p.first ? p.first[b] : 0, p.last[b])) * p.hkv;
+    return static_cast<long long>(read_pages(p.first ? p.first[b] : 0, p.last[b])) * 2 * p.hkv;
   });
-  long long at = sh.start;
-  long long pos = sh.lo;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const uint32_t per_page = 2 * p.hkv;
+  long long at = sh.start, pos = sh.lo;
   for (int b = sh.b; b < p.batch && pos < sh.hi; ++b) {
     const int first = p.first ? p.first[b] : 0, last = p.last[b], st = p.status[b];
+    const int held = min(p.n_blocks[b], p.max_blocks), out_held = min(p.out_n_blocks[b], p.out_max_blocks);
     const int pages = read_pages(first, last);
-    const long long end = at + static_cast<long long>(pages) * p.hkv;
+    const long long end = at + static_cast<long long>(pages) * per_page;
     if (pos >= end) { at = end; continue; }
     const long long stop = end < sh.hi ? end : sh.hi;
     const int page0 = max(first, 0) / TV_BLOCK_SIZE, page1 = page0 + pages - 1;
@@ -248,62 +249,60 @@ __global__ void __launch_bounds__(kReadThreads) kv_quant_read_kernel(const __gri
     int bad = 0;
     if (first < 0 || last < 0) {
       bad = TV_ST_BAD_SIZE;
-    } else if (page1 >= min(p.n_blocks[b], p.max_blocks) || page1 >= min(p.out_n_blocks[b], p.out_max_blocks)) {
+    } else if (page1 >= held || page1 >= out_held) {
       bad = TV_ST_BAD_BLOCK;
     } else {
+#pragma unroll 4
       for (int e = page0 + threadIdx.x; e <= page1; e += kReadThreads) {
         const int s = from[e], d = to[e];
         if (s < 0 || s >= p.num_blocks || d < 0 || d >= p.out_num_blocks) bad = TV_ST_BAD_BLOCK;
       }
     }
-    // status is only OR-ed into after this point of some CTA, by a CTA that found the same fault
+    // (the threads decide together: another CTA may flag the request meanwhile, having found the same)
     if (__syncthreads_or(bad | st)) {
       if (bad && st == 0) atomicOr(p.status + b, bad);
     } else {
-      const int i0 = static_cast<int>((pos - at) % p.hkv);
-      const int p0 = page0 + static_cast<int>((pos - at) / p.hkv);
-      const int count = static_cast<int>(stop - pos);
-      for (int base = 0; base < count; base += kReadBatch) {
-        uint2 c[kReadBatch][kPer];
-        float sc[kReadBatch][kPer];
-        size_t dst[kReadBatch];
-        bool live[kReadBatch][kPer];
+      // item = page, K or V, head; the block ids of a warp's next item are on their way
+      long long item = pos - at + warp;
+      const long long items = stop - at;
+      int page = 0, half = 0, sblk = 0, dblk = 0;
+      auto look_up = [&](long long i, int& pg, int& hf, int& s, int& d) {
+        if (i >= items) return;
+        const uint32_t rel = static_cast<uint32_t>(i / per_page);
+        hf = static_cast<int>(i - static_cast<long long>(rel) * per_page);
+        pg = page0 + static_cast<int>(rel);
+        s = from[pg];
+        d = to[pg];
+      };
+      look_up(item, page, half, sblk, dblk);
+      while (item < items) {
+        const bool isv = half >= p.hkv;
+        const int h = isv ? half - p.hkv : half;
+        const size_t srow = (static_cast<size_t>(sblk) * p.hkv + h) * TV_BLOCK_SIZE;
+        const size_t drow = (static_cast<size_t>(dblk) * p.hkv + h) * TV_BLOCK_SIZE;
+        const uint2* src = reinterpret_cast<const uint2*>((isv ? p.v_cache : p.k_cache) + srow * D) + lane;
+        uint4* dst = reinterpret_cast<uint4*>((isv ? p.v_out : p.k_out) + drow * D) + lane;
+        // rows [r0, r1) of the page
+        const int r0 = max(first - page * TV_BLOCK_SIZE, 0), r1 = min(last - page * TV_BLOCK_SIZE, TV_BLOCK_SIZE);
+        const int lane_row = lane / kPerRow;
+        const float scale = (isv ? p.v_scale : p.k_scale)[srow + lane % TV_BLOCK_SIZE];
+        uint2 c[kPer];
 #pragma unroll
-        for (int e = 0; e < kReadBatch; ++e) {
-          const int i = i0 + base + e;
-          const int page = p0 + i / p.hkv, h = i % p.hkv;
-          const bool there = base + e < count;
-          const size_t src = there ? (static_cast<size_t>(from[page]) * p.hkv + h) * TV_BLOCK_SIZE : 0;
-          dst[e] = there ? (static_cast<size_t>(to[page]) * p.hkv + h) * TV_BLOCK_SIZE : 0;
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            const int idx = threadIdx.x + j * kReadThreads;
-            const bool isv = idx >= kVecs;
-            const int v = isv ? idx - kVecs : idx, row = v / (D / 8), slot = page * TV_BLOCK_SIZE + row;
-            live[e][j] = there && slot >= first && slot < last;
-            c[e][j] = make_uint2(0u, 0u);
-            sc[e][j] = 0.0f;
-            if (live[e][j]) {
-              c[e][j] = __ldcs(reinterpret_cast<const uint2*>((isv ? p.v_cache : p.k_cache) + src * D) + v);
-              sc[e][j] = (isv ? p.v_scale : p.k_scale)[src + row];
-            }
-          }
+        for (int i = 0; i < kPer; ++i) {
+          const int r = i * (32 / kPerRow) + lane_row;
+          c[i] = r >= r0 && r < r1 ? __ldcs(src + 32 * i) : make_uint2(0u, 0u);
         }
+        item += kWarps;
+        look_up(item, page, half, sblk, dblk);
 #pragma unroll
-        for (int e = 0; e < kReadBatch; ++e) {
-#pragma unroll
-          for (int j = 0; j < kPer; ++j) {
-            if (!live[e][j]) continue;
-            const int idx = threadIdx.x + j * kReadThreads;
-            const bool isv = idx >= kVecs;
-            const int v = isv ? idx - kVecs : idx;
-            const float s = sc[e][j];
-            const float2 f0 = kv_decode2<kFmt>(c[e][j].x & 0xffffu), f1 = kv_decode2<kFmt>(c[e][j].x >> 16);
-            const float2 f2 = kv_decode2<kFmt>(c[e][j].y & 0xffffu), f3 = kv_decode2<kFmt>(c[e][j].y >> 16);
-            reinterpret_cast<uint4*>((isv ? p.v_out : p.k_out) + dst[e] * D)[v] =
-                make_uint4(pack_bf16x2(f0.x * s, f0.y * s), pack_bf16x2(f1.x * s, f1.y * s),
-                           pack_bf16x2(f2.x * s, f2.y * s), pack_bf16x2(f3.x * s, f3.y * s));
-          }
+        for (int i = 0; i < kPer; ++i) {
+          const int r = i * (32 / kPerRow) + lane_row;
+          const float s = __shfl_sync(0xffffffffu, scale, r);
+          const float2 f0 = kv_decode2<kFmt>(c[i].x & 0xffffu), f1 = kv_decode2<kFmt>(c[i].x >> 16);
+          const float2 f2 = kv_decode2<kFmt>(c[i].y & 0xffffu), f3 = kv_decode2<kFmt>(c[i].y >> 16);
+          if (r >= r0 && r < r1)
+            dst[32 * i] = make_uint4(pack_bf16x2(f0.x * s, f0.y * s), pack_bf16x2(f1.x * s, f1.y * s),
+                                     pack_bf16x2(f2.x * s, f2.y * s), pack_bf16x2(f3.x * s, f3.y * s));
         }
       }
     }
@@ -354,18 +353,16 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
       ? (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_E4M3, 64> : tv::kv_quant_append_kernel<TV_KV_E4M3, 128>)
       : (geom->head_dim == 64 ? tv::kv_quant_append_kernel<TV_KV_INT8, 64> : tv::kv_quant_append_kernel<TV_KV_INT8, 128>);
   // A CTA takes up to 256 / (D / 16) heads of a row at a time, several rows at
-  // a time when a row has fewer, and two batches of loads a thread where that
-  // still gives every SM eight CTAs (fewer rows than that: down to one sweep).
+  // a time when a row has fewer, and as many rows as fill the SMs once.
   const int parts = tv::kAppendThreads / (geom->head_dim / 16), heads = 2 * p.hkv;
   p.cta_heads = heads < parts ? heads : parts;
   p.slots = parts / p.cta_heads;
   const int head_blocks = (heads + p.cta_heads - 1) / p.cta_heads;
-  const long long ctas = 152 * 8 / head_blocks + 1;
-  long long cta_rows = (rows + ctas - 1) / ctas;
-  const long long most = 2ll * tv::kAppendBatch * p.slots;
-  if (cta_rows > most) cta_rows = most;
+  const long long ctas = 152 * tv::kAppendPerSm;
+  long long cta_rows = (static_cast<long long>(rows) * head_blocks + ctas - 1) / ctas;
   if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
   cta_rows = (cta_rows + p.slots - 1) / p.slots * p.slots;
+  if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
   p.cta_rows = static_cast<int>(cta_rows);
   const dim3 grid(static_cast<unsigned>((rows + cta_rows - 1) / cta_rows), head_blocks);
   const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kAppendThreads), 0, tv::as_stream(stream), p);
@@ -413,7 +410,7 @@ extern "C" int tv_kv_quant_read(const tv_geom* geom, int32_t kv_format, int32_t 
   const int sms = tv::device_sm_count(dev);
   if (sms <= 0) return TV_ERR_CUDA;
   const long long pages = max_blocks_per_req < out_max_blocks_per_req ? max_blocks_per_req : out_max_blocks_per_req;
-  const long long items = pages * batch * p.hkv, most = static_cast<long long>(sms) * 6;
+  const long long items = (pages * batch * p.hkv + 3) / 4, most = static_cast<long long>(sms) * tv::kReadPerSm;   // an item a warp
   const dim3 grid(static_cast<unsigned>(items < most ? items : most));
   const cudaError_t err = tv::launch_pdl(kernel, grid, dim3(tv::kReadThreads), 0, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;

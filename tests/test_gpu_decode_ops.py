@@ -297,6 +297,24 @@ def test_append_offsets_past_the_rows_are_flagged():
     assert run_append(c, k, v, [0, 6, 6, 9], [0, 0, 0]) == [0, 0, 1]    # rows 6..8 of 6
 
 
+@pytest.mark.parametrize("held,hkv,d", [("e4m3", 8, 128), ("int8", 3, 64), ("e4m3", 40, 64)])
+def test_append_many_rows_with_bad_requests_among_them(held, hkv, d):
+    """Requests that reach over many thread blocks, one of them with a missing block far from most
+    of its rows; empty requests between; more requests than a thread block has threads."""
+    rng = np.random.default_rng(29)
+    lens = [700, 0, 1, 900] + rng.integers(0, 4, 300).tolist() + [0, 650]
+    start = [5, 0, 30, 11] + rng.integers(0, 50, 300).tolist() + [3, 16]
+    cu = [0] + np.cumsum(lens).tolist()
+    c = Cache(30, [s + n for s, n in zip(start, lens)], hkv, d, held)
+    c.table[3, 2] = -1                                # the second long request's rows 21 to 36
+    k, v = fresh(31, cu[-1] + 3, hkv, d, 16)
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    want = [0] * len(lens)
+    want[3] = 8
+    assert run_append(c, k, v, cu, start) == want
+    check_append(c, before, k, v, cu, start, [b for b in range(len(lens)) if b != 3])
+
+
 @pytest.mark.parametrize("held", ["e4m3", "int8"])
 def test_append_every_pair_of_significands(held):
     """Every bf16 significand under every largest one, at eight binary distances: all exact ties
