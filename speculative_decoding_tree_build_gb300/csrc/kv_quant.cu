@@ -71,6 +71,15 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
   const int h = isv ? head - p.hkv : head;
   const long long step = p.slots * p.kv_ld;
   const __nv_bfloat16* src = (isv ? p.v_new : p.k_new) + (t0 + slot0) * p.kv_ld + static_cast<long long>(h) * D + lane * 8;
+  // A thread looks at request i with all that it needs of it in one round
+  // trip. Its first request goes ahead of the rows, so as not to queue behind them.
+  struct Request { int c0, c1, st, start, held; };
+  auto look_at = [&](int i) {
+    Request q = {0, 0, 0, 0, 0};
+    if (i < p.batch) q = Request{p.cu_rows[i], p.cu_rows[i + 1], *const_cast<volatile int32_t*>(p.status + i), p.start_len[i], min(p.n_blocks[i], p.max_blocks)};
+    return q;
+  };
+  Request q = look_at(threadIdx.x);
   uint4 x[kAppendAhead][2];            // a warp's loads cover whole sectors: piece lane, piece lane + kLanes
   auto load = [&](uint4 (&to)[2], int r) {
     to[0] = to[1] = make_uint4(0u, 0u, 0u, 0u);
@@ -83,29 +92,25 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
 #pragma unroll
   for (int e = 0; e < kAppendAhead; ++e) load(x[e], slot0 + e * p.slots);    // on their way while slots are found
 
-  // A thread looks at request i with all that it needs of it in one round
-  // trip, and describes those of the CTA's rows that the request owns.
   if (threadIdx.x < kAppendMaxRows) s_bad[threadIdx.x] = 0;
   if (threadIdx.x < kAppendMaxRows / 32) s_heads[threadIdx.x] = 0u;
   if (threadIdx.x < 8) s_cross[threadIdx.x / 4][threadIdx.x % 4] = 0;
   __syncthreads();
-#pragma unroll 2
-  for (int i = threadIdx.x; i < p.batch; i += kAppendThreads) {
-    const int c0 = p.cu_rows[i], c1 = p.cu_rows[i + 1], st = p.status[i], start = p.start_len[i];
-    const int held = min(p.n_blocks[i], p.max_blocks);
-    if (c1 <= c0 || st != 0) continue;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && (c1 > p.rows || c0 < 0 || start < 0)) atomicOr(p.status + i, TV_ST_BAD_SIZE);
-    if (c0 < 0 || c1 > p.rows || start < 0 || c0 >= t1 || c1 <= t0) continue;
-    const int first = max(c0, t0) - t0;
-    const long long end = static_cast<long long>(start) + (c1 - c0);
-    const bool fits = (end - 1) / TV_BLOCK_SIZE < held;      // (which also keeps slots below 2^31)
+  // the CTA's rows that each request owns
+  for (int i = threadIdx.x; i < p.batch; i += kAppendThreads, q = look_at(i)) {
+    if (q.c1 <= q.c0 || q.st != 0) continue;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && (q.c1 > p.rows || q.c0 < 0 || q.start < 0)) atomicOr(p.status + i, TV_ST_BAD_SIZE);
+    if (q.c0 < 0 || q.c1 > p.rows || q.start < 0 || q.c0 >= t1 || q.c1 <= t0) continue;
+    const int first = max(q.c0, t0) - t0;
+    const long long end = static_cast<long long>(q.start) + (q.c1 - q.c0);
+    const bool fits = (end - 1) / TV_BLOCK_SIZE < q.held;    // (which also keeps slots below 2^31)
     if (!fits) s_bad[first] = TV_ST_BAD_BLOCK;
-    s_run[first] = AppendRun{i, c0, start, min(c1, t1) - t0};
+    s_run[first] = AppendRun{i, q.c0, q.start, min(q.c1, t1) - t0};
     atomicOr(&s_heads[first / 32], 1u << (first % 32));
-    if (fits && (c0 < t0 || c1 > t1)) {
-      int* cross = s_cross[c0 < t0 ? 0 : 1];
+    if (fits && (q.c0 < t0 || q.c1 > t1)) {
+      int* cross = s_cross[q.c0 < t0 ? 0 : 1];
       cross[0] = i;
-      cross[1] = start / TV_BLOCK_SIZE;
+      cross[1] = q.start / TV_BLOCK_SIZE;
       cross[3] = first;
       cross[2] = static_cast<int>((end - 1) / TV_BLOCK_SIZE) - cross[1] + 1;
     }
@@ -173,8 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
       if (sc.mul != 0.0f) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          code[u].x = kv_encode2<kFmt>(bf16_lo(x[e][u].x), bf16_hi(x[e][u].x), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].y), bf16_hi(x[e][u].y), sc) << 16);
-          code[u].y = kv_encode2<kFmt>(bf16_lo(x[e][u].z), bf16_hi(x[e][u].z), sc) | (kv_encode2<kFmt>(bf16_lo(x[e][u].w), bf16_hi(x[e][u].w), sc) << 16);
+          code[u] = make_uint2(kv_encode4<kFmt>(x[e][u].x, x[e][u].y, sc), kv_encode4<kFmt>(x[e][u].z, x[e][u].w, sc));
         }
       }
       load(x[e], r + kAppendAhead * p.slots);

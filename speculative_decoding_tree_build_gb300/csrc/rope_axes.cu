@@ -188,18 +188,27 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
       if (kTwo) vb[e] = *reinterpret_cast<const Vec*>(src + cb);
     }
   };
-  if (at_work) {                       // the first row is on its way while the angles are made
+  // the angles' inputs go ahead of the first row, which is on its way while the angles are made
+  const int step = kRopeAxThreads / p.pairs;                 // rows taken at a time, a thread keeps its pair
+  const int r0 = threadIdx.x / p.pairs, pr = threadIdx.x - r0 * p.pairs;
+  const bool turning = r0 < step && r0 < nrows;
+  const int32_t* position = p.positions + p.axis[turning ? pr : 0] * p.pos_ld + row0;
+  float inv_freq = 0.0f;
+  int pos = 0;
+  if (turning) {
+    inv_freq = *const_cast<const volatile float*>(p.inv_freq + pr);
+    pos = *const_cast<const volatile int32_t*>(position + r0);
+  }
+  if (at_work) {
     point();
     load();
   }
-
-  {
-    const int step = kRopeAxThreads / p.pairs;               // rows taken at a time, a thread keeps its pair
-    const int r0 = threadIdx.x / p.pairs, pr = threadIdx.x - r0 * p.pairs;
-    if (r0 < step && r0 < nrows) {
-      const unsigned long long f = rope_turns(p.inv_freq[pr]);
-      const int32_t* position = p.positions + p.axis[pr] * p.pos_ld + row0;
-      for (int r = r0; r < nrows; r += step) s_cs[r * p.pairs + pr] = rope_cos_sin(position[r], f);
+  if (turning) {
+    const unsigned long long f = rope_turns(inv_freq);
+    for (int r = r0;; pos = position[r]) {
+      s_cs[r * p.pairs + pr] = rope_cos_sin(pos, f);
+      r += step;
+      if (r >= nrows) break;
     }
   }
   __syncthreads();

@@ -9,11 +9,11 @@ namespace tv {
 
 constexpr int kKvMaxBatch = 4096;
 
-// What a row's codes are made from: its scale and the factor of its values.
+// What a row's codes are made from: its scale and the factors of its values.
 struct KvRowScale {
   float scale;   // stored beside the codes; NaN when the row is not finite
-  float mul;     // e4m3: 1 / scale; int8: 127 / largest magnitude; 0: all codes are 0
-  float pre;     // int8: a power of two that keeps mul in range, applied first
+  float mul;     // e4m3: 1 / scale; int8: 1 / largest magnitude; 0: all codes are 0
+  float top;     // int8: the largest magnitude, at least 2^-100
 };
 
 // `top` = largest magnitude of the row's bf16 values as bits 14..0 of bf16.
@@ -22,8 +22,6 @@ struct KvRowScale {
 template <int kFmt>
 __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
   KvRowScale r;
-  const float a = __uint_as_float(top << 16);
-  r.pre = 1.0f;
   if constexpr (kFmt == TV_KV_E4M3) {
     // a = 2^E * m, 1 <= m < 2: 448 = 1.75 * 2^8, so n = E - 8, one more when
     // m > 1.75 (bf16 significand bits above 0x60), and not below -100
@@ -31,11 +29,11 @@ __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
     n = max(n, -100);
     r.scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
     r.mul = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);   // n <= 120: exact, as is x * mul
+    r.top = 0.0f;
   } else {
-    const float b = fmaxf(a, 7.888609052210118e-31f);                // 2^-100
-    r.scale = __fdiv_rn(b, 127.0f);
-    if (b > 1e30f) r.pre = 9.5367431640625e-07f;                     // 2^-20: keeps mul a normal number
-    r.mul = __fdiv_rn(127.0f, b * r.pre);
+    r.top = fmaxf(__uint_as_float(top << 16), 7.888609052210118e-31f);         // 2^-100
+    r.scale = __fdiv_rn(r.top, 127.0f);
+    r.mul = __frcp_rn(r.top);
   }
   if (top >= 0x7f80u) {
     r.scale = __uint_as_float(0x7fc00000u);
@@ -44,27 +42,38 @@ __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
   return r;
 }
 
-// The int8 code of x in the low byte. The exact quotient Q = 127 x / a of two
-// bf16 numbers is 127 X / (A 2^k) with X, A < 2^8, so unless it is a tie (an
-// integer and a half) it lies at least |Q| / (254 X) > 2^-16 |Q| away from
-// one. x * fl(127 / a) is within 2^-22 |Q| of it. So a product within
-// 2^-18 |Q| of half an integer IS that number, and is set to it before it is
-// rounded to even; every other one rounds as Q does.
+// The int8 code of x in the low byte: 127 x / top to the nearest integer. The
+// product 127 x is exact (15 bits), and one Newton step from the reciprocal
+// leaves the quotient within 2^-24 of itself, exactly where it is a float32
+// number - so exactly at ties, integers and a half. Any other quotient of two
+// bf16 numbers, 127 X / (A 2^k) with X, A < 2^8, is 1 / (254 X) > 2^-16 of
+// itself away from the nearest tie and rounds the way the exact one does.
 __device__ __forceinline__ uint32_t kv_int8_code(float x, const KvRowScale& r) {
-  const float magic = 12582912.0f;                                   // 1.5 * 2^23: rounds to an integer
-  const float y = x * r.pre * r.mul;
-  const float twice = __fadd_rn(__fadd_rn(2.0f * y, magic), -magic); // nearest half integer, doubled
-  const float snapped = fabsf(2.0f * y - twice) <= 7.62939453125e-06f * fabsf(y) ? 0.5f * twice : y;
-  return __float_as_uint(__fadd_rn(snapped, magic)) & 0xffu;
+  const float n = 127.0f * x;
+  const float q = n * r.mul;
+  const float y = fmaf(fmaf(-q, r.top, n), r.mul, q);
+  return __float_as_uint(__fadd_rn(y, 12582912.0f));                 // 1.5 * 2^23: rounds to an integer
 }
 
-// Two values to two codes (first in the low byte).
+// Four values (two bf16 pairs) to four codes.
 template <int kFmt>
-__device__ __forceinline__ uint32_t kv_encode2(float x, float y, const KvRowScale& r) {
+__device__ __forceinline__ uint32_t kv_encode4(uint32_t a, uint32_t b, const KvRowScale& r) {
   if constexpr (kFmt == TV_KV_E4M3) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(x * r.mul, y * r.mul), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(a) * r.mul, bf16_hi(a) * r.mul), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(b) * r.mul, bf16_hi(b) * r.mul), __NV_SATFINITE, __NV_E4M3);
+    return lo | (hi << 16);
   } else {
-    return kv_int8_code(x, r) | (kv_int8_code(y, r) << 8);
+    KvRowScale s = r;
+    float x[4] = {bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
+    if (r.top > 1e30f) {               // 127 x must not overflow: the quotient of both by 2^20, exactly
+      s.top *= 9.5367431640625e-07f;
+      s.mul *= 1048576.0f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= 9.5367431640625e-07f;
+    }
+    const uint32_t lo = __byte_perm(kv_int8_code(x[0], s), kv_int8_code(x[1], s), 0x0040);
+    const uint32_t hi = __byte_perm(kv_int8_code(x[2], s), kv_int8_code(x[3], s), 0x0040);
+    return __byte_perm(lo, hi, 0x5410);
   }
 }
 
