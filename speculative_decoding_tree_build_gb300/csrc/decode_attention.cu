@@ -193,8 +193,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
   __shared__ float4 s_stat[kDecWarps][16];                     // (m, M, l, -)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
 
   // ---- this CTA's share of the tiles
   const Share sh = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int b) {
@@ -583,8 +583,8 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   using Vec = typename std::conditional<kVec == 4, float4, float2>::type;
   __shared__ float s_acc[kMergeMaxParts][D];
   __shared__ float4 s_stat[kMergeMaxParts];
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const DecBegin task = p.begins[blockIdx.x];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const int part = warp % p.parts, qi = blockIdx.y * (warps / p.parts) + warp / p.parts;

@@ -60,8 +60,8 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
   __shared__ int s_head[kAppendMaxRows];
   __shared__ int s_cross[2][4];        // requests that reach past the CTA's rows, before and behind:
                                        // request, first page, pages, first row of the run
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int t0 = blockIdx.x * p.cta_rows;
   const int nrows = min(p.cta_rows, p.rows - t0), t1 = t0 + nrows;
   const int part = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -232,8 +232,8 @@ __global__ void __launch_bounds__(kReadThreads, kReadPerSm) kv_quant_read_kernel
   constexpr int kWarps = kReadThreads / 32;
   constexpr int kPerRow = D / 8;                             // 8-code vectors of a row
   constexpr int kPer = TV_BLOCK_SIZE * kPerRow / 32;         // a lane's vectors: 8 or 4
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const Share sh = find_share<kReadThreads>(p.batch, 1, [&](int b) {
     return static_cast<long long>(read_pages(p.first ? p.first[b] : 0, p.last[b])) * 2 * p.hkv;
   });

@@ -137,8 +137,8 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   constexpr bool kPacked = sizeof(T) == 2 && N > 1;
   using Vec = RopeVec<T, N>;
   __shared__ __align__(16) float2 s_cs[kRopeAxAngles];
-  grid_dependency_wait();
   grid_launch_dependents();
+  grid_dependency_wait();
   const int block = blockIdx.x / p.groups, group = blockIdx.x - block * p.groups;
   const int row0 = block * p.cta_rows, nrows = min(p.cta_rows, p.rows - row0);
   const int head_end = min(p.heads, (group + 1) * p.cta_heads);
