@@ -179,8 +179,17 @@ struct DecTraits {
   static constexpr int kRowBytes = D * kElem;
   static constexpr int kKPieces = kRowBytes / 64;              // 16-byte pieces of a K row a thread holds
   static constexpr int kSteps = D / 16;                        // MMA steps over D (QK), tiles of D (PV)
-  // registers: K and V of a page, the queries and the output accumulators
-  static constexpr int kPerSm = kHalf ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+  static constexpr int kVPieces = kRowBytes >= 128 ? kRowBytes / 128 : 1;    // of a V row (8 bytes at 64)
+  // Pages that a warp takes at a time: two of the smallest ones, whose chain of
+  // products, exponentials and waits would else be as long for half the bytes
+  // (64 sequences of 4096 to 16384 keys, D = 64, e4m3: 129 -> 110 us).
+  static constexpr int kPages = kRowBytes == 64 && NT == 1 ? 2 : 1;
+  // CTAs an SM: registers for the pages, the queries and the output
+  // accumulators. More warps are worth more than more pages a warp (D = 128,
+  // e4m3, 1.9 GB: 4 CTAs 293 us, 3 CTAs 309 us, 3 CTAs with two pages in
+  // flight a warp 357 us), until the registers spill (two groups of queries,
+  // D = 128: 2 CTAs 21 us, 3 CTAs 23 us).
+  static constexpr int kPerSm = NT == 2 ? (D == 64 ? 3 : 2) : kRowBytes == 256 ? 3 : 4;
 };
 
 template <int kFmt, int D, int NT>
@@ -188,7 +197,8 @@ __global__ void __launch_bounds__(kDecThreads, (DecTraits<kFmt, D, NT>::kPerSm))
 decode_kernel(const __grid_constant__ DecodeParams p) {
   using Tr = DecTraits<kFmt, D, NT>;
   constexpr bool kHalf = Tr::kHalf;
-  constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kSteps = Tr::kSteps;
+  constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kVPieces = Tr::kVPieces, kSteps = Tr::kSteps;
+  constexpr int kPages = Tr::kPages;
   constexpr int kRowPad = D + 4;
   extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
   __shared__ float4 s_stat[kDecWarps][16];                     // (m, M, l, -)
@@ -325,101 +335,126 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       if (blk < 0 || blk >= p.num_blocks) { bad = TV_ST_BAD_BLOCK; blk = 0; }
       return blk;
     };
-    uint4 kf[2][kKPieces];
-    uint4 vf[4][kRowBytes >= 128 ? kRowBytes / 128 : 1];
-    float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};
+    uint4 kf[kPages][2][kKPieces], vf[kPages][4][kVPieces];
+    float ks[kPages][2], vs[kPages][2];
     auto head_row = [&](int it) {      // the page's first row of this head, as a row number of the pool
       const int blk = __shfl_sync(0xffffffffu, ids, it % 32);
       return (static_cast<size_t>(blk) * p.hkv + h) * TV_BLOCK_SIZE;
     };
-    auto load_k = [&](size_t r) {
+    auto load_k = [&](int pg, size_t r) {
       const uint8_t* base = p.k_cache + r * kRowBytes + t * 16;
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int c = 0; c < kKPieces; ++c) kf[u][c] = ldg_stream(base + (g + 8 * u) * kRowBytes + c * 64);
+        for (int c = 0; c < kKPieces; ++c) kf[pg][u][c] = ldg_stream(base + (g + 8 * u) * kRowBytes + c * 64);
       if constexpr (kHalf) {
-        ks[0] = ldg_float(p.k_scale + r + g);
-        ks[1] = ldg_float(p.k_scale + r + g + 8);
+        ks[pg][0] = ldg_float(p.k_scale + r + g);
+        ks[pg][1] = ldg_float(p.k_scale + r + g + 8);
       }
     };
-    auto load_v = [&](size_t r) {
+    auto load_v = [&](int pg, size_t r) {
       const uint8_t* base = p.v_cache + r * kRowBytes;
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const uint8_t* src = base + (2 * t + (u & 1) + (u >> 1) * 8) * kRowBytes;
         if constexpr (kRowBytes >= 128) {
 #pragma unroll
-          for (int c = 0; c < kRowBytes / 128; ++c) vf[u][c] = ldg_stream(src + g * 16 + c * 128);
+          for (int c = 0; c < kVPieces; ++c) vf[pg][u][c] = ldg_stream(src + g * 16 + c * 128);
         } else {
           const uint2 w = ldg_stream8(src + g * 8);
-          vf[u][0] = make_uint4(w.x, w.y, 0u, 0u);
+          vf[pg][u][0] = make_uint4(w.x, w.y, 0u, 0u);
         }
       }
       if constexpr (kHalf) {
-        vs[0] = ldg_float(p.v_scale + r + g);
-        vs[1] = ldg_float(p.v_scale + r + g + 8);
+        vs[pg][0] = ldg_float(p.v_scale + r + g);
+        vs[pg][1] = ldg_float(p.v_scale + r + g + 8);
       }
     };
-    size_t r_now = 0;
+    // the segment's keys end here; a page from here on is not loaded and masked like any tail
+    const int key_end = min(n, page_end * TV_BLOCK_SIZE);
+    size_t rows[kPages];
     if (iters > 0) {
       ids = valid(ids_first);
-      r_now = head_row(0);
-      load_k(r_now);
-      load_v(r_now);
+#pragma unroll
+      for (int pg = 0; pg < kPages; ++pg) {
+        if (pg < iters) {
+          rows[pg] = head_row(pg);
+          load_k(pg, rows[pg]);
+          load_v(pg, rows[pg]);
+        }
+      }
       ids_next = fetch_ids(32);
     }
-    for (int it = 0; it < iters; ++it) {
-      const int key0 = (first + it * kDecWarps) * TV_BLOCK_SIZE;
-      const bool tail = key0 + TV_BLOCK_SIZE > n;
-      // scores of 16 keys: thread holds keys g, g + 8 of queries 2t, 2t + 1
-      float s[NT][4];
+    for (int it = 0; it < iters; it += kPages) {
+      const int key0 = (first + it * kDecWarps) * TV_BLOCK_SIZE;           // of the first page
+      constexpr int kNextPage = kDecWarps * TV_BLOCK_SIZE;
+      const bool tail = key0 + (kPages - 1) * kNextPage + TV_BLOCK_SIZE > key_end;
+      // scores of 16 keys a page: thread holds keys g, g + 8 of queries 2t, 2t + 1
+      float s[kPages][NT][4], k0[kPages], k1[kPages];
 #pragma unroll
-      for (int x = 0; x < NT; ++x)
+      for (int pg = 0; pg < kPages; ++pg) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[x][e] = 0.0f;
+        for (int x = 0; x < NT; ++x)
 #pragma unroll
-      for (int c = 0; c < kKPieces; ++c) {
-        const uint32_t a[4] = {kf[0][c].x, kf[0][c].y, kf[0][c].z, kf[0][c].w};
-        const uint32_t e[4] = {kf[1][c].x, kf[1][c].y, kf[1][c].z, kf[1][c].w};
-        if constexpr (kHalf) {
+          for (int e = 0; e < 4; ++e) s[pg][x][e] = 0.0f;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t a0, a1, a2, a3;
-            codes_to_half<kFmt>(a[j], a0, a2);
-            codes_to_half<kFmt>(e[j], a1, a3);
+        for (int c = 0; c < kKPieces; ++c) {
+          const uint4 &ka = kf[pg][0][c], &kb = kf[pg][1][c];
+          const uint32_t a[4] = {ka.x, ka.y, ka.z, ka.w};
+          const uint32_t e[4] = {kb.x, kb.y, kb.z, kb.w};
+          if constexpr (kHalf) {
 #pragma unroll
-            for (int x = 0; x < NT; ++x) mma16816<true>(s[x], a0, a1, a2, a3, qf[x][4 * c + j][0], qf[x][4 * c + j][1]);
+            for (int j = 0; j < 4; ++j) {
+              uint32_t a0, a1, a2, a3;
+              codes_to_half<kFmt>(a[j], a0, a2);
+              codes_to_half<kFmt>(e[j], a1, a3);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16816<true>(s[pg][x], a0, a1, a2, a3, qf[x][4 * c + j][0], qf[x][4 * c + j][1]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int x = 0; x < NT; ++x)
+                mma16816<false>(s[pg][x], a[2 * j], e[2 * j], a[2 * j + 1], e[2 * j + 1], qf[x][2 * c + j][0], qf[x][2 * c + j][1]);
           }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int x = 0; x < NT; ++x)
-              mma16816<false>(s[x], a[2 * j], e[2 * j], a[2 * j + 1], e[2 * j + 1], qf[x][2 * c + j][0], qf[x][2 * c + j][1]);
         }
+        k0[pg] = kHalf ? ks[pg][0] : 1.0f;
+        k1[pg] = kHalf ? ks[pg][1] : 1.0f;
       }
-      const float k0 = ks[0], k1 = ks[1];
-      if (it + 1 < iters) {
-        if ((it + 1) % 32 == 0) {
+      const int next = it + kPages;
+      if (next < iters) {
+        if (next % 32 == 0) {
           ids = valid(ids_next);
-          ids_next = fetch_ids(it + 33);
+          ids_next = fetch_ids(next + 32);
         }
-        r_now = head_row(it + 1);
-        load_k(r_now);
+#pragma unroll
+        for (int pg = 0; pg < kPages; ++pg) {
+          if (next + pg < iters) {
+            rows[pg] = head_row(next + pg);
+            load_k(pg, rows[pg]);
+          }
+        }
       }
-      const bool live0 = !tail || key0 + g < n, live1 = !tail || key0 + g + 8 < n;
-      float lv0 = 0.0f, lv1 = 0.0f;
-      if constexpr (kHalf) { lv0 = __log2f(vs[0]); lv1 = __log2f(vs[1]); }
+      bool live[kPages][2];
+      float lv[kPages][2];
       bool over = false;
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
+      for (int pg = 0; pg < kPages; ++pg) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = kHalf ? fac[x][e & 1] * (e < 2 ? k0 : k1) : fac[x][e & 1];
-          s[x][e] = (e < 2 ? live0 : live1) ? s[x][e] * f : -INFINITY;
-          over |= s[x][e] > m[x][e & 1] + 8.0f;
-          if (kHalf) over |= s[x][e] + (e < 2 ? lv0 : lv1) > ref[x][e & 1] + 8.0f;
+        for (int u = 0; u < 2; ++u) {
+          live[pg][u] = !tail || key0 + pg * kNextPage + g + 8 * u < key_end;
+          lv[pg][u] = kHalf ? __log2f(vs[pg][u]) : 0.0f;
+        }
+#pragma unroll
+        for (int x = 0; x < NT; ++x) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float f = kHalf ? fac[x][e & 1] * (e < 2 ? k0[pg] : k1[pg]) : fac[x][e & 1];
+            s[pg][x][e] = live[pg][e / 2] ? s[pg][x][e] * f : -INFINITY;
+            over |= s[pg][x][e] > m[x][e & 1] + 8.0f;
+            if (kHalf) over |= s[pg][x][e] + lv[pg][e / 2] > ref[x][e & 1] + 8.0f;
+          }
         }
       }
       if (__any_sync(0xffffffffu, over)) {
@@ -427,9 +462,12 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         for (int x = 0; x < NT; ++x) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float a = fmaxf(s[x][e], s[x][e + 2]);
-            float c = a;
-            if (kHalf) c = fmaxf(s[x][e] + (live0 ? lv0 : 0.0f), s[x][e + 2] + (live1 ? lv1 : 0.0f));
+            float a = kLowest, c = kLowest;
+#pragma unroll
+            for (int pg = 0; pg < kPages; ++pg) {
+              a = fmaxf(a, fmaxf(s[pg][x][e], s[pg][x][e + 2]));
+              if (kHalf) c = fmaxf(c, fmaxf(s[pg][x][e] + (live[pg][0] ? lv[pg][0] : 0.0f), s[pg][x][e + 2] + (live[pg][1] ? lv[pg][1] : 0.0f)));
+            }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
               a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
@@ -446,59 +484,63 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           }
         }
       }
-      // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8)
-      uint32_t pf[NT][2];
 #pragma unroll
-      for (int x = 0; x < NT; ++x) {
-        float w[4];
+      for (int pg = 0; pg < kPages; ++pg) {
+        // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8)
+        uint32_t pf[NT][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = fast_exp2(s[x][e] - m[x][e & 1]);
-          l[x][e & 1] += w[e];
-          if (kHalf) {
-            w[e] = fast_exp2(s[x][e] + (e < 2 ? lv0 : lv1) - ref[x][e & 1]);
-            if (tail && !(e < 2 ? live0 : live1)) w[e] = 0.0f;
-          }
-        }
-        pf[x][0] = transpose8x8(kHalf ? pack_half2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
-        pf[x][1] = transpose8x8(kHalf ? pack_half2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
-      }
-      if (tail) {                      // rows past the end may hold anything, NaN among it
+        for (int x = 0; x < NT; ++x) {
+          float w[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (key0 + 2 * t + (u & 1) + (u >> 1) * 8 < n) continue;
-#pragma unroll
-          for (int c = 0; c < (kRowBytes >= 128 ? kRowBytes / 128 : 1); ++c) vf[u][c] = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-#pragma unroll
-      for (int c = 0; c < (kRowBytes >= 128 ? kRowBytes / 128 : 1); ++c) {
-        const uint32_t v0[4] = {vf[0][c].x, vf[0][c].y, vf[0][c].z, vf[0][c].w};
-        const uint32_t v1[4] = {vf[1][c].x, vf[1][c].y, vf[1][c].z, vf[1][c].w};
-        const uint32_t v2[4] = {vf[2][c].x, vf[2][c].y, vf[2][c].z, vf[2][c].w};
-        const uint32_t v3[4] = {vf[3][c].x, vf[3][c].y, vf[3][c].z, vf[3][c].w};
-        constexpr int kWords = kRowBytes >= 128 ? 4 : 2;
-#pragma unroll
-        for (int j = 0; j < kWords; ++j) {
-          if constexpr (kHalf) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {        // two columns of two rows, by bytes
-              const uint32_t sel = i ? 0x7362 : 0x5140;
-              uint32_t a0, a1, a2, a3;
-              codes_to_half<kFmt>(__byte_perm(v0[j], v1[j], sel), a0, a1);
-              codes_to_half<kFmt>(__byte_perm(v2[j], v3[j], sel), a2, a3);
-#pragma unroll
-              for (int x = 0; x < NT; ++x) mma16816<true>(o[x][2 * j + i], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+          for (int e = 0; e < 4; ++e) {
+            w[e] = fast_exp2(s[pg][x][e] - m[x][e & 1]);
+            l[x][e & 1] += w[e];
+            if (kHalf) {
+              w[e] = fast_exp2(s[pg][x][e] + lv[pg][e / 2] - ref[x][e & 1]);
+              if (tail && !live[pg][e / 2]) w[e] = 0.0f;
             }
-          } else {
-            const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
-            const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+          }
+          pf[x][0] = transpose8x8(kHalf ? pack_half2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
+          pf[x][1] = transpose8x8(kHalf ? pack_half2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+        }
+        if (tail) {                    // rows past the end may hold anything, NaN among it
 #pragma unroll
-            for (int x = 0; x < NT; ++x) mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+          for (int u = 0; u < 4; ++u) {
+            if (key0 + pg * kNextPage + 2 * t + (u & 1) + (u >> 1) * 8 < key_end) continue;
+#pragma unroll
+            for (int c = 0; c < kVPieces; ++c) vf[pg][u][c] = make_uint4(0u, 0u, 0u, 0u);
           }
         }
+#pragma unroll
+        for (int c = 0; c < kVPieces; ++c) {
+          const uint4 (&v)[4][kVPieces] = vf[pg];
+          const uint32_t v0[4] = {v[0][c].x, v[0][c].y, v[0][c].z, v[0][c].w};
+          const uint32_t v1[4] = {v[1][c].x, v[1][c].y, v[1][c].z, v[1][c].w};
+          const uint32_t v2[4] = {v[2][c].x, v[2][c].y, v[2][c].z, v[2][c].w};
+          const uint32_t v3[4] = {v[3][c].x, v[3][c].y, v[3][c].z, v[3][c].w};
+          constexpr int kWords = kRowBytes >= 128 ? 4 : 2;
+#pragma unroll
+          for (int j = 0; j < kWords; ++j) {
+            if constexpr (kHalf) {
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {      // two columns of two rows, by bytes
+                const uint32_t sel = i ? 0x7362 : 0x5140;
+                uint32_t a0, a1, a2, a3;
+                codes_to_half<kFmt>(__byte_perm(v0[j], v1[j], sel), a0, a1);
+                codes_to_half<kFmt>(__byte_perm(v2[j], v3[j], sel), a2, a3);
+#pragma unroll
+                for (int x = 0; x < NT; ++x) mma16816<true>(o[x][2 * j + i], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+              }
+            } else {
+              const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
+              const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
+#pragma unroll
+              for (int x = 0; x < NT; ++x) mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+            }
+          }
+        }
+        if (next + pg < iters) load_v(pg, rows[pg]);
       }
-      if (it + 1 < iters) load_v(r_now);
     }
 
     // ---- join the warps
