@@ -486,8 +486,10 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       }
 #pragma unroll
       for (int pg = 0; pg < kPages; ++pg) {
-        // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8)
-        uint32_t pf[NT][2];
+        // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8). Beside
+        // bf16 values they have to be bf16 too, and go in two parts: with one, their rounding would
+        // add as much to the error as the output's own does.
+        uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
           float w[4];
@@ -500,8 +502,12 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
               if (tail && !live[pg][e / 2]) w[e] = 0.0f;
             }
           }
-          pf[x][0] = transpose8x8(kHalf ? pack_half2(w[0], w[1]) : pack_bf16x2(w[0], w[1]));
-          pf[x][1] = transpose8x8(kHalf ? pack_half2(w[2], w[3]) : pack_bf16x2(w[2], w[3]));
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t hi = kHalf ? pack_half2(w[2 * u], w[2 * u + 1]) : pack_bf16x2(w[2 * u], w[2 * u + 1]);
+            pf[x][u] = transpose8x8(hi);
+            if (!kHalf) pl[x][u] = transpose8x8(pack_bf16x2(w[2 * u] - bf16_lo(hi), w[2 * u + 1] - bf16_hi(hi)));
+          }
         }
         if (tail) {                    // rows past the end may hold anything, NaN among it
 #pragma unroll
@@ -535,7 +541,10 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
               const uint32_t a0 = __byte_perm(v0[j], v1[j], 0x5410), a1 = __byte_perm(v0[j], v1[j], 0x7632);
               const uint32_t a2 = __byte_perm(v2[j], v3[j], 0x5410), a3 = __byte_perm(v2[j], v3[j], 0x7632);
 #pragma unroll
-              for (int x = 0; x < NT; ++x) mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+              for (int x = 0; x < NT; ++x) {
+                mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
+                mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+              }
             }
           }
         }

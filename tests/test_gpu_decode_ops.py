@@ -399,7 +399,7 @@ def decode_tolerance(q, k, v, scale, held, vs=None):
     # terms that one lane adds up, at most n, 2^-24 each
     score = (d + 4) * 2.0 ** -24 * big + 2.0 ** -21
     sums = max(n, 1) * 2.0 ** -24
-    weight = HALF[BF16] if held == "bf16" else 2.0 ** -11           # weights as tensor-core operands
+    weight = 2.0 ** -16 if held == "bf16" else 2.0 ** -11           # weights as two bf16 parts, or f16
     rel = weight + 2 * score + 2 * sums
     tol = absv * rel[:, None] + HALF[BF16] * np.abs(out) + 1e-30
     if held != "bf16" and n:
