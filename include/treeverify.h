@@ -570,8 +570,9 @@ typedef struct tv_rope_axes_geom {
  *                 are q_ld / k_ld ELEMENTS apart (>= heads * D), so slices of
  *                 a fused projection need no copy. Element alignment suffices;
  *                 16-byte aligned rows and heads take wider loads.
- *  positions      int32 [num_axes][pos_ld], pos_ld >= rows; may be negative
- *  inv_freq       float32 [R], radians per position of each pair
+ *  positions      int32 [num_axes][pos_ld], pos_ld >= rows (or 0: the same row
+ *                 for all axes); may be negative
+ *  inv_freq       float32 [R], radians per position of each pair (finite)
  *  q_out, k_out   as q and k, row strides q_out_ld / k_out_ld; an output may be
  *                 its own input (same pointer and stride), else no array of
  *                 the call may overlap an output

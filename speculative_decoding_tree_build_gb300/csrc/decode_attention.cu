@@ -167,7 +167,7 @@ __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t
 // one tile that computes nothing.
 __device__ __forceinline__ int dec_tiles(int n, int max_blocks) {
   if (n <= 0 || n > static_cast<long long>(max_blocks) * TV_BLOCK_SIZE) return 1;
-  return (n + kDecTileKeys - 1) / kDecTileKeys;
+  return (n - 1) / kDecTileKeys + 1;
 }
 
 // ------------------------------------------------------------------ the kernel
@@ -254,8 +254,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 
     // the loads that need nothing but (b, h): status, held blocks, the first block ids, the queries
     const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
-    const int pages = fits ? (n + TV_BLOCK_SIZE - 1) / TV_BLOCK_SIZE : 0;
-    const int page_end = min(pages, tile1 * kDecWarps);
+    const int pages = fits && n > 0 ? (n - 1) / TV_BLOCK_SIZE + 1 : 0;
+    const int page_end = tile1 < nt ? tile1 * kDecWarps : pages;
     const int first = tile0 * kDecWarps + warp;
     const int iters = page_end > first ? (page_end - first + kDecWarps - 1) / kDecWarps : 0;
     const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
@@ -371,7 +371,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       }
     };
     // the segment's keys end here; a page from here on is not loaded and masked like any tail
-    const int key_end = min(n, page_end * TV_BLOCK_SIZE);
+    const int key_end = tile1 < nt ? page_end * TV_BLOCK_SIZE : n;
     size_t rows[kPages];
     if (iters > 0) {
       ids = valid(ids_first);
@@ -386,9 +386,9 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       ids_next = fetch_ids(32);
     }
     for (int it = 0; it < iters; it += kPages) {
-      const int key0 = (first + it * kDecWarps) * TV_BLOCK_SIZE;           // of the first page
       constexpr int kNextPage = kDecWarps * TV_BLOCK_SIZE;
-      const bool tail = key0 + (kPages - 1) * kNextPage + TV_BLOCK_SIZE > key_end;
+      const int left = key_end - (first + it * kDecWarps) * TV_BLOCK_SIZE; // keys from the first page's first on
+      const bool tail = left < (kPages - 1) * kNextPage + TV_BLOCK_SIZE;
       // scores of 16 keys a page: thread holds keys g, g + 8 of queries 2t, 2t + 1
       float s[kPages][NT][4], k0[kPages], k1[kPages];
 #pragma unroll
@@ -443,7 +443,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       for (int pg = 0; pg < kPages; ++pg) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          live[pg][u] = !tail || key0 + pg * kNextPage + g + 8 * u < key_end;
+          live[pg][u] = !tail || pg * kNextPage + g + 8 * u < left;
           lv[pg][u] = kHalf ? __log2f(vs[pg][u]) : 0.0f;
         }
 #pragma unroll
@@ -512,7 +512,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         if (tail) {                    // rows past the end may hold anything, NaN among it
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            if (key0 + pg * kNextPage + 2 * t + (u & 1) + (u >> 1) * 8 < key_end) continue;
+            if (pg * kNextPage + 2 * t + (u & 1) + (u >> 1) * 8 < left) continue;
 #pragma unroll
             for (int c = 0; c < kVPieces; ++c) vf[pg][u][c] = make_uint4(0u, 0u, 0u, 0u);
           }

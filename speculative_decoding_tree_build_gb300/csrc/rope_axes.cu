@@ -253,16 +253,19 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
   p.units = p.rot_units + (p.d - 2 * p.pairs) / N;
   const int slots = p.units < kRopeAxThreads ? kRopeAxThreads / p.units : 1;
   // Little work (less than a vector a thread for eight CTAs an SM): a CTA takes
-  // one sweep of one row, so that few rows still spread over the chip. Else
+  // one sweep, of as many rows as still leave two CTAs for every SM. Else
   // about ten vectors a thread: all heads of some rows, in the 1 to 4 sweeps
   // over a row's heads that leave the fewest threads idle (40 heads of 8
   // units: 32 + 8 heads would idle 3 threads in 8; 4 x 10 heads of 3 rows 1 in 16).
   const long long row_items = static_cast<long long>(p.heads) * p.units;
   const long long per = row_items * p.rows / (152 * 8);
-  p.cta_rows = 1;
-  p.row_slots = 1;
   p.head_slots = p.heads < slots ? p.heads : slots;
   p.cta_heads = p.head_slots;
+  p.row_slots = slots / p.head_slots;
+  if (p.row_slots > p.rows / (152 * 2)) p.row_slots = p.rows / (152 * 2);
+  if (p.row_slots > kRopeAxAngles / p.pairs) p.row_slots = kRopeAxAngles / p.pairs;
+  if (p.row_slots < 1) p.row_slots = 1;
+  p.cta_rows = p.row_slots;
   if (per >= kRopeAxThreads) {
     p.cta_heads = p.heads < kRopeAxBatch * slots ? p.heads : kRopeAxBatch * slots;
     int best = 0;
@@ -331,7 +334,7 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
   const bool keys = g->num_kv_heads > 0;
   const long long qn = static_cast<long long>(g->num_q_heads) * g->head_dim;
   const long long kn = static_cast<long long>(g->num_kv_heads) * g->head_dim;
-  if (rows < 0 || pos_ld < rows || q_ld < qn || q_out_ld < qn || (keys && (k_ld < kn || k_out_ld < kn)))
+  if (rows < 0 || (pos_ld != 0 && pos_ld < rows) || q_ld < qn || q_out_ld < qn || (keys && (k_ld < kn || k_out_ld < kn)))
     return TV_ERR_BAD_SIZE;
   if (rows == 0) return TV_OK;
   if (!q || !q_out || !positions || !inv_freq || (keys && (!k || !k_out))) return TV_ERR_NULL_POINTER;

@@ -1,6 +1,10 @@
 """The plain-decoding and 8-bit-cache calls on the GPU against their float64
 restatement (oracle/decode_ref.py)."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -10,6 +14,7 @@ from oracle import decode_attention_ref, kv_quant_ref, rope_axes_ref
 
 pytestmark = pytest.mark.gpu
 
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 BF16, F32, I32 = torch.bfloat16, torch.float32, torch.int32
 HALF = {BF16: 2.0 ** -8, F32: 2.0 ** -24}        # largest relative error of one rounding
 HELD = {"bf16": BF16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
@@ -81,6 +86,8 @@ def check_rope(x, out, pos, inv, sections, style, order):
     (11, 4, 4, 512, [256], 0, 0, 0),
     (3, 130, 0, 96, [0, 40, 8], 0, 0, 0),           # no keys
     (4, 2, 2, 33, [7, 9], 1, 0, 0),                 # an odd head dimension
+    (2500, 2, 1, 64, [16, 16], 0, 0, 0),            # many rows of few heads
+    (2000, 10, 2, 72, [36], 0, 0, 0),
 ])
 def test_rope_axes(rows, hq, hkv, d, sections, order, pad, shift, style, dtype):
     g, q, k, pos, inv = rope_case(11, rows, hq, hkv, d, sections, style, order, dtype, 5000, pad, shift)
@@ -114,6 +121,10 @@ def test_rope_axes_no_rows_and_other_stream():
     tv.rope_axes(g, q, k, pos, inv, qo, ko, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     check_rope(q, qo, pos, inv, [32], 1, 0)
+    # one row of positions stands for all axes
+    g3 = tv.rope_axes_geom(4, 2, 64, [10, 12, 10], 1, 1)
+    tv.rope_axes(g3, q, k, pos.expand(3, -1), inv, qo, ko)
+    check_rope(q, qo, pos.expand(3, -1), inv, [10, 12, 10], 1, 1)
     with pytest.raises(ValueError):
         tv.rope_axes(g, q, k, pos, inv[:-1], qo, ko)
     with pytest.raises(ValueError):
@@ -648,6 +659,51 @@ def test_decode_step_together(held):
         assert np.array_equal(f64(c.k.view(torch.int8)[page, :, at].view(c.k.dtype))[0], code)
         assert np.array_equal(c.ks[page, :, at].cpu().numpy()[0], sc)
     check_decode(c, q, lens, b["out"], b["lse"])
+
+
+def test_first_calls_of_a_process_may_be_captured(tmp_path):
+    """No call needs an eager one before it: a fresh process captures all four at once."""
+    code = """
+import sys, torch
+sys.path.insert(0, %r)
+sys.path.insert(0, %r)
+import test_gpu_decode_ops as t
+from speculative_decoding_tree_build_gb300 import kv_quant_read
+c, qkv, hq, pos, inv, start, b, lens = t.step_setup("e4m3")
+ko = torch.zeros(c.pool, c.hkv, 16, c.d, dtype=torch.bfloat16, device="cuda")
+vo = torch.zeros_like(ko)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    t.decode_step(c, qkv, hq, pos, inv, start, b)
+    kv_quant_read(c.geom, start, b["len"], c.table, c.n_blocks, c.k, c.v, c.ks, c.vs, c.table, c.n_blocks, ko, vo, b["status"])
+g.replay()
+torch.cuda.synchronize()
+t.check_decode(c, qkv[:, :hq * c.d].unflatten(1, (hq, c.d)), lens, b["out"], b["lse"])
+assert bool(ko.any()) and b["status"].tolist() == [0] * 4
+print("captured")
+""" % (ROOT, os.path.join(ROOT, "tests"))
+    out = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert out.returncode == 0 and "captured" in out.stdout, out.stderr[-2000:]
+
+
+def test_two_decodes_at_once_on_two_streams():
+    """Two calls in flight on two streams, each with a workspace of its own."""
+    sets = []
+    for seed, held in ((95, "e4m3"), (97, "bf16")):
+        lens = [3000, 70, 1200]
+        c = filled(seed, lens, 2, 128, held)
+        q = torch.randn(3, 8, 128, generator=gen(seed + 1), device="cuda").to(BF16)
+        sets.append((c, q, lens, run_decode(c, q, lens), torch.cuda.Stream()))
+    for _ in range(10):
+        got = []
+        for c, q, lens, _, s in sets:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(run_decode(c, q, lens))
+        torch.cuda.synchronize()
+        for (out, lse, _), (_, _, _, want, _) in zip(got, sets):
+            assert np.array_equal(bits(out), bits(want[0])) and np.array_equal(bits(lse), bits(want[1]))
 
 
 def test_decode_step_captured_and_replayed():
