@@ -27,7 +27,8 @@
 //    and no reduction; weights stay below 2^8. A value row's scale joins the
 //    exponent: w_j = 2^(s_j + log2 vscale_j - M), with its own reference M, so
 //    the largest contribution is near 1 in f16 whatever the scales are. The
-//    sum of the softmax is float32 of unrounded terms.
+//    sum of the softmax is float32 of unrounded terms. Beside bf16 values the
+//    weights go as two bf16 parts.
 //
 // Work plan: a unit is (request, KV head), its tiles are 64 keys (a page for
 // each of the CTA's four warps). All units' tiles are laid end to end and
@@ -36,6 +37,10 @@
 // between CTAs leaves one partial result a CTA in the workspace and a second
 // grid joins them in order. Where the block table holds at most
 // kNoSplitPages pages a request, units are never cut and there is one launch.
+//
+// Measured: 64 requests of 4096 to 32768 keys, 32/8 heads of 128, e4m3 (1.9
+// GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 26 us, of which the
+// first grid 20.
 #include <cuda_fp16.h>
 
 #include <type_traits>

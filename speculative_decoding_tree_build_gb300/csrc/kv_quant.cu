@@ -8,6 +8,8 @@
 // largest magnitude takes log2(D / 16) shuffles of a paired integer maximum.
 // The append's rows are loaded before their slots are known, so the chain of
 // small loads (offsets, lengths, block ids) overlaps the one large one.
+// Measured: append 34.5 us for 201 MB (5.8 TB/s), read back 119 us for 692 MB
+// (5.8 TB/s, two thirds of it writes).
 #include "tv_kv8.cuh"
 #include "tv_share.cuh"
 
