@@ -683,7 +683,7 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  *  block_table, n_blocks, max_blocks_per_req, num_blocks
  *                 as elsewhere; requests may share blocks
  *  k_cache, v_cache   pools of the given format, 16-byte aligned
- *  k_scale, v_scale   float32 [num_blocks][Hkv][16], 16-byte aligned; NULL for
+ *  k_scale, v_scale   float32 [num_blocks][Hkv][16], not negative; NULL for
  *                 TV_KV_BF16
  *  out            bf16 [batch][Hq][D] out
  *  lse            float32 [batch][Hq] out, or NULL

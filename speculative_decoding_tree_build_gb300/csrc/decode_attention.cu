@@ -386,6 +386,14 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           rows[pg] = head_row(pg);
           load_k(pg, rows[pg]);
           load_v(pg, rows[pg]);
+        } else {                       // (masked; zeroed so that nothing is read that was never set)
+#pragma unroll
+          for (int c = 0; c < kKPieces; ++c) kf[pg][0][c] = kf[pg][1][c] = make_uint4(0u, 0u, 0u, 0u);
+          ks[pg][0] = ks[pg][1] = vs[pg][0] = vs[pg][1] = 0.0f;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int c = 0; c < kVPieces; ++c) vf[pg][u][c] = make_uint4(0u, 0u, 0u, 0u);
         }
       }
       ids_next = fetch_ids(32);
@@ -804,7 +812,7 @@ extern "C" int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32
     return TV_ERR_NULL_POINTER;
   if (!tv::aligned(q, 16) || q_ld % 8 != 0 || !tv::aligned(k_cache, 16) || !tv::aligned(v_cache, 16) ||
       !tv::aligned(out, 16) || (lse && !tv::aligned(lse, 4)) || !tv::aligned(workspace, 256) ||
-      (scaled && (!tv::aligned(k_scale, 16) || !tv::aligned(v_scale, 16))))
+      (scaled && (!tv::aligned(k_scale, 4) || !tv::aligned(v_scale, 4))))
     return TV_ERR_MISALIGNED;
   size_t need = 0;
   rc = tv_decode_workspace_bytes(geom, batch, &need);

@@ -113,7 +113,7 @@ def test_decode_attention_refusals(lib):
         assert call(swap(args, **{f"_{i}": v})) == SIZE
     for i in (3, 5, 6, 7, 9, 10, 11, 12, 14, 16, 18):
         assert call(swap(args, **{f"_{i}": None})) == NULL
-    for i, v in ((3, P + 8), (4, 4100), (9, P + 8), (10, P + 8), (11, P + 8), (12, P + 4), (14, P + 8),
+    for i, v in ((3, P + 8), (4, 4100), (9, P + 8), (10, P + 8), (11, P + 2), (12, P + 1), (14, P + 8),
                  (15, P + 2), (16, P + 128)):
         assert call(swap(args, **{f"_{i}": v})) == MIS
     n = ctypes.c_size_t()
