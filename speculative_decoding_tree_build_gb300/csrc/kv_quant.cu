@@ -18,7 +18,7 @@ namespace tv {
 constexpr int kAppendThreads = 256;
 constexpr int kAppendPerSm = 3;      // CTAs an SM
 constexpr int kAppendAhead = 4;      // rows whose loads a thread has in flight
-constexpr int kAppendMaxRows = 128;  // rows of k_new / v_new per CTA at most
+constexpr int kAppendMaxRows = 256;  // rows of k_new / v_new per CTA at most (a thread describes a row)
 
 struct AppendParams {
   const __nv_bfloat16* k_new;
@@ -364,9 +364,10 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   p.cta_heads = heads < parts ? heads : parts;
   p.slots = parts / p.cta_heads;
   const int head_blocks = (heads + p.cta_heads - 1) / p.cta_heads;
-  const long long ctas = 152 * tv::kAppendPerSm;
-  long long cta_rows = (static_cast<long long>(rows) * head_blocks + ctas - 1) / ctas;
-  if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
+  // (or a whole number of times)
+  const long long work = static_cast<long long>(rows) * head_blocks, wave = 152 * tv::kAppendPerSm;
+  const long long waves = (work + wave * tv::kAppendMaxRows - 1) / (wave * tv::kAppendMaxRows);
+  long long cta_rows = (work + waves * wave - 1) / (waves * wave);
   cta_rows = (cta_rows + p.slots - 1) / p.slots * p.slots;
   if (cta_rows > tv::kAppendMaxRows) cta_rows = tv::kAppendMaxRows;
   p.cta_rows = static_cast<int>(cta_rows);

@@ -94,12 +94,13 @@ __device__ __forceinline__ float2 rope_cos_sin(int position, unsigned long long 
   return make_float2(quarter == 1u || quarter == 2u ? -cs : cs, quarter & 2u ? -sn : sn);
 }
 
-// Turn the N values of a vector of a pair-interleaved head (N / 2 pairs), or
-// the pairs of two vectors.
+// Turn the N values of a vector of a pair-interleaved head (N / 2 pairs; the
+// first `pairs` of them), or the pairs of two vectors.
 template <typename T, int N, int P, bool kTwo>
-__device__ __forceinline__ void rope_turn(RopeVec<T, N>& va, RopeVec<T, N>& vb, const float2 (&cs)[P]) {
+__device__ __forceinline__ void rope_turn(RopeVec<T, N>& va, RopeVec<T, N>& vb, const float2 (&cs)[P], int pairs) {
 #pragma unroll
   for (int j = 0; j < P; ++j) {
+    if (j >= pairs) break;
     T& xa = kTwo ? va.x[j] : va.x[2 * j];
     T& xb = kTwo ? vb.x[j] : va.x[2 * j + (N > 1 ? 1 : 0)];
     const float a = rope_float(xa), b = rope_float(xb);
@@ -129,8 +130,9 @@ __device__ __forceinline__ void rope_turn_bf16(RopeVec<__nv_bfloat16, N>& va, Ro
 }
 
 // T: element, N: elements of a vector, kHalves: rotary style 1 (a pair's two
-// columns lie in two vectors; else N = 1 or both are in one vector).
-template <typename T, int N, bool kHalves>
+// columns lie in two vectors; else N = 1 or both are in one vector), kEdge:
+// the rotated columns end inside a vector (where both are in one).
+template <typename T, int N, bool kHalves, bool kEdge>
 __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_kernel(const __grid_constant__ RopeAxParams p) {
   // pairs of a unit, and whether it holds a second vector
   constexpr int P = kHalves ? N : (N == 1 ? 1 : N / 2);
@@ -155,8 +157,8 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
     if (u < p.rot_units) {
       ca = kHalves ? u * N : u * (N == 1 ? 2 : N);
       cb = kHalves ? ca + p.pairs : ca + 1;
-    } else {
-      ca = 2 * p.pairs + (u - p.rot_units) * N;
+    } else {                           // (a pair-interleaved head's units of two columns or more cover it in order)
+      ca = kTwo ? 2 * p.pairs + (u - p.rot_units) * N : u * N;
       cb = ca;
     }
   };
@@ -206,10 +208,15 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   }
   if (turning) {
     const unsigned long long f = rope_turns(inv_freq);
-    for (int r = r0;; pos = position[r]) {
-      s_cs[r * p.pairs + pr] = rope_cos_sin(pos, f);
-      r += step;
-      if (r >= nrows) break;
+    s_cs[r0 * p.pairs + pr] = rope_cos_sin(pos, f);
+    constexpr int kAhead = 4;                                // further positions in flight together
+    for (int r = r0 + step; r < nrows; r += kAhead * step) {
+      int next[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) next[i] = r + i * step < nrows ? *const_cast<const volatile int32_t*>(position + r + i * step) : 0;
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (r + i * step < nrows) s_cs[(r + i * step) * p.pairs + pr] = rope_cos_sin(next[i], f);
     }
   }
   __syncthreads();
@@ -226,14 +233,17 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
       float2 cs[P];
       if (turns) {
 #pragma unroll
-        for (int j = 0; j < P; ++j) cs[j] = s_cs[r * p.pairs + u * P + j];
+        for (int j = 0; j < P; ++j) cs[j] = s_cs[kEdge ? min(r * p.pairs + u * P + j, kRopeAxAngles - 1) : r * p.pairs + u * P + j];
       }
 #pragma unroll
       for (int e = 0; e < kRopeAxBatch; ++e) {
         if (head0 + e * p.head_slots >= head_end) break;
         if (turns) {
-          if constexpr (kPacked) rope_turn_bf16<N, P, kTwo>(va[e], vb[e], cs);
-          else rope_turn<T, N, P, kTwo>(va[e], vb[e], cs);
+          if (kPacked && (!kEdge || u * P + P <= p.pairs)) {
+            if constexpr (kPacked) rope_turn_bf16<N, P, kTwo>(va[e], vb[e], cs);
+          } else {
+            rope_turn<T, N, P, kTwo>(va[e], vb[e], cs, kEdge ? p.pairs - u * P : P);
+          }
         }
         T* dst = (is_q(e) ? qd : kd) + off[e];
         *reinterpret_cast<Vec*>(dst + ca) = va[e];
@@ -250,8 +260,8 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
 template <typename T, int N>
 static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t stream) {
   const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
-  p.rot_units = p.pairs / per_unit;
-  p.units = p.rot_units + (p.d - 2 * p.pairs) / N;
+  p.rot_units = (p.pairs + per_unit - 1) / per_unit;
+  p.units = halves || N == 1 ? p.rot_units + (p.d - 2 * p.pairs) / N : p.d / N;
   const int slots = p.units < kRopeAxThreads ? kRopeAxThreads / p.units : 1;
   // Little work (less than a vector a thread for eight CTAs an SM): a CTA takes
   // one sweep, of as many rows as still leave two CTAs for every SM. Else
@@ -274,12 +284,12 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
       const int hs = (p.cta_heads + k - 1) / k;
       if (hs > slots) continue;
       const int busy = slots / hs * p.cta_heads * 16 / k;      // threads at work, in sixteenths of a slot
-      if (busy >= best) {
-        best = busy;
-        p.head_slots = hs;
-        p.row_slots = slots / hs;
-      }
+      if (busy <= best) continue;
+      best = busy;
+      p.head_slots = hs;
+      p.row_slots = slots / hs;
     }
+    if (p.row_slots > kRopeAxAngles / p.pairs) p.row_slots = kRopeAxAngles / p.pairs;
     const long long items = static_cast<long long>(p.cta_heads) * p.units;
     long long rows = (per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per) / items;
     rows = (rows + p.row_slots - 1) / p.row_slots * p.row_slots;
@@ -293,24 +303,29 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
   p.groups = (p.heads + p.cta_heads - 1) / p.cta_heads;
   const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  auto* kernel = halves ? rope_axes_kernel<T, N, true> : rope_axes_kernel<T, N, false>;
+  auto* kernel = halves ? rope_axes_kernel<T, N, true, false> : rope_axes_kernel<T, N, false, false>;
+  if constexpr (N > 1) {
+    if (!halves && 2 * p.pairs % N != 0) kernel = rope_axes_kernel<T, N, false, true>;
+  }
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRopeAxThreads), 0, stream, p);
 }
 
-// The widest vector (16 or 8 bytes, else single elements) that the addresses,
-// strides, head dimension and pairs allow.
+// The widest vector (16, 8 or 4 bytes, else single elements) that the addresses,
+// strides, head dimension and, for pairs of two halves, the pairs allow.
 template <typename T>
 static cudaError_t launch_rope_axes_any(const RopeAxParams& p, bool halves, bool keys, cudaStream_t stream) {
   auto fits = [&](int n) {
     const uintptr_t bytes = n * sizeof(T);
-    const int cols = halves ? p.pairs : 2 * p.pairs;
-    return p.d % n == 0 && cols % n == 0 && p.q_ld % n == 0 && p.q_out_ld % n == 0 && aligned(p.q, bytes) &&
+    return p.d % n == 0 && (!halves || p.pairs % n == 0) && p.q_ld % n == 0 && p.q_out_ld % n == 0 && aligned(p.q, bytes) &&
            aligned(p.q_out, bytes) &&
            (!keys || (p.k_ld % n == 0 && p.k_out_ld % n == 0 && aligned(p.k, bytes) && aligned(p.k_out, bytes)));
   };
   constexpr int kFull = 16 / sizeof(T);
   if (fits(kFull)) return launch_rope_axes<T, kFull>(p, halves, stream);
   if (fits(kFull / 2)) return launch_rope_axes<T, kFull / 2>(p, halves, stream);
+  if constexpr (kFull / 4 > 1) {
+    if (fits(kFull / 4)) return launch_rope_axes<T, kFull / 4>(p, halves, stream);
+  }
   return launch_rope_axes<T, 1>(p, halves, stream);
 }
 

@@ -56,6 +56,20 @@ def rope_case(seed, rows, hq, hkv, d, sections, style, order, dtype, far, pad=0,
     return geom, q, k, pos, inv
 
 
+def test_rope_axes_leaves_the_other_columns_alone():
+    """Infinities and NaN behind the rotated columns pass through and touch nothing else."""
+    for style in (0, 1):
+        for pairs in (1, 3, 5, 13, 16):
+            g, q, k, pos, inv = rope_case(17, 6, 2, 1, 40, [pairs], style, 0, BF16, 50)
+            q = q.clone()
+            q[:, :, 2 * pairs] = float("nan")
+            q[:, :, -1] = float("inf")
+            qo, ko = torch.empty_like(q), torch.empty(6, 1, 40, dtype=BF16, device="cuda")
+            tv.rope_axes(g, q, k, pos, inv, qo, ko)
+            assert np.array_equal(bits(qo[..., 2 * pairs:].contiguous()), bits(q[..., 2 * pairs:].contiguous()))
+            assert bool(torch.isfinite(qo[..., :2 * pairs]).all())
+
+
 def check_rope(x, out, pos, inv, sections, style, order):
     want = rope_axes_ref(f64(x), pos.cpu().numpy(), f64(inv), sections, style, order)
     got = f64(out)
@@ -88,6 +102,9 @@ def check_rope(x, out, pos, inv, sections, style, order):
     (4, 2, 2, 33, [7, 9], 1, 0, 0),                 # an odd head dimension
     (2500, 2, 1, 64, [16, 16], 0, 0, 0),            # many rows of few heads
     (2000, 10, 2, 72, [36], 0, 0, 0),
+    (40, 19, 1, 80, [20, 7, 10], 1, 0, 0),          # 74 columns turn: a vector on both sides of their end
+    (300, 3, 3, 32, [1], 0, 4, 2),                  # one pair, rows aligned to 4 bytes in bf16
+    (5, 2, 2, 48, [11], 0, 2, 0),
 ])
 def test_rope_axes(rows, hq, hkv, d, sections, order, pad, shift, style, dtype):
     g, q, k, pos, inv = rope_case(11, rows, hq, hkv, d, sections, style, order, dtype, 5000, pad, shift)
