@@ -279,19 +279,21 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
   p.cta_rows = p.row_slots;
   if (per >= kRopeAxThreads) {
     p.cta_heads = p.heads < kRopeAxBatch * slots ? p.heads : kRopeAxBatch * slots;
+    const long long items = static_cast<long long>(p.cta_heads) * p.units;
+    long long rows = (per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per) / items;
     int best = 0;
     for (int k = 1; k <= kRopeAxBatch; ++k) {
       const int hs = (p.cta_heads + k - 1) / k;
       if (hs > slots) continue;
-      const int busy = slots / hs * p.cta_heads * 16 / k;      // threads at work, in sixteenths of a slot
-      if (busy <= best) continue;
+      // threads at work, in sixteenths of a slot; of two equals the one with more loads in flight a
+      // thread, where there are rows enough for it (38 heads of 10 units: 45.7 -> 38.2 us)
+      const int busy = slots / hs * p.cta_heads * 16 / k;
+      if (busy < best || (busy == best && slots / hs > rows)) continue;
       best = busy;
       p.head_slots = hs;
       p.row_slots = slots / hs;
     }
     if (p.row_slots > kRopeAxAngles / p.pairs) p.row_slots = kRopeAxAngles / p.pairs;
-    const long long items = static_cast<long long>(p.cta_heads) * p.units;
-    long long rows = (per > 10 * kRopeAxThreads ? 10 * kRopeAxThreads : per) / items;
     rows = (rows + p.row_slots - 1) / p.row_slots * p.row_slots;
     if (rows > kRopeAxAngles / p.pairs) rows = kRopeAxAngles / p.pairs;
     p.cta_rows = rows < 1 ? 1 : static_cast<int>(rows);
