@@ -35,8 +35,10 @@
 // every CTA takes a contiguous share, whatever the mix of lengths; the share
 // is computed by each CTA from seq_len, so no host round trip. A unit cut
 // between CTAs leaves one partial result a CTA in the workspace and a second
-// grid joins them in order. Where the block table holds at most
-// kNoSplitPages pages a request, units are never cut and there is one launch.
+// grid joins them in order. Where the block table is short and there are few
+// units, every unit goes to a cluster of 1 to 8 CTAs instead, which join their
+// results through distributed shared memory: one launch, and one round trip
+// less ahead of the first cached row (launch_decode has the rule).
 //
 // Measured: 64 requests of 4096 to 32768 keys, 32/8 heads of 128, e4m3 (1.9
 // GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 26 us, of which the
@@ -45,6 +47,7 @@
 
 #include <type_traits>
 
+#include "tv_cluster.cuh"
 #include "tv_kv8.cuh"
 #include "tv_share.cuh"
 
@@ -55,7 +58,7 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecTileKeys = TV_BLOCK_SIZE * kDecWarps;
 constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
 constexpr int kDecMinShare = 3;        // least cost worth a CTA of its own: a unit of one tile
-constexpr int kNoSplitPages = 16;
+constexpr int kDecMaxCluster = 8;
 constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
 constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay below 2^24
 constexpr int kMergeWarps = 4;         // warps of a joining CTA at least
@@ -86,7 +89,8 @@ struct DecodeParams {
   int* mids;           // [CTAs] the unit whose partial is in slot 0, -1: none
   float* partials;     // two slots a CTA: [group][D] sums, then [group] x (m, M, l, -)
   int32_t* status;
-  int batch, hq, hkv, group, max_blocks, num_blocks, split;
+  int batch, hq, hkv, group, max_blocks, num_blocks;
+  int cluster;         // CTAs of a unit in the one-launch form
   int by_unit;         // how begins is indexed
   int parts;           // warps that share a query head's partials
   float scale_log2;
@@ -175,6 +179,19 @@ __device__ __forceinline__ int dec_tiles(int n, int max_blocks) {
   return (n - 1) / kDecTileKeys + 1;
 }
 
+// Two columns of a query head's output from the joined sums, and its log-sum-exp.
+template <int D>
+__device__ __forceinline__ void dec_store(const DecodeParams& p, int b, int h, int qi, int d, int n, float2 acc, float mm, float mr, float ll) {
+  const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
+  const float f = n == 0 ? 0.0f : fast_exp2(mr - mm) / ll;
+  *reinterpret_cast<uint32_t*>(p.out + at * D + d) = pack_bf16x2(acc.x * f, acc.y * f);
+  if (p.lse != nullptr && d == 0) p.lse[at] = n == 0 ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+}
+
+__device__ __forceinline__ float2 as_float2(uint64_t v) {
+  return make_float2(__uint_as_float(static_cast<uint32_t>(v)), __uint_as_float(static_cast<uint32_t>(v >> 32)));
+}
+
 // ------------------------------------------------------------------ the kernel
 
 template <int kFmt, int D, int NT>
@@ -197,7 +214,9 @@ struct DecTraits {
   static constexpr int kPerSm = NT == 2 ? (D == 64 ? 3 : 2) : kRowBytes == 256 ? 3 : 4;
 };
 
-template <int kFmt, int D, int NT>
+// kOneGrid: a unit belongs to a cluster of p.cluster CTAs, which take its
+// tiles in turn; else a CTA takes a share of all units' tiles.
+template <int kFmt, int D, int NT, bool kOneGrid>
 __global__ void __launch_bounds__(kDecThreads, (DecTraits<kFmt, D, NT>::kPerSm))
 decode_kernel(const __grid_constant__ DecodeParams p) {
   using Tr = DecTraits<kFmt, D, NT>;
@@ -211,38 +230,50 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   grid_launch_dependents();
   grid_dependency_wait();
 
-  // ---- this CTA's share of the tiles
-  const Share sh = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int b) {
-    return static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[b], p.max_blocks));
-  });
-  const int cta = blockIdx.x, grid = sh.ctas;
-  const long long hi = sh.hi, total = sh.total;
+  __shared__ float4 s_joined[16];                              // the CTA's (m, M, l, faulty) for its cluster
+  const int cta = blockIdx.x;
+  int b, h, n, nt, tile0 = 0, rank = 0, grid = 0;
+  long long hi = 0, total = 0;
+  long long unit = 0;                  // where the unit starts in the sequence of costs
   int mid = -1;                        // the unit whose partial this CTA leaves in slot 0
   DecBegin begun = {0, 0, -1, 0};      // the unit that it begins and does not finish
-  if (sh.lo >= sh.hi) {
-    if (p.split && threadIdx.x == 0) {
-      p.mids[cta] = -1;
-      if (!p.by_unit) p.begins[cta] = begun;
+  if constexpr (kOneGrid) {
+    const int u = cta / p.cluster;
+    rank = cta - u * p.cluster;
+    b = u / p.hkv;
+    h = u - b * p.hkv;
+    n = ldg_int(p.seq_len + b);
+    nt = 1;
+  } else {
+    // ---- this CTA's share of the tiles
+    const Share sh = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int i) {
+      return static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[i], p.max_blocks));
+    });
+    grid = sh.ctas;
+    hi = sh.hi;
+    total = sh.total;
+    if (sh.lo >= sh.hi) {
+      if (threadIdx.x == 0) {
+        p.mids[cta] = -1;
+        if (!p.by_unit) p.begins[cta] = begun;
+      }
+      return;
     }
-    return;
-  }
-  int b = sh.b;
-  int n = p.seq_len[b], nt = dec_tiles(n, p.max_blocks);
-  long long unit;                      // where the unit starts in the sequence of costs
-  int h, tile0;
-  {
+    b = sh.b;
+    n = p.seq_len[b];
+    nt = dec_tiles(n, p.max_blocks);
     const long long cost = kDecUnitCost + nt, rel = sh.lo - sh.start;
     h = static_cast<int>(rel / cost);
     const long long off = rel - h * cost;
     unit = sh.start + h * cost;
     // tile 0 starts at 0, tile k at kDecUnitCost + k
     tile0 = off == 0 ? 0 : off <= kDecUnitCost + 1 ? 1 : static_cast<int>(off - kDecUnitCost);
-    if (!p.split && off != 0) tile0 = nt;              // the unit belongs to the CTA of its start
   }
 
   for (;;) {
     // ---- the next unit, or part of one
     if (tile0 >= nt) {
+      if (kOneGrid) break;
       unit += kDecUnitCost + nt;
       tile0 = 0;
       if (++h == p.hkv) {
@@ -253,19 +284,23 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       }
       continue;
     }
-    if (tile0 == 0 ? unit >= hi : unit + kDecUnitCost + tile0 >= hi) break;
+    if (!kOneGrid && (tile0 == 0 ? unit >= hi : unit + kDecUnitCost + tile0 >= hi)) break;
     int tile1 = nt;
-    if (p.split && hi - unit - kDecUnitCost < nt) tile1 = max(tile0 + 1, static_cast<int>(hi - unit - kDecUnitCost));
+    if (!kOneGrid && hi - unit - kDecUnitCost < nt) tile1 = max(tile0 + 1, static_cast<int>(hi - unit - kDecUnitCost));
 
     // the loads that need nothing but (b, h): status, held blocks, the first block ids, the queries
+    const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+    // pages of a warp: first, first + stride, ...
+    const int stride = kOneGrid ? kDecWarps * p.cluster : kDecWarps;
+    const int first = kOneGrid ? rank * kDecWarps + warp : tile0 * kDecWarps + warp;
+    int ids_first = 0;
+    if (kOneGrid && first + lane * stride < p.max_blocks) ids_first = ldg_int(row + first + lane * stride);
     const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
     const int pages = fits && n > 0 ? (n - 1) / TV_BLOCK_SIZE + 1 : 0;
-    const int page_end = tile1 < nt ? tile1 * kDecWarps : pages;
-    const int first = tile0 * kDecWarps + warp;
-    const int iters = page_end > first ? (page_end - first + kDecWarps - 1) / kDecWarps : 0;
-    const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-    auto fetch_ids = [&](int base) { return base + lane < iters ? ldg_int(row + first + (base + lane) * kDecWarps) : 0; };
-    const int ids_first = fetch_ids(0);
+    const int page_end = !kOneGrid && tile1 < nt ? tile1 * kDecWarps : pages;
+    int iters = page_end > first ? (page_end - first + stride - 1) / stride : 0;
+    auto fetch_ids = [&](int base) { return base + lane < iters ? ldg_int(row + first + (base + lane) * stride) : 0; };
+    if (!kOneGrid) ids_first = fetch_ids(0);
     const int st = *const_cast<volatile int32_t*>(p.status + b), held = min(ldg_int(p.n_blocks + b), p.max_blocks);
 
     // ---- queries: the thread's columns of query g (and g + 8), as MMA operands
@@ -286,11 +321,16 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     int bad = n < 0 ? TV_ST_BAD_SIZE : (!fits || pages > held) ? TV_ST_BAD_BLOCK : 0;
     // another CTA may flag the request while this one's threads read its status: they decide
     // together. (The barrier also keeps the last unit's shared sums until they are read.)
-    if (__syncthreads_or(st | bad)) {
+    int hold = __syncthreads_or(st | bad);
+    if (hold) {
       if (st == 0 && threadIdx.x == 0) atomicOr(p.status + b, bad);
-      if (tile0 == 0 && p.split && p.by_unit && threadIdx.x == 0) p.begins[b * p.hkv + h] = DecBegin{0, 0, -1, 0};
-      tile0 = nt;
-      continue;
+      if (kOneGrid) {
+        iters = 0;                     // on to the cluster's barriers with nothing
+      } else {
+        if (tile0 == 0 && p.by_unit && threadIdx.x == 0) p.begins[b * p.hkv + h] = DecBegin{0, 0, -1, 0};
+        tile0 = nt;
+        continue;
+      }
     }
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
@@ -376,10 +416,11 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       }
     };
     // the segment's keys end here; a page from here on is not loaded and masked like any tail
-    const int key_end = tile1 < nt ? page_end * TV_BLOCK_SIZE : n;
+    const int key_end = !kOneGrid && tile1 < nt ? page_end * TV_BLOCK_SIZE : n;
+    const int next_page = stride * TV_BLOCK_SIZE;              // keys from a page of the warp to its next one
     size_t rows[kPages];
     if (iters > 0) {
-      ids = valid(ids_first);
+      ids = valid(lane < iters ? ids_first : 0);
 #pragma unroll
       for (int pg = 0; pg < kPages; ++pg) {
         if (pg < iters) {
@@ -399,9 +440,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       ids_next = fetch_ids(32);
     }
     for (int it = 0; it < iters; it += kPages) {
-      constexpr int kNextPage = kDecWarps * TV_BLOCK_SIZE;
-      const int left = key_end - (first + it * kDecWarps) * TV_BLOCK_SIZE; // keys from the first page's first on
-      const bool tail = left < (kPages - 1) * kNextPage + TV_BLOCK_SIZE;
+      const int left = key_end - (first + it * stride) * TV_BLOCK_SIZE; // keys from the first page's first on
+      const bool tail = left < (kPages - 1) * next_page + TV_BLOCK_SIZE;
       // scores of 16 keys a page: thread holds keys g, g + 8 of queries 2t, 2t + 1
       float s[kPages][NT][4], k0[kPages], k1[kPages];
 #pragma unroll
@@ -456,7 +496,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       for (int pg = 0; pg < kPages; ++pg) {
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          live[pg][u] = !tail || pg * kNextPage + g + 8 * u < left;
+          live[pg][u] = !tail || pg * next_page + g + 8 * u < left;
           lv[pg][u] = kHalf ? __log2f(vs[pg][u]) : 0.0f;
         }
 #pragma unroll
@@ -525,7 +565,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         if (tail) {                    // rows past the end may hold anything, NaN among it
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-            if (pg * kNextPage + 2 * t + (u & 1) + (u >> 1) * 8 < left) continue;
+            if (pg * next_page + 2 * t + (u & 1) + (u >> 1) * 8 < left) continue;
 #pragma unroll
             for (int c = 0; c < kVPieces; ++c) vf[pg][u][c] = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -582,10 +622,12 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           *reinterpret_cast<float2*>(dst + d) = make_float2(o[x][i][e], o[x][i][e + 2]);
         }
       }
-    const bool any_bad = __syncthreads_or(bad);
+    const bool any_bad = __syncthreads_or(bad | hold);
     if (bad) atomicOr(p.status + b, bad);
-    const bool whole = tile0 == 0 && tile1 == nt;
-    float* slot = p.partials + (static_cast<size_t>(cta) * 2 + (tile0 == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
+    const bool whole = kOneGrid ? p.cluster == 1 : tile0 == 0 && tile1 == nt;
+    // where the CTA's sums go: the output, its cluster's sight, or a slot of the workspace
+    float* const s_part = s_o + kDecWarps * 8 * NT * kRowPad;  // [group][D]
+    float* const slot = kOneGrid ? s_part : p.partials + (static_cast<size_t>(cta) * 2 + (tile0 == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
     if (!any_bad || !whole) {
       for (int i = threadIdx.x; i < p.group * (D / 2); i += kDecThreads) {
         const int qi = i / (D / 2), d = i % (D / 2) * 2;
@@ -606,19 +648,59 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           ll += s4.z * fast_exp2(s4.x - mm);
         }
         if (whole) {
-          const size_t at = static_cast<size_t>(b) * p.hq + static_cast<size_t>(h) * p.group + qi;
-          const float f = n == 0 ? 0.0f : fast_exp2(mr - mm) / ll;
-          *reinterpret_cast<uint32_t*>(p.out + at * D + d) = pack_bf16x2(acc.x * f, acc.y * f);
-          if (p.lse != nullptr && d == 0) p.lse[at] = n == 0 ? -INFINITY : (mm + log2f(ll)) * 0.69314718055994531f;
+          dec_store<D>(p, b, h, qi, d, n, acc, mm, mr, ll);
         } else {
           *reinterpret_cast<float2*>(slot + static_cast<size_t>(qi) * D + d) = acc;
-          if (d == 0) *reinterpret_cast<float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi) = make_float4(mm, mr, ll, 0.0f);
+          if (d == 0) {
+            const float4 stat = make_float4(mm, mr, ll, any_bad ? 1.0f : 0.0f);
+            if (kOneGrid) s_joined[qi] = stat;
+            else *reinterpret_cast<float4*>(slot + static_cast<size_t>(p.group) * D + 4 * qi) = stat;
+          }
         }
       }
     }
+    if constexpr (kOneGrid) {
+      if (p.cluster > 1) {
+        // the CTAs of the cluster share the output's columns and read each other's sums
+        __syncwarp();
+        cluster_sync_all();
+        for (int i = rank * kDecThreads + threadIdx.x; i < p.group * (D / 2); i += kDecThreads * p.cluster) {
+          const int qi = i / (D / 2), d = i % (D / 2) * 2;
+          float2 v[kDecMaxCluster], mM[kDecMaxCluster], lf[kDecMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kDecMaxCluster; ++r) {
+            if (r >= p.cluster) break;
+            v[r] = as_float2(ld_cluster_u64(s_part + qi * D + d, r));
+            mM[r] = as_float2(ld_cluster_u64(&s_joined[qi].x, r));
+            lf[r] = as_float2(ld_cluster_u64(&s_joined[qi].z, r));
+          }
+          float mm = kLowest, mr = kLowest, ll = 0.0f, faulty = 0.0f;
+          float2 acc = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int r = 0; r < kDecMaxCluster; ++r) {
+            if (r >= p.cluster) break;
+            mm = fmaxf(mm, mM[r].x);
+            mr = fmaxf(mr, mM[r].y);
+            faulty += lf[r].y;
+          }
+#pragma unroll
+          for (int r = 0; r < kDecMaxCluster; ++r) {
+            if (r >= p.cluster) break;
+            const float f = fast_exp2(mM[r].y - mr);
+            acc.x += v[r].x * f;
+            acc.y += v[r].y * f;
+            ll += lf[r].x * fast_exp2(mM[r].x - mm);
+          }
+          if (faulty == 0.0f) dec_store<D>(p, b, h, qi, d, n, acc, mm, mr, ll);
+        }
+        __syncwarp();
+        cluster_sync_all();            // a CTA's shared memory outlives its readers
+      }
+      return;
+    }
     if (tile0 > 0) {
       mid = b * p.hkv + h;
-    } else if (p.split) {
+    } else {
       DecBegin d = {b * p.hkv + h, cta, -1, 0};
       if (!whole) {
         // the CTA of the unit's last tile: the largest c with total * c / grid <= its start
@@ -631,7 +713,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     if (tile1 < nt) break;
     tile0 = nt;
   }
-  if (p.split && threadIdx.x == 0) {
+  if (!kOneGrid && threadIdx.x == 0) {
     p.mids[cta] = mid;
     if (!p.by_unit) p.begins[cta] = begun;
   }
@@ -743,18 +825,50 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
+#ifndef WANT
+#define WANT 2
+#endif
+#ifndef LIM1
+#define LIM1 4
+#endif
+#ifndef LIMC
+#define LIMC 8
+#endif
 template <int kFmt, int D, int NT>
 static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) {
   using Tr = DecTraits<kFmt, D, NT>;
-  constexpr size_t smem = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
-  static size_t smem_set[kMaxDevices] = {0};
-  auto* kernel = decode_kernel<kFmt, D, NT>;
-  if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+  constexpr size_t sums = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
   const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
+  const int tiles = (p.max_blocks + kDecWarps - 1) / kDecWarps;        // of the longest request that the table holds
+  p.cluster = 1;
+  while (p.cluster < kDecMaxCluster && p.cluster * WANT < tiles && 2ll * p.cluster * units <= grid) p.cluster *= 2;
+  if (tiles <= p.cluster * (p.cluster == 1 ? LIM1 : LIMC)) {
+    constexpr size_t smem = sums + sizeof(float) * 8 * NT * D;
+    static size_t smem_set[kMaxDevices] = {0};
+    auto* kernel = decode_kernel<kFmt, D, NT, true>;
+    if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(units) * p.cluster);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+  }
+  static size_t smem_set[kMaxDevices] = {0};
+  auto* kernel = decode_kernel<kFmt, D, NT, false>;
+  if (!ensure_smem(kernel, sums, smem_set, dev)) return TV_ERR_CUDA;
   p.by_unit = units <= grid ? 1 : 0;
   p.parts = 1;
-  if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), smem, stream, p) != cudaSuccess) return TV_ERR_CUDA;
-  if (!p.split) return TV_OK;
+  if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), sums, stream, p) != cudaSuccess) return TV_ERR_CUDA;
   // a unit's partials: about grid / units and both ends; eight of them a warp
   const int partials = grid / units + 2;
   while (p.parts < kMergeMaxParts && p.parts * kMergeBatch < partials) p.parts *= 2;
@@ -835,7 +949,6 @@ extern "C" int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32
   p.batch = batch; p.hq = geom->num_q_heads; p.hkv = geom->num_kv_heads;
   p.group = geom->num_q_heads / geom->num_kv_heads;
   p.max_blocks = max_blocks_per_req; p.num_blocks = num_blocks;
-  p.split = max_blocks_per_req > tv::kNoSplitPages ? 1 : 0;
   const float scale = geom->softmax_scale > 0.0f ? geom->softmax_scale : 1.0f / sqrtf(static_cast<float>(geom->head_dim));
   p.scale_log2 = scale * 1.4426950408889634f;
   const cudaStream_t s = tv::as_stream(stream);

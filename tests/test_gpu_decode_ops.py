@@ -507,6 +507,13 @@ def test_decode_attention(hq, hkv, d, lens, held):
     assert np.array_equal(bits(out), bits(again)) and np.array_equal(bits(lse), bits(lse2))
     alone, none, _ = run_decode(c, q, lens, with_lse=False)
     assert none is None and np.array_equal(bits(out), bits(alone))
+    # a block table with room for long requests takes the other way of cutting and joining
+    wide = torch.full((len(lens), 640), -1, dtype=I32, device="cuda")
+    wide[:, :c.table.shape[1]] = c.table
+    c.table = wide
+    out, lse, status = run_decode(c, q, lens)
+    assert status == [0] * len(lens)
+    check_decode(c, q, lens, out, lse)
 
 
 @pytest.mark.parametrize("held", ["bf16", "e4m3", "int8"])
@@ -556,9 +563,31 @@ def test_decode_attention_row_scales_of_every_size(held):
     check_decode(c, q, lens, out, lse)
 
 
-def test_decode_attention_shared_pages_skips_and_flags():
+@pytest.mark.parametrize("hkv,lens", [(1, [1900, 33, 900]), (2, [500, 0, 1, 129]), (16, [300, 200])])
+@pytest.mark.parametrize("held", ["bf16", "e4m3", "int8"])
+def test_decode_attention_bad_page_in_a_short_table(hkv, lens, held):
+    """One request of a short table lacks a page that one of the blocks of a cluster alone reads."""
+    c = filled(99, lens, hkv, 128, held)
+    q = torch.randn(len(lens), 4 * hkv, 128, generator=gen(100), device="cuda").to(BF16)
+    page = (lens[0] - 1) // 16 - 1
+    good = int(c.table[0, page])
+    for bad in (-1, c.pool, 2 ** 31 - 1):
+        c.table[0, page] = bad
+        out, lse, st = run_decode(c, q, lens)
+        assert st == [8] + [0] * (len(lens) - 1)
+        assert bool((out[0] == 9.0).all()) and bool((lse[0] == 9.0).all())
+        check_decode(c, q, lens, out, lse, which=range(1, len(lens)))
+    c.table[0, page] = good
+    out, lse, st = run_decode(c, q, lens)
+    assert st == [0] * len(lens)
+    check_decode(c, q, lens, out, lse)
+
+
+@pytest.mark.parametrize("width", [3, 640])
+def test_decode_attention_shared_pages_skips_and_flags(width):
     lens = [40, 40, 33, 20, 18, 9]
     c = filled(71, lens, 2, 128, "e4m3")
+    c.table = torch.cat([c.table, torch.full((6, width), -1, dtype=I32, device="cuda")], 1)[:, :max(width, 3)].contiguous()
     c.table[1] = c.table[0]                          # two requests read the same pages
     c.table[2, 1] = c.pool
     c.n_blocks[3] = 1
