@@ -59,6 +59,8 @@ constexpr int kDecTileKeys = TV_BLOCK_SIZE * kDecWarps;
 constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
 constexpr int kDecMinShare = 3;        // least cost worth a CTA of its own: a unit of one tile
 constexpr int kDecMaxCluster = 8;
+constexpr int kClusterTiles = 2;       // tiles of a CTA below which its cluster does not grow
+constexpr int kOneGridTiles = 16;      // tiles of a CTA at most in the one-launch form
 constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
 constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay below 2^24
 constexpr int kMergeWarps = 4;         // warps of a joining CTA at least
@@ -825,24 +827,23 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
-#ifndef WANT
-#define WANT 2
-#endif
-#ifndef LIM1
-#define LIM1 4
-#endif
-#ifndef LIMC
-#define LIMC 8
-#endif
 template <int kFmt, int D, int NT>
 static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) {
   using Tr = DecTraits<kFmt, D, NT>;
   constexpr size_t sums = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
   const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
   const int tiles = (p.max_blocks + kDecWarps - 1) / kDecWarps;        // of the longest request that the table holds
+  // One launch where the longest request that the table holds leaves a CTA at
+  // most kOneGridTiles tiles, in clusters of as many CTAs as fit at once (powers
+  // of two: clusters of 5 or 7 CTAs start late, 28 -> 35 us) down to kClusterTiles
+  // tiles a CTA. It saves the joining grid and a round trip, but its CTAs are as
+  // uneven as the requests. One launch against two, us: 35 heads, 287 keys 4.3 /
+  // 8.2; 8 x 512..2048 keys, bf16 14.6 / 15.8; 64 x 1000 keys, int8 28.4 / 34.9;
+  // 16 x 4000..4096 keys, 64/8 heads, int8 30.0 / 33.7; with 32 tiles a CTA it
+  // loses: 128 x 100..2048 keys, e4m3 47.8 / 41.7.
   p.cluster = 1;
-  while (p.cluster < kDecMaxCluster && p.cluster * WANT < tiles && 2ll * p.cluster * units <= grid) p.cluster *= 2;
-  if (tiles <= p.cluster * (p.cluster == 1 ? LIM1 : LIMC)) {
+  while (p.cluster < kDecMaxCluster && p.cluster * kClusterTiles < tiles && 2ll * p.cluster * units <= grid) p.cluster *= 2;
+  if (tiles <= p.cluster * kOneGridTiles) {
     constexpr size_t smem = sums + sizeof(float) * 8 * NT * D;
     static size_t smem_set[kMaxDevices] = {0};
     auto* kernel = decode_kernel<kFmt, D, NT, true>;

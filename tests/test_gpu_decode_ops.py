@@ -508,7 +508,7 @@ def test_decode_attention(hq, hkv, d, lens, held):
     alone, none, _ = run_decode(c, q, lens, with_lse=False)
     assert none is None and np.array_equal(bits(out), bits(alone))
     # a block table with room for long requests takes the other way of cutting and joining
-    wide = torch.full((len(lens), 640), -1, dtype=I32, device="cuda")
+    wide = torch.full((len(lens), 2400), -1, dtype=I32, device="cuda")
     wide[:, :c.table.shape[1]] = c.table
     c.table = wide
     out, lse, status = run_decode(c, q, lens)
@@ -583,7 +583,7 @@ def test_decode_attention_bad_page_in_a_short_table(hkv, lens, held):
     check_decode(c, q, lens, out, lse)
 
 
-@pytest.mark.parametrize("width", [3, 640])
+@pytest.mark.parametrize("width", [3, 2400])
 def test_decode_attention_shared_pages_skips_and_flags(width):
     lens = [40, 40, 33, 20, 18, 9]
     c = filled(71, lens, 2, 128, "e4m3")
