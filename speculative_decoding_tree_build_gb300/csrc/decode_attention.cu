@@ -327,7 +327,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     if (hold) {
       if (st == 0 && threadIdx.x == 0) atomicOr(p.status + b, bad);
       if (kOneGrid) {
-        iters = 0;                     // on to the cluster's barriers with nothing
+        iters = 0;                     // on to the cluster's barriers with nothing, reported once
+        bad = 0;
       } else {
         if (tile0 == 0 && p.by_unit && threadIdx.x == 0) p.begins[b * p.hkv + h] = DecBegin{0, 0, -1, 0};
         tile0 = nt;

@@ -596,6 +596,8 @@ def test_decode_attention_shared_pages_skips_and_flags(width):
     run = [40, 40, 33, 20, -1, 9]
     out, lse, st = run_decode(c, q, run, status)
     assert st == [0, 0, 8, 8, 1, 4]
+    # a flagged request is not looked at again, whatever else is wrong with it
+    assert run_decode(c, q, [40, 40, 33, 20, -1, -9], i32([0, 0, 2, 2, 2, 2]))[2] == [0, 0, 2, 2, 2, 2]
     check_decode(c, q, run, out, lse, which=[0, 1])
     assert bool((out[2:] == 9.0).all()) and bool((lse[2:] == 9.0).all())
 
