@@ -36,7 +36,7 @@
 // is computed by each CTA from seq_len, so no host round trip. A unit cut
 // between CTAs leaves one partial result a CTA in the workspace and a second
 // grid joins them in order. Where the block table is short and there are few
-// units, every unit goes to a cluster of 1 to 8 CTAs instead, which join their
+// units, every unit goes to a cluster of 1 to 8 CTAs of 4 or 8 warps instead, which join their
 // results through distributed shared memory: one launch, and one round trip
 // less ahead of the first cached row (launch_decode has the rule).
 //
@@ -59,8 +59,11 @@ constexpr int kDecTileKeys = TV_BLOCK_SIZE * kDecWarps;
 constexpr int kDecUnitCost = 2;        // fixed cost of a unit, in tiles
 constexpr int kDecMinShare = 3;        // least cost worth a CTA of its own: a unit of one tile
 constexpr int kDecMaxCluster = 8;
-constexpr int kClusterTiles = 2;       // tiles of a CTA below which its cluster does not grow
-constexpr int kOneGridTiles = 16;      // tiles of a CTA at most in the one-launch form
+constexpr int kFewWarps = 8;           // warps an SM that are few, and pages of a warp up to which a
+constexpr int kClusterPagesFew = 3;    // unit's warps are not doubled with no more than those
+constexpr int kClusterPages = 4;       // or with more
+constexpr int kOneGridPages = 16;      // pages of a warp at most in the one-launch form,
+constexpr int kOneGridExcess = 5;      // and how many more than in an even share
 constexpr int kDecMaxPerSm = 4;        // CTAs an SM at most, for the workspace
 constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay below 2^24
 constexpr int kMergeWarps = 4;         // warps of a joining CTA at least
@@ -214,20 +217,25 @@ struct DecTraits {
   // flight a warp 357 us), until the registers spill (two groups of queries,
   // D = 128: 2 CTAs 21 us, 3 CTAs 23 us).
   static constexpr int kPerSm = NT == 2 ? (D == 64 ? 3 : 2) : kRowBytes == 256 ? 3 : 4;
+  // Warps of a CTA at most in the one-launch form: two CTAs' worth where that
+  // leaves a thread its registers.
+  static constexpr int kMaxWarps = kPerSm == 4 ? 2 * kDecWarps : kDecWarps;
 };
 
-// kOneGrid: a unit belongs to a cluster of p.cluster CTAs, which take its
-// tiles in turn; else a CTA takes a share of all units' tiles.
-template <int kFmt, int D, int NT, bool kOneGrid>
-__global__ void __launch_bounds__(kDecThreads, (DecTraits<kFmt, D, NT>::kPerSm))
+// kOneGrid: a unit belongs to a cluster of p.cluster CTAs, whose kWarps warps
+// take its pages in turn; else a CTA takes a share of all units' tiles.
+template <int kFmt, int D, int NT, bool kOneGrid, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (DecTraits<kFmt, D, NT>::kPerSm * kDecWarps / kWarps))
 decode_kernel(const __grid_constant__ DecodeParams p) {
   using Tr = DecTraits<kFmt, D, NT>;
+  static_assert(kOneGrid || kWarps == kDecWarps, "a tile is a page for each warp");
   constexpr bool kHalf = Tr::kHalf;
   constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kVPieces = Tr::kVPieces, kSteps = Tr::kSteps;
   constexpr int kPages = Tr::kPages;
   constexpr int kRowPad = D + 4;
   extern __shared__ float s_o[];                               // [warps][8 NT][D + 4]
-  __shared__ float4 s_stat[kDecWarps][16];                     // (m, M, l, -)
+  constexpr int kThreads = 32 * kWarps;
+  __shared__ float4 s_stat[kWarps][16];                        // (m, M, l, -)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_launch_dependents();
   grid_dependency_wait();
@@ -293,8 +301,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     // the loads that need nothing but (b, h): status, held blocks, the first block ids, the queries
     const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
     // pages of a warp: first, first + stride, ...
-    const int stride = kOneGrid ? kDecWarps * p.cluster : kDecWarps;
-    const int first = kOneGrid ? rank * kDecWarps + warp : tile0 * kDecWarps + warp;
+    const int stride = kOneGrid ? kWarps * p.cluster : kWarps;
+    const int first = (kOneGrid ? rank : tile0) * kWarps + warp;
     int ids_first = 0;
     if (kOneGrid && first + lane * stride < p.max_blocks) ids_first = ldg_int(row + first + lane * stride);
     const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
@@ -629,20 +637,20 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     if (bad) atomicOr(p.status + b, bad);
     const bool whole = kOneGrid ? p.cluster == 1 : tile0 == 0 && tile1 == nt;
     // where the CTA's sums go: the output, its cluster's sight, or a slot of the workspace
-    float* const s_part = s_o + kDecWarps * 8 * NT * kRowPad;  // [group][D]
+    float* const s_part = s_o + kWarps * 8 * NT * kRowPad;     // [group][D]
     float* const slot = kOneGrid ? s_part : p.partials + (static_cast<size_t>(cta) * 2 + (tile0 == 0 ? 1 : 0)) * dec_slot_floats(p.group, D);
     if (!any_bad || !whole) {
-      for (int i = threadIdx.x; i < p.group * (D / 2); i += kDecThreads) {
+      for (int i = threadIdx.x; i < p.group * (D / 2); i += kThreads) {
         const int qi = i / (D / 2), d = i % (D / 2) * 2;
         float mm = kLowest, mr = kLowest, ll = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           mm = fmaxf(mm, s_stat[w][qi].x);
           mr = fmaxf(mr, s_stat[w][qi].y);
         }
         float2 acc = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int w = 0; w < kDecWarps; ++w) {
+        for (int w = 0; w < kWarps; ++w) {
           const float4 s4 = s_stat[w][qi];
           const float f = fast_exp2(s4.y - mr);
           const float2 v = *reinterpret_cast<const float2*>(s_o + (static_cast<size_t>(w) * 8 * NT + qi) * kRowPad + d);
@@ -667,7 +675,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         // the CTAs of the cluster share the output's columns and read each other's sums
         __syncwarp();
         cluster_sync_all();
-        for (int i = rank * kDecThreads + threadIdx.x; i < p.group * (D / 2); i += kDecThreads * p.cluster) {
+        for (int i = rank * kThreads + threadIdx.x; i < p.group * (D / 2); i += kThreads * p.cluster) {
           const int qi = i / (D / 2), d = i % (D / 2) * 2;
           float2 v[kDecMaxCluster], mM[kDecMaxCluster], lf[kDecMaxCluster];
 #pragma unroll
@@ -828,45 +836,70 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
+template <int kFmt, int D, int NT, int kWarps>
+static int launch_decode_one(const DecodeParams& p, int units, int dev, cudaStream_t stream) {
+  constexpr size_t smem = sizeof(float) * 8 * NT * (kWarps * (D + 4) + D);
+  static size_t smem_set[kMaxDevices] = {0};
+  auto* kernel = decode_kernel<kFmt, D, NT, true, kWarps>;
+  if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(units) * p.cluster);
+  cfg.blockDim = dim3(32 * kWarps);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+}
+
 template <int kFmt, int D, int NT>
 static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) {
   using Tr = DecTraits<kFmt, D, NT>;
   constexpr size_t sums = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
   const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
-  const int tiles = (p.max_blocks + kDecWarps - 1) / kDecWarps;        // of the longest request that the table holds
-  // One launch where the longest request that the table holds leaves a CTA at
-  // most kOneGridTiles tiles, in clusters of as many CTAs as fit at once (powers
-  // of two: clusters of 5 or 7 CTAs start late, 28 -> 35 us) down to kClusterTiles
-  // tiles a CTA. It saves the joining grid and a round trip, but its CTAs are as
-  // uneven as the requests. One launch against two, us: 35 heads, 287 keys 4.3 /
-  // 8.2; 8 x 512..2048 keys, bf16 14.6 / 15.8; 64 x 1000 keys, int8 28.4 / 34.9;
-  // 16 x 4000..4096 keys, 64/8 heads, int8 30.0 / 33.7; with 32 tiles a CTA it
-  // loses: 128 x 100..2048 keys, e4m3 47.8 / 41.7.
-  p.cluster = 1;
-  while (p.cluster < kDecMaxCluster && p.cluster * kClusterTiles < tiles && 2ll * p.cluster * units <= grid) p.cluster *= 2;
-  if (tiles <= p.cluster * kOneGridTiles) {
-    constexpr size_t smem = sums + sizeof(float) * 8 * NT * D;
-    static size_t smem_set[kMaxDevices] = {0};
-    auto* kernel = decode_kernel<kFmt, D, NT, true>;
-    if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = p.cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(units) * p.cluster);
-    cfg.blockDim = dim3(kDecThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+  const long long all_warps = static_cast<long long>(grid) * kDecWarps;
+  auto fits = [&](long long unit_warps, long long most) { return units * unit_warps <= most; };
+  // The warps of a unit in the one-launch form: doubled while the table's
+  // longest request leaves each enough pages and all fit at once (powers of
+  // two: clusters of 5 or 7 CTAs start late, 28 -> 35 us). One CTA of eight
+  // warps rather than two of four saves the cluster (296 units, 16 pages, int8:
+  // 6.7 / 8.2 us) and reaches twice the warps (12 units, 298 pages: 7.8 / 10.2),
+  // but clusters of four-warp CTAs are the lighter ones in between (128 units,
+  // 256 pages: 27.4 / 28.2). Past a few warps an SM another doubling adds loads in
+  // flight but no SM, and needs more pages to pay for its cluster (96 units, 29
+  // pages: 5.0 with 8 warps, 5.7 with 16; 15 units, 30 pages: 5.7 and 5.0).
+  int unit_warps = kDecWarps;
+  while (unit_warps < kDecMaxCluster * Tr::kMaxWarps) {
+    const int pages = unit_warps < Tr::kMaxWarps ? Tr::kPages : fits(2 * unit_warps, kFewWarps * sms) ? kClusterPagesFew : kClusterPages;
+    if (unit_warps * pages >= p.max_blocks || !fits(2 * unit_warps, all_warps)) break;
+    unit_warps *= 2;
+  }
+  const bool wide = unit_warps == Tr::kMaxWarps || unit_warps == kDecMaxCluster * Tr::kMaxWarps;
+  p.cluster = unit_warps / (wide ? Tr::kMaxWarps : kDecWarps);
+  // One launch saves the joining grid and a round trip, but its CTAs are as
+  // uneven as the requests and may leave SMs without work. So it is taken up to
+  // kOneGridPages pages a warp, kOneGridExcess of them above an even share. One
+  // launch against two, us: 35 heads, 287 keys 4.3 / 8.2; 8 x 512..2048 keys,
+  // bf16 14.6 / 15.8; 32 units, 7683 keys, int8 11.0 / 14.2; 64 x 1000 keys, int8
+  // 28.4 / 34.9; it loses with 32 pages a warp (128 x 100..2048 keys, e4m3 47.8 /
+  // 41.7) or an excess of 5.1 (16 units, 9002 keys, int8 17.2 / 15.2).
+  const long long by_unit = static_cast<long long>(units) * unit_warps;
+  if (p.max_blocks <= unit_warps * kOneGridPages &&
+      p.max_blocks * (all_warps - by_unit) <= kOneGridExcess * unit_warps * all_warps) {
+    if constexpr (Tr::kMaxWarps > kDecWarps) {
+      if (wide) return launch_decode_one<kFmt, D, NT, Tr::kMaxWarps>(p, units, dev, stream);
+    }
+    return launch_decode_one<kFmt, D, NT, kDecWarps>(p, units, dev, stream);
   }
   static size_t smem_set[kMaxDevices] = {0};
-  auto* kernel = decode_kernel<kFmt, D, NT, false>;
+  auto* kernel = decode_kernel<kFmt, D, NT, false, kDecWarps>;
   if (!ensure_smem(kernel, sums, smem_set, dev)) return TV_ERR_CUDA;
   p.by_unit = units <= grid ? 1 : 0;
   p.parts = 1;
@@ -874,8 +907,8 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
   // a unit's partials: about grid / units and both ends; eight of them a warp
   const int partials = grid / units + 2;
   while (p.parts < kMergeMaxParts && p.parts * kMergeBatch < partials) p.parts *= 2;
-  const int warps = p.parts > kMergeWarps ? p.parts : kMergeWarps, heads = warps / p.parts;
-  if (launch_pdl(decode_merge_kernel<D>, dim3(p.by_unit ? units : grid, (p.group + heads - 1) / heads), dim3(32 * warps), 0, stream, p) != cudaSuccess)
+  const int join_warps = p.parts > kMergeWarps ? p.parts : kMergeWarps, heads = join_warps / p.parts;
+  if (launch_pdl(decode_merge_kernel<D>, dim3(p.by_unit ? units : grid, (p.group + heads - 1) / heads), dim3(32 * join_warps), 0, stream, p) != cudaSuccess)
     return TV_ERR_CUDA;
   return TV_OK;
 }

@@ -583,6 +583,24 @@ def test_decode_attention_bad_page_in_a_short_table(hkv, lens, held):
     check_decode(c, q, lens, out, lse)
 
 
+@pytest.mark.parametrize("held", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("group,d", [(3, 64), (8, 128), (13, 128)])
+@pytest.mark.parametrize("pages", [4, 5, 9, 13, 25, 49, 97, 300, 400])
+def test_decode_attention_warps_of_a_request(pages, group, d, held):
+    """Tables of one length after the other at which a request gets more warps, blocks and launches."""
+    lens = [16 * pages - 3, 1, 16 * (pages // 2) + 1]
+    c = filled(103, lens, 1, d, held)
+    q = torch.randn(3, group, d, generator=gen(104), device="cuda").to(BF16)
+    out, lse, st = run_decode(c, q, lens)
+    assert st == [0, 0, 0]
+    check_decode(c, q, lens, out, lse)
+    c.table[2, pages // 2] = -1
+    out, lse, st = run_decode(c, q, lens, i32([0, 2, 0]))
+    assert st == [0, 2, 8]
+    check_decode(c, q, lens, out, lse, which=[0])
+    assert bool((out[1:] == 9.0).all()) and bool((lse[1:] == 9.0).all())
+
+
 @pytest.mark.parametrize("width", [3, 2400])
 def test_decode_attention_shared_pages_skips_and_flags(width):
     lens = [40, 40, 33, 20, 18, 9]
