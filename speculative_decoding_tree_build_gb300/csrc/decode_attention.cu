@@ -36,9 +36,9 @@
 // is computed by each CTA from seq_len, so no host round trip. A unit cut
 // between CTAs leaves one partial result a CTA in the workspace and a second
 // grid joins them in order. Where the block table is short and there are few
-// units, every unit goes to a cluster of 1 to 8 CTAs of 4 or 8 warps instead, which join their
-// results through distributed shared memory: one launch, and one round trip
-// less ahead of the first cached row (launch_decode has the rule).
+// units, every unit goes to a cluster of 1 to 8 CTAs of 4 or 8 warps instead,
+// which join their results through distributed shared memory: one launch, and one
+// round trip less ahead of the first cached row (launch_decode has the rule).
 //
 // Measured: 64 requests of 4096 to 32768 keys, 32/8 heads of 128, e4m3 (1.9
 // GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 26 us, of which the
