@@ -242,40 +242,39 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 
   __shared__ float4 s_joined[16];                              // the CTA's (m, M, l, faulty) for its cluster
   const int cta = blockIdx.x;
-  int b, h, n, nt, tile0 = 0, rank = 0, grid = 0;
-  long long hi = 0, total = 0;
+  int b, h, n, nt, tile0 = 0, rank = 0;
+  __shared__ Share s_share;            // thread 0's, for the end of a unit
+  long long hi = 0;
   long long unit = 0;                  // where the unit starts in the sequence of costs
   int mid = -1;                        // the unit whose partial this CTA leaves in slot 0
   DecBegin begun = {0, 0, -1, 0};      // the unit that it begins and does not finish
   if constexpr (kOneGrid) {
-    const int u = cta / p.cluster;
-    rank = cta - u * p.cluster;
-    b = u / p.hkv;
-    h = u - b * p.hkv;
+    rank = blockIdx.x;
+    h = blockIdx.y;
+    b = blockIdx.z;
     n = ldg_int(p.seq_len + b);
     nt = 1;
   } else {
     // ---- this CTA's share of the tiles
-    const Share sh = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int i) {
+    const Share share = find_share<kDecThreads>(p.batch, kDecMinShare, [&](int i) {
       return static_cast<long long>(p.hkv) * (kDecUnitCost + dec_tiles(p.seq_len[i], p.max_blocks));
     });
-    grid = sh.ctas;
-    hi = sh.hi;
-    total = sh.total;
-    if (sh.lo >= sh.hi) {
+    hi = share.hi;
+    if (threadIdx.x == 0) s_share = share;
+    if (share.lo >= share.hi) {
       if (threadIdx.x == 0) {
         p.mids[cta] = -1;
         if (!p.by_unit) p.begins[cta] = begun;
       }
       return;
     }
-    b = sh.b;
+    b = share.b;
     n = p.seq_len[b];
     nt = dec_tiles(n, p.max_blocks);
-    const long long cost = kDecUnitCost + nt, rel = sh.lo - sh.start;
-    h = static_cast<int>(rel / cost);
+    const long long cost = kDecUnitCost + nt, rel = share.lo - share.start;
+    h = static_cast<int>(divide(rel, cost));
     const long long off = rel - h * cost;
-    unit = sh.start + h * cost;
+    unit = share.start + h * cost;
     // tile 0 starts at 0, tile k at kDecUnitCost + k
     tile0 = off == 0 ? 0 : off <= kDecUnitCost + 1 ? 1 : static_cast<int>(off - kDecUnitCost);
   }
@@ -713,10 +712,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       mid = b * p.hkv + h;
     } else {
       DecBegin d = {b * p.hkv + h, cta, -1, 0};
-      if (!whole) {
-        // the CTA of the unit's last tile: the largest c with total * c / grid <= its start
-        const long long e = unit + kDecUnitCost + nt;
-        d.last = static_cast<int>((e * grid + total - 1) / total - 1);
+      if (!whole && threadIdx.x == 0) {
+        d.last = s_share.owner(unit + kDecUnitCost + nt - 1);  // of the unit's last tile
         begun = d;
       }
       if (p.by_unit && threadIdx.x == 0) p.begins[d.unit] = d;
@@ -837,7 +834,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
 }
 
 template <int kFmt, int D, int NT, int kWarps>
-static int launch_decode_one(const DecodeParams& p, int units, int dev, cudaStream_t stream) {
+static int launch_decode_one(const DecodeParams& p, int dev, cudaStream_t stream) {
   constexpr size_t smem = sizeof(float) * 8 * NT * (kWarps * (D + 4) + D);
   static size_t smem_set[kMaxDevices] = {0};
   auto* kernel = decode_kernel<kFmt, D, NT, true, kWarps>;
@@ -850,7 +847,7 @@ static int launch_decode_one(const DecodeParams& p, int units, int dev, cudaStre
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(units) * p.cluster);
+  cfg.gridDim = dim3(p.cluster, p.hkv, p.batch);             // (no divisions by variables in the kernel)
   cfg.blockDim = dim3(32 * kWarps);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
@@ -894,9 +891,9 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
   if (p.max_blocks <= unit_warps * kOneGridPages &&
       p.max_blocks * (all_warps - by_unit) <= kOneGridExcess * unit_warps * all_warps) {
     if constexpr (Tr::kMaxWarps > kDecWarps) {
-      if (wide) return launch_decode_one<kFmt, D, NT, Tr::kMaxWarps>(p, units, dev, stream);
+      if (wide) return launch_decode_one<kFmt, D, NT, Tr::kMaxWarps>(p, dev, stream);
     }
-    return launch_decode_one<kFmt, D, NT, kDecWarps>(p, units, dev, stream);
+    return launch_decode_one<kFmt, D, NT, kDecWarps>(p, dev, stream);
   }
   static size_t smem_set[kMaxDevices] = {0};
   auto* kernel = decode_kernel<kFmt, D, NT, false, kDecWarps>;

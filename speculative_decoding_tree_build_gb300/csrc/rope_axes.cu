@@ -19,7 +19,9 @@
 // 16201 rows of 40 heads of 128 (332 MB, 5.8 TB/s, half of it writes).
 // (Items numbered across rows, heads and columns, with divisions for each,
 // float64 for F and sincospif took 175 instructions a vector and were bound
-// by issue: 93 us for 332 MB.)
+// by issue: 93 us for 332 MB. Divisions of thread numbers by variables took a
+// tenth of a small call's time and more: 8 rows 2.3 us, now 2.1; 300 rows of 9
+// heads of 72 2.5 us, now 1.9.)
 #include "tv_common.cuh"
 
 namespace tv {
@@ -43,7 +45,7 @@ struct RopeAxParams {
   int units, rot_units;                // column units of a head; those of them that rotate
   int head_slots, row_slots;           // heads and rows that the CTA's threads take at a time
   int angle_rows;                      // rows whose angles they make at a time
-  uint32_t by_span, by_head_slots, by_pairs;          // divisors of thread numbers (rope_divisor)
+  uint32_t by_span, by_head_slots, by_pairs;          // divisors of thread numbers (thread_divisor)
   uint8_t axis[kRopeAxMaxPairs];
 };
 
@@ -56,14 +58,6 @@ __device__ __forceinline__ float rope_float(float x) { return x; }
 __device__ __forceinline__ float rope_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ void rope_round(float& y, float x) { y = x; }
 __device__ __forceinline__ void rope_round(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
-
-// n / d = n * rope_divisor(d) >> 16 for n < 256: 65536 times the quotient is
-// exceeded by at most n, and a quotient ends at least 1 / d below the next
-// integer (from d = 256 on the product stays below 65536). The compiler's
-// divisions by a variable took a fifth of a small call's time (8 rows 2.3 -> 2.1
-// us, 300 rows of 9 heads of 72 2.5 -> 1.9 us).
-static_assert(kRopeAxThreads <= 256, "rope_divisor is for thread numbers");
-static uint32_t rope_divisor(int d) { return 65536u / d + 1u; }
 
 // inv_freq as a 64-bit fraction of a turn: |inv_freq| = m 2^(e - 150) with an
 // integer m < 2^24, and 1 / 2 pi = C 2^-66, so F = m C 2^(e - 152) modulo 2^64.
@@ -314,9 +308,9 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
   p.k_out_step = p.row_slots * p.k_out_ld;
   p.groups = (p.heads + p.cta_heads - 1) / p.cta_heads;
   p.angle_rows = kRopeAxThreads / p.pairs;
-  p.by_span = rope_divisor(p.units < kRopeAxThreads ? p.units : kRopeAxThreads);
-  p.by_head_slots = rope_divisor(p.head_slots);
-  p.by_pairs = rope_divisor(p.pairs);
+  p.by_span = thread_divisor(p.units < kRopeAxThreads ? p.units : kRopeAxThreads);
+  p.by_head_slots = thread_divisor(p.head_slots);
+  p.by_pairs = thread_divisor(p.pairs);
   const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   auto* kernel = halves ? rope_axes_kernel<T, N, true, false> : rope_axes_kernel<T, N, false, false>;

@@ -53,6 +53,11 @@ inline int device_is_sm103(int dev) {
   return cache[dev] == 1 ? 1 : 0;
 }
 
+// n / d = n * thread_divisor(d) >> 16 for n < 256: 65536 times the quotient is
+// exceeded by at most n, and a quotient ends at least 1 / d below the next
+// integer (from d = 256 on the product stays below 65536).
+inline uint32_t thread_divisor(int d) { return 65536u / d + 1u; }
+
 // Raise a kernel's dynamic shared-memory limit once per device (and again
 // only if a larger size is needed).
 template <typename Kernel>

@@ -7,12 +7,29 @@
 
 namespace tv {
 
+// a / b for b > 0; in 32 bits where they fit (a 64-bit division is a routine of
+// some hundred instructions, and the shares stand ahead of all other loads).
+__device__ __forceinline__ long long divide(long long a, long long b) {
+  if ((static_cast<unsigned long long>(a) | static_cast<unsigned long long>(b)) >> 32) return a / b;
+  return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+}
+
 struct Share {
   long long lo, hi;      // the CTA's range of the sequence; lo >= hi: nothing to do
   long long total;       // the whole sequence
   long long start;       // where request b starts in it
   int b;                 // the request that holds lo
-  int ctas;              // CTAs that share the work
+  int ctas;              // CTAs that share the work: the first `longer` take each + 1 of it, the others each
+  int longer;            // (those come in the order of the SMs: longer shares strewn among the others 20.2 us, first
+                         // 19.4 us for 168 units of 8 to 69 tiles)
+  long long each;
+
+  __device__ __forceinline__ long long start_of(int cta) const { return each * cta + min(cta, longer); }
+  // the CTA that has position x of the sequence
+  __device__ __forceinline__ int owner(long long x) const {
+    const long long edge = (each + 1) * longer;
+    return static_cast<int>(x < edge ? divide(x, each + 1) : longer + divide(x - edge, each));
+  }
 };
 
 // work(b) >= 0 is request b's amount. At least `least` of it goes to a CTA.
@@ -49,8 +66,10 @@ __device__ __forceinline__ Share find_share(int batch, int least, Work work) {
   const long long most = (r.total + least - 1) / least;
   r.ctas = static_cast<int>(most < static_cast<long long>(gridDim.x) ? most : gridDim.x);
   const int cta = blockIdx.x;
-  r.lo = cta < r.ctas ? r.total * cta / r.ctas : r.total;
-  r.hi = cta < r.ctas ? r.total * (cta + 1) / r.ctas : r.total;
+  r.each = divide(r.total, max(r.ctas, 1));
+  r.longer = static_cast<int>(r.total - r.each * r.ctas);
+  r.lo = cta < r.ctas ? r.start_of(cta) : r.total;
+  r.hi = cta < r.ctas ? r.start_of(cta + 1) : r.total;
   r.b = 0;
   r.start = 0;
   if (r.lo >= r.hi) return r;
