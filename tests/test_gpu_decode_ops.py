@@ -116,6 +116,22 @@ def test_rope_axes(rows, hq, hkv, d, sections, order, pad, shift, style, dtype):
         check_rope(k, ko, pos, inv, sections, style, order)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("place", ["apart", "in place"])
+@pytest.mark.parametrize("rows,d,pairs", [
+    (3, 128, 1), (700, 64, 2), (5, 72, 4), (9, 128, 6), (600, 32, 9), (17, 80, 12), (40, 128, 46),
+    (3, 256, 63), (9, 72, 36), (200, 96, 47), (4, 512, 254), (6, 512, 3),
+])
+def test_rope_axes_halves_of_any_length(rows, d, pairs, place, dtype):
+    """The second half starts inside a vector, and the columns left alone may too."""
+    g, q, k, pos, inv = rope_case(14, rows, 5, 2, d, [pairs], 1, 0, dtype, 5000, 64, 0, True)
+    q0, k0 = q.clone(), k.clone()
+    qo, ko = (q, k) if place == "in place" else (torch.full_like(q0, 7.0), torch.full_like(k0, 7.0))
+    tv.rope_axes(g, q, k, pos, inv, qo, ko)
+    check_rope(q0, qo, pos, inv, [pairs], 1, 0)
+    check_rope(k0, ko, pos, inv, [pairs], 1, 0)
+
+
 @pytest.mark.parametrize("style", [0, 1])
 def test_rope_axes_far_negative_and_in_place(style):
     g, q, k, pos, inv = rope_case(12, 40, 4, 2, 64, [12, 10, 10], style, 1, F32, 2 ** 31 - 1, 64, 0, True)
