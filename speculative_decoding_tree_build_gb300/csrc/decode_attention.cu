@@ -238,7 +238,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   __shared__ float4 s_stat[kWarps][16];                        // (m, M, l, -)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
   grid_launch_dependents();
-  grid_dependency_wait();
+  if (!kOneGrid) grid_dependency_wait();
 
   __shared__ float4 s_joined[16];                              // the CTA's (m, M, l, faulty) for its cluster
   const int cta = blockIdx.x;
@@ -252,7 +252,6 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     rank = blockIdx.x;
     h = blockIdx.y;
     b = blockIdx.z;
-    n = ldg_int(p.seq_len + b);
     nt = 1;
   } else {
     // ---- this CTA's share of the tiles
@@ -302,6 +301,15 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     // pages of a warp: first, first + stride, ...
     const int stride = kOneGrid ? kWarps * p.cluster : kWarps;
     const int first = (kOneGrid ? rank : tile0) * kWarps + warp;
+    // queries: the thread's columns of query g (and g + 8), as MMA operands
+    const __nv_bfloat16* q_row[NT];
+#pragma unroll
+    for (int x = 0; x < NT; ++x)
+      q_row[x] = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + min(x * 8 + g, p.group - 1)) * D;
+    if (kOneGrid) {                    // (all of the above while the grid before this one ends)
+      grid_dependency_wait();
+      n = ldg_int(p.seq_len + b);
+    }
     int ids_first = 0;
     if (kOneGrid && first + lane * stride < p.max_blocks) ids_first = ldg_int(row + first + lane * stride);
     const bool fits = n >= 0 && n <= static_cast<long long>(p.max_blocks) * TV_BLOCK_SIZE;
@@ -312,17 +320,14 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     if (!kOneGrid) ids_first = fetch_ids(0);
     const int st = *const_cast<volatile int32_t*>(p.status + b), held = min(ldg_int(p.n_blocks + b), p.max_blocks);
 
-    // ---- queries: the thread's columns of query g (and g + 8), as MMA operands
     uint32_t qf[NT][kSteps][2];
     float fac[NT][2];                  // score factor of queries 2t and 2t + 1
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      const int qi = x * 8 + g;
-      const __nv_bfloat16* src = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + min(qi, p.group - 1)) * D;
 #pragma unroll
       for (int s = 0; s < kSteps; s += 2) {
         // 8 values: bf16 pieces t + 4 c of the row, or half a 16-value piece
-        const uint4 w = ldg_stream(kHalf ? src + (t + 4 * (s / 4)) * 16 + 4 * (s % 4) : src + (t + 2 * s) * 8);
+        const uint4 w = ldg_stream(kHalf ? q_row[x] + (t + 4 * (s / 4)) * 16 + 4 * (s % 4) : q_row[x] + (t + 2 * s) * 8);
         qf[x][s][0] = w.x; qf[x][s][1] = w.y;
         qf[x][s + 1][0] = w.z; qf[x][s + 1][1] = w.w;
       }
@@ -738,10 +743,10 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   __shared__ float s_acc[kMergeMaxParts][D];
   __shared__ float4 s_stat[kMergeMaxParts];
   grid_launch_dependents();
-  grid_dependency_wait();
-  const DecBegin task = p.begins[blockIdx.x];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, warps = blockDim.x / 32;
   const int part = warp % p.parts, qi = blockIdx.y * (warps / p.parts) + warp / p.parts;
+  grid_dependency_wait();
+  const DecBegin task = p.begins[blockIdx.x];
   if (task.last < 0) return;
   const int b = task.unit / p.hkv, h = task.unit - b * p.hkv;
   const bool live = qi < p.group;

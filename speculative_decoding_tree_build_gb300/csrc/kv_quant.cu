@@ -64,7 +64,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
   __shared__ int s_cross[2][4];        // requests that reach past the CTA's rows, before and behind:
                                        // request, first page, pages, first row of the run
   grid_launch_dependents();
-  grid_dependency_wait();
   const int t0 = blockIdx.x * p.cta_rows;
   const int nrows = min(p.cta_rows, p.rows - t0), t1 = t0 + nrows;
   const int part = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
@@ -82,6 +81,10 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
     if (i < p.batch) q = Request{p.cu_rows[i], p.cu_rows[i + 1], *const_cast<volatile int32_t*>(p.status + i), p.start_len[i], min(p.n_blocks[i], p.max_blocks)};
     return q;
   };
+  if (threadIdx.x < kAppendMaxRows) s_bad[threadIdx.x] = 0;
+  if (threadIdx.x < kAppendMaxRows / 32) s_heads[threadIdx.x] = 0u;
+  if (threadIdx.x < 8) s_cross[threadIdx.x / 4][threadIdx.x % 4] = 0;
+  grid_dependency_wait();              // (all of the above while the grid before this one ends)
   Request q = look_at(threadIdx.x);
   uint4 x[kAppendAhead][2];            // a warp's loads cover whole sectors: piece lane, piece lane + kLanes
   auto load = [&](uint4 (&to)[2], int r) {
@@ -95,9 +98,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
 #pragma unroll
   for (int e = 0; e < kAppendAhead; ++e) load(x[e], slot0 + e * p.slots);    // on their way while slots are found
 
-  if (threadIdx.x < kAppendMaxRows) s_bad[threadIdx.x] = 0;
-  if (threadIdx.x < kAppendMaxRows / 32) s_heads[threadIdx.x] = 0u;
-  if (threadIdx.x < 8) s_cross[threadIdx.x / 4][threadIdx.x % 4] = 0;
   __syncthreads();
   // the CTA's rows that each request owns
   for (int i = threadIdx.x; i < p.batch; i += kAppendThreads, q = look_at(i)) {

@@ -19,9 +19,10 @@
 // 16201 rows of 40 heads of 128 (332 MB, 5.8 TB/s, half of it writes).
 // (Items numbered across rows, heads and columns, with divisions for each,
 // float64 for F and sincospif took 175 instructions a vector and were bound
-// by issue: 93 us for 332 MB. Divisions of thread numbers by variables took a
-// tenth of a small call's time and more: 8 rows 2.3 us, now 2.1; 300 rows of 9
-// heads of 72 2.5 us, now 1.9.)
+// by issue: 93 us for 332 MB. A small call's time went into divisions of thread
+// numbers by variables, and into working out the layout behind the wait for the
+// grid before: 8 rows 2.3 us, 2.1 with multiplications, 1.8 with that ahead of
+// the wait.)
 #include "tv_common.cuh"
 
 namespace tv {
@@ -145,7 +146,6 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   using Vec = RopeVec<T, N>;
   __shared__ __align__(16) float2 s_cs[kRopeAxAngles];
   grid_launch_dependents();
-  grid_dependency_wait();
   const int block = p.groups == 1 ? blockIdx.x : blockIdx.x / p.groups, group = blockIdx.x - block * p.groups;
   const int row0 = block * p.cta_rows, nrows = min(p.cta_rows, p.rows - row0);
   const int head_end = min(p.heads, (group + 1) * p.cta_heads);
@@ -202,14 +202,13 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   const int32_t* position = p.positions + p.axis[turning ? pr : 0] * p.pos_ld + row0;
   float inv_freq = 0.0f;
   int pos = 0;
+  if (at_work) point();
+  grid_dependency_wait();              // (all of the above while the grid before this one ends)
   if (turning) {
     inv_freq = *const_cast<const volatile float*>(p.inv_freq + pr);
     pos = *const_cast<const volatile int32_t*>(position + r0);
   }
-  if (at_work) {
-    point();
-    load();
-  }
+  if (at_work) load();
   if (turning) {
     const unsigned long long f = rope_turns(inv_freq);
     s_cs[r0 * p.pairs + pr] = rope_cos_sin(pos, f);
