@@ -41,7 +41,7 @@
 // round trip less ahead of the first cached row (launch_decode has the rule).
 //
 // Measured: 64 requests of 4096 to 32768 keys, 32/8 heads of 128, e4m3 (1.9
-// GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 26 us, of which the
+// GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 28 us, of which the
 // first grid 20.
 #include <cuda_fp16.h>
 

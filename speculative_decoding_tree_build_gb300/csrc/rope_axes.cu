@@ -23,6 +23,8 @@
 // numbers by variables, and into working out the layout behind the wait for the
 // grid before: 8 rows 2.3 us, 2.1 with multiplications, 1.8 with that ahead of
 // the wait.)
+#include <cstring>
+
 #include "tv_common.cuh"
 
 namespace tv {
@@ -261,7 +263,7 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
 }
 
 template <typename T, int N>
-static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t stream) {
+static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t stream) {
   const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
   p.rot_units = (p.pairs + per_unit - 1) / per_unit;
   p.units = halves || N == 1 ? p.rot_units + (p.d - 2 * p.pairs) / N : p.d / N;
@@ -322,7 +324,7 @@ static cudaError_t launch_rope_axes(RopeAxParams p, bool halves, cudaStream_t st
 // The widest vector (16, 8 or 4 bytes, else single elements) that the addresses,
 // strides, head dimension and, for pairs of two halves, the pairs allow.
 template <typename T>
-static cudaError_t launch_rope_axes_any(const RopeAxParams& p, bool halves, bool keys, cudaStream_t stream) {
+static cudaError_t launch_rope_axes_any(RopeAxParams& p, bool halves, bool keys, cudaStream_t stream) {
   auto fits = [&](int n) {
     const uintptr_t bytes = n * sizeof(T);
     return p.d % n == 0 && (!halves || p.pairs % n == 0) && p.q_ld % n == 0 && p.q_out_ld % n == 0 && aligned(p.q, bytes) &&
@@ -371,15 +373,17 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
   p.q = q; p.k = k; p.positions = positions; p.inv_freq = inv_freq; p.q_out = q_out; p.k_out = k_out;
   p.q_ld = q_ld; p.k_ld = k_ld; p.q_out_ld = q_out_ld; p.k_out_ld = k_out_ld; p.pos_ld = pos_ld;
   p.rows = rows; p.hq = g->num_q_heads; p.heads = g->num_q_heads + g->num_kv_heads; p.d = g->head_dim; p.pairs = pairs;
-  int left[TV_MAX_ROPE_AXES] = {0};
-  for (int a = 0; a < g->num_axes; ++a) left[a] = g->section[a];
-  for (int i = 0, a = 0; i < pairs;) {
-    if (left[a] > 0) {
-      p.axis[i++] = static_cast<uint8_t>(a);
-      --left[a];
-      if (g->section_order == 1) a = (a + 1) % g->num_axes;
-    } else {
-      a = (a + 1) % g->num_axes;
+  if (g->section_order == 0) {
+    for (int i = 0, a = 0; a < g->num_axes; i += g->section[a++]) memset(p.axis + i, a, g->section[a]);
+  } else {
+    int left[TV_MAX_ROPE_AXES] = {0};
+    for (int a = 0; a < g->num_axes; ++a) left[a] = g->section[a];
+    for (int i = 0; i < pairs;) {
+      for (int a = 0; a < g->num_axes; ++a) {
+        if (left[a] == 0) continue;
+        p.axis[i++] = static_cast<uint8_t>(a);
+        --left[a];
+      }
     }
   }
   const bool halves = g->rope_style == 1;
