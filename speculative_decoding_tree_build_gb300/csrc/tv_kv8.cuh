@@ -12,8 +12,7 @@ constexpr int kKvMaxBatch = 4096;
 // What a row's codes are made from: its scale and the factors of its values.
 struct KvRowScale {
   float scale;   // stored beside the codes; NaN when the row is not finite
-  float mul;     // e4m3: 1 / scale; int8: 1 / largest magnitude; 0: all codes are 0
-  float top;     // int8: the largest magnitude, at least 2^-100
+  float mul;     // e4m3: 1 / scale; int8: 127 / largest magnitude; 0: all codes are 0
 };
 
 // `top` = largest magnitude of the row's bf16 values as bits 14..0 of bf16.
@@ -29,11 +28,10 @@ __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
     n = max(n, -100);
     r.scale = __uint_as_float(static_cast<uint32_t>(n + 127) << 23);
     r.mul = __uint_as_float(static_cast<uint32_t>(127 - n) << 23);   // n <= 120: exact, as is x * mul
-    r.top = 0.0f;
   } else {
-    r.top = fmaxf(__uint_as_float(top << 16), 7.888609052210118e-31f);         // 2^-100
-    r.scale = __fdiv_rn(r.top, 127.0f);
-    r.mul = __frcp_rn(r.top);
+    const float largest = fmaxf(__uint_as_float(top << 16), 7.888609052210118e-31f);     // 2^-100
+    r.scale = __fdiv_rn(largest, 127.0f);
+    r.mul = __fdiv_rn(127.0f, largest);
   }
   if (top >= 0x7f80u) {
     r.scale = __uint_as_float(0x7fc00000u);
@@ -42,17 +40,17 @@ __device__ __forceinline__ KvRowScale kv_row_scale(uint32_t top) {
   return r;
 }
 
-// The int8 code of x in the low byte: 127 x / top to the nearest integer. The
-// product 127 x is exact (15 bits), and one Newton step from the reciprocal
-// leaves the quotient within 2^-24 of itself, exactly where it is a float32
-// number - so exactly at ties, integers and a half. Any other quotient of two
-// bf16 numbers, 127 X / (A 2^k) with X, A < 2^8, is 1 / (254 X) > 2^-16 of
-// itself away from the nearest tie and rounds the way the exact one does.
+// The int8 code of x in the low byte: the exact quotient q = 127 x / top to the
+// nearest integer, ties to even. mul is 127 / top within 2^-24 of itself, so x mul
+// is within |q| 2^-24 < 2^-17 of q; the sum with 384, rounded once, lies in [256,
+// 512), where float32 has steps of 2^-15. A q that ends in exactly a half, or an
+// integer, is a step, so the sum lands on it. Any other q = 127 X 2^s / A (X, A <
+// 2^8) lies at least 2^s / A = |q| / (127 X) from the nearest half, which is 1.543
+// 10^-5 or more next to 0.5 and three times that next to 1.5; half a step and the
+// error of x mul there are 1.529 10^-5, so it stays on its side. The second sum is
+// exact up to its rounding to an integer.
 __device__ __forceinline__ uint32_t kv_int8_code(float x, const KvRowScale& r) {
-  const float n = 127.0f * x;
-  const float q = n * r.mul;
-  const float y = fmaf(fmaf(-q, r.top, n), r.mul, q);
-  return __float_as_uint(__fadd_rn(y, 12582912.0f));                 // 1.5 * 2^23: rounds to an integer
+  return __float_as_uint(__fadd_rn(fmaf(x, r.mul, 384.0f), 12582912.0f - 384.0f));   // 1.5 * 2^23 + q
 }
 
 // (x.x * f, x.y * f) in one instruction, each rounded as on its own.
@@ -67,8 +65,8 @@ __device__ __forceinline__ float2 mul_both(float2 x, float f) {
   return r;
 }
 
-// Four values (two bf16 pairs) to four codes. (Paired instructions take 3 % off
-// an e4m3 append of 16 to 26 MB; the int8 codes are slower with them.)
+// Four values (two bf16 pairs) to four codes. (The paired product takes 3 % off an
+// e4m3 append of 16 to 26 MB.)
 template <int kFmt>
 __device__ __forceinline__ uint32_t kv_encode4(uint32_t a, uint32_t b, const KvRowScale& r) {
   if constexpr (kFmt == TV_KV_E4M3) {
@@ -76,16 +74,8 @@ __device__ __forceinline__ uint32_t kv_encode4(uint32_t a, uint32_t b, const KvR
     const uint32_t hi = __nv_cvt_float2_to_fp8x2(mul_both(make_float2(bf16_lo(b), bf16_hi(b)), r.mul), __NV_SATFINITE, __NV_E4M3);
     return lo | (hi << 16);
   } else {
-    KvRowScale s = r;
-    float x[4] = {bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b)};
-    if (r.top > 1e30f) {               // 127 x must not overflow: the quotient of both by 2^20, exactly
-      s.top *= 9.5367431640625e-07f;
-      s.mul *= 1048576.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= 9.5367431640625e-07f;
-    }
-    const uint32_t lo = __byte_perm(kv_int8_code(x[0], s), kv_int8_code(x[1], s), 0x0040);
-    const uint32_t hi = __byte_perm(kv_int8_code(x[2], s), kv_int8_code(x[3], s), 0x0040);
+    const uint32_t lo = __byte_perm(kv_int8_code(bf16_lo(a), r), kv_int8_code(bf16_hi(a), r), 0x0040);
+    const uint32_t hi = __byte_perm(kv_int8_code(bf16_lo(b), r), kv_int8_code(bf16_hi(b), r), 0x0040);
     return __byte_perm(lo, hi, 0x5410);
   }
 }
