@@ -13,7 +13,7 @@
 // Memory bound: every value is read and written once, 6 float operations a
 // pair. One CTA rotates a few rows (or some heads of one row); the sines and
 // cosines of a row are computed once in shared memory. A thread keeps the same
-// columns and the same (at most four) heads of every row it takes, so it
+// columns and the same (at most four or eight) heads of every row it takes, so it
 // reads a row's sines once into registers and steps its pointers by a fixed
 // stride; its first vectors are in flight while the angles are made. 57 us for
 // 16201 rows of 40 heads of 128 (332 MB, 5.8 TB/s, half of it writes).
@@ -32,7 +32,8 @@ namespace tv {
 constexpr int kRopeAxThreads = 256;
 constexpr int kRopeAxMaxPairs = 256;
 constexpr int kRopeAxAngles = 2048;    // rows x pairs of a CTA at most
-constexpr int kRopeAxBatch = 4;        // heads of a row that a thread takes at most
+constexpr int kRopeAxBatch = 4;        // heads of a row that a thread takes at most,
+constexpr int kRopeAxNarrow = 8;       // and with vectors of 4 or 8 bytes, of rows with more heads than that
 
 struct RopeAxParams {
   const void* q;
@@ -138,8 +139,9 @@ __device__ __forceinline__ void rope_turn_bf16(RopeVec<__nv_bfloat16, N>& va, Ro
 
 // T: element, N: elements of a vector, kHalves: rotary style 1 (a pair's two
 // columns lie in two vectors; else N = 1 or both are in one vector), kEdge:
-// the rotated columns end inside a vector (where both are in one).
-template <typename T, int N, bool kHalves, bool kEdge>
+// the rotated columns end inside a vector (where both are in one), kBatch: heads
+// of a row that a thread takes at most.
+template <typename T, int N, bool kHalves, bool kEdge, int kBatch>
 __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_kernel(const __grid_constant__ RopeAxParams p) {
   // pairs of a unit, and whether it holds a second vector
   constexpr int P = kHalves ? N : (N == 1 ? 1 : N / 2);
@@ -168,13 +170,13 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
       cb = ca;
     }
   };
-  Vec va[kRopeAxBatch], vb[kRopeAxBatch];
+  Vec va[kBatch], vb[kBatch];
   // the row's heads of q and of k, and the thread's heads in them
   const T *qs, *ks;
   T *qd, *kd;
-  int off[kRopeAxBatch];
+  int off[kBatch];
 #pragma unroll
-  for (int e = 0; e < kRopeAxBatch; ++e) {
+  for (int e = 0; e < kBatch; ++e) {
     const int h = head0 + e * p.head_slots;
     off[e] = (h < p.hq ? h : h - p.hq) * p.d;
   }
@@ -190,7 +192,7 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   };
   auto load = [&]() {
 #pragma unroll
-    for (int e = 0; e < kRopeAxBatch; ++e) {
+    for (int e = 0; e < kBatch; ++e) {
       if (head0 + e * p.head_slots >= head_end) break;
       const T* src = (is_q(e) ? qs : ks) + off[e];
       va[e] = *reinterpret_cast<const Vec*>(src + ca);
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
         for (int j = 0; j < P; ++j) cs[j] = s_cs[kEdge ? min(r * p.pairs + u * P + j, kRopeAxAngles - 1) : r * p.pairs + u * P + j];
       }
 #pragma unroll
-      for (int e = 0; e < kRopeAxBatch; ++e) {
+      for (int e = 0; e < kBatch; ++e) {
         if (head0 + e * p.head_slots >= head_end) break;
         if (turns) {
           if (kPacked && (!kEdge || u * P + P <= p.pairs)) {
@@ -262,8 +264,8 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
   }
 }
 
-template <typename T, int N>
-static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t stream) {
+template <typename T, int N, int kBatch>
+static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStream_t stream) {
   const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
   p.rot_units = (p.pairs + per_unit - 1) / per_unit;
   p.units = halves || N == 1 ? p.rot_units + (p.d - 2 * p.pairs) / N : p.d / N;
@@ -286,13 +288,13 @@ static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t s
   p.cta_rows = p.row_slots;
   const long long sweeps = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>((p.heads + p.cta_heads - 1) / p.cta_heads);
   if (per >= kRopeAxThreads || sweeps > 152 * 4) {
-    p.cta_heads = p.heads < kRopeAxBatch * slots ? p.heads : kRopeAxBatch * slots;
+    p.cta_heads = p.heads < kBatch * slots ? p.heads : kBatch * slots;
     const long long items = static_cast<long long>(p.cta_heads) * p.units;
     // (twenty narrow vectors: 10181 rows of 26 heads with 50 pairs, float32, 63.5 -> 55.3 us; single elements not)
     constexpr long long kMost = (N > 1 && N * sizeof(T) < 16 ? 20ll : 10ll) * kRopeAxThreads;
     long long rows = (per > kMost ? kMost : per) / items;
     int best = 0;
-    for (int k = 1; k <= kRopeAxBatch; ++k) {
+    for (int k = 1; k <= kBatch; ++k) {
       const int hs = (p.cta_heads + k - 1) / k;
       if (hs > slots) continue;
       // threads at work, in sixteenths of a slot; of two equals the one with more loads in flight a
@@ -319,11 +321,23 @@ static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t s
   p.by_pairs = thread_divisor(p.pairs);
   const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  auto* kernel = halves ? rope_axes_kernel<T, N, true, false> : rope_axes_kernel<T, N, false, false>;
+  auto* kernel = halves ? rope_axes_kernel<T, N, true, false, kBatch> : rope_axes_kernel<T, N, false, false, kBatch>;
   if constexpr (N > 1) {
-    if (!halves && 2 * p.pairs % N != 0) kernel = rope_axes_kernel<T, N, false, true>;
+    if (!halves && 2 * p.pairs % N != 0) kernel = rope_axes_kernel<T, N, false, true, kBatch>;
   }
   return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kRopeAxThreads), 0, stream, p);
+}
+
+// Narrow vectors leave little in flight with four heads a thread: with eight, 16
+// heads with 59 pairs, float32, 18602 rows 85 -> 73 us, 26 heads with 50 pairs 55
+// -> 49 us. With few heads there is nothing to gain (2 + 2 heads with 41 pairs 23 ->
+// 26 us), nor with single bf16 values (32 heads with 63 pairs 23 -> 29 us).
+template <typename T, int N>
+static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t stream) {
+  if constexpr (N * sizeof(T) == 4 || N * sizeof(T) == 8) {
+    if (p.heads > kRopeAxNarrow) return launch_rope_axes_with<T, N, kRopeAxNarrow>(p, halves, stream);
+  }
+  return launch_rope_axes_with<T, N, kRopeAxBatch>(p, halves, stream);
 }
 
 // The widest vector (16, 8 or 4 bytes, else single elements) that the addresses,
