@@ -182,16 +182,28 @@ int32_t count(int64_t n, const char* name) {
   return static_cast<int32_t>(n);
 }
 
-// Run the call with the tensors' device current and without the interpreter's lock.
+// The interpreter's lock, let go for a scope (an exception takes it back too).
+class Unlocked {
+ public:
+  Unlocked() : state_(PyEval_SaveThread()) {}
+  ~Unlocked() { PyEval_RestoreThread(state_); }
+  Unlocked(const Unlocked&) = delete;
+  Unlocked& operator=(const Unlocked&) = delete;
+
+ private:
+  PyThreadState* state_;
+};
+
+// Run the call with the tensors' device current and without the interpreter's
+// lock. What can be refused is refused before: the call itself only returns codes.
 template <typename F>
 PyObject* launch(const Call& c, PyObject* stream, F f) {
   void* s = stream_of(stream, c.device());
   int rc;
   {
     const c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(c.device()));
-    PyThreadState* state = PyEval_SaveThread();
+    const Unlocked unlocked;
     rc = f(s);
-    PyEval_RestoreThread(state);
   }
   return PyLong_FromLong(rc);
 }
@@ -232,8 +244,9 @@ PyObject* rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
     for (int i = 0; i < g.num_axes && i < TV_MAX_ROPE_AXES; ++i) pairs += g.section[i];
     const Tensor& inv = c.typed(4, ScalarType::Float, "inv_freq");
     if (inv.numel() != pairs || !inv.is_contiguous()) refuse("inv_freq must hold one frequency per rotated pair");
+    const int32_t rows = count(q.rows, "rows");
     return launch(c, a[7], [&](void* s) {
-      return tv_rope_axes(&g, count(q.rows, "rows"), q.type == ScalarType::Float ? TV_DTYPE_F32 : TV_DTYPE_BF16, q.ptr, q.ld,
+      return tv_rope_axes(&g, rows, q.type == ScalarType::Float ? TV_DTYPE_F32 : TV_DTYPE_BF16, q.ptr, q.ld,
                           k.ptr, k.ld, pos.data_ptr<int32_t>(), g.num_axes > 1 ? pos.stride(0) : q.rows,
                           inv.data_ptr<float>(), qo.ptr, qo.ld, ko.ptr, ko.ld, s);
     });
@@ -256,9 +269,10 @@ PyObject* kv_quant_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t* held = c.ints(6, "n_blocks", batch);
     const Pools p = pools_of(c, g, 7, 9);
     int32_t* status = const_cast<int32_t*>(c.ints(11, "status", batch));
+    const int32_t requests = count(batch, "batch"), rows = count(k.rows, "rows");
     return launch(c, a[12], [&](void* s) {
-      return tv_kv_quant_append(&g, p.format, count(batch, "batch"), count(k.rows, "rows"), k.ptr, v.ptr, k.ld, cu, start, t.ptr,
-                                held, t.width, p.k, p.v, p.ks, p.vs, p.blocks, status, s);
+      return tv_kv_quant_append(&g, p.format, requests, rows, k.ptr, v.ptr, k.ld, cu, start, t.ptr, held,
+                                t.width, p.k, p.v, p.ks, p.vs, p.blocks, status, s);
     });
   });
 }
@@ -280,8 +294,9 @@ PyObject* kv_quant_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Pools out = pools_of(c, g, 11, -1);
     if (out.format != TV_KV_BF16) refuse("k_out and v_out must be bfloat16 pools");
     int32_t* status = const_cast<int32_t*>(c.ints(13, "status", batch));
+    const int32_t requests = count(batch, "batch");
     return launch(c, a[14], [&](void* s) {
-      return tv_kv_quant_read(&g, p.format, count(batch, "batch"), first, last, t.ptr, held, t.width, p.k, p.v, p.ks, p.vs,
+      return tv_kv_quant_read(&g, p.format, requests, first, last, t.ptr, held, t.width, p.k, p.v, p.ks, p.vs,
                               p.blocks, to.ptr, to_held, to.width, out.k, out.v, out.blocks, status, s);
     });
   });
@@ -307,8 +322,9 @@ PyObject* decode_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& ws = c.tensor(11, "workspace");
     if (!ws.is_contiguous()) refuse("workspace must be contiguous");
     int32_t* status = const_cast<int32_t*>(c.ints(12, "status", batch));
+    const int32_t requests = count(batch, "batch");
     return launch(c, a[13], [&](void* s) {
-      return tv_decode_attention(&g, p.format, count(batch, "batch"), q.ptr, q.ld, len, t.ptr, held, t.width, p.k, p.v, p.ks,
+      return tv_decode_attention(&g, p.format, requests, q.ptr, q.ld, len, t.ptr, held, t.width, p.k, p.v, p.ks,
                                  p.vs, p.blocks, out, lse, ws.data_ptr(), ws.nbytes(), status, s);
     });
   });
