@@ -669,7 +669,12 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  *   lse = log sum_j exp(s_j)
  * with k_j, v_j the cached values (code * scale for 8-bit pools). Scores, the
  * softmax and its sums are float32. A request without keys (seq_len 0) gets
- * out = 0 and lse = -inf. Slots from seq_len[b] on may hold anything. The
+ * out = 0 and lse = -inf. Slots from seq_len[b] on may hold anything.
+ * Infinities and NaN act as in the formula: an infinite value of a bf16 pool
+ * reaches the output (beside a weight below 2^-126 of the largest, which is 0
+ * in float32, it makes a NaN), a score of -inf has no weight, a score of +inf or
+ * NaN makes the query's out and lse NaN. Weighted sums are float32 before they
+ * are divided: over bf16 pools |v| * keys has to stay below 2^120. The
  * result does not depend on timing: the split over the cache's length is a
  * function of the arguments, and its parts are joined in a fixed order.
  *

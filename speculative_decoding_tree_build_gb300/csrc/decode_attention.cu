@@ -157,6 +157,16 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What a weight w >= 0 cut off to the bf16 number h leaves, never 0 beside an h
+// above 0: two positive parts carry an infinite value to the output, where a
+// second part of 0 or below would make inf * 0 or inf - inf of it. It is taken as
+// 2^-24 of h (float32's own rounding) at least, and as the smallest bf16 number
+// where that underflows. The parts miss w by 2^-16 of it at the most: the rest is
+// below 2^-7 of w's power of two and is rounded to 8 bits.
+__device__ __forceinline__ float weight_rest(float w, float h) {
+  return fmaxf(fmaxf(w - h, h * 0x1p-24f), fminf(h, 0x1p-133f));
+}
+
 // Four codes of a word to two f16x2: (byte 0, byte 1) and (byte 2, byte 3).
 template <int kFmt>
 __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -556,7 +566,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       for (int pg = 0; pg < kPages; ++pg) {
         // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8). Beside
         // bf16 values they have to be bf16 too, and go in two parts: with one, their rounding would
-        // add as much to the error as the output's own does.
+        // add as much to the error as the output's own does (weight_rest).
         uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -572,9 +582,13 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            const uint32_t hi = kHalf ? pack_half2(w[2 * u], w[2 * u + 1]) : pack_bf16x2(w[2 * u], w[2 * u + 1]);
-            pf[x][u] = transpose8x8(hi);
-            if (!kHalf) pl[x][u] = transpose8x8(pack_bf16x2(w[2 * u] - bf16_lo(hi), w[2 * u + 1] - bf16_hi(hi)));
+            if constexpr (kHalf) {
+              pf[x][u] = transpose8x8(pack_half2(w[2 * u], w[2 * u + 1]));
+            } else {
+              const uint32_t hi = __byte_perm(__float_as_uint(w[2 * u]), __float_as_uint(w[2 * u + 1]), 0x7632);
+              pf[x][u] = transpose8x8(hi);
+              pl[x][u] = transpose8x8(pack_bf16x2(weight_rest(w[2 * u], bf16_lo(hi)), weight_rest(w[2 * u + 1], bf16_hi(hi))));
+            }
           }
         }
         if (tail) {                    // rows past the end may hold anything, NaN among it

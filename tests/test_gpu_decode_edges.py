@@ -53,3 +53,139 @@ tv.rope_axes(tv.rope_axes_geom(1, 0, 2, [1]), q, None, torch.zeros(1, 1, dtype=t
 print("and again", q.flatten().tolist())
 """ % call)
     assert "refused:" in said and "out of range" in said and "and again [1.0, 1.0]" in said
+
+
+# ---------------------------------------------------------------- one-token attention: values that are not finite
+
+
+def widened(c, width):
+    """The same cache behind a block table of `width` pages (many take the form of two launches)."""
+    if width > c.table.shape[1]:
+        wide = torch.full((c.table.shape[0], width), -1, dtype=I32, device="cuda")
+        wide[:, :c.table.shape[1]] = c.table
+        c.table = wide
+    return c
+
+
+def put_values(c, b, row, pool, values):
+    """values: {column: value} of one cached row, all heads, of a bf16 pool."""
+    page, at = c.at(b, [row])
+    for col, x in values.items():
+        pool[page, :, at, col] = x
+
+
+def check_special(c, q, lens, out, lse):
+    """As base.check_decode, but infinities and NaN have to be where the definition has them."""
+    with np.errstate(invalid="ignore"):
+        for b, n in enumerate(lens):
+            k, v = c.rows(b, n)
+            want, wl, tol, ltol = base.decode_tolerance(base.f64(q[b]), k, v, q.shape[2] ** -0.5, c.held,
+                                                        c.value_scales(b, n))
+            got, gl = base.f64(out[b]), base.f64(lse[b])
+            fin = np.isfinite(want)
+            assert np.array_equal(np.isnan(got), np.isnan(want)), b
+            assert np.array_equal(np.isposinf(got), np.isposinf(want)) and np.array_equal(np.isneginf(got), np.isneginf(want)), b
+            assert np.all(np.abs(got - want)[fin] <= tol[fin]), b
+            fin = np.isfinite(wl)
+            assert np.array_equal(np.isnan(gl), np.isnan(wl)) and np.all(np.abs(gl - wl)[fin] <= ltol[fin]), b
+
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 64), (8, 2, 128), (24, 2, 128), (9, 1, 64)])
+def test_infinite_values_reach_the_output(hq, hkv, d, width):
+    """Infinities and NaN of a bf16 value pool, beside weights of every kind: exactly 1 (one key),
+    rounded up and rounded down; in the last, a middle and the first row."""
+    lens = [1, 2, 16, 17, 40, 300, 1200]
+    c = widened(base.filled(201, lens, hkv, d, "bf16"), width)
+    q = torch.randn(len(lens), hq, d, generator=base.gen(202), device="cuda").to(BF16)
+    for b, n in enumerate(lens):
+        put_values(c, b, n - 1, c.v, {3: INF, 7: -INF, 11: INF, 13: NAN})
+        put_values(c, b, n // 2, c.v, {5: INF, d - 1: -INF, 11: -INF if n > 1 else INF})
+        put_values(c, b, 0, c.v, {20: INF, 21: 3e38, 22: -INF})
+    out, lse, status = base.run_decode(c, q, lens)
+    assert status == [0] * len(lens)
+    assert bool(torch.isposinf(out[:, :, [3, 5, 20]]).all()) and bool(torch.isneginf(out[:, :, [7, 22, d - 1]]).all())
+    check_special(c, q, lens, out, lse)
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+def test_scores_that_are_not_finite(width):
+    """bf16 keys: a score of -inf has no weight, one of +inf or NaN makes the query's output NaN, and
+    no other query's, head's or request's. A query that is not finite spoils itself alone."""
+    lens, hkv, d = [1, 33, 700, 50], 2, 64
+    c = widened(base.filled(203, lens, hkv, d, "bf16"), width)
+    q = torch.randn(4, 8, d, generator=base.gen(204), device="cuda").to(BF16)
+    q[:, :, 9] = torch.tensor([1.0, 0.5, -1.0, 2.0, 1.0, 1.0, 1.0, 3.0], device="cuda").to(BF16)
+    for b in (1, 2):
+        put_values(c, b, lens[b] // 2, c.k, {9: -INF})    # queries 0, 1, 3..7: -inf; query 2: +inf
+    q[0, 1, 4], q[0, 6, 4], q[3, 5, 0] = NAN, INF, -INF
+    out, lse, status = base.run_decode(c, q, lens)
+    assert status == [0] * 4
+    nan = torch.isnan(out).all(-1).tolist()
+    assert torch.isnan(out).any(-1).tolist() == nan
+    assert nan[1] == nan[2] == [i == 2 for i in range(8)]
+    assert nan[0] == [i in (1, 6) for i in range(8)] and nan[3] == [i == 5 for i in range(8)]
+    good = ~torch.tensor(nan, device="cuda")
+    for b in range(4):
+        k, v = c.rows(b, lens[b])
+        keep = np.isfinite(k).all((1, 2))                  # the key with a score of -inf left out
+        want, wl, tol, ltol = base.decode_tolerance(base.f64(torch.nan_to_num(q[b], 0, 0, 0)), k[keep], v[keep], d ** -0.5, "bf16")
+        ok = good[b].cpu().numpy()
+        assert np.all(np.abs(base.f64(out[b]) - want)[ok] <= tol[ok])
+        assert np.all(np.abs(base.f64(lse[b]) - wl)[ok] <= ltol[ok])
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+def test_marked_rows_of_an_8_bit_cache(held, width):
+    """A row that was not finite reads as NaN: a value row makes its head's outputs NaN and leaves the
+    log-sum-exp, a key row makes both NaN."""
+    lens, hkv, d = [20, 1, 600, 33], 2, 128
+    c = widened(base.filled(205, lens, hkv, d, held), width)
+    q = torch.randn(4, 8, d, generator=base.gen(206), device="cuda").to(BF16)
+    page, at = c.at(0, [7])
+    c.vs[page, 0, at] = NAN                               # a value row of request 0, head 0
+    page, at = c.at(2, [599])
+    c.ks[page, 1, at] = NAN                               # a key row of request 2, head 1
+    out, lse, status = base.run_decode(c, q, lens)
+    assert status == [0] * 4
+    bad = torch.zeros(4, 8, dtype=torch.bool, device="cuda")
+    bad[0, :4] = bad[2, 4:] = True
+    assert torch.equal(torch.isnan(out).all(-1), bad) and torch.equal(torch.isnan(out).any(-1), bad)
+    bad[0] = False
+    assert torch.equal(torch.isnan(lse), bad)
+    base.check_decode(c, q, lens, out, lse, which=[1, 3])
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+def test_an_infinite_value_of_little_weight(width):
+    """Down to float32's smallest normal number (2^-126 of the largest weight) an infinity reaches the
+    output, whether the heavier keys come after it or before; large finite values keep their size."""
+    far = [20.0, 60.0, 100.0, 104.0, 112.0, 120.0, 125.0]                # log2 of the weight, negated
+    lens, d = [200] * len(far), 64
+    c = widened(base.filled(207, lens, 1, d, "bf16"), width)
+    q = torch.zeros(len(far), 2, d, device="cuda")
+    q[:, :, 0] = 1.0
+    rows = (3, 190)
+    for b, x in enumerate(far):
+        page, at = c.at(b, range(200))
+        c.k[page, :, at] = 0.0
+        for row in rows:
+            put_values(c, b, row, c.k, {0: -round(x * np.log(2) * 4) / 4})
+        put_values(c, b, rows[0], c.v, {1: INF, 2: 2.0 ** 100})
+        put_values(c, b, rows[1], c.v, {1: INF, 3: -INF, 4: 2.0 ** 100})
+    out, lse, status = base.run_decode(c, q.to(BF16), lens, scale=1.0)
+    assert status == [0] * len(far)
+    assert bool(torch.isposinf(out[:, :, 1]).all()) and bool(torch.isneginf(out[:, :, 3]).all())
+    for b, x in enumerate(far):
+        k, v = c.rows(b, 200)
+        v = np.where(np.isfinite(v), v, 0.0)
+        want, wl, tol, ltol = base.decode_tolerance(base.f64(q[b].to(BF16)), k, v, 1.0, "bf16")
+        cols = [i for i in range(d) if i not in (1, 3)]
+        if x > 100:                                       # the smallest bf16 number, 2^-133, beside 2^100
+            tol = tol + 2.0 ** -33
+        assert np.all(np.abs(base.f64(out[b]) - want)[:, cols] <= tol[:, cols])
+        assert np.all(np.abs(base.f64(lse[b]) - wl) <= ltol)
