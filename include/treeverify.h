@@ -668,7 +668,10 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  *   s_j = softmax_scale * q . k_j,  out = sum_j softmax(s)_j v_j,
  *   lse = log sum_j exp(s_j)
  * with k_j, v_j the cached values (code * scale for 8-bit pools). Scores, the
- * softmax and its sums are float32. A request without keys (seq_len 0) gets
+ * softmax and its sums are float32. A weight multiplies its values rounded by
+ * at most 2^-16 of it over bf16 pools; over 8-bit pools, where it includes the
+ * value row's scale, by 2^-22 for Hq / Hkv <= 4 and 2^-11 for more, or by 2^-32
+ * of the largest one if that is more. A request without keys (seq_len 0) gets
  * out = 0 and lse = -inf. Slots from seq_len[b] on may hold anything.
  * Infinities and NaN act as in the formula: an infinite value of a bf16 pool
  * reaches the output (beside a weight below 2^-126 of the largest, which is 0

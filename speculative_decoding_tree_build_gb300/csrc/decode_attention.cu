@@ -25,10 +25,11 @@
 //  - The softmax's reference is not the exact running maximum: it moves only
 //    when a score exceeds it by 2^8, so the common page takes one warp vote
 //    and no reduction; weights stay below 2^8. A value row's scale joins the
-//    exponent: w_j = 2^(s_j + log2 vscale_j - M), with its own reference M, so
-//    the largest contribution is near 1 in f16 whatever the scales are. The
-//    sum of the softmax is float32 of unrounded terms. Beside bf16 values the
-//    weights go as two bf16 parts.
+//    exponent: w_j = 2^(s_j + log2 vscale_j - M), with its own reference M that
+//    moves to 2^7 below the largest: that one is 2^7 to 2^15 in f16 whatever the
+//    scales are, and half of f16's smallest step at most 2^-32 of it. The sum of
+//    the softmax is float32 of unrounded terms. DecTraits::kTwice tells in how
+//    many parts the weights go.
 //
 // Work plan: a unit is (request, KV head), its tiles are 64 keys (a page for
 // each of the CTA's four warps). All units' tiles are laid end to end and
@@ -69,6 +70,7 @@ constexpr int kDecMaxHeads = 4096;     // KV heads at most: unit numbers stay be
 constexpr int kMergeWarps = 4;         // warps of a joining CTA at least
 constexpr int kMergeMaxParts = 8;      // warps that share a query head's partials at most
 constexpr int kMergeBatch = 8;         // partials whose sums a warp has in flight
+constexpr float kRefBelow = 7.0f;      // log2 of the largest weight over 8-bit values when its reference moves
 constexpr float kLowest = -3.4028234663852886e38f;
 
 // What the CTA that begins a unit tells the joining grid: the CTAs that work
@@ -209,8 +211,20 @@ __device__ __forceinline__ float2 as_float2(uint64_t v) {
 
 // ------------------------------------------------------------------ the kernel
 
-template <int kFmt, int D, int NT>
+// kQ: query heads to a cached head at most, 4, 8 or 16.
+template <int kFmt, int D, int kQ>
 struct DecTraits {
+  static constexpr int NT = kQ > 8 ? 2 : 1;                    // MMA tiles of eight queries
+  // A weight goes to the MMA as a number of the values' 16-bit type. In one part
+  // bf16's rounding would add as much to the error as the output's own does, so
+  // over bf16 pools it goes in two parts. f16's is an eighth of that: 0.00168
+  // against 64 bits, with two parts 0.00167, all of it the output's rounding.
+  // Up to four queries stand twice among the MMA's eight, the first four for the
+  // first parts and the others for the second, so there two parts cost no product
+  // (e4m3, 1.9 GB: 293.7 -> 295.4 us) and are taken for all formats. With more
+  // queries over 8-bit pools it is one part: a second product takes 27.2 -> 29.1
+  // us (101 MB, 8 queries, int8) for a hundredth of the error.
+  static constexpr bool kTwice = kQ == 4;
   static constexpr bool kHalf = kFmt != TV_KV_BF16;
   static constexpr int kElem = kHalf ? 1 : 2;
   static constexpr int kRowBytes = D * kElem;
@@ -234,10 +248,12 @@ struct DecTraits {
 
 // kOneGrid: a unit belongs to a cluster of p.cluster CTAs, whose kWarps warps
 // take its pages in turn; else a CTA takes a share of all units' tiles.
-template <int kFmt, int D, int NT, bool kOneGrid, int kWarps>
-__global__ void __launch_bounds__(32 * kWarps, (DecTraits<kFmt, D, NT>::kPerSm * kDecWarps / kWarps))
+template <int kFmt, int D, int kQ, bool kOneGrid, int kWarps>
+__global__ void __launch_bounds__(32 * kWarps, (DecTraits<kFmt, D, kQ>::kPerSm * kDecWarps / kWarps))
 decode_kernel(const __grid_constant__ DecodeParams p) {
-  using Tr = DecTraits<kFmt, D, NT>;
+  using Tr = DecTraits<kFmt, D, kQ>;
+  constexpr int NT = Tr::NT;
+  constexpr bool kTwice = Tr::kTwice;
   static_assert(kOneGrid || kWarps == kDecWarps, "a tile is a page for each warp");
   constexpr bool kHalf = Tr::kHalf;
   constexpr int kRowBytes = Tr::kRowBytes, kKPieces = Tr::kKPieces, kVPieces = Tr::kVPieces, kSteps = Tr::kSteps;
@@ -247,6 +263,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
   constexpr int kThreads = 32 * kWarps;
   __shared__ float4 s_stat[kWarps][16];                        // (m, M, l, -)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g = lane / 4, t = lane % 4;
+  auto query = [&](int x) { return kTwice ? g % 4 : x * 8 + g; };        // of the MMA's column g
   grid_launch_dependents();
   if (!kOneGrid) grid_dependency_wait();
 
@@ -315,7 +332,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     const __nv_bfloat16* q_row[NT];
 #pragma unroll
     for (int x = 0; x < NT; ++x)
-      q_row[x] = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + min(x * 8 + g, p.group - 1)) * D;
+      q_row[x] = p.q + static_cast<long long>(b) * p.q_ld + (static_cast<long long>(h) * p.group + min(query(x), p.group - 1)) * D;
     if (kOneGrid) {                    // (all of the above while the grid before this one ends)
       grid_dependency_wait();
       n = ldg_int(p.seq_len + b);
@@ -359,7 +376,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
     }
 #pragma unroll
     for (int x = 0; x < NT; ++x) {
-      if (x * 8 + g >= p.group) {
+      if (query(x) >= p.group) {
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) qf[x][s][0] = qf[x][s][1] = 0u;
       }
@@ -531,7 +548,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
             const float f = kHalf ? fac[x][e & 1] * (e < 2 ? k0[pg] : k1[pg]) : fac[x][e & 1];
             s[pg][x][e] = live[pg][e / 2] ? s[pg][x][e] * f : -INFINITY;
             over |= s[pg][x][e] > m[x][e & 1] + 8.0f;
-            if (kHalf) over |= s[pg][x][e] + lv[pg][e / 2] > ref[x][e & 1] + 8.0f;
+            if (kHalf) over |= s[pg][x][e] + lv[pg][e / 2] > ref[x][e & 1] + 8.0f + kRefBelow;
           }
         }
       }
@@ -554,7 +571,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
             a = fmaxf(a, m[x][e]);
             l[x][e] *= fast_exp2(m[x][e] - a);
             m[x][e] = a;
-            c = kHalf ? fmaxf(c, ref[x][e]) : a;
+            c = kHalf ? fmaxf(c - kRefBelow, ref[x][e]) : a;
             const float down = fast_exp2(ref[x][e] - c);
             ref[x][e] = c;
 #pragma unroll
@@ -564,9 +581,8 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
       }
 #pragma unroll
       for (int pg = 0; pg < kPages; ++pg) {
-        // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8). Beside
-        // bf16 values they have to be bf16 too, and go in two parts: with one, their rounding would
-        // add as much to the error as the output's own does (weight_rest).
+        // weights, transposed into the MMA's B operand: query g, keys 2t, 2t + 1 (and + 8), in the
+        // parts that DecTraits::kTwice tells of
         uint32_t pf[NT][2], pl[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; ++x) {
@@ -582,13 +598,17 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
           }
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
+            uint32_t hi, rest;
             if constexpr (kHalf) {
-              pf[x][u] = transpose8x8(pack_half2(w[2 * u], w[2 * u + 1]));
+              hi = pack_half2(w[2 * u], w[2 * u + 1]);
+              const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+              rest = pack_half2(w[2 * u] - h.x, w[2 * u + 1] - h.y);
             } else {
-              const uint32_t hi = __byte_perm(__float_as_uint(w[2 * u]), __float_as_uint(w[2 * u + 1]), 0x7632);
-              pf[x][u] = transpose8x8(hi);
-              pl[x][u] = transpose8x8(pack_bf16x2(weight_rest(w[2 * u], bf16_lo(hi)), weight_rest(w[2 * u + 1], bf16_hi(hi))));
+              hi = __byte_perm(__float_as_uint(w[2 * u]), __float_as_uint(w[2 * u + 1]), 0x7632);
+              rest = pack_bf16x2(weight_rest(w[2 * u], bf16_lo(hi)), weight_rest(w[2 * u + 1], bf16_hi(hi)));
             }
+            pf[x][u] = transpose8x8(kTwice && t >= 2 ? rest : hi);
+            if (!kHalf && !kTwice) pl[x][u] = transpose8x8(rest);
           }
         }
         if (tail) {                    // rows past the end may hold anything, NaN among it
@@ -625,7 +645,7 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
 #pragma unroll
               for (int x = 0; x < NT; ++x) {
                 mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pf[x][0], pf[x][1]);
-                mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+                if (!kTwice) mma16816<false>(o[x][4 * c + j], a0, a1, a2, a3, pl[x][0], pl[x][1]);
               }
             }
           }
@@ -671,7 +691,13 @@ decode_kernel(const __grid_constant__ DecodeParams p) {
         for (int w = 0; w < kWarps; ++w) {
           const float4 s4 = s_stat[w][qi];
           const float f = fast_exp2(s4.y - mr);
-          const float2 v = *reinterpret_cast<const float2*>(s_o + (static_cast<size_t>(w) * 8 * NT + qi) * kRowPad + d);
+          const float* sums = s_o + (static_cast<size_t>(w) * 8 * NT + qi) * kRowPad + d;
+          float2 v = *reinterpret_cast<const float2*>(sums);
+          if (kTwice) {
+            const float2 rest = *reinterpret_cast<const float2*>(sums + 4 * kRowPad);
+            v.x += rest.x;
+            v.y += rest.y;
+          }
           acc.x += v.x * f;
           acc.y += v.y * f;
           ll += s4.z * fast_exp2(s4.x - mm);
@@ -852,11 +878,11 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
   if (p.lse != nullptr && lane == 0) p.lse[at] = (mm + log2f(ll)) * 0.69314718055994531f;
 }
 
-template <int kFmt, int D, int NT, int kWarps>
+template <int kFmt, int D, int kQ, int kWarps>
 static int launch_decode_one(const DecodeParams& p, int dev, cudaStream_t stream) {
-  constexpr size_t smem = sizeof(float) * 8 * NT * (kWarps * (D + 4) + D);
+  constexpr size_t smem = sizeof(float) * 8 * DecTraits<kFmt, D, kQ>::NT * (kWarps * (D + 4) + D);
   static size_t smem_set[kMaxDevices] = {0};
-  auto* kernel = decode_kernel<kFmt, D, NT, true, kWarps>;
+  auto* kernel = decode_kernel<kFmt, D, kQ, true, kWarps>;
   if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -875,10 +901,10 @@ static int launch_decode_one(const DecodeParams& p, int dev, cudaStream_t stream
   return cudaLaunchKernelEx(&cfg, kernel, p) == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
-template <int kFmt, int D, int NT>
+template <int kFmt, int D, int kQ>
 static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) {
-  using Tr = DecTraits<kFmt, D, NT>;
-  constexpr size_t sums = sizeof(float) * kDecWarps * 8 * NT * (D + 4);
+  using Tr = DecTraits<kFmt, D, kQ>;
+  constexpr size_t sums = sizeof(float) * kDecWarps * 8 * Tr::NT * (D + 4);
   const int grid = sms * Tr::kPerSm, units = p.batch * p.hkv;
   const long long all_warps = static_cast<long long>(grid) * kDecWarps;
   auto fits = [&](long long unit_warps, long long most) { return units * unit_warps <= most; };
@@ -910,12 +936,12 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
   if (p.max_blocks <= unit_warps * kOneGridPages &&
       p.max_blocks * (all_warps - by_unit) <= kOneGridExcess * unit_warps * all_warps) {
     if constexpr (Tr::kMaxWarps > kDecWarps) {
-      if (wide) return launch_decode_one<kFmt, D, NT, Tr::kMaxWarps>(p, dev, stream);
+      if (wide) return launch_decode_one<kFmt, D, kQ, Tr::kMaxWarps>(p, dev, stream);
     }
-    return launch_decode_one<kFmt, D, NT, kDecWarps>(p, dev, stream);
+    return launch_decode_one<kFmt, D, kQ, kDecWarps>(p, dev, stream);
   }
   static size_t smem_set[kMaxDevices] = {0};
-  auto* kernel = decode_kernel<kFmt, D, NT, false, kDecWarps>;
+  auto* kernel = decode_kernel<kFmt, D, kQ, false, kDecWarps>;
   if (!ensure_smem(kernel, sums, smem_set, dev)) return TV_ERR_CUDA;
   p.by_unit = units <= grid ? 1 : 0;
   p.parts = 1;
@@ -931,9 +957,12 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
 
 template <int kFmt>
 static int launch_decode_fmt(const DecodeParams& p, int d, int sms, int dev, cudaStream_t stream) {
-  if (d == 64)
-    return p.group <= 8 ? launch_decode<kFmt, 64, 1>(p, sms, dev, stream) : launch_decode<kFmt, 64, 2>(p, sms, dev, stream);
-  return p.group <= 8 ? launch_decode<kFmt, 128, 1>(p, sms, dev, stream) : launch_decode<kFmt, 128, 2>(p, sms, dev, stream);
+  if (d == 64) {
+    if (p.group <= 4) return launch_decode<kFmt, 64, 4>(p, sms, dev, stream);
+    return p.group <= 8 ? launch_decode<kFmt, 64, 8>(p, sms, dev, stream) : launch_decode<kFmt, 64, 16>(p, sms, dev, stream);
+  }
+  if (p.group <= 4) return launch_decode<kFmt, 128, 4>(p, sms, dev, stream);
+  return p.group <= 8 ? launch_decode<kFmt, 128, 8>(p, sms, dev, stream) : launch_decode<kFmt, 128, 16>(p, sms, dev, stream);
 }
 
 static size_t dec_task_bytes(int ctas) { return ((sizeof(DecBegin) + sizeof(int)) * ctas + 255) / 256 * 256; }

@@ -189,3 +189,78 @@ def test_an_infinite_value_of_little_weight(width):
             tol = tol + 2.0 ** -33
         assert np.all(np.abs(base.f64(out[b]) - want)[:, cols] <= tol[:, cols])
         assert np.all(np.abs(base.f64(lse[b]) - wl) <= ltol)
+
+
+# ---------------------------------------------------------------- one-token attention: weights over 8-bit values
+
+
+def weight_bound(c, q, b, n, scale, part):
+    """Bound of the output's error from the kernel's roundings, `part` being that of a weight: the
+    weights p_j vs_j are f16 numbers over a reference that keeps the largest at 2^7 or above, so that
+    half of f16's smallest step, 2^-25, is 2^-32 of it."""
+    k, v = c.rows(b, n)
+    vs = c.value_scales(b, n)
+    want, lse, absv, big = base.decode_attention_ref(base.f64(q[b]), k, v, scale)
+    d, group = q.shape[2], q.shape[1] // k.shape[1]
+    # score and exponent as in base.decode_tolerance; log2 of the value's scale: 2^-22 of an exponent, of which
+    # the sums with it keep 2^-24 of their size (at most 2^7)
+    rel = part + 2 * ((d + 4) * 2.0 ** -24 * big + 2.0 ** -21) + 2 * n * 2.0 ** -24 + 2.0 ** -16
+    tol = absv * rel[:, None] + base.HALF[BF16] * np.abs(want) + 1e-30
+    for h in range(q.shape[1]):
+        g = h // group
+        p = np.exp(scale * (k[:, g] @ base.f64(q[b])[h]) - lse[h])
+        tol[h] += 2.0 ** -32 * (p * vs[:, g]).max() * (np.abs(v[:, g]) / vs[:, g][:, None]).sum(0)
+    return want, tol
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+@pytest.mark.parametrize("group", [1, 4, 8, 12])
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+def test_many_light_rows_beside_a_heavy_one(held, group, width):
+    """A column in which the heaviest row is 0 consists of rows of 2^-26 of its weight: they are not
+    lost, before it or behind it."""
+    n, d = 2500, 64
+    for at in (5, 2400):
+        c = widened(base.Cache(211, [n], 1, d, held), width)
+        k = torch.zeros(n, 1, d, device="cuda")
+        k[at, 0, 0] = 18.0                                # exp(18) = 2^25.97; exact in both formats
+        v = torch.ones(n, 1, d, device="cuda")
+        v[:, 0, ::2] = -0.5
+        v[at, 0, 1:9] = 0.0
+        c.put(0, k.to(BF16), v.to(BF16))
+        q = torch.zeros(1, group, d, device="cuda", dtype=BF16)
+        q[:, :, 0] = 1.0
+        out, lse, status = base.run_decode(c, q, [n], scale=1.0)
+        assert status == [0]
+        want, tol = weight_bound(c, q, 0, n, 1.0, 2.0 ** -11)
+        assert np.all(np.abs(base.f64(out[0]) - want) <= tol)
+        assert np.all(tol[:, 1] < np.abs(want[:, 1]) / 8)           # the bound tells lost from kept
+        assert np.abs(base.f64(out[0]))[:, 1:9].min() > 0
+
+
+@pytest.mark.parametrize("width", [1, 2400])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 4, 64), (8, 2, 128), (6, 2, 128), (4, 1, 64)])
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+def test_weights_of_up_to_four_queries_keep_22_bits(held, hq, hkv, d, width):
+    """Two keys whose values nearly cancel: the weights' own roundings are what is left. Keys 0 and 1
+    have the values 1 and -1 times 1.75, weights p and 1 - p around a half."""
+    cases = 64
+    c = widened(base.Cache(213, [2] * cases, hkv, d, held), width)
+    q = torch.zeros(cases, hq, d, device="cuda")
+    k = torch.zeros(2, hkv, d, device="cuda")
+    k[0, :, 0] = 1.0
+    v = torch.full((2, hkv, d), 1.75, device="cuda")
+    v[1] = -1.75
+    for b in range(cases):
+        c.put(b, k.to(BF16), v.to(BF16))
+        q[b, :, 0] = (b - 32) * 2.0 ** -12 + 2.0 ** -13 * torch.arange(hq, device="cuda")
+    q = q.to(BF16)
+    out, lse, status = base.run_decode(c, q, [2] * cases, scale=1.0)
+    assert status == [0] * cases
+    for b in range(cases):
+        kk, vv = c.rows(b, 2)
+        want, _, absv, _ = base.decode_attention_ref(base.f64(q[b]), kk, vv, 1.0)
+        # scores below 2^-6: products and factors of 2^-24 of that, exponents and the base-2 logarithm 2^-22 each,
+        # sums 2^-24, the two parts 2^-22
+        tol = absv * (8 * 2.0 ** -22) + base.HALF[BF16] * np.abs(want)
+        assert np.all(np.abs(base.f64(out[b]) - want) <= tol), b
