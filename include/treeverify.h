@@ -608,8 +608,11 @@ int tv_rope_axes(const tv_rope_axes_geom* geom, int32_t rows, int32_t dtype, con
  *                 on are ignored
  *  k_new, v_new   bf16 [rows][Hkv][D], heads back to back, rows kv_ld ELEMENTS
  *                 apart (>= Hkv * D, a multiple of 8); already rotated keys
- *  cu_rows        int32 [batch+1] offsets of the requests' rows (as cu_nodes;
- *                 a request may have none)
+ *  cu_rows        int32 [batch+1] offsets of the requests' rows, non-decreasing;
+ *                 a request may have none, and rows before cu_rows[0] are
+ *                 ignored too. Where offsets decrease, the requests that end
+ *                 before they begin, or have rows and begin before an earlier
+ *                 offset, are flagged: no row goes to two requests
  *  start_len      int32 [batch] row i of request b goes to slot start_len[b] + i
  *  block_table, n_blocks, max_blocks_per_req, num_blocks
  *                 as elsewhere; the blocks of the written slots must be held.

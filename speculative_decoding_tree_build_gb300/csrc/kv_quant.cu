@@ -10,6 +10,8 @@
 // small loads (offsets, lengths, block ids) overlaps the one large one.
 // Measured: append 34.5 us for 201 MB (5.8 TB/s), read back 119 us for 692 MB
 // (5.8 TB/s, two thirds of it writes).
+#include <climits>
+
 #include "tv_kv8.cuh"
 #include "tv_share.cuh"
 
@@ -19,6 +21,7 @@ constexpr int kAppendThreads = 256;
 constexpr int kAppendPerSm = 3;      // CTAs an SM
 constexpr int kAppendAhead = 4;      // rows whose loads a thread has in flight
 constexpr int kAppendMaxRows = 256;  // rows of k_new / v_new per CTA at most (a thread describes a row)
+static_assert(kAppendMaxRows == kAppendThreads, "arrays by row also serve by thread");
 
 struct AppendParams {
   const __nv_bfloat16* k_new;
@@ -99,26 +102,53 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
   for (int e = 0; e < kAppendAhead; ++e) load(x[e], slot0 + e * p.slots);    // on their way while slots are found
 
   __syncthreads();
-  // the CTA's rows that each request owns
-  for (int i = threadIdx.x; i < p.batch; i += kAppendThreads, q = look_at(i)) {
-    if (q.c1 <= q.c0 || q.st != 0) continue;
-    if (blockIdx.x == 0 && blockIdx.y == 0 && (q.c1 > p.rows || q.c0 < 0 || q.start < 0)) atomicOr(p.status + i, TV_ST_BAD_SIZE);
-    if (q.c0 < 0 || q.c1 > p.rows || q.start < 0 || q.c0 >= t1 || q.c1 <= t0) continue;
-    const int first = max(q.c0, t0) - t0;
-    const long long end = static_cast<long long>(q.start) + (q.c1 - q.c0);
-    const bool fits = (end - 1) / TV_BLOCK_SIZE < q.held;    // (which also keeps slots below 2^31)
+  // the CTA's rows that each request owns (the first CTA reports bad offsets)
+  auto claim = [&](int i, const Request& r, bool bad) {
+    if ((r.c1 <= r.c0 && !bad) || r.st != 0) return;
+    bad |= r.c1 > p.rows || r.c0 < 0 || r.start < 0;
+    if (bad && blockIdx.x == 0 && blockIdx.y == 0) atomicOr(p.status + i, TV_ST_BAD_SIZE);
+    if (bad || r.c0 >= t1 || r.c1 <= t0) return;
+    const int first = max(r.c0, t0) - t0;
+    const long long end = static_cast<long long>(r.start) + (r.c1 - r.c0);
+    const bool fits = (end - 1) / TV_BLOCK_SIZE < r.held;    // (which also keeps slots below 2^31)
     if (!fits) s_bad[first] = TV_ST_BAD_BLOCK;
-    s_run[first] = AppendRun{i, q.c0, q.start, min(q.c1, t1) - t0};
+    s_run[first] = AppendRun{i, r.c0, r.start, min(r.c1, t1) - t0};
     atomicOr(&s_heads[first / 32], 1u << (first % 32));
-    if (fits && (q.c0 < t0 || q.c1 > t1)) {
-      int* cross = s_cross[q.c0 < t0 ? 0 : 1];
+    if (fits && (r.c0 < t0 || r.c1 > t1)) {
+      int* cross = s_cross[r.c0 < t0 ? 0 : 1];
       cross[0] = i;
-      cross[1] = q.start / TV_BLOCK_SIZE;
+      cross[1] = r.start / TV_BLOCK_SIZE;
       cross[3] = first;
       cross[2] = static_cast<int>((end - 1) / TV_BLOCK_SIZE) - cross[1] + 1;
     }
+  };
+  bool back = false;
+  for (int i = threadIdx.x; i < p.batch; i += kAppendThreads, q = look_at(i)) {
+    back |= q.c1 < q.c0;
+    claim(i, q, false);
   }
-  __syncthreads();
+  // Offsets that run backwards let requests claim the same rows: all is claimed
+  // again, without the requests that begin before an earlier offset or end before
+  // they begin. (Every CTA looks at all offsets, so all of them decide alike.)
+  if (__syncthreads_or(back)) {
+    const int per = (p.batch + kAppendThreads - 1) / kAppendThreads;
+    const int i0 = min(p.batch, static_cast<int>(threadIdx.x) * per), i1 = min(p.batch, i0 + per);
+    int most = INT_MIN;
+    for (int i = i0; i < i1; ++i) most = max(most, p.cu_rows[i]);
+    if (threadIdx.x < kAppendMaxRows) s_bad[threadIdx.x] = 0;
+    if (threadIdx.x < kAppendMaxRows / 32) s_heads[threadIdx.x] = 0u;
+    if (threadIdx.x < 8) s_cross[threadIdx.x / 4][threadIdx.x % 4] = 0;
+    s_head[threadIdx.x] = most;
+    __syncthreads();
+    most = INT_MIN;                    // of the offsets before the thread's requests
+    for (int t = 0; t < static_cast<int>(threadIdx.x); ++t) most = max(most, s_head[t]);
+    for (int i = i0; i < i1; ++i) {
+      const Request r = look_at(i);
+      claim(i, r, r.c1 < r.c0 || (r.c1 > r.c0 && r.c0 < most));
+      most = max(most, r.c0);
+    }
+    __syncthreads();
+  }
   // the rows' blocks, and all other blocks of a request that other CTAs have rows of
   if (threadIdx.x < nrows) {
     const int r = threadIdx.x;
@@ -130,7 +160,6 @@ __global__ void __launch_bounds__(kAppendThreads, kAppendPerSm) kv_quant_append_
     s_head[r] = 0;
     if (first >= 0 && r < s_run[first].last && s_bad[first] == 0) {
       const AppendRun run = s_run[first];
-      // (offsets that overlap let two requests describe one run: the index stays inside the table)
       const int slot = run.start + (t0 + r - run.c0);
       const int page = slot / TV_BLOCK_SIZE;
       const int blk = slot >= 0 && page < p.max_blocks ? p.block_table[static_cast<size_t>(run.req) * p.max_blocks + page] : -1;

@@ -264,3 +264,61 @@ def test_weights_of_up_to_four_queries_keep_22_bits(held, hq, hkv, d, width):
         # sums 2^-24, the two parts 2^-22
         tol = absv * (8 * 2.0 ** -22) + base.HALF[BF16] * np.abs(want)
         assert np.all(np.abs(base.f64(out[b]) - want) <= tol), b
+
+
+# ---------------------------------------------------------------- append: offsets that run backwards
+
+
+def claims(cu, rows, start):
+    """Which requests' offsets are refused, by the header's words."""
+    bad = []
+    for b in range(len(cu) - 1):
+        n = cu[b + 1] - cu[b]
+        over = n < 0 or (n > 0 and b > 0 and cu[b] < max(cu[:b]))
+        bad.append(over or (n > 0 and (cu[b] < 0 or cu[b + 1] > rows or start[b] < 0)))
+    return bad
+
+
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+@pytest.mark.parametrize("cu,rows", [
+    ([0, 5, 3, 8], 8),                      # the second ends before it begins, the third begins inside the first
+    ([0, 8, 4, 12], 12),
+    ([0, 4, 0, 4], 4),                      # two begin at the same row
+    ([4, 0, 4, 8], 8),
+    ([0, 6, 2, 2, 6, 9], 9),                # an empty one among those that overlap has nothing to object to
+    ([2, 5, 9, 7], 12),                     # the last alone; rows before the first offset are nobody's
+    ([0, 3, 2 ** 31 - 1, 3, 6], 6),
+    ([0, 3, -2 ** 31, 3, 6], 6),
+    ([0, 700, 350, 1000], 1000),            # over many thread blocks
+])
+def test_append_offsets_that_run_backwards(cu, rows, held):
+    n = len(cu) - 1
+    start = [3 + 5 * b for b in range(n)]
+    # room for what is written, and for the most that an overlapping request could ask for
+    c = base.Cache(221, [start[b] + min(max(cu[b + 1] - cu[b], 1), rows) for b in range(n)], 2, 64, held)
+    k, v = base.fresh(222, rows, 2, 64)
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    bad = claims(cu, rows, start)
+    assert base.run_append(c, k, v, cu, start) == [int(x) for x in bad]
+    base.check_append(c, before, k, v, cu, start, [b for b in range(n) if not bad[b] and cu[b + 1] > cu[b]])
+
+
+def test_append_many_offsets_some_of_which_run_backwards():
+    """More requests than a thread block has threads; flagged ones keep their status."""
+    rng = np.random.default_rng(223)
+    lens = rng.integers(0, 5, 700)
+    cu = [0] + np.cumsum(lens).tolist()
+    rows = cu[-1]
+    for b in (40, 41, 300, 555):
+        cu[b] = max(0, cu[b] - int(rng.integers(5, 200)))
+    start = rng.integers(0, 40, 700).tolist()
+    c = base.Cache(224, [s + max(cu[b + 1] - cu[b], 1) for b, s in enumerate(start)], 1, 64, "int8")
+    k, v = base.fresh(225, rows, 1, 64)
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    bad = claims(cu, rows, start)
+    assert 4 <= sum(bad) < 200          # each lowered offset spoils the request before it, or its own
+    status = [0] * 700
+    status[bad.index(True)], status[0] = 4, 2
+    want = [int(x) if s == 0 else s for x, s in zip(bad, status)]
+    assert base.run_append(c, k, v, cu, start, base.i32(status)) == want
+    base.check_append(c, before, k, v, cu, start, [b for b in range(700) if want[b] == 0 and cu[b + 1] > cu[b]])
