@@ -558,9 +558,10 @@ typedef struct tv_rope_axes_geom {
  * has the same position on all of them). Pair i of row t is turned by the
  * angle positions[axis(i)][t] * inv_freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin)
- * Columns from 2R on pass through. The angle is the exact product reduced
- * modulo one turn in 64-bit fixed point, so it does not lose digits at far
- * positions; the rotation is float32, rounded once to the output type.
+ * Columns from 2R on pass through. The angle is the product reduced modulo one
+ * turn in 64-bit fixed point, so it does not lose digits at far positions: it is
+ * within 2^-30 turns (6e-9 rad) for every position and every finite inv_freq. The
+ * rotation is float32, rounded once to the output type.
  * tv_tree_attention_verify rotates a tree's own nodes; this call serves the
  * prompts, and decode steps ahead of tv_kv_quant_append / tv_decode_attention.
  *

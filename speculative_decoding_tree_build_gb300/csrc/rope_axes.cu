@@ -4,11 +4,12 @@
 // wanted modulo one turn, and float32 has no digits left for that at far
 // positions (at position 10^6 its last bit is 0.06 rad). So inv_freq is held
 // as a 64-bit fraction of a turn, F = frac(inv_freq / 2 pi) * 2^64, made from
-// the float's significand and a 64-bit 1 / 2 pi by integer arithmetic, and
+// the float's significand and the bits of 1 / 2 pi by integer arithmetic, and
 // the integer product position * F modulo 2^64 IS the angle's fraction of a
-// turn, within |position| * 2^-63 turns. Its top 32 bits give the quadrant and
-// a remainder of at most an eighth of a turn, for which the Taylor series of
-// sine and cosine end below float32's last bit after five and six terms.
+// turn, within |position| * 2^-63 turns. Its top 32 bits (the angle, cut off to
+// 2^-32 turns, 1.5e-9 rad) give the quadrant and a remainder of at most an eighth
+// of a turn, for which the Taylor series of sine and cosine end below float32's
+// last bit after five and six terms.
 //
 // Memory bound: every value is read and written once, 6 float operations a
 // pair. One CTA rotates a few rows (or some heads of one row); the sines and
@@ -63,19 +64,34 @@ __device__ __forceinline__ float rope_float(__nv_bfloat16 x) { return __bfloat16
 __device__ __forceinline__ void rope_round(float& y, float x) { y = x; }
 __device__ __forceinline__ void rope_round(__nv_bfloat16& y, float x) { y = __float2bfloat16_rn(x); }
 
-// inv_freq as a 64-bit fraction of a turn: |inv_freq| = m 2^(e - 150) with an
-// integer m < 2^24, and 1 / 2 pi = C 2^-66, so F = m C 2^(e - 152) modulo 2^64.
+// inv_freq as a 64-bit fraction of a turn, F = frac(inv_freq / 2 pi) 2^64, within
+// 2 of its units. |inv_freq| = m 2^(e - 150) with an integer m < 2^24. Below 8, 64
+// bits of 1 / 2 pi = C 2^-66 are enough: F = m C 2^(e - 152) modulo 2^64, where
+// half a unit of C weighs inv_freq / 8. Above, the bits of 1 / 2 pi ahead of the
+// e - 150th make whole turns, and F comes from the 128 bits from there on (the
+// reduction of Payne and Hanek, 1983).
 __device__ __forceinline__ unsigned long long rope_turns(float inv_freq) {
   constexpr unsigned long long kC = 11743562013128004906ull;         // 2^66 / 2 pi
   const uint32_t bits = __float_as_uint(inv_freq);
   const uint32_t field = (bits >> 23) & 0xffu;
   const unsigned long long m = (bits & 0x7fffffu) | (field ? 0x800000u : 0u);
-  const int shift = 152 - static_cast<int>(field ? field : 1u);
-  const unsigned long long lo = m * kC, hi = __umul64hi(m, kC);
   unsigned long long f;
-  if (shift <= 0) f = shift > -64 ? lo << -shift : 0ull;
-  else if (shift < 64) f = (lo >> shift) | (hi << (64 - shift));
-  else f = shift < 128 ? hi >> (shift - 64) : 0ull;
+  if (field < 130) {
+    const int shift = 152 - static_cast<int>(field ? field : 1u);
+    const unsigned long long lo = m * kC, hi = __umul64hi(m, kC);
+    if (shift < 64) f = (lo >> shift) | (hi << (64 - shift));
+    else f = shift < 128 ? hi >> (shift - 64) : 0ull;
+  } else {
+    constexpr unsigned long long kB0 = 0x28be60db9391054aull, kB1 = 0x7f09d5f47d4d3770ull;     // 1 / 2 pi
+    constexpr unsigned long long kB2 = 0x36d8a5664f10e410ull, kB3 = 0x7f9458eaf7aef158ull;
+    const int at = static_cast<int>(field) - 86;                     // the first bit, 64 zeros going ahead
+    const int word = at / 64, shift = at % 64;
+    const unsigned long long w0 = word == 0 ? 0ull : word == 1 ? kB0 : kB1;
+    const unsigned long long w1 = word == 0 ? kB0 : word == 1 ? kB1 : kB2;
+    const unsigned long long w2 = word == 0 ? kB1 : word == 1 ? kB2 : kB3;
+    const unsigned long long hi = (w0 << shift) | (w1 >> 1 >> (63 - shift)), lo = (w1 << shift) | (w2 >> 1 >> (63 - shift));
+    f = m * hi + __umul64hi(m, lo);
+  }
   return bits >> 31 ? 0ull - f : f;
 }
 

@@ -322,3 +322,66 @@ def test_append_many_offsets_some_of_which_run_backwards():
     want = [int(x) if s == 0 else s for x, s in zip(bad, status)]
     assert base.run_append(c, k, v, cu, start, base.i32(status)) == want
     base.check_append(c, before, k, v, cu, start, [b for b in range(700) if want[b] == 0 and cu[b + 1] > cu[b]])
+
+
+# ---------------------------------------------------------------- rotary positions: angles
+
+
+def two_pi_fraction(n):
+    """floor(2^n / 2 pi), pi from Machin's 16 arctan(1/5) - 4 arctan(1/239) in integers."""
+    def arctan_of_one_over(x):
+        term = total = (1 << (n + 64)) // x
+        k, sign = 1, -1
+        while term:
+            term //= x * x
+            k += 2
+            total += sign * (term // k)
+            sign = -sign
+        return total
+    pi = (16 * arctan_of_one_over(5) - 4 * arctan_of_one_over(239)) >> 64
+    return (1 << 2 * n) // (2 * pi)
+
+
+def turned(positions, inv_freq):
+    """cos and sin of position * inv_freq, reduced by whole turns in integers ([rows][pairs])."""
+    n = 640                                               # bits behind the point: 2^-640 * 2^31 * 2^128 is far below
+    unit = two_pi_fraction(n)
+    cos, sin = np.empty((len(positions), len(inv_freq))), np.empty((len(positions), len(inv_freq)))
+    for i, f in enumerate(inv_freq):
+        num, den = float(f).as_integer_ratio()            # a power of two below, 2^149 at the most
+        for r, p in enumerate(positions):
+            turns = ((p * num * unit << 160) // den) % (1 << (n + 160))
+            angle = (turns >> (n + 160 - 80)) / 2.0 ** 80 * 2 * np.pi
+            cos[r, i], sin[r, i] = np.cos(angle), np.sin(angle)
+    return cos, sin
+
+
+FREQS = [1e-45, 1.2e-38, 3e-20, 1e-6, 0.00133, 0.31, 1.0, 3.99, 7.9999995, 8.0, 9.25, 100.7, 1030.3, 65537.0, 1e6, 33554430.0,
+         33554432.0, 2.5e9, 2.0 ** 40 + 2.0 ** 20, 1.5e19, 1e24, 3.3e30, 1e38, 3.4028234e38]
+
+
+@pytest.mark.parametrize("style", [0, 1])
+@pytest.mark.parametrize("negative", [False, True])
+def test_angles_of_every_size(style, negative):
+    """Frequencies over all of float32 and positions over all of int32, against angles reduced in
+    integers (a float64 product would itself be off by 2^-22 rad at 2^31)."""
+    positions = [0, 1, 2, 3, 7, 1000, 4097, 123457, 2 ** 20 + 1, 10 ** 8 + 7, 2 ** 30, 2 ** 31 - 1, -1, -2, -77, -65536, -2 ** 31 + 1, -2 ** 31]
+    freqs = np.array(FREQS, np.float32) * np.float32(-1.0 if negative else 1.0)
+    rows, pairs = len(positions), len(freqs)
+    q = torch.randn(rows, 2, 2 * pairs, generator=base.gen(231), device="cuda")
+    x, out = base.f64(q), torch.empty_like(q)
+    tv.rope_axes(tv.rope_axes_geom(2, 0, 2 * pairs, [pairs], style), q, None, base.i32([positions]),
+                 torch.from_numpy(freqs).cuda(), out, None)
+    cos, sin = turned(positions, freqs)
+    a, b = (x[..., :pairs], x[..., pairs:]) if style else (x[..., 0::2], x[..., 1::2])
+    ra, rb = a * cos[:, None] - b * sin[:, None], b * cos[:, None] + a * sin[:, None]
+    # The angle: 2^31 * 2^-63 + 2 * 2^-32 turns = 3 * 2^-32 turns, 2 pi times that in rad. The remainder as a
+    # float and times 2 pi 2^-32 (a constant of 24 bits): 3 roundings, 3 * 2^-24 of at most pi / 4. The series:
+    # 2^-29 left out, the last sum's rounding 2^-25, those inside it 2^-24 of z / 2 < 0.31 or less each, three that
+    # matter. A product each and the sum: 3 * 2^-24 of |a| + |b| at the most.
+    angle = 2 * np.pi * 3 * 2.0 ** -32 + 3 * 2.0 ** -24 * np.pi / 4
+    tol = (np.abs(a) + np.abs(b)) * (angle + 2.0 ** -29 + 2.0 ** -25 + 3 * 0.31 * 2.0 ** -24 + 3 * 2.0 ** -24)
+    got = base.f64(out)
+    ga, gb = (got[..., :pairs], got[..., pairs:]) if style else (got[..., 0::2], got[..., 1::2])
+    worst = max((np.abs(ga - ra) / tol).max(), (np.abs(gb - rb) / tol).max())
+    assert worst <= 1, (worst, [FREQS[i] for i in np.unique(np.nonzero(np.abs(ga - ra) > tol)[2])])
