@@ -302,7 +302,8 @@ static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStrea
   if (p.row_slots > kRopeAxAngles / p.pairs) p.row_slots = kRopeAxAngles / p.pairs;
   if (p.row_slots < 1) p.row_slots = 1;
   p.cta_rows = p.row_slots;
-  const long long sweeps = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>((p.heads + p.cta_heads - 1) / p.cta_heads);
+  auto row_blocks = [&] { return (static_cast<long long>(p.rows) + p.cta_rows - 1) / p.cta_rows; };    // (rows up to 2^31 - 1)
+  const long long sweeps = row_blocks() * ((p.heads + p.cta_heads - 1) / p.cta_heads);
   if (per >= kRopeAxThreads || sweeps > 152 * 4) {
     p.cta_heads = p.heads < kBatch * slots ? p.heads : kBatch * slots;
     const long long items = static_cast<long long>(p.cta_heads) * p.units;
@@ -335,7 +336,7 @@ static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStrea
   p.by_span = thread_divisor(p.units < kRopeAxThreads ? p.units : kRopeAxThreads);
   p.by_head_slots = thread_divisor(p.head_slots);
   p.by_pairs = thread_divisor(p.pairs);
-  const long long blocks = (p.rows + p.cta_rows - 1) / p.cta_rows * static_cast<long long>(p.groups);
+  const long long blocks = row_blocks() * p.groups;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   auto* kernel = halves ? rope_axes_kernel<T, N, true, false, kBatch> : rope_axes_kernel<T, N, false, false, kBatch>;
   if constexpr (N > 1) {

@@ -385,3 +385,18 @@ def test_angles_of_every_size(style, negative):
     ga, gb = (got[..., :pairs], got[..., pairs:]) if style else (got[..., 0::2], got[..., 1::2])
     worst = max((np.abs(ga - ra) / tol).max(), (np.abs(gb - rb) / tol).max())
     assert worst <= 1, (worst, [FREQS[i] for i in np.unique(np.nonzero(np.abs(ga - ra) > tol)[2])])
+
+
+@pytest.mark.parametrize("rows", [2 ** 31 - 1, 2 ** 31 - 2049])
+def test_the_most_rows(rows):
+    """Row counts up to int32's largest (8.6 GB of queries and of positions)."""
+    pos = torch.arange(rows, dtype=I32, device="cuda")
+    q = torch.ones(rows, 1, 2, dtype=BF16, device="cuda")
+    q[..., 1] = 0.5
+    inv = torch.tensor([0.25], device="cuda")
+    tv.rope_axes(tv.rope_axes_geom(1, 0, 2, [1], 0), q, None, pos[None], inv, q, None)
+    at = torch.cat([torch.arange(5000), torch.arange(rows - 5000, rows), torch.randint(0, rows, (200000,))]).cuda()
+    angle = at.double() * 0.25
+    want = torch.stack([angle.cos() - 0.5 * angle.sin(), 0.5 * angle.cos() + angle.sin()], 1)
+    # the float64 angle is exact (a power of two times an integer); bf16's rounding and float32's, as above
+    assert bool(((q[at, 0].double() - want).abs() <= base.HALF[BF16] * want.abs() + 1.5 * 8 * 2.0 ** -24).all())
