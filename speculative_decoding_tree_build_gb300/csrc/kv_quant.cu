@@ -376,6 +376,10 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
       !tv::aligned(k_cache, 16) || !tv::aligned(v_cache, 16) || !tv::aligned(k_scale, 4) ||
       !tv::aligned(v_scale, 4))
     return TV_ERR_MISALIGNED;
+  const int dev = tv::current_device();
+  if (dev < 0) return TV_ERR_CUDA;
+  const int sms = tv::device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
   tv::AppendParams p = {};
   p.k_new = static_cast<const __nv_bfloat16*>(k_new);
   p.v_new = static_cast<const __nv_bfloat16*>(v_new);
@@ -396,7 +400,7 @@ extern "C" int tv_kv_quant_append(const tv_geom* geom, int32_t kv_format, int32_
   p.by_heads = tv::thread_divisor(p.cta_heads);
   const int head_blocks = (heads + p.cta_heads - 1) / p.cta_heads;
   // (or a whole number of times)
-  const long long work = static_cast<long long>(rows) * head_blocks, wave = 152 * tv::kAppendPerSm;
+  const long long work = static_cast<long long>(rows) * head_blocks, wave = static_cast<long long>(sms) * tv::kAppendPerSm;
   const long long waves = (work + wave * tv::kAppendMaxRows - 1) / (wave * tv::kAppendMaxRows);
   long long cta_rows = (work + waves * wave - 1) / (waves * wave);
   cta_rows = (cta_rows + p.slots - 1) / p.slots * p.slots;

@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kRopeAxThreads, kHalves ? 3 : 4) rope_axes_ker
 }
 
 template <typename T, int N, int kBatch>
-static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStream_t stream) {
+static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, int sms, cudaStream_t stream) {
   const int per_unit = halves ? N : (N == 1 ? 1 : N / 2);
   p.rot_units = (p.pairs + per_unit - 1) / per_unit;
   p.units = halves || N == 1 ? p.rot_units + (p.d - 2 * p.pairs) / N : p.d / N;
@@ -294,17 +294,17 @@ static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStrea
   // 3 rows 1 in 16). Single sweeps that do not fit at once cost a second wave:
   // 502 rows of 20 heads of 17 units 3.3 us in 1004 CTAs, 1.8 us in 502.
   const long long row_items = static_cast<long long>(p.heads) * p.units;
-  const long long per = row_items * p.rows / (152 * 8);
+  const long long per = row_items * p.rows / (sms * 8);
   p.head_slots = p.heads < slots ? p.heads : slots;
   p.cta_heads = p.head_slots;
   p.row_slots = slots / p.head_slots;
-  if (p.row_slots > p.rows / (152 * 2)) p.row_slots = p.rows / (152 * 2);
+  if (p.row_slots > p.rows / (sms * 2)) p.row_slots = p.rows / (sms * 2);
   if (p.row_slots > kRopeAxAngles / p.pairs) p.row_slots = kRopeAxAngles / p.pairs;
   if (p.row_slots < 1) p.row_slots = 1;
   p.cta_rows = p.row_slots;
   auto row_blocks = [&] { return (static_cast<long long>(p.rows) + p.cta_rows - 1) / p.cta_rows; };    // (rows up to 2^31 - 1)
   const long long sweeps = row_blocks() * ((p.heads + p.cta_heads - 1) / p.cta_heads);
-  if (per >= kRopeAxThreads || sweeps > 152 * 4) {
+  if (per >= kRopeAxThreads || sweeps > sms * 4) {
     p.cta_heads = p.heads < kBatch * slots ? p.heads : kBatch * slots;
     const long long items = static_cast<long long>(p.cta_heads) * p.units;
     // (twenty narrow vectors: 10181 rows of 26 heads with 50 pairs, float32, 63.5 -> 55.3 us; single elements not)
@@ -350,17 +350,17 @@ static cudaError_t launch_rope_axes_with(RopeAxParams& p, bool halves, cudaStrea
 // -> 49 us. With few heads there is nothing to gain (2 + 2 heads with 41 pairs 23 ->
 // 26 us), nor with single bf16 values (32 heads with 63 pairs 23 -> 29 us).
 template <typename T, int N>
-static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, cudaStream_t stream) {
+static cudaError_t launch_rope_axes(RopeAxParams& p, bool halves, int sms, cudaStream_t stream) {
   if constexpr (N * sizeof(T) == 4 || N * sizeof(T) == 8) {
-    if (p.heads > kRopeAxNarrow) return launch_rope_axes_with<T, N, kRopeAxNarrow>(p, halves, stream);
+    if (p.heads > kRopeAxNarrow) return launch_rope_axes_with<T, N, kRopeAxNarrow>(p, halves, sms, stream);
   }
-  return launch_rope_axes_with<T, N, kRopeAxBatch>(p, halves, stream);
+  return launch_rope_axes_with<T, N, kRopeAxBatch>(p, halves, sms, stream);
 }
 
 // The widest vector (16, 8 or 4 bytes, else single elements) that the addresses,
 // strides, head dimension and, for pairs of two halves, the pairs allow.
 template <typename T>
-static cudaError_t launch_rope_axes_any(RopeAxParams& p, bool halves, bool keys, cudaStream_t stream) {
+static cudaError_t launch_rope_axes_any(RopeAxParams& p, bool halves, bool keys, int sms, cudaStream_t stream) {
   auto fits = [&](int n) {
     const uintptr_t bytes = n * sizeof(T);
     return p.d % n == 0 && (!halves || p.pairs % n == 0) && p.q_ld % n == 0 && p.q_out_ld % n == 0 && aligned(p.q, bytes) &&
@@ -368,12 +368,12 @@ static cudaError_t launch_rope_axes_any(RopeAxParams& p, bool halves, bool keys,
            (!keys || (p.k_ld % n == 0 && p.k_out_ld % n == 0 && aligned(p.k, bytes) && aligned(p.k_out, bytes)));
   };
   constexpr int kFull = 16 / sizeof(T);
-  if (fits(kFull)) return launch_rope_axes<T, kFull>(p, halves, stream);
-  if (fits(kFull / 2)) return launch_rope_axes<T, kFull / 2>(p, halves, stream);
+  if (fits(kFull)) return launch_rope_axes<T, kFull>(p, halves, sms, stream);
+  if (fits(kFull / 2)) return launch_rope_axes<T, kFull / 2>(p, halves, sms, stream);
   if constexpr (kFull / 4 > 1) {
-    if (fits(kFull / 4)) return launch_rope_axes<T, kFull / 4>(p, halves, stream);
+    if (fits(kFull / 4)) return launch_rope_axes<T, kFull / 4>(p, halves, sms, stream);
   }
-  return launch_rope_axes<T, 1>(p, halves, stream);
+  return launch_rope_axes<T, 1>(p, halves, sms, stream);
 }
 
 }  // namespace tv
@@ -405,6 +405,10 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
   if (!tv::aligned(q, size) || !tv::aligned(q_out, size) || !tv::aligned(positions, 4) ||
       !tv::aligned(inv_freq, 4) || (keys && (!tv::aligned(k, size) || !tv::aligned(k_out, size))))
     return TV_ERR_MISALIGNED;
+  const int dev = tv::current_device();
+  if (dev < 0) return TV_ERR_CUDA;
+  const int sms = tv::device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
   tv::RopeAxParams p = {};
   p.q = q; p.k = k; p.positions = positions; p.inv_freq = inv_freq; p.q_out = q_out; p.k_out = k_out;
   p.q_ld = q_ld; p.k_ld = k_ld; p.q_out_ld = q_out_ld; p.k_out_ld = k_out_ld; p.pos_ld = pos_ld;
@@ -424,7 +428,7 @@ extern "C" int tv_rope_axes(const tv_rope_axes_geom* g, int32_t rows, int32_t dt
   }
   const bool halves = g->rope_style == 1;
   const cudaError_t err = dtype == TV_DTYPE_BF16
-      ? tv::launch_rope_axes_any<__nv_bfloat16>(p, halves, keys, tv::as_stream(stream))
-      : tv::launch_rope_axes_any<float>(p, halves, keys, tv::as_stream(stream));
+      ? tv::launch_rope_axes_any<__nv_bfloat16>(p, halves, keys, sms, tv::as_stream(stream))
+      : tv::launch_rope_axes_any<float>(p, halves, keys, sms, tv::as_stream(stream));
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
