@@ -402,8 +402,15 @@ def _native():
                 "speculative_decoding_tree_build_gb300.build` (or __graft_entry__.build()); there is "
                 "no fallback implementation")
         spec = importlib.util.spec_from_file_location("_treeverify_torch", ext_path)
-        _ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_ext)
+        try:
+            ext = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(ext)
+            built_for = ext.torch_version
+        except ImportError as e:
+            built_for = f"another version ({e})"
+        if built_for != torch.__version__:
+            raise ImportError(f"{ext_path} was built for torch {built_for}, this is {torch.__version__}: build it again")
+        _ext = ext
     return _ext
 
 

@@ -337,4 +337,9 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_treeverify_torch", nullptr, -1, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__treeverify_torch() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__treeverify_torch() {
+  PyObject* m = PyModule_Create(&kModule);
+  // the loader compares it with the torch that is running
+  if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", TV_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}
