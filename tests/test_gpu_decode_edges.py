@@ -400,3 +400,77 @@ def test_the_most_rows(rows):
     want = torch.stack([angle.cos() - 0.5 * angle.sin(), 0.5 * angle.cos() + angle.sin()], 1)
     # the float64 angle is exact (a power of two times an integer); bf16's rounding and float32's, as above
     assert bool(((q[at, 0].double() - want).abs() <= base.HALF[BF16] * want.abs() + 1.5 * 8 * 2.0 ** -24).all())
+
+
+# ---------------------------------------------------------------- one-token attention: more units than thread blocks
+
+
+def ragged_batch(seed, batch, longest, rng):
+    lens = np.exp(rng.uniform(0, np.log(longest), batch)).astype(int).tolist()
+    lens[0], lens[1], lens[2], lens[-1] = 0, 1, longest, 0
+    return lens
+
+
+@pytest.mark.parametrize("held", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("batch,hkv,group,d,longest", [
+    (1500, 1, 3, 64, 40),
+    (100, 8, 4, 128, 700),
+    (100, 8, 8, 64, 400),
+    (90, 8, 5, 128, 300),
+    (60, 12, 11, 128, 250),
+    (700, 1, 16, 64, 90),
+])
+def test_more_units_than_blocks_in_two_launches(batch, hkv, group, d, longest, held):
+    """Tables wide enough for two launches, and more (request, head) units than thread blocks, whose
+    records then go by block: empty, tiny and longer requests, a flagged one and one with a missing
+    page, in a unit that two blocks share."""
+    rng = np.random.default_rng(241)
+    lens = ragged_batch(242, batch, longest, rng)
+    c = widened(base.filled(243, lens, hkv, d, held), 2400)
+    q = torch.randn(batch, group * hkv, d, generator=base.gen(244), device="cuda").to(BF16)
+    assert batch * hkv > 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    status = [0] * batch
+    missing, flagged = 2, batch // 2                      # the longest one lacks its last page but one
+    lens[flagged] = max(lens[flagged], 1)
+    status[flagged] = 16
+    page = max((lens[missing] - 1) // 16 - 1, 0)
+    good = int(c.table[missing, page])
+    some = sorted(set(rng.choice(batch, 20).tolist() + [0, 1, batch - 1]) - {missing, flagged})
+    for bad in (good, -1, c.pool):
+        c.table[missing, page] = bad
+        out, lse, got = base.run_decode(c, q, lens, base.i32(status))
+        want = list(status)
+        if bad != good:
+            want[missing] = 8
+        assert got == want
+        for b in range(batch):
+            if want[b]:
+                assert bool((out[b] == 9.0).all()) and bool((lse[b] == 9.0).all())
+        base.check_decode(c, q, lens, out, lse, which=some + ([missing] if bad == good else []))
+    again = base.run_decode(c, q, lens, base.i32(status))
+    assert np.array_equal(base.bits(out), base.bits(again[0])) and np.array_equal(base.bits(lse), base.bits(again[1]))
+
+
+def test_every_request_of_a_batch_in_two_launches():
+    """All of 1500 requests checked against float32 arithmetic on the same GPU, not a sample of them."""
+    rng = np.random.default_rng(245)
+    lens = ragged_batch(246, 1500, 300, rng)
+    c = widened(base.filled(247, lens, 1, 64, "bf16"), 2400)
+    q = torch.randn(1500, 2, 64, generator=base.gen(248), device="cuda").to(BF16)
+    out, lse, status = base.run_decode(c, q, lens)
+    assert status == [0] * 1500
+    page = c.table.long()[:, :19].clamp(min=0)
+    seen = torch.arange(19 * 16, device="cuda") < torch.tensor(lens, device="cuda")[:, None]
+    k = c.k[page].double().permute(0, 2, 1, 3, 4).reshape(1500, 304, 64)
+    v = torch.where(seen[..., None], c.v[page].double().permute(0, 2, 1, 3, 4).reshape(1500, 304, 64), 0.0)
+    score = torch.where(seen[:, None], torch.einsum("bhd,bnd->bhn", q.double(), torch.where(seen[..., None], k, 0.0)) / 8, -INF)
+    want_lse = torch.logsumexp(score, -1)
+    p = torch.where(seen[:, None], torch.exp(score - torch.where(want_lse > -INF, want_lse, 0.0)[..., None]), 0.0)
+    want = p @ v
+    # as base.decode_tolerance
+    big = torch.einsum("bhd,bnd->bhn", q.double().abs(), torch.where(seen[..., None], k, 0.0).abs()).amax(-1, keepdim=True) / 8
+    rel = 2.0 ** -16 + 2 * (68 * 2.0 ** -24 * big + 2.0 ** -21) + 2 * 300 * 2.0 ** -24
+    tol = rel * (p @ v.abs()) + base.HALF[BF16] * want.abs() + 1e-30
+    assert bool(((out.double() - want).abs() <= tol).all())
+    fin = want_lse > -INF
+    assert bool(((lse.double() - want_lse).abs() <= rel[..., 0] + 2.0 ** -22 * want_lse.abs())[fin].all()) and bool(torch.isneginf(lse[~fin]).all())
