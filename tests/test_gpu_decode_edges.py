@@ -2,7 +2,9 @@
 counts past 32 bits, offsets that overlap, values that are not finite, more
 units than thread blocks, and the measured cases' own plain forms."""
 
+import importlib.util
 import os
+import random
 import subprocess
 import sys
 
@@ -474,3 +476,66 @@ def test_every_request_of_a_batch_in_two_launches():
     assert bool(((out.double() - want).abs() <= tol).all())
     fin = want_lse > -INF
     assert bool(((lse.double() - want_lse).abs() <= rel[..., 0] + 2.0 ** -22 * want_lse.abs())[fin].all()) and bool(torch.isneginf(lse[~fin]).all())
+
+
+# ---------------------------------------------------------------- the measured cases
+
+
+def measured():
+    spec = importlib.util.spec_from_file_location("operators", os.path.join(ROOT, "perf", "operators.py"))
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def largest(t):
+    return float(t.double().nan_to_num(0.0).abs().max()) if t.numel() else 0.0
+
+
+def close_to_exact(m, case, seed):
+    """Both forms of a measured case against its definition in 64 bits and against each other."""
+    exact = m.exact(case, seed)
+    got = {}
+    for own in (False, True):
+        m.own = own
+        state = m.prepare(case, seed)
+        got[own] = {k: t.clone() for k, t in m.run(state).items()}
+        for name, want in exact.items():
+            if want is None:
+                continue
+            x = got[own][name]
+            if case["op"] == "decode":
+                s = state
+                scale = [1.0 if t is None else largest(t) for t in (s["ks"], s["vs"])]
+                v = largest(s["v"]) * scale[1]
+                score = 132 * 2.0 ** -24 * (largest(s["q"]) * largest(s["k"]) * scale[0] * case["d"] ** 0.5) + 2.0 ** -21
+                err = 2.0 ** -11 + 2 * score + case["hi"] * 2.0 ** -23
+                tol = base.HALF[BF16] * want.abs() + err * v if name == "out" else err + 2.0 ** -22 * want.abs()
+            elif case["op"] == "rope":
+                tol = base.HALF[x.dtype] * want.abs() + 2 * largest(state[name]) * 7 * 2.0 ** -24
+            else:                                         # one rounding, of a scale to float32 or a value to bf16
+                tol = base.HALF.get(x.dtype, 0.0) * want.abs()
+            same = (x.double() == want) | ((x.double() - want).abs() <= tol)
+            assert bool(same.all()), (case.get("name"), own, name)
+    assert torch.equal(got[False].get("status", torch.zeros(1)), got[True].get("status", torch.zeros(1)))
+    if case["op"] in ("append", "read"):
+        for name in got[True]:
+            assert torch.equal(got[False][name].view(torch.uint8), got[True][name].view(torch.uint8)), name
+
+
+@pytest.mark.parametrize("name", ["rope-step", "rope-image", "append-step", "append-ragged", "read-step", "decode-short",
+                                  "decode-wide"])
+def test_measured_cases(name):
+    m = measured()
+    close_to_exact(m, next(c for c in m.listed() if c["name"] == name), 3)
+
+
+def test_measured_cases_drawn():
+    m = measured()
+    rng, seen = random.Random(7), 0
+    while seen < 8:
+        case = m.draw(rng)
+        work = m.work(case)
+        if work["bytes"] < 3e7 and work["flops"] < 1e9:
+            close_to_exact(m, case, seen)
+            seen += 1
