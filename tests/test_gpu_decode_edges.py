@@ -539,3 +539,48 @@ def test_measured_cases_drawn():
         if work["bytes"] < 3e7 and work["flops"] < 1e9:
             close_to_exact(m, case, seen)
             seen += 1
+
+
+# ---------------------------------------------------------------- together with the tree step
+
+
+@pytest.mark.parametrize("held", ["e4m3", "int8"])
+def test_a_tree_step_over_an_8_bit_cache_and_back(held):
+    """The cache read back, the tree step on the bf16 pools, its accepted rows gathered from them and
+    appended, and the next token's attention over the 8-bit cache."""
+    from gen import workloads as wl
+    from speculative_decoding_tree_build_gb300.step import DeviceBatch
+    w = wl.make_config(2, batch=3, prompt_scale=0.1)
+    z = DeviceBatch(w)
+    hq, hkv, d = w["num_q_heads"], w["num_kv_heads"], w["head_dim"]
+    plen = [int(x) for x in w["prompt_len"]]
+    depth = int(w["max_depth"])
+    c = base.Cache(251, [n + depth + 1 for n in plen], hkv, d, held)
+    cu = [0] + np.cumsum(plen).tolist()
+
+    def gathered(first, counts):
+        """Rows first[b].. of each request from the bf16 pools, [rows][Hkv][D]."""
+        req = torch.repeat_interleave(torch.arange(len(counts), device="cuda"), torch.tensor(counts, device="cuda"))
+        slot = torch.cat([torch.arange(f, f + n, device="cuda") for f, n in zip(first, counts)])
+        page = z.block_table[req, slot // 16].long()
+        return z.k_cache[page, :, slot % 16], z.v_cache[page, :, slot % 16]
+
+    k, v = gathered([0] * 3, plen)
+    assert base.run_append(c, k, v, cu, [0] * 3) == [0] * 3
+    status = base.i32([0] * 3)
+    tv.kv_quant_read(c.geom, None, base.i32(plen), c.table, c.n_blocks, c.k, c.v, c.ks, c.vs, z.block_table, z.n_blocks,
+                     z.k_cache, z.v_cache, status)
+    z.step()
+    assert status.tolist() == z.status.tolist() == [0] * 3
+    new = z.new_len.tolist()
+    count = [b - a for a, b in zip(plen, new)]
+    assert min(count) >= 1 and max(count) <= depth + 1
+    k, v = gathered(plen, count)
+    cu = [0] + np.cumsum(count).tolist()
+    before = [t.clone() for t in (c.k, c.v, c.ks, c.vs)]
+    assert base.run_append(c, k, v, cu, plen) == [0] * 3
+    base.check_append(c, before, k, v, cu, plen, range(3))
+    q = torch.randn(3, hq, d, generator=base.gen(252), device="cuda").to(BF16)
+    out, lse, got = base.run_decode(c, q, new)
+    assert got == [0] * 3
+    base.check_decode(c, q, new, out, lse)
