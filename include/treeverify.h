@@ -562,8 +562,13 @@ typedef struct tv_rope_axes_geom {
  * turn in 64-bit fixed point, so it does not lose digits at far positions: it is
  * within 2^-30 turns (6e-9 rad) for every position and every finite inv_freq. The
  * rotation is float32, rounded once to the output type.
- * tv_tree_attention_verify rotates a tree's own nodes; this call serves the
- * prompts, and decode steps ahead of tv_kv_quant_append / tv_decode_attention.
+ * This call serves prompts, and decode steps ahead of tv_kv_quant_append /
+ * tv_decode_attention. tv_tree_attention_verify rotates a tree's own nodes, over
+ * all D / 2 pairs, with rope_base's frequencies and at the positions that it is
+ * given (tv_tree_build's are prompt length + depth). So a prompt rotated in part,
+ * by sections at different positions or with other frequencies goes on with
+ * tv_decode_attention and not in a tree; after one whose last position is not its
+ * length - 1 (images), a tree's positions have to be written by the caller.
  *
  *  rows           tokens (0 is a no-op)
  *  dtype          TV_DTYPE_* of q, k and the outputs
@@ -695,8 +700,8 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  *  block_table, n_blocks, max_blocks_per_req, num_blocks
  *                 as elsewhere; requests may share blocks
  *  k_cache, v_cache   pools of the given format, 16-byte aligned
- *  k_scale, v_scale   float32 [num_blocks][Hkv][16], not negative; NULL for
- *                 TV_KV_BF16
+ *  k_scale, v_scale   float32 [num_blocks][Hkv][16], finite and not negative,
+ *                 or NaN for a row that reads as NaN; NULL for TV_KV_BF16
  *  out            bf16 [batch][Hq][D] out
  *  lse            float32 [batch][Hq] out, or NULL
  *  workspace      device scratch of tv_decode_workspace_bytes() bytes

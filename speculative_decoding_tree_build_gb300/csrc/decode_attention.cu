@@ -42,7 +42,7 @@
 // round trip less ahead of the first cached row (launch_decode has the rule).
 //
 // Measured: 64 requests of 4096 to 32768 keys, 32/8 heads of 128, e4m3 (1.9
-// GB) 290 us, 6.5 TB/s; one of 32768 keys, bf16 (134 MB) 28 us, of which the
+// GB) 295 us, 6.4 TB/s; one of 32768 keys, bf16 (134 MB) 28 us, of which the
 // first grid 20.
 #include <cuda_fp16.h>
 
@@ -217,8 +217,8 @@ struct DecTraits {
   static constexpr int NT = kQ > 8 ? 2 : 1;                    // MMA tiles of eight queries
   // A weight goes to the MMA as a number of the values' 16-bit type. In one part
   // bf16's rounding would add as much to the error as the output's own does, so
-  // over bf16 pools it goes in two parts. f16's is an eighth of that: 0.00168
-  // against 64 bits, with two parts 0.00167, all of it the output's rounding.
+  // over bf16 pools it goes in two parts. f16's is an eighth of that: 0.00167
+  // against 64 bits, where the output's own rounding makes 0.00166.
   // Up to four queries stand twice among the MMA's eight, the first four for the
   // first parts and the others for the second, so there two parts cost no product
   // (e4m3, 1.9 GB: 293.7 -> 295.4 us) and are taken for all formats. With more

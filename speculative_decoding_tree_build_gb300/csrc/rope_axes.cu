@@ -16,8 +16,8 @@
 // cosines of a row are computed once in shared memory. A thread keeps the same
 // columns and the same (at most four or eight) heads of every row it takes, so it
 // reads a row's sines once into registers and steps its pointers by a fixed
-// stride; its first vectors are in flight while the angles are made. 57 us for
-// 16201 rows of 40 heads of 128 (332 MB, 5.8 TB/s, half of it writes).
+// stride; its first vectors are in flight while the angles are made. 56 us for
+// 16201 rows of 40 heads of 128 (332 MB, 5.9 TB/s, half of it writes).
 // (Items numbered across rows, heads and columns, with divisions for each,
 // float64 for F and sincospif took 175 instructions a vector and were bound
 // by issue: 93 us for 332 MB. A small call's time went into divisions of thread
