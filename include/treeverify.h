@@ -684,7 +684,7 @@ int tv_decode_workspace_bytes(const tv_geom* geom, int32_t batch, size_t* bytes)
  * out = 0 and lse = -inf. Slots from seq_len[b] on may hold anything.
  * Infinities and NaN act as in the formula: an infinite value of a bf16 pool
  * reaches the output (beside a weight below 2^-126 of the largest, which is 0
- * in float32, it makes a NaN), a score of -inf has no weight, a score of +inf or
+ * in float32, it may make a NaN), a score of -inf has no weight, a score of +inf or
  * NaN makes the query's out and lse NaN. Weighted sums are float32 before they
  * are divided: over bf16 pools |v| * keys has to stay below 2^120. The
  * result does not depend on timing: the split over the cache's length is a
