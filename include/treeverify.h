@@ -55,6 +55,13 @@
  *   tv_decode_attention       attention of one new token per request over a
  *                             paged cache (bf16 or 8 bits)
  *
+ * Around a serving step, pages and slots:
+ *
+ *   tv_block_tables           block tables grown and shrunk to the requests' lengths
+ *                             from a free list on the device
+ *   tv_slot_map               the slot of every new row
+ *   tv_kv_rows_write / _read  bf16 K/V rows to and from slots of the paged cache
+ *
  * Conventions shared by every call
  * --------------------------------
  *  - All array arguments are DEVICE pointers owned by the caller. The library
@@ -108,6 +115,7 @@ extern "C" {
 #define TV_ST_PATH_OVERFLOW 16     /* accepted path longer than max_depth */
 #define TV_ST_TIMEOUT 32           /* a bounded device wait gave up; that request's outputs are invalid */
 #define TV_ST_BAD_TEMPERATURE 64   /* temperature negative or NaN, or > 0 with no noise array */
+#define TV_ST_NO_BLOCKS 128        /* the free list is too short for the blocks that the request lacks */
 
 #define TV_MAX_NODES 1024          /* largest tree (root included) per request */
 #define TV_BLOCK_SIZE 16
@@ -716,6 +724,97 @@ int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32_t batch, c
                         const void* v_cache, const float* k_scale, const float* v_scale,
                         int32_t num_blocks, void* out, float* lse, void* workspace,
                         size_t workspace_bytes, int32_t* status, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Pages and slots
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Bring the requests' block tables to the lengths that they are to hold,
+ * from and to a list of free blocks on the device. Request b shall hold
+ * ceil(want_len[b] / 16) blocks. free_blocks[0 .. free_count[0]) is a stack, its
+ * last entry the top. In this order:
+ *   1. the released_count[b] ids of released[b] (as tv_kv_commit leaves them) go
+ *      onto the list; released_count[b] becomes 0, so none goes there twice;
+ *   2. a request that holds more than it wants gives the blocks past its end
+ *      back, and these table entries become -1;
+ *   3. a request that holds less takes blocks from the list, if there are enough:
+ *      requests are served in their order, and from the first one on whose blocks
+ *      the list does not hold, all that lack blocks get TV_ST_NO_BLOCKS and keep
+ *      what they hold.
+ * Each step takes requests in ascending order and a request's blocks in
+ * ascending order; taking starts at the top, giving back fills the list so that
+ * taking the same numbers again yields the same blocks (a call that shrinks what
+ * the call before it grew restores list and tables).
+ *
+ *  batch          0..4096
+ *  want_len       int32 [batch] slots (prompt, or prompt + nodes for a step); 0
+ *                 gives all blocks back
+ *  block_table, n_blocks   in/out; table entries from n_blocks[b] on are not read
+ *  num_blocks     blocks of the pools, and the list's capacity
+ *  free_blocks    int32 [num_blocks] in/out, distinct ids in [0, num_blocks)
+ *  free_count     int32 [1] in/out
+ *  released       int32 [batch][max_blocks_per_req] and
+ *  released_count int32 [batch] in/out, or both NULL
+ *  status         in/out: requests with non-zero status are skipped;
+ *                 TV_ST_NO_BLOCKS, TV_ST_BAD_SIZE (want_len < 0 or past the table,
+ *                 n_blocks or released_count outside [0, max_blocks_per_req]) and
+ *                 TV_ST_BAD_BLOCK (an id to give back outside [0, num_blocks)) are
+ *                 OR-ed in. A request flagged for its size or ids is left as it is;
+ *                 one without blocks has given its released ids back. Where the
+ *                 list could not hold all that comes back (some of it is there
+ *                 already) or free_count is outside [0, num_blocks], every request
+ *                 gets TV_ST_BAD_SIZE and nothing changes.
+ * tv_tree_build overwrites status, so it comes before this call in a step.
+ */
+int tv_block_tables(int32_t batch, const int32_t* want_len, int32_t* block_table,
+                    int32_t* n_blocks, int32_t max_blocks_per_req, int32_t num_blocks,
+                    int32_t* free_blocks, int32_t* free_count, const int32_t* released,
+                    int32_t* released_count, int32_t* status, void* stream);
+
+/*
+ * The slot of every row of a ragged batch: row i of request b (array row
+ * cu_rows[b] + i) goes to slot s = start_len[b] + i of the request, which is
+ * slots[row] = block_table[b][s / 16] * 16 + s % 16 in the pools. Rows of no
+ * request and rows of a flagged request get -1, so that a reader of the whole
+ * array (tv_kv_rows_write, or an indexing operation that masks them) never meets
+ * the slots of an earlier step.
+ *
+ *  batch          0..4096 (0: every row gets -1)
+ *  rows           entries of slots (0 is a no-op); all of them are written
+ *  cu_rows        int32 [batch+1], offsets as for tv_kv_quant_append: requests that
+ *                 end before they begin, or have rows and begin before an earlier
+ *                 offset or end behind `rows`, are flagged
+ *  start_len, block_table, n_blocks, max_blocks_per_req, num_blocks
+ *                 as for tv_kv_quant_append; the blocks of all slots must be held
+ *  slots          int64 [rows] out
+ *  status         in/out: requests with non-zero status get -1; TV_ST_BAD_SIZE and
+ *                 TV_ST_BAD_BLOCK are OR-ed in (all of the request's rows get -1)
+ */
+int tv_slot_map(int32_t batch, int32_t rows, const int32_t* cu_rows, const int32_t* start_len,
+                const int32_t* block_table, const int32_t* n_blocks, int32_t max_blocks_per_req,
+                int32_t num_blocks, int64_t* slots, int32_t* status, void* stream);
+
+/*
+ * Copy K/V rows to slots of the bf16 pools (a prompt's rows, a token's own row
+ * ahead of tv_decode_attention), and back (rows that a tree step accepted, ahead
+ * of tv_kv_quant_append). Rows whose slot lies outside [0, 16 * num_blocks) are
+ * skipped: nothing is written for them, in the pools or in k_out / v_out.
+ *
+ *  geom           num_kv_heads (<= 4096), head_dim and block_size are used
+ *  rows           0 is a no-op
+ *  k_new, v_new, k_out, v_out
+ *                 bf16 [rows][Hkv][D], heads back to back, rows k_ld / v_ld
+ *                 ELEMENTS apart (>= Hkv * D, a multiple of 8), 16-byte aligned
+ *  slots          int64 [rows] (tv_slot_map); no slot twice in a write
+ *  k_cache, v_cache   bf16 pools; no array of the call may overlap what it writes
+ */
+int tv_kv_rows_write(const tv_geom* geom, int32_t rows, const void* k_new, int64_t k_ld,
+                     const void* v_new, int64_t v_ld, const int64_t* slots, void* k_cache,
+                     void* v_cache, int32_t num_blocks, void* stream);
+int tv_kv_rows_read(const tv_geom* geom, int32_t rows, const int64_t* slots, const void* k_cache,
+                    const void* v_cache, int32_t num_blocks, void* k_out, int64_t k_ld, void* v_out,
+                    int64_t v_ld, void* stream);
 
 /* Name of a TV_ERR_* code or of a single TV_ST_* flag. */
 const char* tv_status_string(int code);

@@ -24,6 +24,7 @@ __all__ = [
     "eagle_expand_select", "eagle_rerank", "tree_mask_dense", "dense_mask_elements",
     "TvRopeAxes", "rope_axes_geom", "rope_axes", "KV_BF16", "KV_E4M3", "KV_INT8", "kv_quant_append",
     "kv_quant_read", "decode_workspace_bytes", "decode_attention",
+    "block_tables", "slot_map", "kv_rows_write", "kv_rows_read",
     "status_string", "version",
 ]
 
@@ -32,7 +33,7 @@ lib_path = os.path.join(_PKG, "libtreeverify.so")
 
 TV_OK = 0
 TV_ST = {"BAD_SIZE": 1, "BAD_ROOT": 2, "BAD_PARENT": 4, "BAD_BLOCK": 8,
-         "PATH_OVERFLOW": 16, "TIMEOUT": 32, "BAD_TEMPERATURE": 64}
+         "PATH_OVERFLOW": 16, "TIMEOUT": 32, "BAD_TEMPERATURE": 64, "NO_BLOCKS": 128}
 
 
 class TvGeom(ctypes.Structure):
@@ -91,6 +92,10 @@ _SIGS = {
     "tv_decode_workspace_bytes": [ctypes.POINTER(TvGeom), _I, ctypes.POINTER(_SZ)],
     "tv_decode_attention": [ctypes.POINTER(TvGeom), _I, _I, _P, _I64, _P, _P, _P, _I, _P, _P, _P, _P,
                             _I, _P, _P, _P, _SZ, _P, _P],
+    "tv_block_tables": [_I, _P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P],
+    "tv_slot_map": [_I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P],
+    "tv_kv_rows_write": [ctypes.POINTER(TvGeom), _I, _P, _I64, _P, _I64, _P, _P, _P, _I, _P],
+    "tv_kv_rows_read": [ctypes.POINTER(TvGeom), _I, _P, _P, _P, _I, _P, _I64, _P, _I64, _P],
     "tv_status_string": [ctypes.c_int],
     "tv_version": [],
 }
@@ -467,3 +472,39 @@ def decode_attention(g: TvGeom, q, seq_len, block_table, n_blocks, k_cache, v_ca
     rc = (_ext or _native()).decode_attention(g, q, seq_len, block_table, n_blocks, k_cache, v_cache,
                                               k_scale, v_scale, out, lse, workspace, status, stream)
     return rc and _check("tv_decode_attention", rc)
+
+
+# ---------------------------------------------------------------- pages and slots
+
+def block_tables(want_len, block_table, n_blocks, free_blocks, free_count, status, released=None,
+                 released_count=None, stream=None):
+    """Bring the requests' block tables to ``want_len`` slots each, from and to
+    the list ``free_blocks[:free_count]`` (int32, one entry per block of the
+    pools); ``released``/``released_count`` as kv_commit leaves them go onto the
+    list first. A request that the list has no blocks for gets NO_BLOCKS."""
+    rc = (_ext or _native()).block_tables(want_len, block_table, n_blocks, free_blocks, free_count,
+                                          released, released_count, status, stream)
+    return rc and _check("tv_block_tables", rc)
+
+
+def slot_map(cu_rows, start_len, block_table, n_blocks, num_blocks, slots, status, stream=None):
+    """``slots`` (int64 [rows]): where row i of request b, array row
+    ``cu_rows[b] + i``, lies in the pools (block * 16 + slot % 16 of the request's
+    slot ``start_len[b] + i``); -1 for rows of no request or of a flagged one."""
+    rc = (_ext or _native()).slot_map(cu_rows, start_len, block_table, n_blocks, num_blocks, slots,
+                                      status, stream)
+    return rc and _check("tv_slot_map", rc)
+
+
+def kv_rows_write(g: TvGeom, k_new, v_new, slots, k_cache, v_cache, stream=None):
+    """Copy rows [rows][Hkv][D] (bf16) to ``slots`` of the bf16 pools; rows
+    whose slot lies outside the pools are skipped."""
+    rc = (_ext or _native()).kv_rows_write(g, k_new, v_new, slots, k_cache, v_cache, stream)
+    return rc and _check("tv_kv_rows_write", rc)
+
+
+def kv_rows_read(g: TvGeom, slots, k_cache, v_cache, k_out, v_out, stream=None):
+    """Copy the rows at ``slots`` of the bf16 pools to [rows][Hkv][D] arrays;
+    rows whose slot lies outside the pools are left as they are."""
+    rc = (_ext or _native()).kv_rows_read(g, slots, k_cache, v_cache, k_out, v_out, stream)
+    return rc and _check("tv_kv_rows_read", rc)

@@ -1,6 +1,7 @@
-// Python entry points of the plain-decoding and 8-bit-cache calls.
+// Python entry points of the plain-decoding and 8-bit-cache calls, and of those
+// around a serving step (pages, slots, filtered sampling).
 //
-// A decode step makes these calls once a layer, and at one token a request
+// A decode step makes the first ones once a layer, and at one token a request
 // the GPU needs 2 to 5 us for each: checking a dozen tensors attribute by
 // attribute from Python and converting twenty arguments took 17 us a call.
 // Here the same checks read the tensors directly. Each function returns the
@@ -330,8 +331,98 @@ PyObject* decode_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// [batch] of one type, None allowed where `optional`
+template <typename T>
+T* per_request(Call& c, int i, ScalarType type, const char* name, int64_t batch, bool optional = false) {
+  if (optional && c.none(i)) return nullptr;
+  return static_cast<T*>(c.flat(i, type, name, batch));
+}
+
+int32_t number(PyObject* o, const char* name) {
+  const long long n = PyLong_AsLongLong(o);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be an int");
+  }
+  return count(n, name);
+}
+
+// block_tables(want_len, block_table, n_blocks, free_blocks, free_count, released, released_count, status, stream)
+PyObject* block_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 9);
+    const int32_t* want = c.ints(0, "want_len", 0);
+    const int64_t batch = c.tensor(0, "want_len").numel();
+    const Table t = table_of(c, 1, batch, "block_table");
+    auto* held = per_request<int32_t>(c, 2, ScalarType::Int, "n_blocks", batch);
+    auto* list = static_cast<int32_t*>(c.flat(3, ScalarType::Int, "free_blocks"));
+    const int32_t pool = count(c.tensor(3, "free_blocks").numel(), "free_blocks");
+    auto* top = static_cast<int32_t*>(c.flat(4, ScalarType::Int, "free_count", 1));
+    if (c.none(5) != c.none(6)) refuse("released and released_count come together");
+    const int32_t* released = nullptr;
+    if (!c.none(5)) {
+      const Table r = table_of(c, 5, batch, "released");
+      if (r.width != t.width) refuse("released must be as wide as block_table");
+      released = r.ptr;
+    }
+    auto* released_count = per_request<int32_t>(c, 6, ScalarType::Int, "released_count", batch, true);
+    auto* status = per_request<int32_t>(c, 7, ScalarType::Int, "status", batch);
+    const int32_t requests = count(batch, "batch");
+    return launch(c, a[8], [&](void* s) {
+      return tv_block_tables(requests, want, const_cast<int32_t*>(t.ptr), held, t.width, pool, list, top, released,
+                             released_count, status, s);
+    });
+  });
+}
+
+// slot_map(cu_rows, start_len, block_table, n_blocks, num_blocks, slots, status, stream)
+PyObject* slot_map(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 8);
+    const int32_t* cu = c.ints(0, "cu_rows", 1);
+    const int64_t batch = c.tensor(0, "cu_rows").numel() - 1;
+    const int32_t* start = c.ints(1, "start_len", batch);
+    const Table t = table_of(c, 2, batch, "block_table");
+    const int32_t* held = c.ints(3, "n_blocks", batch);
+    const int32_t blocks = number(a[4], "num_blocks");
+    auto* slots = static_cast<int64_t*>(c.flat(5, ScalarType::Long, "slots"));
+    const int32_t rows = count(c.tensor(5, "slots").numel(), "rows"), requests = count(batch, "batch");
+    auto* status = per_request<int32_t>(c, 6, ScalarType::Int, "status", batch);
+    return launch(c, a[7], [&](void* s) {
+      return tv_slot_map(requests, rows, cu, start, t.ptr, held, t.width, blocks, slots, status, s);
+    });
+  });
+}
+
+// kv_rows_write(geom, k_new, v_new, slots, k_cache, v_cache, stream)
+// kv_rows_read(geom, slots, k_cache, v_cache, k_out, v_out, stream)
+template <bool kWrite>
+PyObject* kv_rows(PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 7);
+    const auto g = structure<tv_geom>(a[0], "geom");
+    const int at = kWrite ? 1 : 4, slot_at = kWrite ? 3 : 1, pool_at = kWrite ? 4 : 2;
+    const Rows k = heads_of(c, at, g.num_kv_heads, g.head_dim, kWrite ? "k_new" : "k_out");
+    const Rows v = heads_of(c, at + 1, g.num_kv_heads, g.head_dim, kWrite ? "v_new" : "v_out");
+    if (k.type != ScalarType::BFloat16 || v.type != ScalarType::BFloat16) refuse("K and V rows must be bfloat16");
+    if (k.rows != v.rows) refuse("K and V must have the same rows");
+    const auto* slots = static_cast<const int64_t*>(c.flat(slot_at, ScalarType::Long, "slots"));
+    if (c.tensor(slot_at, "slots").numel() != k.rows) refuse("slots must hold one slot per row");
+    const Pools p = pools_of(c, g, pool_at, -1);
+    if (p.format != TV_KV_BF16) refuse("k_cache and v_cache must be bfloat16 pools");
+    const int32_t rows = count(k.rows, "rows");
+    return launch(c, a[6], [&](void* s) {
+      return kWrite ? tv_kv_rows_write(&g, rows, k.ptr, k.ld, v.ptr, v.ld, slots, p.k, p.v, p.blocks, s)
+                    : tv_kv_rows_read(&g, rows, slots, p.k, p.v, p.blocks, k.ptr, k.ld, v.ptr, v.ld, s);
+    });
+  });
+}
+PyObject* kv_rows_write(PyObject*, PyObject* const* a, Py_ssize_t n) { return kv_rows<true>(a, n); }
+PyObject* kv_rows_read(PyObject*, PyObject* const* a, Py_ssize_t n) { return kv_rows<false>(a, n); }
+
 #define TV_FN(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TV_FN(rope_axes), TV_FN(kv_quant_append), TV_FN(kv_quant_read), TV_FN(decode_attention),
+                          TV_FN(block_tables), TV_FN(slot_map), TV_FN(kv_rows_write), TV_FN(kv_rows_read),
                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_treeverify_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 

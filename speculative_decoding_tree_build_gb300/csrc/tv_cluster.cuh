@@ -111,8 +111,8 @@ __device__ __forceinline__ void row_barrier(int csize) {
 }
 
 template <typename... KArgs, typename... Args>
-inline cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, int csize,
-                                      cudaStream_t stream, Args&&... args) {
+inline cudaError_t launch_cluster_smem_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, int csize,
+                                           size_t smem, cudaStream_t stream, Args&&... args) {
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -123,11 +123,17 @@ inline cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = block;
-  cfg.dynamicSmemBytes = 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... KArgs, typename... Args>
+inline cudaError_t launch_cluster_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, int csize,
+                                      cudaStream_t stream, Args&&... args) {
+  return launch_cluster_smem_pdl(kernel, grid, block, csize, 0, stream, std::forward<Args>(args)...);
 }
 
 }  // namespace tv
