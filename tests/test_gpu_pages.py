@@ -38,7 +38,7 @@ class Pages:
     def __init__(self, rng, batch, width, pool, released=0):
         ids = rng.sample(range(pool), pool)
         self.pool = pool
-        self.n = [min(rng.randint(0, width), len(ids) // (batch - b)) for b in range(batch)]
+        self.n = [min(rng.randint(0, width), pool // batch) for _ in range(batch)]
         self.table = [[ids.pop() for _ in range(c)] + [-1] * (width - c) for c in self.n]
         self.count = [min(rng.randint(0, released), width, len(ids) // batch) for _ in range(batch)]
         self.released = [[ids.pop() for _ in range(c)] + [-7] * (width - c) for c in self.count]
