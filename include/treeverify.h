@@ -55,12 +55,14 @@
  *   tv_decode_attention       attention of one new token per request over a
  *                             paged cache (bf16 or 8 bits)
  *
- * Around a serving step, pages and slots:
+ * Around a serving step: pages, slots, and the distribution that is sampled:
  *
  *   tv_block_tables           block tables grown and shrunk to the requests' lengths
  *                             from a free list on the device
  *   tv_slot_map               the slot of every new row
  *   tv_kv_rows_write / _read  bf16 K/V rows to and from slots of the paged cache
+ *   tv_sample_filtered        temperature, top-k, top-p, min-p sampling at every node
+ *   tv_filter_logits          the same filter as masked logits
  *
  * Conventions shared by every call
  * --------------------------------
@@ -116,6 +118,7 @@ extern "C" {
 #define TV_ST_TIMEOUT 32           /* a bounded device wait gave up; that request's outputs are invalid */
 #define TV_ST_BAD_TEMPERATURE 64   /* temperature negative or NaN, or > 0 with no noise array */
 #define TV_ST_NO_BLOCKS 128        /* the free list is too short for the blocks that the request lacks */
+#define TV_ST_BAD_FILTER 256       /* top_k negative, or top_p or min_p outside [0, 1] */
 
 #define TV_MAX_NODES 1024          /* largest tree (root included) per request */
 #define TV_BLOCK_SIZE 16
@@ -815,6 +818,73 @@ int tv_kv_rows_write(const tv_geom* geom, int32_t rows, const void* k_new, int64
 int tv_kv_rows_read(const tv_geom* geom, int32_t rows, const int64_t* slots, const void* k_cache,
                     const void* v_cache, int32_t num_blocks, void* k_out, int64_t k_ld, void* v_out,
                     int64_t v_ld, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Sampling from a filtered distribution
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A token per node from what temperature, top-k, top-p and min-p leave of the
+ * target's distribution ([DECODE], its sampling strategies, and "Gumbel Max技巧"
+ * for the draw).
+ *
+ * For node t of request b with temperature T > 0, tokens v are ordered by
+ * (logits[t][v] descending, v ascending), NaN counting as the largest value and
+ * -0 as +0; s_v = fl(logits[t][v] * fl(1/T)) in float32, w_v = exp(s_v - s_max).
+ *   top-k   the first top_k[b] tokens (0, or vocab and more: all)
+ *   top-p   of these, the tokens in whose front weights of less than
+ *           top_p[b] * (the weights of all of these) lie, and always the first one
+ *           (1: all)
+ *   min-p   the tokens with s_v - s_max >= ln min_p[b], that is w_v >= min_p[b]
+ *           (0: all)
+ * A token is kept if all three keep it; a logit of -inf never is. The token drawn
+ * is the first argmax over the kept ones of fl(s_v + gumbel[t][v]), and
+ * logp = s_token - s_max - ln(sum of kept w). T == 0 keeps the first argmax of the
+ * logits alone (logp 0). Without filters tokens equal tv_sample_tokens' (for
+ * finite noise).
+ * Which tokens are kept is decided on weights that are within 2^-35 of exp and
+ * added exactly, so a decision can differ from an exact evaluation only where a
+ * border's sum is within about 2^-35 of it; results do not depend on timing. Where
+ * s_max is infinite or NaN, tokens equal to it weigh 1, others 0. A row without a
+ * logit above -inf (a mask that leaves nothing) gets token 0 and logp -inf.
+ *
+ *  dtype          TV_DTYPE_* of logits
+ *  logits         [T][logits_ld], 16-byte aligned, rows a multiple of 16 bytes apart
+ *  gumbel         float32 [T][gumbel_ld], as for tv_sample_tokens; read where a
+ *                 token is kept
+ *  cu_nodes, max_nodes, vocab   as for tv_sample_tokens
+ *  temperature    float32 [batch]
+ *  top_k          int32 [batch], or NULL for 0
+ *  top_p, min_p   float32 [batch], or NULL for 1 and 0
+ *  tokens         int32 [T] out
+ *  logp           float32 [T] out, or NULL
+ *  status         in/out: requests with non-zero status are skipped;
+ *                 TV_ST_BAD_SIZE, TV_ST_BAD_TEMPERATURE (negative, NaN, infinite,
+ *                 so small that 1/T overflows, or > 0 without noise) and
+ *                 TV_ST_BAD_FILTER are OR-ed in (outputs untouched)
+ */
+int tv_sample_filtered(int32_t dtype, const void* logits, int64_t logits_ld, const float* gumbel,
+                       int64_t gumbel_ld, const int32_t* cu_nodes, const float* temperature,
+                       const int32_t* top_k, const float* top_p, const float* min_p, int32_t batch,
+                       int32_t max_nodes, int32_t vocab, int32_t* tokens, float* logp,
+                       int32_t* status, void* stream);
+
+/*
+ * The same filter as masked logits: out[t][v] = logits[t][v] where v is kept, else
+ * -inf. tv_sampled_accept and tv_rejection_accept on the result follow the
+ * filtered distribution (with the same temperature; for a drafter's logits, whose
+ * softmax is taken as it is, filter with temperature 1).
+ *
+ *  out            [T][out_ld] of the logits' type, aligned like them; may be the
+ *                 logits themselves (same pointer and stride), else may not overlap
+ *                 them. Columns from vocab on are left as they are
+ *  kept           int32 [T] out: how many tokens are kept, or NULL
+ * All else as for tv_sample_filtered.
+ */
+int tv_filter_logits(int32_t dtype, const void* logits, int64_t logits_ld, const int32_t* cu_nodes,
+                     const float* temperature, const int32_t* top_k, const float* top_p,
+                     const float* min_p, int32_t batch, int32_t max_nodes, int32_t vocab, void* out,
+                     int64_t out_ld, int32_t* kept, int32_t* status, void* stream);
 
 /* Name of a TV_ERR_* code or of a single TV_ST_* flag. */
 const char* tv_status_string(int code);

@@ -48,6 +48,7 @@ from .rejection_ref import chosen_path_ref, rejection_walk_ref
 from .decode_ref import (
     axis_of_pair_ref, decode_attention_ref, kv_quant_ref, rope_axes_ref, round_e4m3_ref,
 )
+from .filter_ref import draw_ref, filter_ref
 from .pages_ref import block_tables_ref, slot_map_ref
 
 __all__ = [
@@ -63,5 +64,5 @@ __all__ = [
     "eagle_scores_ref", "eagle_expand_select_ref", "eagle_rerank_ref",
     "chosen_path_ref", "rejection_walk_ref",
     "axis_of_pair_ref", "decode_attention_ref", "kv_quant_ref", "rope_axes_ref", "round_e4m3_ref",
-    "block_tables_ref", "slot_map_ref",
+    "block_tables_ref", "slot_map_ref", "draw_ref", "filter_ref",
 ]

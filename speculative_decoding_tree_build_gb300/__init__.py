@@ -24,7 +24,7 @@ __all__ = [
     "eagle_expand_select", "eagle_rerank", "tree_mask_dense", "dense_mask_elements",
     "TvRopeAxes", "rope_axes_geom", "rope_axes", "KV_BF16", "KV_E4M3", "KV_INT8", "kv_quant_append",
     "kv_quant_read", "decode_workspace_bytes", "decode_attention",
-    "block_tables", "slot_map", "kv_rows_write", "kv_rows_read",
+    "block_tables", "slot_map", "kv_rows_write", "kv_rows_read", "sample_filtered", "filter_logits",
     "status_string", "version",
 ]
 
@@ -33,7 +33,7 @@ lib_path = os.path.join(_PKG, "libtreeverify.so")
 
 TV_OK = 0
 TV_ST = {"BAD_SIZE": 1, "BAD_ROOT": 2, "BAD_PARENT": 4, "BAD_BLOCK": 8,
-         "PATH_OVERFLOW": 16, "TIMEOUT": 32, "BAD_TEMPERATURE": 64, "NO_BLOCKS": 128}
+         "PATH_OVERFLOW": 16, "TIMEOUT": 32, "BAD_TEMPERATURE": 64, "NO_BLOCKS": 128, "BAD_FILTER": 256}
 
 
 class TvGeom(ctypes.Structure):
@@ -96,6 +96,8 @@ _SIGS = {
     "tv_slot_map": [_I, _I, _P, _P, _P, _P, _I, _I, _P, _P, _P],
     "tv_kv_rows_write": [ctypes.POINTER(TvGeom), _I, _P, _I64, _P, _I64, _P, _P, _P, _I, _P],
     "tv_kv_rows_read": [ctypes.POINTER(TvGeom), _I, _P, _P, _P, _I, _P, _I64, _P, _I64, _P],
+    "tv_sample_filtered": [_I, _P, _I64, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P],
+    "tv_filter_logits": [_I, _P, _I64, _P, _P, _P, _P, _P, _I, _I, _I, _P, _I64, _P, _P, _P],
     "tv_status_string": [ctypes.c_int],
     "tv_version": [],
 }
@@ -474,7 +476,7 @@ def decode_attention(g: TvGeom, q, seq_len, block_table, n_blocks, k_cache, v_ca
     return rc and _check("tv_decode_attention", rc)
 
 
-# ---------------------------------------------------------------- pages and slots
+# ---------------------------------------------------------------- pages, slots, filtered sampling
 
 def block_tables(want_len, block_table, n_blocks, free_blocks, free_count, status, released=None,
                  released_count=None, stream=None):
@@ -508,3 +510,23 @@ def kv_rows_read(g: TvGeom, slots, k_cache, v_cache, k_out, v_out, stream=None):
     rows whose slot lies outside the pools are left as they are."""
     rc = (_ext or _native()).kv_rows_read(g, slots, k_cache, v_cache, k_out, v_out, stream)
     return rc and _check("tv_kv_rows_read", rc)
+
+
+def sample_filtered(logits, gumbel, cu_nodes, temperature, top_k, top_p, min_p, max_nodes, tokens,
+                    logp, status, stream=None):
+    """A token per node from what temperature, top-k, top-p and min-p leave
+    (``logits`` [T][vocab] bf16 or float32, ``gumbel`` float32 noise or None when
+    every temperature is 0; the filters int32 / float32 [batch] or None), with the
+    log-probability in what is left (``logp`` float32 [T] or None)."""
+    rc = (_ext or _native()).sample_filtered(logits, gumbel, cu_nodes, temperature, top_k, top_p, min_p,
+                                             max_nodes, tokens, logp, status, stream)
+    return rc and _check("tv_sample_filtered", rc)
+
+
+def filter_logits(logits, cu_nodes, temperature, top_k, top_p, min_p, max_nodes, out, kept, status,
+                  stream=None):
+    """The logits with -inf for every token that sample_filtered would not keep
+    (``out`` may be ``logits``), and how many are kept (int32 [T] or None)."""
+    rc = (_ext or _native()).filter_logits(logits, cu_nodes, temperature, top_k, top_p, min_p, max_nodes,
+                                           out, kept, status, stream)
+    return rc and _check("tv_filter_logits", rc)

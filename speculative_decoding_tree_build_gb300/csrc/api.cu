@@ -84,6 +84,7 @@ extern "C" const char* tv_status_string(int code) {
     case TV_ST_TIMEOUT: return "TV_ST_TIMEOUT";
     case TV_ST_BAD_TEMPERATURE: return "TV_ST_BAD_TEMPERATURE";
     case TV_ST_NO_BLOCKS: return "TV_ST_NO_BLOCKS";
+    case TV_ST_BAD_FILTER: return "TV_ST_BAD_FILTER";
     default: return "unknown";
   }
 }

@@ -420,10 +420,90 @@ PyObject* kv_rows(PyObject* const* a, Py_ssize_t n) {
 PyObject* kv_rows_write(PyObject*, PyObject* const* a, Py_ssize_t n) { return kv_rows<true>(a, n); }
 PyObject* kv_rows_read(PyObject*, PyObject* const* a, Py_ssize_t n) { return kv_rows<false>(a, n); }
 
+struct Matrix {
+  void* ptr;
+  int64_t rows, cols, ld;
+  ScalarType type;
+};
+
+// [rows][cols] with contiguous rows; the stride of a single row is free: the next legal one
+Matrix matrix_of(Call& c, int i, const char* name, int64_t step) {
+  const Tensor& t = c.tensor(i, name);
+  if (t.dim() != 2 || (t.numel() != 0 && ((t.size(1) > 1 && t.stride(1) != 1) || (t.size(0) > 1 && t.stride(0) < t.size(1)))))
+    refuse(std::string(name) + " must be a CUDA matrix with contiguous rows");
+  return {t.data_ptr(), t.size(0), t.size(1), t.size(0) > 1 ? t.stride(0) : (t.size(1) + step - 1) / step * step, t.scalar_type()};
+}
+
+struct Filter {
+  Matrix logits;
+  int32_t dtype, batch, max_nodes, vocab;
+  const int32_t* cu;
+  const float* temperature;
+  const int32_t* top_k;
+  const float *top_p, *min_p;
+};
+
+// logits at 0; from `at` on cu_nodes, temperature, top_k, top_p, min_p, max_nodes
+Filter filter_of(Call& c, PyObject* const* a, int at) {
+  Filter f{};
+  f.logits = matrix_of(c, 0, "logits", 8);
+  if (f.logits.type != ScalarType::BFloat16 && f.logits.type != ScalarType::Float) refuse("logits must be bfloat16 or float32");
+  f.dtype = f.logits.type == ScalarType::Float ? TV_DTYPE_F32 : TV_DTYPE_BF16;
+  f.cu = c.ints(at, "cu_nodes", 1);
+  const int64_t batch = c.tensor(at, "cu_nodes").numel() - 1;
+  f.temperature = per_request<float>(c, at + 1, ScalarType::Float, "temperature", batch);
+  f.top_k = per_request<int32_t>(c, at + 2, ScalarType::Int, "top_k", batch, true);
+  f.top_p = per_request<float>(c, at + 3, ScalarType::Float, "top_p", batch, true);
+  f.min_p = per_request<float>(c, at + 4, ScalarType::Float, "min_p", batch, true);
+  f.max_nodes = number(a[at + 5], "max_nodes");
+  f.batch = count(batch, "batch");
+  f.vocab = count(f.logits.cols, "vocab");
+  return f;
+}
+
+// sample_filtered(logits, gumbel, cu_nodes, temperature, top_k, top_p, min_p, max_nodes, tokens, logp, status, stream)
+PyObject* sample_filtered(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 12);
+    const Filter f = filter_of(c, a, 2);
+    Matrix g{};
+    if (!c.none(1)) {
+      g = matrix_of(c, 1, "gumbel", 4);
+      if (g.type != ScalarType::Float) refuse("gumbel must be float32");
+      if (g.rows < f.logits.rows || g.cols < f.logits.cols) refuse("gumbel must have the logits' rows and columns");
+    }
+    auto* tokens = static_cast<int32_t*>(c.flat(8, ScalarType::Int, "tokens", f.logits.rows));
+    auto* logp = c.none(9) ? nullptr : static_cast<float*>(c.flat(9, ScalarType::Float, "logp", f.logits.rows));
+    auto* status = per_request<int32_t>(c, 10, ScalarType::Int, "status", f.batch);
+    return launch(c, a[11], [&](void* s) {
+      return tv_sample_filtered(f.dtype, f.logits.ptr, f.logits.ld, static_cast<const float*>(g.ptr), g.ld, f.cu,
+                                f.temperature, f.top_k, f.top_p, f.min_p, f.batch, f.max_nodes, f.vocab, tokens, logp,
+                                status, s);
+    });
+  });
+}
+
+// filter_logits(logits, cu_nodes, temperature, top_k, top_p, min_p, max_nodes, out, kept, status, stream)
+PyObject* filter_logits(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c(a, n, 11);
+    const Filter f = filter_of(c, a, 1);
+    const Matrix out = matrix_of(c, 7, "out", 8);
+    if (out.type != f.logits.type || out.rows != f.logits.rows || out.cols != f.logits.cols)
+      refuse("out must have the logits' type, rows and columns");
+    auto* kept = c.none(8) ? nullptr : static_cast<int32_t*>(c.flat(8, ScalarType::Int, "kept", f.logits.rows));
+    auto* status = per_request<int32_t>(c, 9, ScalarType::Int, "status", f.batch);
+    return launch(c, a[10], [&](void* s) {
+      return tv_filter_logits(f.dtype, f.logits.ptr, f.logits.ld, f.cu, f.temperature, f.top_k, f.top_p, f.min_p,
+                              f.batch, f.max_nodes, f.vocab, out.ptr, out.ld, kept, status, s);
+    });
+  });
+}
+
 #define TV_FN(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef kMethods[] = {TV_FN(rope_axes), TV_FN(kv_quant_append), TV_FN(kv_quant_read), TV_FN(decode_attention),
                           TV_FN(block_tables), TV_FN(slot_map), TV_FN(kv_rows_write), TV_FN(kv_rows_read),
-                          {nullptr, nullptr, 0, nullptr}};
+                          TV_FN(sample_filtered), TV_FN(filter_logits), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_treeverify_torch", nullptr, -1, kMethods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace
