@@ -26,7 +26,8 @@ def filter_ref(logits, temperature, top_k=0, top_p=1.0, min_p=0.0):
     """One row: (keep bool [V], scaled float32 [V], weights float128 [V] of all
     tokens relative to the largest, margin). margin is how far the top-p border's
     sum is from its target, as a share of the whole (inf where top-p is off): where
-    it is tiny, an evaluation with rounded sums may put the border elsewhere."""
+    it is tiny, an evaluation with rounded weights may put the border elsewhere (inf too
+    where all weights that count are equal)."""
     x = np.asarray(logits, np.float32)
     v = len(x)
     keep = np.zeros(v, bool)
@@ -58,7 +59,9 @@ def filter_ref(logits, temperature, top_k=0, top_p=1.0, min_p=0.0):
         m = int(np.searchsorted(sums, target, side="left")) + 1      # the first sum that reaches it
         m = min(m, n)
         near = [abs(sums[i] - target) / sums[-1] for i in (m - 2, m - 1) if 0 <= i < n - 1]
-        margin = float(min(near)) if near and np.isfinite(top) else math.inf
+        some = w[order[:len(sums)]]
+        equal = bool(((some == some[0]) | (some < 2.0 ** -70)).all())   # sums of one weight are exact everywhere
+        margin = float(min(near)) if near and np.isfinite(top) and not equal else math.inf
         n = m
     keep[order[:n]] = True
     if min_p > 0:

@@ -55,7 +55,7 @@ def logp_bound(keep, s, w, token, v, filtered):
     return tol
 
 
-def check(x, temps, ks, ps, ms, nodes=1, dtype=F32, seed=0, gumbel=None, exact_logp=True):
+def check(x, temps, ks, ps, ms, nodes=1, dtype=F32, seed=0, gumbel=None, exact_logp=True, skip=None):
     """Rows x [batch * nodes][v] of requests with settings of their own through both
     calls; returns the kept counts."""
     rng = np.random.default_rng(seed)
@@ -98,7 +98,7 @@ def check(x, temps, ks, ps, ms, nodes=1, dtype=F32, seed=0, gumbel=None, exact_l
         else:
             filtered = 0 < k < v or p < 1 or m > 0
             assert abs(logp[r] - lp) <= logp_bound(keep, s, w, token, v, filtered), (r, logp[r], lp)
-    assert undecided <= max(1, rows // 50)
+    assert undecided <= (max(1, rows // 50) if skip is None else skip)
     return kept
 
 
@@ -218,7 +218,9 @@ def test_temperatures(v, t):
     x = np.concatenate([bulk(rng, 3, v), bulk(rng, 2, v) * 1e-30, bulk(rng, 1, v) * 1e30, bulk(rng, 2, v) + 3000.0,
                         bulk(rng, 2, v) - 700.0]).astype(np.float32)
     for k, p, m in ((0, 0.9, 0.0), (30, 1.0, 0.0), (0, 1.0, 0.1), (100, 0.5, 0.01)):
-        check(x, [t] * 10, [k] * 10, [p] * 10, [m] * 10, seed=7, exact_logp=False)
+        # of the two rows of 1e-30 every weight is 1 within 2^-70: where p of k is a whole
+        # number (50 of 100), the border is the rounding's
+        check(x, [t] * 10, [k] * 10, [p] * 10, [m] * 10, seed=7, exact_logp=False, skip=2 if k * p == 50 else 1)
 
 
 def test_far_from_zero_at_the_bound():
@@ -407,8 +409,9 @@ def test_sampled_and_rejection_walks_on_filtered_logits():
     th, dh = target.cpu().numpy(), drafter.cpu().numpy()
     for b in range(batch):
         sl = slice(int(w["cu_nodes"][b]), int(w["cu_nodes"][b + 1]))
-        rs, acc, bo, close = rejection_walk_ref(w["parents"][sl], w["draft_tokens"][sl], lp[sl], th[sl], dh[sl], un[sl], gb[sl], 0.9, md)
-        if not close:
+        rs, acc, bo, det = rejection_walk_ref(w["parents"][sl], w["draft_tokens"][sl], lp[sl], th[sl], dh[sl], un[sl], gb[sl], 0.9, md)
+        key = np.sort(det["stop"][1])
+        if all(abs(u - x) > 1e-5 for u, x in det["ratios"]) and key[-1] - key[-2] > 1e-5:      # no near ties
             assert rs == 0 and int(alen[b]) == len(acc) - 1 and int(bonus[b]) == bo
         last = sl.start + int(path[b, int(alen[b])])
         assert th[last, int(bonus[b])] > -np.inf     # the draw is of a token that the target keeps
