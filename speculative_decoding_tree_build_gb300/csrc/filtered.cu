@@ -7,20 +7,27 @@
 // anywhere else.
 //
 // Finding the place without sorting the row:
-//   1. a sample of the row in 128-byte lines gives a place below which some
-//      thousand tokens of the row lie above;
-//   2. one pass over the row lists those (shared memory) and sums the weights
-//      of the others where top-p needs the total;
+//   1. a sample of the row in 128-byte lines gives a place above which some
+//      hundred tokens of the row lie;
+//   2. one pass over the row lists those (shared memory) and, where top-p needs
+//      the total, sums the weights of the others in float32 with a bound on the
+//      error;
 //   3. on the list, a histogram over places finds the bin in which the count
 //      (top-k) or the sum of weights (top-p) is reached; its few tokens are
 //      ranked by one warp.
-// Where the place is not on the list (top-k larger than the list, a flat row
-// whose top-p set is a tenth of the vocabulary, many equal logits), bounds on
-// the place are narrowed by another sample and another pass. Every pass shrinks
-// the bounds, and from the fifth on it halves them.
+// Where the place is not on the list (top-k larger than the list, a flat row whose
+// top-p set is a tenth of the vocabulary, many equal logits), another pass lists
+// the tokens around a place that a sample gives and sums those above and below
+// with a tighter bound. Every pass shrinks the bounds on the place, and from the
+// fifth on it halves them. Where a bound on the sums leaves the border open, a
+// pass with exact weights settles it.
 //
-// Sums are integers (tv_weight.cuh): no result depends on the order of the
-// atomics that build lists and histograms.
+// Weights of listed tokens are integers (tv_weight.cuh) and their sums exact: no
+// result depends on the order of the atomics that build lists and histograms.
+//
+// One CTA has a row, or a cluster where rows are few: its CTAs pass over slices,
+// exchange lists and sums through distributed shared memory, and all of them
+// take the same decisions.
 #include <cuda_bf16.h>
 
 #include "tv_cluster.cuh"
@@ -28,10 +35,15 @@
 
 namespace tv {
 
-constexpr int kFiltThreads = 512;
+constexpr int kFiltThreads = 256;
 constexpr int kFiltWarps = kFiltThreads / 32;
-constexpr int kListCap = 8192;
-constexpr int kSampleSize = 4096;
+constexpr int kFiltPerSm = 4;              // CTAs an SM
+constexpr int kFiltMaxCluster = 8;
+constexpr int kListCap = 5120;
+constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
+constexpr int kSampleEach = 16;            // sampled tokens a thread
+constexpr int kSampleSize = kSampleEach * kFiltThreads;
+constexpr int kFirstList = 384;            // tokens that the first list is made for without top-k
 constexpr int kBins = 1024;
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
@@ -57,7 +69,7 @@ struct FiltParams {
   const int32_t* top_k;
   const float* top_p;
   const float* min_p;
-  int max_nodes, vocab, bits;
+  int max_nodes, vocab, bits, csize;
   int32_t* tokens;
   float* logp;
   void* out;
@@ -67,51 +79,68 @@ struct FiltParams {
 };
 
 struct FiltSmem {
-  uint64_t list[kListCap];
-  unsigned long long hist[kBins];
-  uint32_t count[kBins];
+  uint32_t bins[4][kBins];                 // counts; weights in three parts
   unsigned long long table[kWeightTable];
-  uint64_t red[kFiltWarps];
+  uint64_t red[6][kFiltWarps];
   uint64_t small[kSmall];
-  uint64_t found, base;
-  int bin, bin_count, n_small;
-  int n_list;
+  uint64_t found, before, weight;          // of select
+  uint64_t stat[6];                        // of a pass: listed, above, three sums, the largest key
+  int bin, bin_count, n_small, n_list;
+  int rank, lo_bin, hi_bin;                // of a bracket
+  uint64_t list[kListCap];                 // in a cluster the CTA's own part follows
 };
 
 // ---------------------------------------------------------------- reductions
 
-__device__ __forceinline__ uint64_t block_sum(uint64_t v, FiltSmem& s) {
+__device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < kFiltWarps; ++w) t += s.red[w];
-  return t;
+  return v;
 }
 
+// Sums (or, from kMax on, maxima) of kN numbers over the CTA.
+template <int kN, int kMax>
+__device__ __forceinline__ void block_reduce(uint64_t (&v)[kN], FiltSmem& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int i = 0; i < kN; ++i) v[i] = i >= kMax ? warp_max_u64(v[i]) : warp_sum_u64(v[i]);
+  __syncthreads();                         // what was there is read
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < kN; ++i) s.red[i][warp] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    uint64_t all = 0;
+#pragma unroll
+    for (int w = 0; w < kFiltWarps; ++w) {
+      const uint64_t x = s.red[i][w];
+      all = i >= kMax ? (x > all ? x : all) : all + x;
+    }
+    v[i] = all;
+  }
+}
+
+__device__ __forceinline__ uint64_t block_sum(uint64_t v, FiltSmem& s) {
+  uint64_t x[1] = {v};
+  block_reduce<1, 1>(x, s);
+  return x[0];
+}
+__device__ __forceinline__ uint64_t block_max(uint64_t v, FiltSmem& s) {
+  uint64_t x[1] = {v};
+  block_reduce<1, 0>(x, s);
+  return x[0];
+}
 __device__ __forceinline__ float block_sum(float v, FiltSmem& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = __float_as_uint(v);
+  if ((threadIdx.x & 31) == 0) s.red[0][threadIdx.x >> 5] = __float_as_uint(v);
   __syncthreads();
   float t = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kFiltWarps; ++w) t += __uint_as_float(static_cast<uint32_t>(s.red[w]));
-  return t;
-}
-
-__device__ __forceinline__ uint64_t block_max(uint64_t v, FiltSmem& s) {
-  v = warp_max_u64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  uint64_t t = 0;
-#pragma unroll
-  for (int w = 0; w < kFiltWarps; ++w) t = s.red[w] > t ? s.red[w] : t;
+  for (int w = 0; w < kFiltWarps; ++w) t += __uint_as_float(static_cast<uint32_t>(s.red[0][w]));
   return t;
 }
 
@@ -147,13 +176,23 @@ __device__ __forceinline__ void store_one(__nv_bfloat16* p, float x) {
   *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(__float_as_uint(x) >> 16);
 }
 
-// f.many<n>(x, first index) for all entries of the row, n at a time (the ragged
-// end one by one).
+// A row and the CTA's slice [v0, v1) of it; v0 is a multiple of 8.
+template <typename T>
+struct Row {
+  const T* x;
+  int vocab, v0, v1;
+  int rank, csize;
+  float inv_t;
+  int bits;
+};
+
+// f.many<n>(x, first index) for all entries of the slice, n at a time (the
+// ragged end one by one).
 template <typename T, typename F>
-__device__ __forceinline__ void for_row(const T* row, int vocab, F& f) {
+__device__ __forceinline__ void for_slice(const Row<T>& row, F& f) {
   constexpr int kLen = Vec<T>::kLen;
-  const uint4* vecs = reinterpret_cast<const uint4*>(row);
-  const int n = vocab / kLen;
+  const uint4* vecs = reinterpret_cast<const uint4*>(row.x + row.v0);
+  const int n = (row.v1 - row.v0) / kLen;
   for (int j0 = threadIdx.x; j0 < n; j0 += kFiltUnroll * kFiltThreads) {
     uint4 v[kFiltUnroll];
 #pragma unroll
@@ -165,314 +204,624 @@ __device__ __forceinline__ void for_row(const T* row, int vocab, F& f) {
       if (j >= n) break;
       float x[kLen];
       Vec<T>::unpack(v[u], x);
-      f.template many<kLen>(x, j * kLen);
+      f.template many<kLen>(x, row.v0 + j * kLen);
     }
   }
-  const int i = n * kLen + threadIdx.x;
-  if (i < vocab) {
-    float x[1] = {load_one(row + i)};
+  const int i = row.v0 + n * kLen + threadIdx.x;
+  if (i < row.v1) {
+    float x[1] = {load_one(row.x + i)};
     f.template many<1>(x, i);
   }
 }
 
+// Sum (or maximum) over the cluster of what each CTA left in s.stat: a lane reads
+// a CTA's (clusters are powers of two up to 8). For whole warps.
+template <bool kMax>
+__device__ __forceinline__ uint64_t cluster_stat(const FiltSmem& s, int i, int csize) {
+  if (csize == 1) return s.stat[i];
+  uint64_t v = ld_cluster_u64(&s.stat[i], (threadIdx.x & 31) & (csize - 1));
+  for (int o = csize >> 1; o > 0; o >>= 1) {
+    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
+    v = kMax ? (w > v ? w : v) : v + w;
+  }
+  return v;
+}
+
 // ------------------------------------------------------------------ the pass
 
-// One pass over the row: places in [lo, hi] are listed (as many as fit, all
-// are counted), those above are counted, those below weighed (kBelow); the
-// others are weighed with kWeigh.
+// What a pass does with the tokens that it does not list: nothing; sum the
+// weights below the list, cheaply; sum those below and above within 2^-20; weigh
+// exactly.
+enum class Weigh { kNone, kBelow, kClose, kExact };
+
+// One pass over the row: places in [lo, hi] are listed (as many as fit, all are
+// counted), those above are counted. Weights are relative to the scale given.
 struct Bracket {
   uint64_t lo, hi;
   int n_in, n_above;
-  uint64_t m_in, m_above, below;     // weights
-  uint64_t best;                     // the largest place from lo on, 0 if there is none
+  uint64_t m_in, m_above, below;
+  bool whole;                        // the list holds all places in [lo, hi]
+  float top;                         // the largest logit from lo on
+  bool any;                          // there is one
 };
 
-template <bool kBelow, bool kWeigh>
+// A float32 sum with its roundings beside it.
+struct FloatSum {
+  float sum, low;
+  __device__ __forceinline__ void add(float part) {
+    const float all = sum + part, back = all - sum;
+    low += (sum - (all - back)) + (part - back);
+    sum = all;
+  }
+  __device__ __forceinline__ uint64_t steps(float unit) const {
+    return static_cast<uint64_t>(__float2ll_rn(sum * unit) + __float2ll_rn(low * unit));
+  }
+};
+
+template <Weigh kWeigh, typename T>
 struct PassBody {
   FiltSmem& s;
+  const Row<T>& row;
+  uint64_t* list;                    // the CTA's own
+  int cap;
   uint64_t lo, hi;
-  float lo_value, inv_t;
+  float lo_value, hi_value, to_y, y_off, floor;
   WeightScale scale;
-  uint64_t n_above, m_in, m_above, below, best;
+  uint32_t best;                     // the largest order key from lo on
+  int n_above;
+  uint64_t m_in, m_above, below;
+  FloatSum f_below, f_above, f_in;
 
+  // kBelow: 2^(y - k), y = x to_y: the factor's rounding makes the exponent good to |y| 2^-22.8.
+  // kClose: 2^(y - k) with y as exact as the exact weights have it, the whole part kept
+  // out of the exponential: good to 2^-21.9 (2^-22 of ex2, 2^-25 of its argument).
+  __device__ __forceinline__ float weight(float x) const {
+    if (kWeigh == Weigh::kBelow) return fast_exp2(__fmaf_rn(x, to_y, y_off));
+    const float sx = fmaxf(__fmul_rn(x, row.inv_t) - scale.ref, floor);
+    const float yh = __fmul_rn(sx, kLog2e);
+    const float steps = yh + y_off;                                     // 1.5 * 2^23 - k
+    const float f = (yh - (steps - y_off)) + __fmaf_rn(sx, kLog2eLow, __fmaf_rn(sx, kLog2e, -yh));
+    return __int_as_float(__float_as_int(fast_exp2(f)) + (__float_as_int(steps) << 23));
+  }
+  __device__ __forceinline__ uint64_t exact(float x) const { return weight_of(__fmul_rn(x, row.inv_t), scale, s.table); }
+
+  // a token that may lie in the bracket
   __device__ __forceinline__ void take(float x, int i) {
-    const uint64_t c = pack_best(order_key(x), i);
+    const uint32_t key = order_key(x);
+    const uint64_t c = pack_best(key, i);
     if (c < lo) {
-      if (kBelow) below += weight_of(__fmul_rn(x, inv_t), scale, s.table);
+      if (kWeigh == Weigh::kExact) below += exact(x);
+      else if (kWeigh != Weigh::kNone) f_below.add(weight(x));
       return;
     }
-    if (c > best) best = c;
-    const uint64_t w = kWeigh ? weight_of(__fmul_rn(x, inv_t), scale, s.table) : 0ull;
+    best = key > best ? key : best;
     if (c > hi) {
       ++n_above;
-      m_above += w;
+      if (kWeigh == Weigh::kExact) m_above += exact(x);
+      else if (kWeigh == Weigh::kClose) f_above.add(weight(x));
     } else {
       const int at = atomicAdd(&s.n_list, 1);
-      if (at < kListCap) s.list[at] = c;
-      m_in += w;
+      if (at < cap) list[at] = c;
+      if (kWeigh == Weigh::kExact) m_in += exact(x);
+      else if (kWeigh == Weigh::kClose) f_in.add(weight(x));
     }
   }
 
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
-    bool any = false;
+    uint32_t in = 0;
+    float low = 0.0f, high = 0.0f, top = -kInf;
 #pragma unroll
-    for (int e = 0; e < kLen; ++e) any |= !(x[e] < lo_value);        // (a NaN is not below)
-    if (kBelow) {
-#pragma unroll
-      for (int e = 0; e < kLen; ++e)
-        if (x[e] < lo_value) below += weight_of(__fmul_rn(x[e], inv_t), scale, s.table);
+    for (int e = 0; e < kLen; ++e) {
+      const bool under = x[e] < lo_value, over = kWeigh != Weigh::kBelow && x[e] > hi_value;      // (a NaN is neither)
+      if (!under && !over) in |= 1u << e;
+      if (kWeigh == Weigh::kBelow) low += under ? weight(x[e]) : 0.0f;
+      if (kWeigh == Weigh::kClose) {
+        const float w = weight(x[e]);
+        low += under ? w : 0.0f;
+        high += over ? w : 0.0f;
+      }
+      if (kWeigh == Weigh::kExact) {
+        const uint64_t w = exact(x[e]);
+        if (under) below += w;
+        if (over) m_above += w;
+      }
+      if (kWeigh != Weigh::kBelow && over) {
+        top = fmaxf(top, x[e]);
+        ++n_above;
+      }
     }
-    if (any) {
-#pragma unroll
-      for (int e = 0; e < kLen; ++e)
-        if (!(x[e] < lo_value)) take(x[e], i0 + e);
+    if (kWeigh == Weigh::kBelow || kWeigh == Weigh::kClose) f_below.add(low);
+    if (kWeigh == Weigh::kClose) f_above.add(high);
+    if (kWeigh != Weigh::kBelow && top > -kInf) best = max(best, order_key(top));
+    while (in) {
+      const int e = __ffs(in) - 1;
+      in &= in - 1;
+      take(load_one(row.x + i0 + e), i0 + e);
     }
   }
 };
 
-template <bool kBelow, bool kWeigh, typename T>
-__device__ __noinline__ Bracket pass(const T* row, int vocab, uint64_t lo, uint64_t hi, float inv_t,
-                                     const WeightScale& scale, FiltSmem& s) {
-  __syncthreads();
+template <Weigh kWeigh, typename T>
+__device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi, const WeightScale& scale, FiltSmem& s) {
+  uint64_t* own = row.csize > 1 ? s.list + kListCap : s.list;
+  const int cap = row.csize > 1 ? kLocalCap : kListCap;
+  __syncwarp();
+  row_barrier(row.csize);                  // the lists and sums of the pass before are read
   if (threadIdx.x == 0) s.n_list = 0;
   __syncthreads();
-  PassBody<kBelow, kWeigh> body = {s, lo, hi, place_value(lo), inv_t, scale, 0, 0, 0, 0, 0};
-  for_row(row, vocab, body);
+  const float k = static_cast<float>(scale.k);
+  PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
+                              row.inv_t * kLog2e, kWeigh == Weigh::kClose ? 0x1.8p23f - k : -k, (k - 100.0f) * kLn2, scale, 0u, 0, 0, 0, 0,
+                              {0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}};
+  for_slice(row, body);
+  // a weight is at most 2: sums stay below 2^31, in steps of 2^-F below 2^63
+  const float unit = exp2f(static_cast<float>(row.bits));
   Bracket out;
   out.lo = lo;
   out.hi = hi;
-  out.best = block_max(body.best, s);        // (its barriers close the list too)
-  out.n_in = s.n_list;
-  out.n_above = static_cast<int>(block_sum(body.n_above, s));
-  out.m_in = out.m_above = out.below = 0;
-  if (kWeigh) {
-    out.m_in = block_sum(body.m_in, s);
-    out.m_above = block_sum(body.m_above, s);
+  uint64_t v[5] = {static_cast<uint64_t>(body.n_above), 0, 0, 0, body.best};
+  if (kWeigh == Weigh::kExact) {
+    v[1] = body.m_in;
+    v[2] = body.m_above;
+    v[3] = body.below;
+  } else {
+    if (kWeigh == Weigh::kClose) {
+      v[1] = body.f_in.steps(unit);
+      v[2] = body.f_above.steps(unit);
+    }
+    if (kWeigh != Weigh::kNone) v[3] = body.f_below.steps(unit);
   }
-  if (kBelow) out.below = block_sum(body.below, s);
+  block_reduce<5, 4>(v, s);                // (its barriers close the list too)
+  const int listed = s.n_list;
+  if (row.csize > 1) {
+    if (threadIdx.x == 0) {
+      s.stat[0] = listed;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) s.stat[i + 1] = v[i];
+    }
+    __syncwarp();
+    cluster_sync_all();
+    out.n_in = static_cast<int>(cluster_stat<false>(s, 0, row.csize));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = cluster_stat<false>(s, i + 1, row.csize);
+    v[4] = cluster_stat<true>(s, 5, row.csize);
+    const uint64_t longest = cluster_stat<true>(s, 0, row.csize);
+    out.whole = out.n_in <= kListCap && longest <= kLocalCap;
+    if (out.whole) {
+      int at = 0;
+      for (int r = 0; r < row.csize; ++r) {
+        const int n = static_cast<int>(ld_cluster_u64(&s.stat[0], r));
+        for (int i = threadIdx.x; i < n; i += kFiltThreads) s.list[at + i] = ld_cluster_u64(&own[i], r);
+        at += n;
+      }
+    }
+    __syncthreads();
+  } else {
+    out.n_in = listed;
+    out.whole = listed <= kListCap;
+  }
+  out.n_above = static_cast<int>(v[0]);
+  out.m_in = v[1];
+  out.m_above = v[2];
+  out.below = v[3];
+  out.any = v[4] != 0;
+  out.top = key_value(static_cast<uint32_t>(v[4]));
   return out;
 }
 
 // ------------------------------------------------------------- the selection
 
+struct Target {
+  uint64_t least, most;    // reached by the sum of amounts; the place looked for is that of `most`
+  float share;             // > 0: of the sum of all, which lies within `off` of (those listed + below)
+  uint64_t below, off;
+};
+
 // Among the n places of the list that lie in [a, b]: the first one, from the
-// largest down, at which the sum of amounts reaches `target` (>= 1): amounts
-// are weights, or 1 each. The sum of all of them has to reach it.
-template <bool kWeigh>
-__device__ __noinline__ uint64_t select(int n, uint64_t a, uint64_t b, uint64_t target, float inv_t,
+// largest down, at which the sum of amounts reaches the target: amounts are
+// weights, or 1 each. Returns 0 where all of them do not reach it, and leaves their
+// sum in `sum`; else the sum in front of the place and its own amount are in
+// s.before and s.weight.
+template <bool kWeights>
+__device__ __noinline__ uint64_t select(int n, uint64_t a, uint64_t b, Target& target, uint64_t& sum, float inv_t,
                                         const WeightScale& scale, FiltSmem& s) {
   auto amount = [&](uint64_t c) -> uint64_t {
-    return kWeigh ? weight_of(__fmul_rn(place_value(c), inv_t), scale, s.table) : 1ull;
+    return kWeights ? weight_of(__fmul_rn(place_value(c), inv_t), scale, s.table) : 1ull;
   };
+  constexpr int kAhead = 4, kEach = kBins / kFiltThreads;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint64_t base = 0, high = 0, low = 0;     // (low: inverted, so that 0 is nothing)
-  for (int i = threadIdx.x; i < n; i += kFiltThreads) {
-    const uint64_t c = s.list[i];
-    if (c < a || c > b) continue;
-    high = c > high ? c : high;
-    low = ~c > low ? ~c : low;
-  }
-  b = block_max(high, s);
-  a = ~block_max(low, s);
-  if (a > b) return b;                     // nothing there (callers see to it that there is)
-  while (true) {
+  uint64_t base = 0;
+  for (bool first = true;; first = false) {
     // bins of 2^sh places, counted from b down
     const int sh = b > a ? max(0, 54 - __clzll(b - a)) : 0;
     __syncthreads();
-    for (int j = threadIdx.x; j < kBins; j += kFiltThreads) {
-      s.hist[j] = 0;
-      s.count[j] = 0;
-    }
+#pragma unroll
+    for (int u = 0; u < (kWeights ? 4 : 1); ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
     if (threadIdx.x == 0) {
       s.bin = -1;
       s.n_small = 0;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kFiltThreads) {
-      const uint64_t c = s.list[i];
-      if (c < a || c > b) continue;
-      const int j = static_cast<int>((b - c) >> sh);
-      atomicAdd(&s.count[j], 1u);
-      if (kWeigh) atomicAdd(&s.hist[j], static_cast<unsigned long long>(amount(c)));
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kFiltThreads) {
+      uint64_t c[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) c[u] = i0 + u * kFiltThreads < n ? s.list[i0 + u * kFiltThreads] : 0ull;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) {
+        if (c[u] < a || c[u] > b) continue;
+        const int j = static_cast<int>((b - c[u]) >> sh);
+        atomicAdd(&s.bins[0][j], 1u);
+        if (kWeights) {                    // at most 5120 parts of 16 bits: 64-bit additions to shared memory are
+          const uint64_t w = amount(c[u]); // loops (14 us for 4096 of them, three parts 1 us)
+          atomicAdd(&s.bins[1][j], static_cast<uint32_t>(w) & 0xffffu);
+          atomicAdd(&s.bins[2][j], static_cast<uint32_t>(w >> 16) & 0xffffu);
+          atomicAdd(&s.bins[3][j], static_cast<uint32_t>(w >> 32));
+        }
+      }
     }
     __syncthreads();
-    constexpr int kEach = kBins / kFiltThreads;
-    uint64_t mine[kEach], sum = 0;
+    uint32_t count[kEach];
+    uint64_t mine[kEach], own = 0;
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
       const int j = threadIdx.x * kEach + u;
-      mine[u] = kWeigh ? static_cast<uint64_t>(s.hist[j]) : s.count[j];
-      sum += mine[u];
+      count[u] = s.bins[0][j];
+      mine[u] = kWeights ? (static_cast<uint64_t>(s.bins[3][j]) << 32) + (static_cast<uint64_t>(s.bins[2][j]) << 16) + s.bins[1][j] : count[u];
+      own += mine[u];
     }
-    uint64_t up = sum;
+    uint64_t up = own;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t v = __shfl_up_sync(0xffffffffu, up, o);
       if (lane >= o) up += v;
     }
-    if (lane == 31) s.red[warp] = up;
+    if (lane == 31) s.red[0][warp] = up;
     __syncthreads();
-    uint64_t at = base + up - sum;
+    uint64_t at = base + up - own, all = base;
 #pragma unroll
-    for (int w = 0; w < kFiltWarps; ++w)
-      if (w < warp) at += s.red[w];
+    for (int w = 0; w < kFiltWarps; ++w) {
+      const uint64_t v = s.red[0][w];
+      if (w < warp) at += v;
+      all += v;
+    }
+    if (first) {
+      sum = all;
+      if (kWeights && target.share > 0.0f) {
+        const uint64_t z = all + target.below;
+        target.least = share_of(target.share, z > target.off ? z - target.off : 0);
+        target.most = target.off ? share_of(target.share, z + target.off) : target.least;
+      }
+      if (all < target.most) return 0;     // (the same for all threads)
+    }
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
-      if (at < target && target <= at + mine[u]) {
-        const int j = threadIdx.x * kEach + u;
-        s.bin = j;
-        s.base = at;
-        s.bin_count = static_cast<int>(s.count[j]);
+      if (at < target.most && target.most <= at + mine[u]) {
+        s.bin = threadIdx.x * kEach + u;
+        s.before = at;
+        s.weight = mine[u];
+        s.bin_count = static_cast<int>(count[u]);
       }
       at += mine[u];
     }
     __syncthreads();
     const int bin = s.bin;
-    if (bin < 0) return a;                 // not reached (as above)
-    base = s.base;
+    if (bin < 0) return 0;                 // (does not happen: the sum reaches it)
+    base = s.before;
     b -= static_cast<uint64_t>(bin) << sh;
     if (sh == 0) return b;
     const uint64_t end = b - ((1ull << sh) - 1);
     a = end > a && end <= b ? end : a;
     if (s.bin_count > kSmall) continue;
     // one warp ranks what is in the bin
-    for (int i = threadIdx.x; i < n; i += kFiltThreads) {
-      const uint64_t c = s.list[i];
-      if (c >= a && c <= b) s.small[atomicAdd(&s.n_small, 1)] = c;
+    for (int i0 = threadIdx.x; i0 < n; i0 += kAhead * kFiltThreads) {
+      uint64_t c[kAhead];
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u) c[u] = i0 + u * kFiltThreads < n ? s.list[i0 + u * kFiltThreads] : 0ull;
+#pragma unroll
+      for (int u = 0; u < kAhead; ++u)
+        if (c[u] >= a && c[u] <= b) s.small[atomicAdd(&s.n_small, 1)] = c[u];
     }
     __syncthreads();
     if (warp == 0) {
-      const uint64_t c = lane < s.n_small ? s.small[lane] : 0ull;
-      const uint64_t w = lane < s.n_small ? amount(c) : 0ull;
+      const int held = s.n_small;
+      const uint64_t c = lane < held ? s.small[lane] : 0ull;
+      const uint64_t w = lane < held ? amount(c) : 0ull;
       uint64_t before = base;
-#pragma unroll
-      for (int o = 0; o < 32; ++o) {
+      for (int o = 0; o < held; ++o) {
         const uint64_t oc = __shfl_sync(0xffffffffu, c, o), ow = __shfl_sync(0xffffffffu, w, o);
         if (oc > c) before += ow;
       }
-      if (w != 0 && before < target && target <= before + w) s.found = c;
+      if (w != 0 && before < target.most && target.most <= before + w) {
+        s.found = c;
+        s.before = before;
+        s.weight = w;
+      }
     }
     __syncthreads();
     return s.found;
   }
 }
 
-// A sample of the row's places in [a, b] becomes the list; returns how many.
-// 128-byte lines lie evenly over the row, `turn` moves them.
 template <typename T>
-__device__ __noinline__ int sample_row(const T* row, int vocab, uint64_t a, uint64_t b, int turn, FiltSmem& s) {
-  constexpr int kLine = 128 / sizeof(T), kLines = kSampleSize / kLine, kEach = kLine / 32;
-  const int lines = vocab / kLine;         // >= kLines: the row does not fit the list
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  if (threadIdx.x == 0) s.n_list = 0;
-  __syncthreads();
-  float x[kLines / kFiltWarps][kEach];
-  int at[kLines / kFiltWarps];
-#pragma unroll
-  for (int u = 0; u < kLines / kFiltWarps; ++u) {
-    const int l = warp + u * kFiltWarps;
-    const long long line = (static_cast<long long>(l) * lines + static_cast<long long>(turn) * (lines / 7 + 1)) / kLines;
-    at[u] = static_cast<int>(line % lines) * kLine + lane;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) x[u][e] = load_one(row + at[u] + e * 32);
-  }
-#pragma unroll
-  for (int u = 0; u < kLines / kFiltWarps; ++u) {
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const uint64_t c = pack_best(order_key(x[u][e]), at[u] + e * 32);
-      const bool in = c >= a && c <= b;
-      const uint32_t who = __ballot_sync(0xffffffffu, in);
-      int first = 0;
-      if (lane == 0 && who) first = atomicAdd(&s.n_list, __popc(who));
-      first = __shfl_sync(0xffffffffu, first, 0);
-      if (in) s.list[first + __popc(who & ((1u << lane) - 1))] = c;
-    }
-  }
-  __syncthreads();
-  return s.n_list;
+__device__ __forceinline__ uint64_t select_rank(const Bracket& view, uint64_t rank, const Row<T>& row, FiltSmem& s) {
+  Target target = {rank, rank, 0.0f, 0, 0};
+  uint64_t sum;
+  const uint64_t top = static_cast<uint64_t>(order_key(view.top)) << 32 | 0xffffffffu;
+  return select<false>(view.n_in, view.lo, top < view.hi ? top : view.hi, target, sum, row.inv_t, weight_scale(0.0f, row.bits), s);
+}
+
+template <typename T>
+__device__ __forceinline__ uint64_t select_weight(const Bracket& view, uint64_t from, Target& target, uint64_t& sum,
+                                                  const WeightScale& scale, const Row<T>& row, FiltSmem& s) {
+  const uint64_t top = static_cast<uint64_t>(order_key(view.top)) << 32 | 0xffffffffu;
+  return select<true>(view.n_in, from, top < view.hi ? top : view.hi, target, sum, row.inv_t, scale, s);
 }
 
 // ------------------------------------------------------------------ the place
 
 // Bounds of the place that is looked for: it lies in [lo, hi], and n places
-// with weight m lie above hi.
+// with weight m (about) lie above hi.
 struct Bounds {
   uint64_t lo, hi;
   int n;
   uint64_t m;
 };
 
-// The next bracket inside the bounds, around the place where the count (or the
-// weight) still missing is reached by a sample. From the fifth try on the
-// bounds are cut in half.
-template <bool kWeigh, typename T>
-__device__ __forceinline__ void next_bracket(const T* row, int vocab, const Bounds& in, uint64_t target, int turn,
-                                             float inv_t, const WeightScale& scale, FiltSmem& s, uint64_t& lo,
-                                             uint64_t& hi) {
+// The part of the bounds that a sample of the row says to look at. 4096 tokens,
+// 128 bytes at a time evenly over the row (`turn` moves them), are sorted into bins
+// of equal width below the largest one; in them the rank at which the count (or,
+// with kWeights, the weight) `missing` is reached is found, and the bins `margin`
+// ranks above and below it are the bracket's ends. Widths go down to 32 / 1024 of
+// the scaled logit; what lies further below shares the last bin.
+template <bool kWeights, typename T>
+__device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in, float missing, int turn, float sigmas,
+                                            float slack, float most, const WeightScale& scale, FiltSmem& s, uint64_t& lo,
+                                            uint64_t& hi) {
+  constexpr int kLen = Vec<T>::kLen, kVecs = kSampleEach / kLen, kLines = kSampleSize / kLen / 8;
+  constexpr int kEach = kBins / kFiltThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = in.lo;
   hi = in.hi;
-  if (vocab <= kListCap) return;
-  if (turn > kSampledTurns) {
-    lo = in.lo + (in.hi - in.lo) / 2 + 1;
-    if (lo > in.hi) lo = in.hi;
+  const int lines = row.vocab / (8 * kLen);        // >= kLines: the row does not fit the list
+  uint4 v[kVecs];
+  int first[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const uint32_t at = u * kFiltThreads + threadIdx.x;
+    uint32_t line = static_cast<uint32_t>((static_cast<uint64_t>(at / 8) * lines + static_cast<uint32_t>(turn) * (lines / 7 + 1)) / kLines);
+    if (line >= static_cast<uint32_t>(lines)) line -= lines;
+    first[u] = (line * 8 + at % 8) * kLen;
+    v[u] = *reinterpret_cast<const uint4*>(row.x + first[u]);
+  }
+  float x[kSampleEach];
+  uint32_t on = 0;
+  const float lo_value = place_value(in.lo), hi_value = place_value(in.hi);
+  float high = -kInf, low = kInf;
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    Vec<T>::unpack(v[u], x + u * kLen);
+#pragma unroll
+    for (int e = 0; e < kLen; ++e) {
+      const float y = x[u * kLen + e];
+      bool mine = !(y < lo_value) && !(y > hi_value);
+      if (mine && (y == lo_value || y == hi_value || y != y)) {
+        const uint64_t c = pack_best(order_key(y), first[u] + e);
+        mine = c >= in.lo && c <= in.hi;
+      }
+      if (mine) {
+        on |= 1u << (u * kLen + e);
+        if (fabsf(y) < kInf) {
+          high = fmaxf(high, y);
+          low = fminf(low, y);
+        }
+      }
+    }
+  }
+  uint64_t r[3] = {static_cast<uint64_t>(__popc(on)), order_key(high), order_key(-low)};
+  __syncthreads();
+#pragma unroll
+  for (int u = 0; u < (kWeights ? 2 : 1); ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  block_reduce<3, 1>(r, s);
+  const int m = static_cast<int>(r[0]);
+  high = key_value(static_cast<uint32_t>(r[1]));
+  low = -key_value(static_cast<uint32_t>(r[2]));
+  if (m == 0 || !(high >= low)) return;
+  // one of the sample stands for `each` of the row
+  const float each = static_cast<float>(row.vocab) / kSampleSize;
+  const float width = fminf(high - low, 32.0f / row.inv_t);
+  if (threadIdx.x == 0) {
+    s.rank = m;
+    s.lo_bin = kBins;
+    s.hi_bin = -1;
+  }
+  if (!(width > 0.0f)) {                   // equal logits: their indices lie evenly, for all that is known
+    __syncthreads();
+    if (kWeights) missing /= fmaxf(fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f)), 1e-30f);
+    const uint32_t key = order_key(high);
+    const float i0 = in.hi >> 32 == key ? static_cast<float>(min(~static_cast<uint32_t>(in.hi), static_cast<uint32_t>(row.vocab))) : 0.0f;
+    const float i1 = in.lo >> 32 == key ? static_cast<float>(min(~static_cast<uint32_t>(in.lo), static_cast<uint32_t>(row.vocab))) : static_cast<float>(row.vocab);
+    const float part = missing / (static_cast<float>(m) * each), span = most / (static_cast<float>(m) * each);
+    const float end = part + span, start = part - span;
+    const uint64_t base = static_cast<uint64_t>(key) << 32;
+    if (end < 1.0f) lo = max(lo, base | ~static_cast<uint32_t>(i0 + end * (i1 - i0)));
+    if (start > 0.0f) hi = min(hi, base | ~static_cast<uint32_t>(i0 + start * (i1 - i0)));
+    if (lo > hi) {
+      lo = in.lo;
+      hi = in.hi;
+    }
     return;
   }
-  const int m = sample_row(row, vocab, in.lo, in.hi, turn, s);
-  if (m == 0) return;
-  // one of the sample stands for `each` of the row
-  const float each = static_cast<float>(vocab) / kSampleSize;
-  float rank;
-  if (kWeigh) {
-    const uint64_t missing = max(1ull, static_cast<unsigned long long>(static_cast<float>(target - in.m) / each));
-    uint64_t all = 0;
-    for (int i = threadIdx.x; i < m; i += kFiltThreads)
-      all += weight_of(__fmul_rn(place_value(s.list[i]), inv_t), scale, s.table);
-    all = block_sum(all, s);
-    if (all < missing) {
-      rank = static_cast<float>(m);
-    } else {
-      const uint64_t c = select<true>(m, in.lo, in.hi, missing, inv_t, scale, s);
-      uint64_t r = 0;
-      for (int i = threadIdx.x; i < m; i += kFiltThreads) r += s.list[i] >= c;
-      rank = static_cast<float>(block_sum(r, s));
-    }
-  } else {
-    rank = static_cast<float>(target - in.n) / each;
+  const float per = kBins / width;
+  const float to_y = row.inv_t * kLog2e;
+#pragma unroll
+  for (int e = 0; e < kSampleEach; ++e) {
+    if (!(on >> e & 1)) continue;
+    const int j = fabsf(x[e]) < kInf ? min(static_cast<int>((high - x[e]) * per), kBins - 1) : 0;
+    atomicAdd(&s.bins[0][j], 1u);
+    // a weight relative to the largest of the sample's, in steps of 2^-18
+    if (kWeights) atomicAdd(&s.bins[1][j], __float2uint_rn(fminf(fast_exp2((x[e] - high) * to_y), 1.0f) * 0x1p18f));
   }
-  const float margin = 4.0f * sqrtf(rank) + 8.0f;
-  const int down = static_cast<int>(fminf(rank + margin, 1e9f)), up = static_cast<int>(rank - margin);
-  if (down <= m) lo = select<false>(m, in.lo, in.hi, down, inv_t, scale, s);
-  if (up >= 1 && up <= m) hi = select<false>(m, in.lo, in.hi, up, inv_t, scale, s);
+  __syncthreads();
+  uint32_t n[kEach], w[kEach], up_n = 0, up_w = 0;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    n[u] = s.bins[0][threadIdx.x * kEach + u];
+    w[u] = kWeights ? s.bins[1][threadIdx.x * kEach + u] : 0u;
+    up_n += n[u];
+    up_w += w[u];
+  }
+  const uint32_t own_n = up_n, own_w = up_w;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, up_n, o), b = kWeights ? __shfl_up_sync(0xffffffffu, up_w, o) : 0u;
+    if (lane >= o) {
+      up_n += a;
+      up_w += b;
+    }
+  }
+  if (lane == 31) s.red[0][warp] = static_cast<uint64_t>(up_w) << 32 | up_n;
+  __syncthreads();
+  uint32_t at_n = up_n - own_n, at_w = up_w - own_w;
+#pragma unroll
+  for (int q = 0; q < kFiltWarps; ++q) {
+    if (q < warp) {
+      at_n += static_cast<uint32_t>(s.red[0][q]);
+      at_w += static_cast<uint32_t>(s.red[0][q] >> 32);
+    }
+  }
+  float rank;
+  if (kWeights) {
+    // missing is in units of 2^k: to steps of the largest sampled weight
+    const float unit = fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f));
+    const float want = fminf(missing / (each * unit) * 0x1p18f, 4e9f);
+    const uint32_t target = max(1u, __float2uint_rn(want));
+    uint32_t a_n = at_n, a_w = at_w;
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      if (a_w < target && target <= a_w + w[u]) s.rank = static_cast<int>(a_n + n[u] / 2);
+      a_n += n[u];
+      a_w += w[u];
+    }
+    __syncthreads();
+    rank = static_cast<float>(s.rank);
+  } else {
+    rank = missing / each;
+  }
+  const float margin = fminf(sigmas * sqrtf(rank) + slack, most / each);
+  const int down = static_cast<int>(fminf(rank + margin, 1e9f)) + 1, up = static_cast<int>(rank - margin);
+  uint32_t a_n = at_n;
+#pragma unroll
+  for (int u = 0; u < kEach; ++u) {
+    const int next = static_cast<int>(a_n + n[u]), before = static_cast<int>(a_n);
+    if (before < down && down <= next) s.lo_bin = threadIdx.x * kEach + u;
+    if (before < up && up <= next) s.hi_bin = threadIdx.x * kEach + u;
+    a_n += n[u];
+  }
+  __syncthreads();
+  const int lo_bin = s.lo_bin, hi_bin = s.hi_bin;
+  if (lo_bin < kBins - 1) lo = max(lo, static_cast<uint64_t>(order_key(high - static_cast<float>(lo_bin + 1) / per)) << 32);
+  if (hi_bin > 0) hi = min(hi, static_cast<uint64_t>(order_key(high - static_cast<float>(hi_bin) / per)) << 32 | 0xffffffffu);
+  if (lo < kLowest) lo = kLowest;
+  if (lo > hi) {                           // (roundings of a narrow range)
+    lo = in.lo;
+    hi = in.hi;
+  }
 }
 
-// The place at which the count (or the weight) from the top reaches target,
-// within the bounds. Leaves the last bracket in `view`, its places on the list.
-template <bool kWeigh, typename T>
-__device__ __noinline__ uint64_t locate(const T* row, int vocab, Bounds in, uint64_t target, float inv_t,
-                                        const WeightScale& scale, FiltSmem& s, Bracket& view) {
+// The next bracket within the bounds: four times around what a sample says, then
+// half of the bounds.
+template <bool kWeights, typename T>
+__device__ __forceinline__ void next_bracket(const Row<T>& row, const Bounds& in, float missing, int turn,
+                                             const WeightScale& scale, FiltSmem& s, uint64_t& lo, uint64_t& hi) {
+  lo = in.lo;
+  hi = in.hi;
+  if (row.vocab <= kListCap) return;       // (one CTA, and all of the row on the list)
+  if (turn <= kSampledTurns) {
+    sample_bracket<kWeights>(row, in, missing, turn, 2.5f, 6.0f, 0.4f * kListCap, scale, s, lo, hi);
+  } else {
+    lo = in.lo + (in.hi - in.lo) / 2 + 1;
+    if (lo > in.hi) lo = in.hi;
+  }
+}
+
+// The place of rank k within the bounds (or their lowest place, where there are
+// fewer). Leaves the last bracket in `view`, its places on the list.
+template <typename T>
+__device__ __noinline__ uint64_t locate_rank(const Row<T>& row, Bounds in, int k, FiltSmem& s, Bracket& view) {
+  const WeightScale none = weight_scale(0.0f, row.bits);
   for (int turn = 1; turn <= kTurns; ++turn) {
     uint64_t lo, hi;
-    next_bracket<kWeigh>(row, vocab, in, target, turn, inv_t, scale, s, lo, hi);
-    view = pass<false, kWeigh>(row, vocab, lo, hi, inv_t, scale, s);
-    const uint64_t above = kWeigh ? view.m_above : static_cast<uint64_t>(view.n_above);
-    const uint64_t with = above + (kWeigh ? view.m_in : static_cast<uint64_t>(view.n_in));
-    if (above >= target) {
-      in.lo = hi + 1;                      // (hi < in.hi, above which the target is not reached)
-    } else if (with < target) {
+    next_bracket<false>(row, in, static_cast<float>(k - in.n), turn, none, s, lo, hi);
+    view = pass<Weigh::kNone>(row, lo, hi, none, s);
+    const int with = view.n_above + view.n_in;
+    if (view.n_above >= k) {
+      in.lo = hi + 1;                      // (hi < in.hi, above which there are fewer)
+    } else if (with < k) {
+      if (lo == in.lo) return in.lo;       // all that there is
+      in.hi = lo - 1;
+      in.n = with;
+    } else if (view.whole) {
+      return select_rank(view, k - view.n_above, row, s);
+    } else {
+      in = {lo, hi, view.n_above, 0};
+    }
+  }
+  return in.lo;                            // (not reached: 64 halvings leave one place)
+}
+
+// The place within the bounds at which the weight from the top reaches the target:
+// target.share of all weights, or target.most itself where share is 0 (target.most
+// is a guess otherwise). `from` > 0 is where the first bracket begins. Leaves the
+// last bracket in `view`, its places on the list, and the weight from the top down
+// to the place in `mass`.
+template <typename T>
+__device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Target target, uint64_t from,
+                                               const WeightScale& scale, FiltSmem& s, Bracket& view, uint64_t& mass) {
+  bool exact = scale.tie, again = from != 0;
+  uint64_t lo = from, hi = in.hi;
+  for (int turn = 1; turn <= kTurns; ++turn) {
+    if (!again) {
+      const float missing = static_cast<float>(target.most - min(target.most, in.m)) * exp2f(static_cast<float>(-row.bits));
+      next_bracket<true>(row, in, missing, turn, scale, s, lo, hi);
+    }
+    again = false;
+    view = exact ? pass<Weigh::kExact>(row, lo, hi, scale, s) : pass<Weigh::kClose>(row, lo, hi, scale, s);
+    uint64_t sum = view.m_in;
+    if (!exact && view.whole) {            // listed weights are exact
+      uint64_t own = 0;
+      for (int i = threadIdx.x; i < view.n_in; i += kFiltThreads) own += weight_of(__fmul_rn(place_value(s.list[i]), row.inv_t), scale, s.table);
+      sum = block_sum(own, s);
+    }
+    // the others' sums are within `off` of what the pass gave: 2^-21.9 a weight, a vector's sum 2^-21
+    const uint64_t others = view.below + view.m_above + (view.whole ? 0 : sum);
+    const uint64_t off = exact ? 0 : static_cast<uint64_t>(static_cast<float>(others) * 0x1.8p-20f) + 2;
+    uint64_t least = target.most, most = target.most;
+    if (target.share > 0.0f) {
+      const uint64_t z = view.below + view.m_above + sum;
+      least = share_of(target.share, z > off ? z - off : 0);
+      most = off ? share_of(target.share, z + off) : least;
+      target.most = most;
+    }
+    const uint64_t above_least = view.m_above > off ? view.m_above - off : 0, above_most = view.m_above + off;
+    if (above_least >= most) {             // above the bracket
+      in.lo = hi + 1;
+    } else if (above_most + sum + off < least) {                       // below it
       if (lo == in.lo) return in.lo;       // all that there is
       in.hi = lo - 1;
       in.n = view.n_above + view.n_in;
-      in.m = view.m_above + view.m_in;
-    } else if (view.n_in <= kListCap) {
-      return select<kWeigh>(view.n_in, lo, hi, target - above, inv_t, scale, s);
+      in.m = view.m_above + sum;
+    } else if (exact ? !view.whole : !view.whole && above_most < least && most + off <= above_least + sum) {
+      in = {lo, hi, view.n_above, view.m_above};                       // in it, and more than the list holds
     } else {
-      in.lo = lo;
-      in.hi = hi;
-      in.n = view.n_above;
-      in.m = view.m_above;
+      Target inner = {least > above_most ? least - above_most : 0, most - above_least, 0.0f, 0, 0};
+      const uint64_t at = view.whole && inner.least > 0 && inner.most <= sum ? select_weight(view, lo, inner, sum, scale, row, s) : 0;
+      if (at != 0 && s.before < inner.least) {
+        mass = view.m_above + s.before + s.weight;
+        return at;
+      }
+      if (exact) return in.lo;             // (does not happen)
+      exact = again = true;                // the border is within the bound: the same bracket, exactly
     }
   }
   return in.lo;                            // (not reached: 64 halvings leave one place)
@@ -497,6 +846,7 @@ __device__ __forceinline__ uint32_t smallest_key(float least, float inv_t) {
 
 struct RowResult {
   uint64_t cut;            // the last place that is kept
+  uint64_t mass;           // the weight of all that is kept, 0: not known
   bool empty;              // nothing above -inf
   bool listed;             // all that is kept is on the list
   int n_list;
@@ -504,74 +854,83 @@ struct RowResult {
 };
 
 template <typename T>
-__device__ __forceinline__ RowResult find_cut(const T* row, int vocab, int bits, float inv_t, int k, float p,
-                                              float min_p, FiltSmem& s) {
-  const bool by_k = k > 0 && k < vocab, by_p = p < 1.0f, by_m = min_p > 0.0f;
+__device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p, float min_p, FiltSmem& s) {
+  const bool by_k = k > 0 && k < row.vocab, by_p = p < 1.0f, by_m = min_p > 0.0f;
+  const int vocab = row.vocab;
   uint64_t lo = kLowest, hi = kHighest;
-  const WeightScale none = weight_scale(0.0f, bits);
+  const WeightScale none = weight_scale(0.0f, row.bits);
   // 1. where the list begins (and ends, for a top-k set that no list holds)
   if (vocab > kListCap) {
-    const int m = sample_row(row, vocab, kLowest, kHighest, 0, s);
-    const float rank = static_cast<float>(by_k ? k : 1024) * kSampleSize / vocab;
-    const float margin = 3.0f * sqrtf(rank) + 8.0f;
-    const int down = static_cast<int>(fminf(rank + margin, 1e9f)), up = static_cast<int>(rank - margin);
-    if (down <= m) lo = select<false>(m, kLowest, kHighest, down, inv_t, none, s);
-    if (static_cast<float>(down) * vocab / kSampleSize > kListCap && up >= 1 && up <= m)
-      hi = select<false>(m, kLowest, kHighest, up, inv_t, none, s);
+    const float wanted = static_cast<float>(by_k ? k : kFirstList);
+    sample_bracket<false>(row, Bounds{kLowest, kHighest, 0, 0}, wanted, 0, 3.0f, 8.0f, 0.4f * kListCap, none, s, lo, hi);
+    if (wanted < 0.5f * kListCap) hi = kHighest;
   }
   // 2. the list; weights below it relative to its first place, a power of two
   // from the row's (not where the reduction differs)
   const bool total = by_p && !by_k;
-  const float s_lo = __fmul_rn(place_value(lo), inv_t);
-  const WeightScale low_scale = weight_scale(s_lo, bits);
+  const float s_lo = __fmul_rn(place_value(lo), row.inv_t);
+  const WeightScale low_scale = weight_scale(s_lo, row.bits);
   const bool low_fits = fabsf(s_lo) < kWeightSpan;
-  Bracket view = total && low_fits ? pass<true, false>(row, vocab, lo, hi, inv_t, low_scale, s)
-                                   : pass<false, false>(row, vocab, lo, hi, inv_t, none, s);
-  if (view.best == 0) return RowResult{kHighest, true, true, 0, none};       // (lo is kLowest then)
-  const WeightScale scale = weight_scale(__fmul_rn(place_value(view.best), inv_t), bits);
-  uint64_t cut = kLowest;
+  Bracket view = total && low_fits ? pass<Weigh::kBelow>(row, lo, hi, low_scale, s)
+                                   : pass<Weigh::kNone>(row, lo, hi, none, s);
+  if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)
+    view = pass<Weigh::kNone>(row, kLowest, kHighest, none, s);
+  if (!view.any) return RowResult{kHighest, 0, true, true, 0, none};
+  const WeightScale scale = weight_scale(__fmul_rn(view.top, row.inv_t), row.bits);
+  uint64_t cut = kLowest, mass = 0;
   // 3. top-k
   if (by_k) {
     const int with = view.n_above + view.n_in;
     if (view.n_above >= k) {
-      cut = locate<false>(row, vocab, Bounds{view.hi + 1, kHighest, 0, 0}, k, inv_t, scale, s, view);
+      cut = locate_rank(row, Bounds{view.hi + 1, kHighest, 0, 0}, k, s, view);
     } else if (with < k) {                 // (from the lowest place on fewer than k: all stay)
-      if (view.lo > kLowest) cut = locate<false>(row, vocab, Bounds{kLowest, view.lo - 1, with, 0}, k, inv_t, scale, s, view);
-    } else if (view.n_in <= kListCap) {
-      cut = select<false>(view.n_in, view.lo, view.hi, k - view.n_above, inv_t, scale, s);
+      if (view.lo > kLowest) cut = locate_rank(row, Bounds{kLowest, view.lo - 1, with, 0}, k, s, view);
+    } else if (view.whole) {
+      cut = select_rank(view, k - view.n_above, row, s);
     } else {
-      cut = locate<false>(row, vocab, Bounds{view.lo, view.hi, view.n_above, 0}, k, inv_t, scale, s, view);
+      cut = locate_rank(row, Bounds{view.lo, view.hi, view.n_above, 0}, k, s, view);
     }
   }
   // 4. top-p of what top-k leaves
   if (by_p) {
-    uint64_t z;
-    bool whole = view.hi == kHighest && view.n_in <= kListCap;      // the list holds all from view.lo on
-    if (total ? !(low_fits && whole && scale.ref == 0.0f && !scale.tie) : !(whole && cut >= view.lo)) {
-      // the sum in a pass of its own, the list anew beside it
-      view = pass<false, true>(row, vocab, cut, kHighest, inv_t, scale, s);
-      z = view.m_in;
-      whole = view.n_in <= kListCap;
-    } else {
-      uint64_t sum = 0;
-      const uint64_t from = by_k ? cut : view.lo;
-      for (int i = threadIdx.x; i < view.n_in; i += kFiltThreads)
-        if (s.list[i] >= from) sum += weight_of(__fmul_rn(place_value(s.list[i]), inv_t), scale, s.table);
-      view.m_in = block_sum(sum, s);
-      z = view.m_in;
-      if (total) {
-        const int down = scale.k - low_scale.k;
-        z += down < 64 ? view.below >> down : 0ull;
+    const bool listed = view.hi == kHighest && view.whole;      // the list holds all from view.lo on
+    uint64_t at = 0, sum = 0;
+    Target target = {1, 1, p, 0, 0};
+    if (by_k) {
+      if (listed && cut >= view.lo) {
+        at = select_weight(view, cut, target, sum, scale, row, s);
+        mass = s.before + s.weight;
+      } else {
+        view = pass<Weigh::kExact>(row, cut, kHighest, scale, s);
+        target = {0, share_of(p, view.m_in), 0.0f, 0, 0};
+        target.least = target.most;
+        if (view.whole) {
+          at = select_weight(view, cut, target, sum, scale, row, s);
+          mass = s.before + s.weight;
+        } else {
+          at = locate_weight(row, Bounds{cut, kHighest, 0, 0}, target, 0, scale, s, view, mass);
+        }
       }
-    }
-    const uint64_t target = share_of(p, z);
-    uint64_t at;
-    if (whole && view.m_in >= target) {
-      at = select<true>(view.n_in, view.lo > cut ? view.lo : cut, kHighest, target, inv_t, scale, s);
     } else {
-      Bounds in = {cut, kHighest, 0, 0};
-      if (whole && view.lo > cut) in = {cut, view.lo - 1, view.n_in, view.m_in};
-      at = locate<true>(row, vocab, in, target, inv_t, scale, s, view);
+      Bounds in = {kLowest, kHighest, 0, 0};
+      uint64_t from = 0;
+      if (listed && low_fits && scale.ref == 0.0f && !scale.tie) {
+        // The total lies within target.off. A weight's exponent y is off by less than |y| 2^-22.8 (the rounded
+        // product, its factor, log2 e) and |y - k| 2^-24, exp2 by 2^-22, a vector's sum by 2^-21; tokens with
+        // y - k below -20 are covered by the second term.
+        const int down = scale.k - low_scale.k;
+        const float rel = (fabsf(static_cast<float>(low_scale.k)) + 24.0f) * 0x1p-22f;
+        const uint64_t few = static_cast<uint64_t>(vocab) << max(row.bits - 42, 0);
+        target.below = down < 64 ? view.below >> down : 0ull;
+        target.off = static_cast<uint64_t>(static_cast<float>(target.below) * rel) + (down < 64 ? few >> down : 0ull) + 2;
+        at = select_weight(view, view.lo, target, sum, scale, row, s);
+        if (at != 0 && s.before < target.least) mass = s.before + s.weight;      // all targets fall on one token
+        else if (sum >= target.least) { at = 0; from = view.lo; }                 // on the list, or close to its end
+        else if (view.lo > kLowest) { at = 0; in = {kLowest, view.lo - 1, view.n_in, sum}; }
+        else at = 0;
+        target.below = target.off = 0;
+      }
+      if (at == 0) at = locate_weight(row, in, target, from, scale, s, view, mass);
     }
     if (at > cut) cut = at;
   }
@@ -579,11 +938,14 @@ __device__ __forceinline__ RowResult find_cut(const T* row, int vocab, int bits,
   if (by_m) {
     float least = scale.s_max;
     if (!scale.tie) least = __double2float_ru(static_cast<double>(scale.s_max) + log(static_cast<double>(min_p)));
-    const uint32_t key = scale.s_max != scale.s_max ? 0xffffffffu : smallest_key(least, inv_t);
+    const uint32_t key = scale.s_max != scale.s_max ? 0xffffffffu : smallest_key(least, row.inv_t);
     const uint64_t at = static_cast<uint64_t>(key) << 32;
-    if (at > cut) cut = at;
+    if (at > cut) {
+      cut = at;
+      mass = 0;
+    }
   }
-  return RowResult{cut, false, view.hi == kHighest && view.n_in <= kListCap && cut >= view.lo, view.n_in, scale};
+  return RowResult{cut, mass, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, scale};
 }
 
 // ------------------------------------------------------------------- endings
@@ -600,27 +962,46 @@ __device__ __forceinline__ float log_share(float s_tok, uint64_t sum, const Weig
   return kLn2 * ((yh - static_cast<float>(w.k)) + yl) - logf(total);
 }
 
+template <typename T>
 struct DrawBody {
+  const Row<T>& row;
   const float* noise;
   uint64_t cut;
-  float cut_value, inv_t;
+  float cut_value;
   bool weigh;
   WeightScale scale;
   const unsigned long long* table;
   uint64_t best, sum;
 
-  __device__ __forceinline__ void take(float x, int i) {
-    if (pack_best(order_key(x), i) < cut) return;
-    const float sx = __fmul_rn(x, inv_t);
-    const uint64_t c = pack_best(order_key(__fadd_rn(sx, noise[i])), i);
+  __device__ __forceinline__ void take(float x, float g, int i) {
+    const float sx = __fmul_rn(x, row.inv_t);
+    const uint64_t c = pack_best(order_key(__fadd_rn(sx, g)), i);
     if (c > best) best = c;
     if (weigh) sum += weight_of(sx, scale, table);
   }
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
+    uint32_t in = 0;
+#pragma unroll
+    for (int e = 0; e < kLen; ++e) {
+      bool keep = !(x[e] < cut_value);
+      if (keep && !(x[e] > cut_value)) keep = pack_best(order_key(x[e]), i0 + e) >= cut;
+      in |= keep ? 1u << e : 0u;
+    }
+    if (!in) return;
+    float g[kLen];
+    if constexpr (kLen % 4 == 0) {
+#pragma unroll
+      for (int e = 0; e < kLen; e += 4) {
+        const float4 v = *reinterpret_cast<const float4*>(noise + i0 + e);
+        g[e] = v.x; g[e + 1] = v.y; g[e + 2] = v.z; g[e + 3] = v.w;
+      }
+    } else {
+      g[0] = noise[i0];
+    }
 #pragma unroll
     for (int e = 0; e < kLen; ++e)
-      if (!(x[e] < cut_value)) take(x[e], i0 + e);
+      if (in >> e & 1) take(x[e], g[e], i0 + e);
   }
 };
 
@@ -693,23 +1074,25 @@ struct MaskBody {
       kept += keep;
     }
     if constexpr (kLen == 1) store_one(out + i0, y[0]);
-    else reinterpret_cast<uint4*>(out)[i0 / kLen] = Vec<T>::pack(y);
+    else *reinterpret_cast<uint4*>(out + i0) = Vec<T>::pack(y);
   }
 };
 
 template <typename T, bool kSampling>
-__global__ void __launch_bounds__(kFiltThreads, 2) filtered_kernel(const __grid_constant__ FiltParams p) {
+__global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
   if (threadIdx.x < kWeightTable) s.table[threadIdx.x] = c_weight_table[threadIdx.x];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int b = blockIdx.y, node = blockIdx.x;
+  const int csize = p.csize, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const int b = blockIdx.y, node = blockIdx.x / csize;
   const int st = p.status[b];
   const int t0 = p.cu_nodes[b], n = p.cu_nodes[b + 1] - t0;
   const float temp = p.temperature[b];
   const int k = p.top_k ? p.top_k[b] : 0;
   const float top_p = p.top_p ? p.top_p[b] : 1.0f, min_p = p.min_p ? p.min_p[b] : 0.0f;
+  // every CTA of a cluster takes the same branches (same b and node)
   if (st != 0 || (node >= n && n >= 0)) return;
   const float inv_t = temp > 0.0f ? __frcp_rn(temp) : 1.0f;
   int flag = 0;
@@ -717,85 +1100,131 @@ __global__ void __launch_bounds__(kFiltThreads, 2) filtered_kernel(const __grid_
   if (!(temp >= 0.0f) || temp == kInf || inv_t == kInf || (kSampling && temp > 0.0f && !p.gumbel)) flag |= TV_ST_BAD_TEMPERATURE;
   if (k < 0 || !(top_p >= 0.0f && top_p <= 1.0f) || !(min_p >= 0.0f && min_p <= 1.0f)) flag |= TV_ST_BAD_FILTER;
   if (flag) {
-    if (node == 0 && threadIdx.x == 0) atomicOr(&p.status[b], flag);
+    if (node == 0 && rank == 0 && threadIdx.x == 0) atomicOr(&p.status[b], flag);
     return;
   }
   const size_t t = static_cast<size_t>(t0) + node;
-  const T* row = static_cast<const T*>(p.logits) + t * p.logits_ld;
-  const int vocab = p.vocab;
+  Row<T> row = {static_cast<const T*>(p.logits) + t * p.logits_ld, p.vocab, 0, p.vocab, rank, csize, inv_t, p.bits};
+  if (csize > 1) {
+    const int per = ((p.vocab + csize - 1) / csize + 7) & ~7;
+    row.v0 = min(p.vocab, rank * per);
+    row.v1 = min(p.vocab, row.v0 + per);
+  }
   const bool greedy = temp == 0.0f;
-  const bool filtered = !greedy && ((k > 0 && k < vocab) || top_p < 1.0f || min_p > 0.0f);
+  const bool filtered = !greedy && ((k > 0 && k < p.vocab) || top_p < 1.0f || min_p > 0.0f);
   __syncthreads();
 
-  RowResult res = {kLowest, false, false, 0, weight_scale(0.0f, p.bits)};
+  // Each CTA's part of an ending goes to s.stat; the first CTA combines them.
+  auto publish = [&](uint64_t a, uint64_t b2, uint64_t c) {
+    __syncwarp();
+    row_barrier(csize);                    // what a pass left there is read
+    if (threadIdx.x == 0) {
+      s.stat[0] = a;
+      s.stat[1] = b2;
+      s.stat[2] = c;
+    }
+    __syncwarp();
+    row_barrier(csize);
+  };
+  auto finish = [&] {                      // no CTA goes while its memory may be read
+    __syncwarp();
+    if (csize > 1) cluster_sync_all();
+  };
+
+  RowResult res = {kLowest, 0, false, false, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
     TopBody body = {0};
-    for_row(row, vocab, body);
-    const uint64_t best = block_max(body.best, s);
+    for_slice(row, body);
+    publish(block_max(body.best, s), 0, 0);
+    const uint64_t best = cluster_stat<true>(s, 0, csize);
     res.empty = best < kLowest;
     res.cut = res.empty ? kHighest : best;
     if (kSampling) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && rank == 0) {
         p.tokens[t] = res.empty ? 0 : best_index(best);
         if (p.logp) p.logp[t] = res.empty ? -kInf : 0.0f;
       }
+      finish();
       return;
     }
   } else if (filtered) {
-    res = find_cut(row, vocab, p.bits, inv_t, k, top_p, min_p, s);
+    res = find_cut(row, k, top_p, min_p, s);
   }
 
   if constexpr (kSampling) {
     const float* noise = p.gumbel + t * p.gumbel_ld;
     if (!filtered) {
       FreeBody body = {noise, inv_t, 0, -kInf, 0.0f, 0.0f};
-      for_row(row, vocab, body);
-      const uint64_t best = block_max(body.best, s);
-      const int token = best ? best_index(best) : 0;
-      if (threadIdx.x == 0) p.tokens[t] = token;
-      if (p.logp) {
-        const float top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
-        const float sum = block_sum(body.top == top ? body.sum : body.sum * fast_exp2((body.top - top) * kLog2e), s);
-        const float nans = block_sum(body.nans, s);
-        if (threadIdx.x == 0) {
-          const float mine = __fmul_rn(load_one(row + token), inv_t);
+      for_slice(row, body);
+      const uint64_t own = block_max(body.best, s);
+      const float own_top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
+      const float own_sum = block_sum(body.top == own_top ? body.sum : body.sum * fast_exp2((body.top - own_top) * kLog2e), s);
+      const float own_nans = block_sum(body.nans, s);
+      publish(own, static_cast<uint64_t>(__float_as_uint(own_sum)) << 32 | order_key(own_top), __float_as_uint(own_nans));
+      const uint64_t best = cluster_stat<true>(s, 0, csize);
+      if (threadIdx.x == 0 && rank == 0) {
+        const int token = best ? best_index(best) : 0;
+        p.tokens[t] = token;
+        if (p.logp) {
+          float top = -kInf, sum = 0.0f, nans = 0.0f;
+          for (int r = 0; r < csize; ++r) {
+            const uint64_t v = csize > 1 ? ld_cluster_u64(&s.stat[1], r) : s.stat[1];
+            top = fmaxf(top, key_value(static_cast<uint32_t>(v)));
+            nans += __uint_as_float(static_cast<uint32_t>(csize > 1 ? ld_cluster_u64(&s.stat[2], r) : s.stat[2]));
+          }
+          for (int r = 0; r < csize; ++r) {
+            const uint64_t v = csize > 1 ? ld_cluster_u64(&s.stat[1], r) : s.stat[1];
+            const float its = key_value(static_cast<uint32_t>(v)), part = __uint_as_float(static_cast<uint32_t>(v >> 32));
+            sum += its == top ? part : part * fast_exp2((its - top) * kLog2e);
+          }
+          const float mine = __fmul_rn(load_one(row.x + token), inv_t);
           float out = (mine == top ? 0.0f : mine - top) - logf(sum);
           if (nans > 0.0f) out = mine != mine ? -logf(nans) : -kInf;
           p.logp[t] = best ? out : -kInf;
         }
       }
+      finish();
       return;
     }
     if (res.empty) {
-      if (threadIdx.x == 0) {
+      if (threadIdx.x == 0 && rank == 0) {
         p.tokens[t] = 0;
         if (p.logp) p.logp[t] = -kInf;
       }
+      finish();
       return;
     }
-    DrawBody body = {noise, res.cut, place_value(res.cut), inv_t, p.logp != nullptr, res.scale, s.table, 0, 0};
+    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table, 0, 0};
     if (res.listed) {
-      for (int i = threadIdx.x; i < res.n_list; i += kFiltThreads) {
+      for (int i = rank * kFiltThreads + threadIdx.x; i < res.n_list; i += csize * kFiltThreads) {
         const uint64_t c = s.list[i];
-        if (c >= res.cut) body.take(place_value(c), best_index(c));
+        if (c >= res.cut) body.take(place_value(c), noise[best_index(c)], best_index(c));
       }
     } else {
-      for_row(row, vocab, body);
+      for_slice(row, body);
     }
-    const uint64_t best = block_max(body.best, s);
-    const uint64_t sum = p.logp ? block_sum(body.sum, s) : 0;
-    if (threadIdx.x == 0) {
-      const int token = best_index(best);
+    const uint64_t own = block_max(body.best, s);
+    publish(own, body.weigh ? block_sum(body.sum, s) : 0, 0);
+    const int token = best_index(cluster_stat<true>(s, 0, csize));
+    const uint64_t sum = body.weigh ? cluster_stat<false>(s, 1, csize) : res.mass;
+    if (threadIdx.x == 0 && rank == 0) {
       p.tokens[t] = token;
-      if (p.logp) p.logp[t] = log_share(__fmul_rn(load_one(row + token), inv_t), sum, res.scale, s.table);
+      if (p.logp) {
+        p.logp[t] = log_share(__fmul_rn(load_one(row.x + token), inv_t), sum, res.scale, s.table);
+      }
     }
+    finish();
   } else {
+    // (in place: no CTA of the cluster writes before all have read the row)
     MaskBody<T> body = {static_cast<T*>(p.out) + t * p.out_ld, res.cut, place_value(res.cut), 0};
-    for_row(row, vocab, body);
-    if (p.kept) {
-      const uint64_t kept = block_sum(body.kept, s);
-      if (threadIdx.x == 0) p.kept[t] = static_cast<int>(kept);
-    }
+    __syncwarp();
+    row_barrier(csize);
+    for_slice(row, body);
+    const uint64_t own = block_sum(body.kept, s);
+    publish(own, 0, 0);
+    const int kept = static_cast<int>(cluster_stat<false>(s, 0, csize));
+    if (p.kept && threadIdx.x == 0 && rank == 0) p.kept[t] = kept;
+    finish();
   }
 }
 
@@ -812,11 +1241,17 @@ template <bool kSampling>
 static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
   static size_t smem_set[2][kMaxDevices] = {};
   const int dev = current_device();
-  if (dev < 0) return TV_ERR_CUDA;
+  const int sms = dev < 0 ? -1 : device_sm_count(dev);
+  if (sms <= 0) return TV_ERR_CUDA;
   auto* kernel = dtype == TV_DTYPE_F32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
-  if (!ensure_smem(kernel, sizeof(FiltSmem), smem_set[dtype], dev)) return TV_ERR_CUDA;
+  const long long rows = static_cast<long long>(batch) * p.max_nodes;
+  p.csize = 1;
+  while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * 3 && p.vocab > kListCap) p.csize *= 2;
+  const size_t most = sizeof(FiltSmem) + kLocalCap * sizeof(uint64_t);
+  if (!ensure_smem(kernel, most, smem_set[dtype], dev)) return TV_ERR_CUDA;
   p.bits = weight_bits(p.vocab);
-  const cudaError_t err = launch_pdl(kernel, dim3(p.max_nodes, batch), dim3(kFiltThreads), sizeof(FiltSmem), as_stream(stream), p);
+  const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(p.max_nodes * p.csize, batch), dim3(kFiltThreads), p.csize,
+                                                  p.csize > 1 ? most : sizeof(FiltSmem), as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 

@@ -4,7 +4,7 @@
 // two sums of weights, and in a flat row that token's share is 1e-5 or less:
 // float32 sums would decide one row in a hundred wrongly, and sums of floats
 // depend on their order. Here a weight is round(2^F * 2^(s log2 e - K)) with
-// K = rint(s_max log2 e): integers, so sums are exact in any order, and equal
+// K = floor(s_max log2 e): integers, so sums are exact in any order, and equal
 // logits have equal weights.
 //
 // exp by table, after Tang, "Table-driven implementation of the exponential
@@ -21,15 +21,16 @@
 
 namespace tv {
 
-constexpr int kWeightTable = 33;         // 2^(j / 32), j = -16 .. 16, times 2^44
+constexpr int kWeightTable = 32;         // 2^(j / 32) times 2^44
 __constant__ const unsigned long long c_weight_table[kWeightTable] = {
-    12439554047902ull, 12711944812080ull, 12990300157313ull, 13274750690919ull, 13565429880144ull,
-    13862474114787ull, 14166022771192ull, 14476218277651ull, 14793206181226ull, 15117135216047ull,
-    15448157373097ull, 15786427971528ull, 16132105731538ull, 16485352848846ull, 16846335070792ull,
-    17215221774115ull, 17592186044416ull, 17977404757381ull, 18371058661769ull, 18773332464219ull,
-    19184414915921ull, 19604498901178ull, 20033781527906ull, 20472464220127ull, 20920752812471ull,
-    21378857646762ull, 21846993670708ull, 22325380538761ull, 22814242715178ull, 23313809579344ull,
-    23824315533396ull, 24346000112214ull, 24879108095804ull};
+    17592186044416ull, 17977404757381ull, 18371058661769ull, 18773332464219ull,
+    19184414915921ull, 19604498901178ull, 20033781527906ull, 20472464220127ull,
+    20920752812471ull, 21378857646762ull, 21846993670708ull, 22325380538761ull,
+    22814242715178ull, 23313809579344ull, 23824315533396ull, 24346000112214ull,
+    24879108095804ull, 25423889624159ull, 25980600314626ull, 26549501381838ull,
+    27130859760289ull, 27724948229574ull, 28332045542385ull, 28952436555301ull,
+    29586412362452ull, 30234270432094ull, 30896314746195ull, 31572855943056ull,
+    32264211463077ull, 32970705697691ull, 33692670141585ull, 34430443548229ull};
 
 constexpr float kLog2e = 1.44269502f, kLog2eLow = 0x1.4ae0c0p-26f;     // together log2 e to 2^-50
 constexpr float kLn2 = 0x1.62e430p-1f, kLn2Low = -0x1.05c610p-29f;
@@ -40,10 +41,15 @@ struct WeightScale {
   float ref;       // subtracted from s first: 0, or s_max where |s_max| >= kWeightSpan (then exact
                    // for every s whose weight is not 0)
   float s_max;
-  int k;           // rint((s_max - ref) log2 e)
+  int k;           // floor((s_max - ref) log2 e), to the reduction's rounding
   int bits;        // F
   bool tie;        // s_max is infinite or NaN: what equals it weighs 2^F, all else nothing
 };
+
+// rint(32 y) for |y| < 2^16: adding a number whose last bit stands for 2^-5
+// leaves it in the sum's last bits.
+constexpr float kSteps = 0x1.8p18f;
+__device__ __forceinline__ int weight_steps(float y) { return __float_as_int(y + kSteps) - __float_as_int(kSteps); }
 
 __device__ __forceinline__ WeightScale weight_scale(float s_max, int bits) {
   WeightScale w;
@@ -51,40 +57,41 @@ __device__ __forceinline__ WeightScale weight_scale(float s_max, int bits) {
   w.bits = bits;
   w.tie = !(fabsf(s_max) < __int_as_float(0x7f800000));
   w.ref = fabsf(s_max) < kWeightSpan || w.tie ? 0.0f : s_max;
-  w.k = w.tie ? 0 : __float2int_rn(__fmul_rn(s_max - w.ref, kLog2e));
+  w.k = w.tie ? 0 : weight_steps(__fmul_rn(s_max - w.ref, kLog2e)) >> 5;
   return w;
 }
 
-// F for sums of n weights (each below 1.5 * 2^F) that stay below 2^63
+// F for sums of n weights (each at most 2^(F+1)) that stay below 2^64
 inline int weight_bits(int n) {
   int log = 0;
   while ((1ll << log) < n) ++log;
   return 62 - log < 44 ? 62 - log : 44;
 }
 
+// Integers come out of floats by adding a number whose last bit stands for the
+// unit wanted: conversion instructions run at a fraction of that rate.
 __device__ __forceinline__ uint64_t weight_of(float s, const WeightScale& w, const unsigned long long* table) {
   if (w.tie) return (s == w.s_max || (s != s && w.s_max != w.s_max)) ? 1ull << w.bits : 0ull;
   s -= w.ref;
   const float yh = __fmul_rn(s, kLog2e);
-  const float kf = rintf(yh);
-  const float down = static_cast<float>(w.k) - kf;       // halvings
-  if (!(down < 63.0f)) return 0ull;                      // (s = -inf too)
+  if (!(yh > static_cast<float>(w.k - 62))) return 0ull;               // (s = -inf too)
   const float yl = __fmaf_rn(s, kLog2eLow, __fmaf_rn(s, kLog2e, -yh));
-  const float f = yh - kf;
-  const float jf = rintf(f * 32.0f);
-  const float r = __fmaf_rn(jf, -0.03125f, f);
+  constexpr float kUpper = 3.0f, kLower = 0x1.8p-12f;    // last bits 2^-22, 2^-35
+  const float steps = yh + kSteps;                       // 32 k + j
+  const float r = yh - (steps - kSteps);
+  const int n = __float_as_int(steps) - __float_as_int(kSteps);
   const float zh = __fmul_rn(r, kLn2);
-  const float zl = __fmaf_rn(r, kLn2, -zh) + __fmaf_rn(r, kLn2Low, yl * kLn2);
+  const float zl = __fmaf_rn(yl, kLn2, __fmaf_rn(r, kLn2Low, __fmaf_rn(r, kLn2, -zh)));
   const float z = zh + zl;
   const float q = __fmaf_rn(z * z, __fmaf_rn(z, __fmaf_rn(z, __fmaf_rn(z, 1.0f / 120, 1.0f / 24), 1.0f / 6), 0.5f), zl);
-  const long long t = static_cast<long long>(table[static_cast<int>(jf) + 16]);
-  const int t30 = static_cast<int>((t + (1 << 13)) >> 14);
-  const int zi = __float2int_rn(zh * 0x1p37f);           // below 2^30.6
-  const int qi = __float2int_rn(q * 0x1p44f);            // below 2^30.7
-  const uint64_t m = static_cast<uint64_t>(t + ((static_cast<long long>(t30) * zi) >> 23) +
-                                           ((static_cast<long long>(t30) * qi) >> 30));
-  const int shift = static_cast<int>(down) + 44 - w.bits;
-  return shift <= 0 ? m : shift > 63 ? 0ull : (m + ((1ull << shift) >> 1)) >> shift;
+  const float upper = zh + kUpper;                       // zh in steps of 2^-22, what is left beside q
+  const float lower = (q + (zh - (upper - kUpper))) + kLower;
+  const int e = ((__float_as_int(upper) - __float_as_int(kUpper)) << 13) + (__float_as_int(lower) - __float_as_int(kLower));
+  const unsigned long long t = table[n & 31];
+  const int g = static_cast<int>(static_cast<uint32_t>(t >> 12) ^ 0x80000000u);   // T - 3/2 in steps of 2^-32
+  const uint64_t m = t + static_cast<uint64_t>(768ll * e + ((static_cast<long long>(g) * e) >> 23));
+  const int shift = w.k - (n >> 5) + 44 - w.bits;
+  return shift <= 0 ? m : shift > 63 ? 0ull : ((m >> (shift - 1)) + 1) >> 1;
 }
 
 // The smallest integer >= p * z for 0 <= p < 1, and 1 at least: a prefix whose
