@@ -81,6 +81,7 @@ struct FiltParams {
 struct FiltSmem {
   uint32_t bins[4][kBins];                 // counts; weights in three parts
   unsigned long long table[kWeightTable];
+  float2 close[kWeightTable];              // the same in float32, the rounding's share beside it
   uint64_t red[6][kFiltWarps];
   uint64_t small[kSmall];
   uint64_t found, before, weight;          // of select
@@ -92,10 +93,18 @@ struct FiltSmem {
 
 // ---------------------------------------------------------------- reductions
 
+// Three parts of 22 bits: sums of 32 fit a register, and a warp adds a register
+// in one instruction.
 __device__ __forceinline__ uint64_t warp_sum_u64(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  const uint64_t a = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0x3fffffu);
+  const uint64_t b = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 22) & 0x3fffffu);
+  const uint64_t c = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 44));
+  return a + (b << 22) + (c << 44);
+}
+// The larger high half, then the larger low half of those that have it.
+__device__ __forceinline__ uint64_t warp_top_u64(uint64_t v) {
+  const uint32_t hi = static_cast<uint32_t>(v >> 32), high = __reduce_max_sync(0xffffffffu, hi);
+  return static_cast<uint64_t>(high) << 32 | __reduce_max_sync(0xffffffffu, hi == high ? static_cast<uint32_t>(v) : 0u);
 }
 
 // Sums (or, from kMax on, maxima) of kN numbers over the CTA.
@@ -103,7 +112,7 @@ template <int kN, int kMax>
 __device__ __forceinline__ void block_reduce(uint64_t (&v)[kN], FiltSmem& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int i = 0; i < kN; ++i) v[i] = i >= kMax ? warp_max_u64(v[i]) : warp_sum_u64(v[i]);
+  for (int i = 0; i < kN; ++i) v[i] = i >= kMax ? warp_top_u64(v[i]) : warp_sum_u64(v[i]);
   __syncthreads();                         // what was there is read
   if (lane == 0) {
 #pragma unroll
@@ -230,7 +239,7 @@ __device__ __forceinline__ uint64_t cluster_stat(const FiltSmem& s, int i, int c
 // ------------------------------------------------------------------ the pass
 
 // What a pass does with the tokens that it does not list: nothing; sum the
-// weights below the list, cheaply; sum those below and above within 2^-20; weigh
+// weights below the list, cheaply; sum those below and above within 2^-28; weigh
 // exactly.
 enum class Weigh { kNone, kBelow, kClose, kExact };
 
@@ -239,7 +248,7 @@ enum class Weigh { kNone, kBelow, kClose, kExact };
 struct Bracket {
   uint64_t lo, hi;
   int n_in, n_above;
-  uint64_t m_in, m_above, below;
+  uint64_t m_in, m_above, below;     // (kBelow: below alone)
   bool whole;                        // the list holds all places in [lo, hi]
   float top;                         // the largest logit from lo on
   bool any;                          // there is one
@@ -258,6 +267,37 @@ struct FloatSum {
   }
 };
 
+// A weight w (1 + q) of at most 2, and a sum of such: the multiples of 2^-12 in w
+// add up without rounding below 2^12; what is left of w, and w q, is small.
+struct Close {
+  float w, q;
+};
+struct ClosePart {                   // of one vector
+  float high, low;
+  __device__ __forceinline__ void add(const Close& c) {
+    constexpr float kGrid = 0x1.8p11f;                                   // last bit 2^-12
+    const float grid = (c.w + kGrid) - kGrid;
+    high += grid;
+    low += __fmaf_rn(c.w, c.q, c.w - grid);
+  }
+};
+struct CloseSum {
+  float high;
+  FloatSum low;
+  uint64_t put;                      // moved out of `high`, in steps
+  __device__ __forceinline__ void add(const ClosePart& p, float unit) {
+    high += p.high;
+    low.add(p.low);
+    if (high >= 2048.0f) {
+      put += static_cast<uint64_t>(__float2ll_rn(high * unit));
+      high = 0.0f;
+    }
+  }
+  __device__ __forceinline__ uint64_t steps(float unit) const {
+    return put + static_cast<uint64_t>(__float2ll_rn(high * unit)) + low.steps(unit);
+  }
+};
+
 template <Weigh kWeigh, typename T>
 struct PassBody {
   FiltSmem& s;
@@ -265,23 +305,29 @@ struct PassBody {
   uint64_t* list;                    // the CTA's own
   int cap;
   uint64_t lo, hi;
-  float lo_value, hi_value, to_y, y_off, floor;
+  float lo_value, hi_value, to_y, y_off, floor, unit;
   WeightScale scale;
   uint32_t best;                     // the largest order key from lo on
   int n_above;
   uint64_t m_in, m_above, below;
-  FloatSum f_below, f_above, f_in;
+  FloatSum f_below;                  // kBelow
+  CloseSum c_all, c_below, c_above;  // kClose
 
-  // kBelow: 2^(y - k), y = x to_y: the factor's rounding makes the exponent good to |y| 2^-22.8.
-  // kClose: 2^(y - k) with y as exact as the exact weights have it, the whole part kept
-  // out of the exponential: good to 2^-21.9 (2^-22 of ex2, 2^-25 of its argument).
-  __device__ __forceinline__ float weight(float x) const {
-    if (kWeigh == Weigh::kBelow) return fast_exp2(__fmaf_rn(x, to_y, y_off));
+  // 2^(y - k), y = x to_y: the factor's rounding makes the exponent good to |y| 2^-22.8.
+  __device__ __forceinline__ float cheap(float x) const { return fast_exp2(__fmaf_rn(x, to_y, y_off)); }
+
+  // The exact weights' reduction in float32: a weight is w (1 + q), w = 2^(k + j / 32) to its rounding, whose
+  // share is in q. Off by 2^-30 of it (z's and q's roundings, 2^-24 of |z| < 2^-6.5; z^5 / 120 left out).
+  __device__ __forceinline__ Close close(float x) const {
     const float sx = fmaxf(__fmul_rn(x, row.inv_t) - scale.ref, floor);
     const float yh = __fmul_rn(sx, kLog2e);
-    const float steps = yh + y_off;                                     // 1.5 * 2^23 - k
-    const float f = (yh - (steps - y_off)) + __fmaf_rn(sx, kLog2eLow, __fmaf_rn(sx, kLog2e, -yh));
-    return __int_as_float(__float_as_int(fast_exp2(f)) + (__float_as_int(steps) << 23));
+    const float steps = yh + y_off;                                     // 1.5 * 2^18 - k, last bit 2^-5
+    const float yl = __fmaf_rn(sx, kLog2eLow, __fmaf_rn(sx, kLog2e, -yh));
+    const float z = __fmaf_rn(yh - (steps - y_off), kLn2, yl * kLn2);
+    const int n = __float_as_int(steps);
+    const float2 t = s.close[n & 31];                                   // 2^(j / 32), its rounding's share
+    const float q = __fmaf_rn(z * z, __fmaf_rn(z, __fmaf_rn(z, 1.0f / 24, 1.0f / 6), 0.5f), z) + t.y;
+    return {__int_as_float(__float_as_int(t.x) + ((n & ~31) << 18)), q};
   }
   __device__ __forceinline__ uint64_t exact(float x) const { return weight_of(__fmul_rn(x, row.inv_t), scale, s.table); }
 
@@ -289,37 +335,44 @@ struct PassBody {
   __device__ __forceinline__ void take(float x, int i) {
     const uint32_t key = order_key(x);
     const uint64_t c = pack_best(key, i);
-    if (c < lo) {
-      if (kWeigh == Weigh::kExact) below += exact(x);
-      else if (kWeigh != Weigh::kNone) f_below.add(weight(x));
+    if (c < lo || c > hi) {
+      if (c < lo) {
+        if (kWeigh == Weigh::kExact) below += exact(x);
+        if (kWeigh == Weigh::kBelow) f_below.add(cheap(x));
+      } else {
+        best = key > best ? key : best;
+        ++n_above;
+        if (kWeigh == Weigh::kExact) m_above += exact(x);
+      }
+      if (kWeigh == Weigh::kClose) {
+        ClosePart part = {0.0f, 0.0f};
+        part.add(close(x));
+        if (c < lo) c_below.add(part, unit);
+        else c_above.add(part, unit);
+      }
       return;
     }
     best = key > best ? key : best;
-    if (c > hi) {
-      ++n_above;
-      if (kWeigh == Weigh::kExact) m_above += exact(x);
-      else if (kWeigh == Weigh::kClose) f_above.add(weight(x));
-    } else {
-      const int at = atomicAdd(&s.n_list, 1);
-      if (at < cap) list[at] = c;
-      if (kWeigh == Weigh::kExact) m_in += exact(x);
-      else if (kWeigh == Weigh::kClose) f_in.add(weight(x));
-    }
+    const int at = atomicAdd(&s.n_list, 1);
+    if (at < cap) list[at] = c;
+    if (kWeigh == Weigh::kExact) m_in += exact(x);
   }
 
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
     uint32_t in = 0;
-    float low = 0.0f, high = 0.0f, top = -kInf;
+    float low = 0.0f, top = -kInf;
+    ClosePart all = {0.0f, 0.0f}, under_part = {0.0f, 0.0f}, over_part = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
       const bool under = x[e] < lo_value, over = kWeigh != Weigh::kBelow && x[e] > hi_value;      // (a NaN is neither)
       if (!under && !over) in |= 1u << e;
-      if (kWeigh == Weigh::kBelow) low += under ? weight(x[e]) : 0.0f;
+      if (kWeigh == Weigh::kBelow) low += under ? cheap(x[e]) : 0.0f;
       if (kWeigh == Weigh::kClose) {
-        const float w = weight(x[e]);
-        low += under ? w : 0.0f;
-        high += over ? w : 0.0f;
+        const Close c = close(x[e]);
+        all.add(c);
+        if (under) under_part.add(c);
+        if (over) over_part.add(c);
       }
       if (kWeigh == Weigh::kExact) {
         const uint64_t w = exact(x[e]);
@@ -331,8 +384,12 @@ struct PassBody {
         ++n_above;
       }
     }
-    if (kWeigh == Weigh::kBelow || kWeigh == Weigh::kClose) f_below.add(low);
-    if (kWeigh == Weigh::kClose) f_above.add(high);
+    if (kWeigh == Weigh::kBelow) f_below.add(low);
+    if (kWeigh == Weigh::kClose) {
+      c_all.add(all, unit);
+      c_below.add(under_part, unit);
+      c_above.add(over_part, unit);
+    }
     if (kWeigh != Weigh::kBelow && top > -kInf) best = max(best, order_key(top));
     while (in) {
       const int e = __ffs(in) - 1;
@@ -350,27 +407,21 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
   row_barrier(row.csize);                  // the lists and sums of the pass before are read
   if (threadIdx.x == 0) s.n_list = 0;
   __syncthreads();
-  const float k = static_cast<float>(scale.k);
-  PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
-                              row.inv_t * kLog2e, kWeigh == Weigh::kClose ? 0x1.8p23f - k : -k, (k - 100.0f) * kLn2, scale, 0u, 0, 0, 0, 0,
-                              {0.0f, 0.0f}, {0.0f, 0.0f}, {0.0f, 0.0f}};
-  for_slice(row, body);
   // a weight is at most 2: sums stay below 2^31, in steps of 2^-F below 2^63
-  const float unit = exp2f(static_cast<float>(row.bits));
+  const float k = static_cast<float>(scale.k), unit = exp2f(static_cast<float>(row.bits));
+  PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
+                              row.inv_t * kLog2e, kWeigh == Weigh::kClose ? kSteps - k : -k, (k - 100.0f) * kLn2, unit, scale,
+                              0u, 0, 0, 0, 0, {}, {}, {}, {}};
+  for_slice(row, body);
   Bracket out;
   out.lo = lo;
   out.hi = hi;
-  uint64_t v[5] = {static_cast<uint64_t>(body.n_above), 0, 0, 0, body.best};
-  if (kWeigh == Weigh::kExact) {
-    v[1] = body.m_in;
-    v[2] = body.m_above;
-    v[3] = body.below;
-  } else {
-    if (kWeigh == Weigh::kClose) {
-      v[1] = body.f_in.steps(unit);
-      v[2] = body.f_above.steps(unit);
-    }
-    if (kWeigh != Weigh::kNone) v[3] = body.f_below.steps(unit);
+  uint64_t v[5] = {static_cast<uint64_t>(body.n_above), body.m_in, body.m_above, body.below, body.best};
+  if (kWeigh == Weigh::kBelow) v[3] = body.f_below.steps(unit);
+  if (kWeigh == Weigh::kClose) {
+    v[2] = body.c_above.steps(unit);
+    v[3] = body.c_below.steps(unit);
+    v[1] = body.c_all.steps(unit) - v[2] - v[3];           // (may be off by the others' roundings, below 0 too)
   }
   block_reduce<5, 4>(v, s);                // (its barriers close the list too)
   const int listed = s.n_list;
@@ -382,18 +433,50 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
     }
     __syncwarp();
     cluster_sync_all();
-    out.n_in = static_cast<int>(cluster_stat<false>(s, 0, row.csize));
+    // one round trip for all numbers (lane by lane: number i of CTA r), one for the lists
+    const int lane = threadIdx.x & 31, shift = __ffs(row.csize) - 1;
+    uint64_t got[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = cluster_stat<false>(s, i + 1, row.csize);
-    v[4] = cluster_stat<true>(s, 5, row.csize);
-    const uint64_t longest = cluster_stat<true>(s, 0, row.csize);
+    for (int j = 0; j < 2; ++j) {
+      const int q = lane + 32 * j;
+      got[j] = q < 6 * row.csize ? ld_cluster_u64(&s.stat[q >> shift], q & (row.csize - 1)) : 0ull;
+    }
+    int end[kFiltMaxCluster], longest = 0;
+    out.n_in = 0;
+#pragma unroll
+    for (int r = 0; r < kFiltMaxCluster; ++r) {
+      const int n = __shfl_sync(0xffffffffu, static_cast<int>(got[0]), r);
+      if (r < row.csize) {
+        out.n_in += n;
+        longest = max(longest, n);
+      }
+      end[r] = out.n_in;
+    }
+    for (int o = row.csize >> 1; o > 0; o >>= 1) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint64_t w = __shfl_xor_sync(0xffffffffu, got[j], o);
+        got[j] = (lane + 32 * j) >> shift == 5 ? (w > got[j] ? w : got[j]) : got[j] + w;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 5; ++i) {
+      const int q = (i + 1) << shift;
+      v[i] = __shfl_sync(0xffffffffu, q < 32 ? got[0] : got[1], q & 31);
+    }
     out.whole = out.n_in <= kListCap && longest <= kLocalCap;
     if (out.whole) {
-      int at = 0;
-      for (int r = 0; r < row.csize; ++r) {
-        const int n = static_cast<int>(ld_cluster_u64(&s.stat[0], r));
-        for (int i = threadIdx.x; i < n; i += kFiltThreads) s.list[at + i] = ld_cluster_u64(&own[i], r);
-        at += n;
+#pragma unroll 4
+      for (int i = threadIdx.x; i < out.n_in; i += kFiltThreads) {
+        int r = 0, from = 0;
+#pragma unroll
+        for (int u = 0; u < kFiltMaxCluster - 1; ++u) {
+          if (u < row.csize - 1 && i >= end[u]) {
+            r = u + 1;
+            from = end[u];
+          }
+        }
+        s.list[i] = ld_cluster_u64(&own[i - from], r);
       }
     }
     __syncthreads();
@@ -568,80 +651,108 @@ struct Bounds {
   uint64_t m;
 };
 
-// The part of the bounds that a sample of the row says to look at. 4096 tokens,
-// 128 bytes at a time evenly over the row (`turn` moves them), are sorted into bins
-// of equal width below the largest one; in them the rank at which the count (or,
-// with kWeights, the weight) `missing` is reached is found, and the bins `margin`
-// ranks above and below it are the bracket's ends. Widths go down to 32 / 1024 of
-// the scaled logit; what lies further below shares the last bin.
+// The part of the bounds that a sample of the row says to look at. 4096 tokens
+// (16384 with kWeights), 128 bytes at a time evenly over the row (`turn` moves
+// them), are sorted into bins of equal width below the largest one; in them the rank at
+// which the count (or, with kWeights, the weight) `missing` is reached is found, and
+// the bins `margin` ranks above and below it are the bracket's ends. The bins go down
+// to 32 below the largest scaled logit; what lies further below shares the last one.
 template <bool kWeights, typename T>
 __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in, float missing, int turn, float sigmas,
                                             float slack, float most, const WeightScale& scale, FiltSmem& s, uint64_t& lo,
                                             uint64_t& hi) {
   constexpr int kLen = Vec<T>::kLen, kVecs = kSampleEach / kLen, kLines = kSampleSize / kLen / 8;
-  constexpr int kEach = kBins / kFiltThreads;
+  constexpr int kSorts = kWeights ? 2 * kBins : kBins, kEach = kSorts / kFiltThreads;
+  uint32_t* counts = s.bins[0];
+  uint32_t* weights = s.bins[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = in.lo;
   hi = in.hi;
   const int lines = row.vocab / (8 * kLen);        // >= kLines: the row does not fit the list
-  uint4 v[kVecs];
-  int first[kVecs];
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const uint32_t at = u * kFiltThreads + threadIdx.x;
-    uint32_t line = static_cast<uint32_t>((static_cast<uint64_t>(at / 8) * lines + static_cast<uint32_t>(turn) * (lines / 7 + 1)) / kLines);
-    if (line >= static_cast<uint32_t>(lines)) line -= lines;
-    first[u] = (line * 8 + at % 8) * kLen;
-    v[u] = *reinterpret_cast<const uint4*>(row.x + first[u]);
-  }
-  float x[kSampleEach];
-  uint32_t on = 0;
+  const int pieces = kWeights && row.vocab >= 4 * kSampleSize ? 4 : 1;
   const float lo_value = place_value(in.lo), hi_value = place_value(in.hi);
-  float high = -kInf, low = kInf;
+  // a piece's vectors; bit e of the answer: x[e] lies within the bounds
+  auto fetch = [&](int piece, float* x) -> uint32_t {
+    uint4 v[kVecs];
+    int first[kVecs];
+    const uint32_t shift = static_cast<uint32_t>(piece) * (lines / 4) + static_cast<uint32_t>(turn) * (lines / 29);
 #pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    Vec<T>::unpack(v[u], x + u * kLen);
+    for (int u = 0; u < kVecs; ++u) {
+      const uint32_t at = u * kFiltThreads + threadIdx.x;
+      uint32_t line = static_cast<uint32_t>((static_cast<uint64_t>(at / 8) * lines + shift) / kLines);
+      if (line >= static_cast<uint32_t>(lines)) line -= lines;
+      first[u] = (line * 8 + at % 8) * kLen;
+      v[u] = *reinterpret_cast<const uint4*>(row.x + first[u]);
+    }
+    uint32_t on = 0;
 #pragma unroll
-    for (int e = 0; e < kLen; ++e) {
-      const float y = x[u * kLen + e];
-      bool mine = !(y < lo_value) && !(y > hi_value);
-      if (mine && (y == lo_value || y == hi_value || y != y)) {
-        const uint64_t c = pack_best(order_key(y), first[u] + e);
-        mine = c >= in.lo && c <= in.hi;
-      }
-      if (mine) {
-        on |= 1u << (u * kLen + e);
-        if (fabsf(y) < kInf) {
-          high = fmaxf(high, y);
-          low = fminf(low, y);
+    for (int u = 0; u < kVecs; ++u) {
+      Vec<T>::unpack(v[u], x + u * kLen);
+#pragma unroll
+      for (int e = 0; e < kLen; ++e) {
+        const float y = x[u * kLen + e];
+        bool mine = !(y < lo_value) && !(y > hi_value);
+        if (mine && (y == lo_value || y == hi_value || y != y)) {
+          const uint64_t c = pack_best(order_key(y), first[u] + e);
+          mine = c >= in.lo && c <= in.hi;
         }
+        if (mine) on |= 1u << (u * kLen + e);
       }
     }
-  }
-  uint64_t r[3] = {static_cast<uint64_t>(__popc(on)), order_key(high), order_key(-low)};
-  __syncthreads();
+    return on;
+  };
+  float x[kSampleEach];
+  uint32_t on = fetch(0, x);
+  float high = -kInf, low = kInf;
 #pragma unroll
-  for (int u = 0; u < (kWeights ? 2 : 1); ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
-  block_reduce<3, 1>(r, s);
-  const int m = static_cast<int>(r[0]);
-  high = key_value(static_cast<uint32_t>(r[1]));
-  low = -key_value(static_cast<uint32_t>(r[2]));
+  for (int e = 0; e < kSampleEach; ++e) {
+    if ((on >> e & 1) && fabsf(x[e]) < kInf) {
+      high = fmaxf(high, x[e]);
+      low = fminf(low, x[e]);
+    }
+  }
+  // (counts in the first piece; the ends of the finite ones, inverted for the lower one)
+  const uint32_t up_key = __reduce_max_sync(0xffffffffu, order_key(high)), low_key = __reduce_max_sync(0xffffffffu, order_key(-low));
+  const uint32_t here = __reduce_add_sync(0xffffffffu, __popc(on));
+  __syncthreads();                         // what was there is read
+  if (lane == 0) {
+    s.red[0][warp] = static_cast<uint64_t>(up_key) << 32 | low_key;
+    s.red[1][warp] = here;
+  }
+  reinterpret_cast<uint4*>(counts)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  if (kWeights) {
+#pragma unroll
+    for (int u = 1; u < 4; ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  if (threadIdx.x == 0) {
+    s.lo_bin = kSorts;
+    s.hi_bin = -1;
+    s.rank = -1;
+  }
+  __syncthreads();
+  uint32_t all_up = 0, all_low = 0;
+  int m = 0;
+#pragma unroll
+  for (int w = 0; w < kFiltWarps; ++w) {
+    const uint64_t v = s.red[0][w];
+    all_up = max(all_up, static_cast<uint32_t>(v >> 32));
+    all_low = max(all_low, static_cast<uint32_t>(v));
+    m += static_cast<int>(s.red[1][w]);
+  }
+  high = key_value(all_up);
+  low = -key_value(all_low);
   if (m == 0 || !(high >= low)) return;
   // one of the sample stands for `each` of the row
-  const float each = static_cast<float>(row.vocab) / kSampleSize;
+  const float each = static_cast<float>(row.vocab) / (kSampleSize * pieces);
   const float width = fminf(high - low, 32.0f / row.inv_t);
-  if (threadIdx.x == 0) {
-    s.rank = m;
-    s.lo_bin = kBins;
-    s.hi_bin = -1;
-  }
+  // (of the weight of the largest sampled token, a power of 2 of the row's scale)
+  const float unit = kWeights ? fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f)) : 1.0f;
   if (!(width > 0.0f)) {                   // equal logits: their indices lie evenly, for all that is known
-    __syncthreads();
-    if (kWeights) missing /= fmaxf(fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f)), 1e-30f);
     const uint32_t key = order_key(high);
     const float i0 = in.hi >> 32 == key ? static_cast<float>(min(~static_cast<uint32_t>(in.hi), static_cast<uint32_t>(row.vocab))) : 0.0f;
     const float i1 = in.lo >> 32 == key ? static_cast<float>(min(~static_cast<uint32_t>(in.lo), static_cast<uint32_t>(row.vocab))) : static_cast<float>(row.vocab);
-    const float part = missing / (static_cast<float>(m) * each), span = most / (static_cast<float>(m) * each);
+    const float ties = static_cast<float>(m) * row.vocab / kSampleSize;
+    const float part = missing / unit / ties, span = most / ties;
     const float end = part + span, start = part - span;
     const uint64_t base = static_cast<uint64_t>(key) << 32;
     if (end < 1.0f) lo = max(lo, base | ~static_cast<uint32_t>(i0 + end * (i1 - i0)));
@@ -652,22 +763,25 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
     }
     return;
   }
-  const float per = kBins / width;
+  const float per = kSorts / width;
   const float to_y = row.inv_t * kLog2e;
+  for (int piece = 0; piece < pieces; ++piece) {
+    if (piece > 0) on = fetch(piece, x);
 #pragma unroll
-  for (int e = 0; e < kSampleEach; ++e) {
-    if (!(on >> e & 1)) continue;
-    const int j = fabsf(x[e]) < kInf ? min(static_cast<int>((high - x[e]) * per), kBins - 1) : 0;
-    atomicAdd(&s.bins[0][j], 1u);
-    // a weight relative to the largest of the sample's, in steps of 2^-18
-    if (kWeights) atomicAdd(&s.bins[1][j], __float2uint_rn(fminf(fast_exp2((x[e] - high) * to_y), 1.0f) * 0x1p18f));
+    for (int e = 0; e < kSampleEach; ++e) {
+      if (!(on >> e & 1)) continue;
+      const int j = fabsf(x[e]) < kInf ? max(0, min(static_cast<int>((high - x[e]) * per), kSorts - 1)) : 0;
+      atomicAdd(&counts[j], 1u);
+      // a weight relative to the largest of the sample's, in steps of 2^-16
+      if (kWeights) atomicAdd(&weights[j], __float2uint_rn(fminf(fast_exp2((x[e] - high) * to_y), 1.0f) * 0x1p16f));
+    }
   }
   __syncthreads();
   uint32_t n[kEach], w[kEach], up_n = 0, up_w = 0;
 #pragma unroll
   for (int u = 0; u < kEach; ++u) {
-    n[u] = s.bins[0][threadIdx.x * kEach + u];
-    w[u] = kWeights ? s.bins[1][threadIdx.x * kEach + u] : 0u;
+    n[u] = counts[threadIdx.x * kEach + u];
+    w[u] = kWeights ? weights[threadIdx.x * kEach + u] : 0u;
     up_n += n[u];
     up_w += w[u];
   }
@@ -682,20 +796,19 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
   }
   if (lane == 31) s.red[0][warp] = static_cast<uint64_t>(up_w) << 32 | up_n;
   __syncthreads();
-  uint32_t at_n = up_n - own_n, at_w = up_w - own_w;
+  uint32_t at_n = up_n - own_n, at_w = up_w - own_w, all_n = 0;
 #pragma unroll
   for (int q = 0; q < kFiltWarps; ++q) {
+    const uint64_t v = s.red[0][q];
     if (q < warp) {
-      at_n += static_cast<uint32_t>(s.red[0][q]);
-      at_w += static_cast<uint32_t>(s.red[0][q] >> 32);
+      at_n += static_cast<uint32_t>(v);
+      at_w += static_cast<uint32_t>(v >> 32);
     }
+    all_n += static_cast<uint32_t>(v);
   }
   float rank;
   if (kWeights) {
-    // missing is in units of 2^k: to steps of the largest sampled weight
-    const float unit = fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f));
-    const float want = fminf(missing / (each * unit) * 0x1p18f, 4e9f);
-    const uint32_t target = max(1u, __float2uint_rn(want));
+    const uint32_t target = max(1u, __float2uint_rn(fminf(missing / (each * unit) * 0x1p16f, 4e9f)));
     uint32_t a_n = at_n, a_w = at_w;
 #pragma unroll
     for (int u = 0; u < kEach; ++u) {
@@ -704,7 +817,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
       a_w += w[u];
     }
     __syncthreads();
-    rank = static_cast<float>(s.rank);
+    rank = static_cast<float>(s.rank >= 0 ? s.rank : static_cast<int>(all_n));
   } else {
     rank = missing / each;
   }
@@ -720,7 +833,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
   }
   __syncthreads();
   const int lo_bin = s.lo_bin, hi_bin = s.hi_bin;
-  if (lo_bin < kBins - 1) lo = max(lo, static_cast<uint64_t>(order_key(high - static_cast<float>(lo_bin + 1) / per)) << 32);
+  if (lo_bin < kSorts - 1) lo = max(lo, static_cast<uint64_t>(order_key(high - static_cast<float>(lo_bin + 1) / per)) << 32);
   if (hi_bin > 0) hi = min(hi, static_cast<uint64_t>(order_key(high - static_cast<float>(hi_bin) / per)) << 32 | 0xffffffffu);
   if (lo < kLowest) lo = kLowest;
   if (lo > hi) {                           // (roundings of a narrow range)
@@ -738,7 +851,8 @@ __device__ __forceinline__ void next_bracket(const Row<T>& row, const Bounds& in
   hi = in.hi;
   if (row.vocab <= kListCap) return;       // (one CTA, and all of the row on the list)
   if (turn <= kSampledTurns) {
-    sample_bracket<kWeights>(row, in, missing, turn, 2.5f, 6.0f, 0.4f * kListCap, scale, s, lo, hi);
+    // 2.5 deviations of a rank; a sum's error is that of fewer, heavier tokens
+    sample_bracket<kWeights>(row, in, missing, turn, kWeights ? 6.0f : 2.5f, 6.0f, 0.4f * kListCap, scale, s, lo, hi);
   } else {
     lo = in.lo + (in.hi - in.lo) / 2 + 1;
     if (lo > in.hi) lo = in.hi;
@@ -778,6 +892,7 @@ __device__ __noinline__ uint64_t locate_rank(const Row<T>& row, Bounds in, int k
 template <typename T>
 __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Target target, uint64_t from,
                                                const WeightScale& scale, FiltSmem& s, Bracket& view, uint64_t& mass) {
+  const uint64_t vocab_steps = static_cast<uint64_t>(row.vocab);       // exact weights are rounded to a step each
   bool exact = scale.tie, again = from != 0;
   uint64_t lo = from, hi = in.hi;
   for (int turn = 1; turn <= kTurns; ++turn) {
@@ -787,15 +902,15 @@ __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Tar
     }
     again = false;
     view = exact ? pass<Weigh::kExact>(row, lo, hi, scale, s) : pass<Weigh::kClose>(row, lo, hi, scale, s);
-    uint64_t sum = view.m_in;
+    uint64_t sum = static_cast<int64_t>(view.m_in) < 0 ? 0 : view.m_in;
     if (!exact && view.whole) {            // listed weights are exact
       uint64_t own = 0;
       for (int i = threadIdx.x; i < view.n_in; i += kFiltThreads) own += weight_of(__fmul_rn(place_value(s.list[i]), row.inv_t), scale, s.table);
       sum = block_sum(own, s);
     }
-    // the others' sums are within `off` of what the pass gave: 2^-21.9 a weight, a vector's sum 2^-21
+    // the others' sums are within `off` of what the pass gave: 2^-29.5 of a weight, 2^-28.5 of a vector's sum
     const uint64_t others = view.below + view.m_above + (view.whole ? 0 : sum);
-    const uint64_t off = exact ? 0 : static_cast<uint64_t>(static_cast<float>(others) * 0x1.8p-20f) + 2;
+    const uint64_t off = exact ? 0 : static_cast<uint64_t>(static_cast<float>(others) * 0x1p-27f) + vocab_steps;
     uint64_t least = target.most, most = target.most;
     if (target.share > 0.0f) {
       const uint64_t z = view.below + view.m_above + sum;
@@ -849,7 +964,7 @@ struct RowResult {
   uint64_t mass;           // the weight of all that is kept, 0: not known
   bool empty;              // nothing above -inf
   bool listed;             // all that is kept is on the list
-  int n_list;
+  int n_list, n_above;     // on the list, and above it
   WeightScale scale;
 };
 
@@ -875,7 +990,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
                                    : pass<Weigh::kNone>(row, lo, hi, none, s);
   if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)
     view = pass<Weigh::kNone>(row, kLowest, kHighest, none, s);
-  if (!view.any) return RowResult{kHighest, 0, true, true, 0, none};
+  if (!view.any) return RowResult{kHighest, 0, true, true, 0, 0, none};
   const WeightScale scale = weight_scale(__fmul_rn(view.top, row.inv_t), row.bits);
   uint64_t cut = kLowest, mass = 0;
   // 3. top-k
@@ -945,7 +1060,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
       mass = 0;
     }
   }
-  return RowResult{cut, mass, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, scale};
+  return RowResult{cut, mass, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, view.n_above, scale};
 }
 
 // ------------------------------------------------------------------- endings
@@ -962,6 +1077,62 @@ __device__ __forceinline__ float log_share(float s_tok, uint64_t sum, const Weig
   return kLn2 * ((yh - static_cast<float>(w.k)) + yl) - logf(total);
 }
 
+// f.many<n>(x, noise, first index) for all entries of the slice, the noise fetched
+// beside the logits.
+template <typename T, typename F>
+__device__ __forceinline__ void for_slice_noise(const Row<T>& row, const float* noise, F& f) {
+  constexpr int kLen = Vec<T>::kLen, kUnroll = 2;
+  const uint4* vecs = reinterpret_cast<const uint4*>(row.x + row.v0);
+  const float4* more = reinterpret_cast<const float4*>(noise + row.v0);
+  const int n = (row.v1 - row.v0) / kLen;
+  for (int j0 = threadIdx.x; j0 < n; j0 += kUnroll * kFiltThreads) {
+    uint4 v[kUnroll];
+    float4 w[kUnroll][kLen / 4];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kFiltThreads;
+      if (j >= n) continue;
+      v[u] = vecs[j];
+#pragma unroll
+      for (int q = 0; q < kLen / 4; ++q) w[u][q] = __ldcs(more + j * (kLen / 4) + q);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int j = j0 + u * kFiltThreads;
+      if (j >= n) break;
+      float x[kLen], g[kLen];
+      Vec<T>::unpack(v[u], x);
+#pragma unroll
+      for (int q = 0; q < kLen / 4; ++q) {
+        g[4 * q] = w[u][q].x; g[4 * q + 1] = w[u][q].y; g[4 * q + 2] = w[u][q].z; g[4 * q + 3] = w[u][q].w;
+      }
+      f.template many<kLen>(x, g, row.v0 + j * kLen);
+    }
+  }
+  const int i = row.v0 + n * kLen + threadIdx.x;
+  if (i < row.v1) {
+    float x[1] = {load_one(row.x + i)}, g[1] = {noise[i]};
+    f.template many<1>(x, g, i);
+  }
+}
+
+// The largest of fl(s + noise), the first one of equal ones: a thread meets
+// indices in increasing order, and few values pass the ones before them.
+struct Draw {
+  float value;             // of `best`, for a first look (a NaN at first, which all pass)
+  uint64_t best;
+  __device__ __forceinline__ bool passes(float v) const { return !(v <= value); }       // (a NaN does)
+  __device__ __forceinline__ void offer(float v, int i) {
+    const uint64_t c = pack_best(order_key(v), i);
+    if (c > best) {
+      best = c;
+      value = v;
+    }
+  }
+};
+
+__device__ __forceinline__ Draw no_draw() { return {__int_as_float(0x7fffffff), 0}; }
+
 template <typename T>
 struct DrawBody {
   const Row<T>& row;
@@ -971,66 +1142,54 @@ struct DrawBody {
   bool weigh;
   WeightScale scale;
   const unsigned long long* table;
-  uint64_t best, sum;
+  Draw draw;
+  uint64_t sum;
 
+  __device__ __forceinline__ bool keeps(float x, int i) const {
+    return !(x < cut_value) && (x > cut_value || pack_best(order_key(x), i) >= cut);
+  }
   __device__ __forceinline__ void take(float x, float g, int i) {
     const float sx = __fmul_rn(x, row.inv_t);
-    const uint64_t c = pack_best(order_key(__fadd_rn(sx, g)), i);
-    if (c > best) best = c;
+    draw.offer(__fadd_rn(sx, g), i);
     if (weigh) sum += weight_of(sx, scale, table);
   }
+  // few are kept: their noise alone is read
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
-    uint32_t in = 0;
-#pragma unroll
-    for (int e = 0; e < kLen; ++e) {
-      bool keep = !(x[e] < cut_value);
-      if (keep && !(x[e] > cut_value)) keep = pack_best(order_key(x[e]), i0 + e) >= cut;
-      in |= keep ? 1u << e : 0u;
-    }
-    if (!in) return;
-    float g[kLen];
-    if constexpr (kLen % 4 == 0) {
-#pragma unroll
-      for (int e = 0; e < kLen; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(noise + i0 + e);
-        g[e] = v.x; g[e + 1] = v.y; g[e + 2] = v.z; g[e + 3] = v.w;
-      }
-    } else {
-      g[0] = noise[i0];
-    }
 #pragma unroll
     for (int e = 0; e < kLen; ++e)
-      if (in >> e & 1) take(x[e], g[e], i0 + e);
+      if (keeps(x[e], i0 + e)) take(x[e], noise[i0 + e], i0 + e);
+  }
+  template <int kLen>
+  __device__ __forceinline__ void many(const float* x, const float* g, int i0) {
+#pragma unroll
+    for (int e = 0; e < kLen; ++e) {
+      const float sx = __fmul_rn(x[e], row.inv_t), v = __fadd_rn(sx, g[e]);
+      if (weigh) {
+        if (keeps(x[e], i0 + e)) take(x[e], g[e], i0 + e);
+      } else if (draw.passes(v) && keeps(x[e], i0 + e)) {
+        draw.offer(v, i0 + e);
+      }
+    }
   }
 };
 
 // No filter: all of the noise is read beside the logits, the sum of weights is
 // float32 relative to a running maximum (nothing is decided by it).
 struct FreeBody {
-  const float* noise;
   float inv_t;
-  uint64_t best;
+  Draw draw;
   float top, sum, nans;
 
   template <int kLen>
-  __device__ __forceinline__ void many(const float* x, int i0) {
-    float s[kLen], g[kLen], high = top;
-    if constexpr (kLen % 4 == 0) {
-#pragma unroll
-      for (int e = 0; e < kLen; e += 4) {
-        const float4 v = *reinterpret_cast<const float4*>(noise + i0 + e);
-        g[e] = v.x; g[e + 1] = v.y; g[e + 2] = v.z; g[e + 3] = v.w;
-      }
-    } else {
-      g[0] = noise[i0];
-    }
+  __device__ __forceinline__ void many(const float* x, const float* g, int i0) {
+    float s[kLen], high = top;
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
       s[e] = __fmul_rn(x[e], inv_t);
       high = fmaxf(high, s[e]);
-      const uint64_t c = pack_best(order_key(__fadd_rn(s[e], g[e])), i0 + e);
-      if (x[e] != -kInf && c > best) best = c;
+      const float v = __fadd_rn(s[e], g[e]);
+      if (draw.passes(v) && x[e] != -kInf) draw.offer(v, i0 + e);
     }
     if (high > top) {
       sum *= fast_exp2((top - high) * kLog2e);
@@ -1045,14 +1204,12 @@ struct FreeBody {
 };
 
 struct TopBody {
-  uint64_t best;
+  Draw draw;
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
 #pragma unroll
-    for (int e = 0; e < kLen; ++e) {
-      const uint64_t c = pack_best(order_key(x[e]), i0 + e);
-      if (c > best) best = c;
-    }
+    for (int e = 0; e < kLen; ++e)
+      if (draw.passes(x[e])) draw.offer(x[e], i0 + e);
   }
 };
 
@@ -1082,7 +1239,12 @@ template <typename T, bool kSampling>
 __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
-  if (threadIdx.x < kWeightTable) s.table[threadIdx.x] = c_weight_table[threadIdx.x];
+  if (threadIdx.x < kWeightTable) {
+    const unsigned long long t = c_weight_table[threadIdx.x];
+    const float f = __ull2float_rn(t);
+    s.table[threadIdx.x] = t;
+    s.close[threadIdx.x] = make_float2(f * 0x1p-44f, static_cast<float>(static_cast<long long>(t) - static_cast<long long>(f)) / f);
+  }
   grid_dependency_wait();
   grid_launch_dependents();
   const int csize = p.csize, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -1131,11 +1293,11 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
     if (csize > 1) cluster_sync_all();
   };
 
-  RowResult res = {kLowest, 0, false, false, 0, weight_scale(0.0f, p.bits)};
+  RowResult res = {kLowest, 0, false, false, 0, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
-    TopBody body = {0};
+    TopBody body = {no_draw()};
     for_slice(row, body);
-    publish(block_max(body.best, s), 0, 0);
+    publish(block_max(body.draw.best, s), 0, 0);
     const uint64_t best = cluster_stat<true>(s, 0, csize);
     res.empty = best < kLowest;
     res.cut = res.empty ? kHighest : best;
@@ -1154,9 +1316,9 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
   if constexpr (kSampling) {
     const float* noise = p.gumbel + t * p.gumbel_ld;
     if (!filtered) {
-      FreeBody body = {noise, inv_t, 0, -kInf, 0.0f, 0.0f};
-      for_slice(row, body);
-      const uint64_t own = block_max(body.best, s);
+      FreeBody body = {inv_t, no_draw(), -kInf, 0.0f, 0.0f};
+      for_slice_noise(row, noise, body);
+      const uint64_t own = block_max(body.draw.best, s);
       const float own_top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
       const float own_sum = block_sum(body.top == own_top ? body.sum : body.sum * fast_exp2((body.top - own_top) * kLog2e), s);
       const float own_nans = block_sum(body.nans, s);
@@ -1194,16 +1356,18 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
       finish();
       return;
     }
-    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table, 0, 0};
+    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table, no_draw(), 0};
     if (res.listed) {
       for (int i = rank * kFiltThreads + threadIdx.x; i < res.n_list; i += csize * kFiltThreads) {
         const uint64_t c = s.list[i];
         if (c >= res.cut) body.take(place_value(c), noise[best_index(c)], best_index(c));
       }
+    } else if (res.n_list + res.n_above > p.vocab / 32) {
+      for_slice_noise(row, noise, body);
     } else {
       for_slice(row, body);
     }
-    const uint64_t own = block_max(body.best, s);
+    const uint64_t own = block_max(body.draw.best, s);
     publish(own, body.weigh ? block_sum(body.sum, s) : 0, 0);
     const int token = best_index(cluster_stat<true>(s, 0, csize));
     const uint64_t sum = body.weigh ? cluster_stat<false>(s, 1, csize) : res.mass;
