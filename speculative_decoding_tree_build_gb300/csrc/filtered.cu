@@ -41,8 +41,9 @@ constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
 constexpr int kListCap = 5120;
 constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
-constexpr int kSampleEach = 16;            // sampled tokens a thread
+constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
+constexpr int kSamplePieces = 4;           // samples that a second look takes
 constexpr int kFirstList = 384;            // tokens that the first list is made for without top-k
 constexpr int kBins = 1024;
 constexpr int kSmall = 32;                 // tokens that a warp ranks
@@ -80,8 +81,7 @@ struct FiltParams {
 
 struct FiltSmem {
   uint32_t bins[4][kBins];                 // counts; weights in three parts
-  unsigned long long table[kWeightTable];
-  float2 close[kWeightTable];              // the same in float32, the rounding's share beside it
+  WeightTable table;
   uint64_t red[6][kFiltWarps];
   uint64_t small[kSmall];
   uint64_t found, before, weight;          // of select
@@ -267,14 +267,11 @@ struct FloatSum {
   }
 };
 
-// A weight w (1 + q) of at most 2, and a sum of such: the multiples of 2^-12 in w
-// add up without rounding below 2^12; what is left of w, and w q, is small.
-struct Close {
-  float w, q;
-};
+// A sum of close weights of at most 2: the multiples of 2^-12 in w add up without
+// rounding below 2^12; what is left of w, and w q, is small.
 struct ClosePart {                   // of one vector
   float high, low;
-  __device__ __forceinline__ void add(const Close& c) {
+  __device__ __forceinline__ void add(const CloseWeight& c) {
     constexpr float kGrid = 0x1.8p11f;                                   // last bit 2^-12
     const float grid = (c.w + kGrid) - kGrid;
     high += grid;
@@ -305,7 +302,7 @@ struct PassBody {
   uint64_t* list;                    // the CTA's own
   int cap;
   uint64_t lo, hi;
-  float lo_value, hi_value, to_y, y_off, floor, unit;
+  float lo_value, hi_value, to_y, y_off, unit;
   WeightScale scale;
   uint32_t best;                     // the largest order key from lo on
   int n_above;
@@ -316,19 +313,7 @@ struct PassBody {
   // 2^(y - k), y = x to_y: the factor's rounding makes the exponent good to |y| 2^-22.8.
   __device__ __forceinline__ float cheap(float x) const { return fast_exp2(__fmaf_rn(x, to_y, y_off)); }
 
-  // The exact weights' reduction in float32: a weight is w (1 + q), w = 2^(k + j / 32) to its rounding, whose
-  // share is in q. Off by 2^-30 of it (z's and q's roundings, 2^-24 of |z| < 2^-6.5; z^5 / 120 left out).
-  __device__ __forceinline__ Close close(float x) const {
-    const float sx = fmaxf(__fmul_rn(x, row.inv_t) - scale.ref, floor);
-    const float yh = __fmul_rn(sx, kLog2e);
-    const float steps = yh + y_off;                                     // 1.5 * 2^18 - k, last bit 2^-5
-    const float yl = __fmaf_rn(sx, kLog2eLow, __fmaf_rn(sx, kLog2e, -yh));
-    const float z = __fmaf_rn(yh - (steps - y_off), kLn2, yl * kLn2);
-    const int n = __float_as_int(steps);
-    const float2 t = s.close[n & 31];                                   // 2^(j / 32), its rounding's share
-    const float q = __fmaf_rn(z * z, __fmaf_rn(z, __fmaf_rn(z, 1.0f / 24, 1.0f / 6), 0.5f), z) + t.y;
-    return {__int_as_float(__float_as_int(t.x) + ((n & ~31) << 18)), q};
-  }
+  __device__ __forceinline__ CloseWeight close(float x) const { return close_weight(__fmul_rn(x, row.inv_t), scale, s.table); }
   __device__ __forceinline__ uint64_t exact(float x) const { return weight_of(__fmul_rn(x, row.inv_t), scale, s.table); }
 
   // a token that may lie in the bracket
@@ -369,7 +354,7 @@ struct PassBody {
       if (!under && !over) in |= 1u << e;
       if (kWeigh == Weigh::kBelow) low += under ? cheap(x[e]) : 0.0f;
       if (kWeigh == Weigh::kClose) {
-        const Close c = close(x[e]);
+        const CloseWeight c = close(x[e]);
         all.add(c);
         if (under) under_part.add(c);
         if (over) over_part.add(c);
@@ -408,9 +393,9 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
   if (threadIdx.x == 0) s.n_list = 0;
   __syncthreads();
   // a weight is at most 2: sums stay below 2^31, in steps of 2^-F below 2^63
-  const float k = static_cast<float>(scale.k), unit = exp2f(static_cast<float>(row.bits));
+  const float unit = exp2f(static_cast<float>(row.bits));
   PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
-                              row.inv_t * kLog2e, kWeigh == Weigh::kClose ? kSteps - k : -k, (k - 100.0f) * kLn2, unit, scale,
+                              row.inv_t * kLog2e, -static_cast<float>(scale.k), unit, scale,
                               0u, 0, 0, 0, 0, {}, {}, {}, {}};
   for_slice(row, body);
   Bracket out;
@@ -643,33 +628,34 @@ __device__ __forceinline__ uint64_t select_weight(const Bracket& view, uint64_t 
 
 // ------------------------------------------------------------------ the place
 
-// Bounds of the place that is looked for: it lies in [lo, hi], and n places
-// with weight m (about) lie above hi.
+// Bounds of the place that is looked for: it lies in [lo, hi], n places with weight
+// m (about) lie above hi, and w (about, 0: not known) is the weight within.
 struct Bounds {
   uint64_t lo, hi;
   int n;
-  uint64_t m;
+  uint64_t m, w;
 };
 
-// The part of the bounds that a sample of the row says to look at. 4096 tokens
-// (16384 with kWeights), 128 bytes at a time evenly over the row (`turn` moves
-// them), are sorted into bins of equal width below the largest one; in them the rank at
-// which the count (or, with kWeights, the weight) `missing` is reached is found, and
-// the bins `margin` ranks above and below it are the bracket's ends. The bins go down
-// to 32 below the largest scaled logit; what lies further below shares the last one.
+// The part of the bounds that a sample of the row says to look at. `pieces` times
+// 2048 tokens, 128 bytes at a time evenly over the row (`turn` moves them), are
+// sorted into bins of equal width below the largest one. In them the rank is found
+// at which `missing` tokens are counted or, with kWeights, at which the weights from
+// the lowest bin up reach `beneath` (-p: all but a share p of them; the light tokens below a place are many and
+// tell its rank far better than the few heavy ones above it). Bins a margin of ranks
+// above and below it are the bracket's ends. They go down to 32 below the largest
+// scaled logit; what lies further below shares the last one.
 template <bool kWeights, typename T>
-__device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in, float missing, int turn, float sigmas,
-                                            float slack, float most, const WeightScale& scale, FiltSmem& s, uint64_t& lo,
-                                            uint64_t& hi) {
+__device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in, float missing, float beneath, int turn,
+                                            int pieces, float sigmas, float most, const WeightScale& scale, FiltSmem& s,
+                                            uint64_t& lo, uint64_t& hi) {
   constexpr int kLen = Vec<T>::kLen, kVecs = kSampleEach / kLen, kLines = kSampleSize / kLen / 8;
-  constexpr int kSorts = kWeights ? 2 * kBins : kBins, kEach = kSorts / kFiltThreads;
+  constexpr int kSorts = 2 * kBins, kEach = kSorts / kFiltThreads;
   uint32_t* counts = s.bins[0];
-  uint32_t* weights = s.bins[2];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = in.lo;
   hi = in.hi;
   const int lines = row.vocab / (8 * kLen);        // >= kLines: the row does not fit the list
-  const int pieces = kWeights && row.vocab >= 4 * kSampleSize ? 4 : 1;
+  if (row.vocab < pieces * kSampleSize) pieces = 1;
   const float lo_value = place_value(in.lo), hi_value = place_value(in.hi);
   // a piece's vectors; bit e of the answer: x[e] lies within the bounds
   auto fetch = [&](int piece, float* x) -> uint32_t {
@@ -679,8 +665,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const uint32_t at = u * kFiltThreads + threadIdx.x;
-      uint32_t line = static_cast<uint32_t>((static_cast<uint64_t>(at / 8) * lines + shift) / kLines);
-      if (line >= static_cast<uint32_t>(lines)) line -= lines;
+      const uint32_t line = static_cast<uint32_t>((static_cast<uint64_t>(at / 8) * lines + shift) / kLines);   // shift < lines
       first[u] = (line * 8 + at % 8) * kLen;
       v[u] = *reinterpret_cast<const uint4*>(row.x + first[u]);
     }
@@ -711,7 +696,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
       low = fminf(low, x[e]);
     }
   }
-  // (counts in the first piece; the ends of the finite ones, inverted for the lower one)
+  // (of the first piece: how many, and the ends of the finite ones, the lower one inverted)
   const uint32_t up_key = __reduce_max_sync(0xffffffffu, order_key(high)), low_key = __reduce_max_sync(0xffffffffu, order_key(-low));
   const uint32_t here = __reduce_add_sync(0xffffffffu, __popc(on));
   __syncthreads();                         // what was there is read
@@ -719,11 +704,8 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
     s.red[0][warp] = static_cast<uint64_t>(up_key) << 32 | low_key;
     s.red[1][warp] = here;
   }
-  reinterpret_cast<uint4*>(counts)[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
-  if (kWeights) {
 #pragma unroll
-    for (int u = 1; u < 4; ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
-  }
+  for (int u = 0; u < kSorts / 4 / kFiltThreads; ++u) reinterpret_cast<uint4*>(counts)[threadIdx.x + u * kFiltThreads] = make_uint4(0u, 0u, 0u, 0u);
   if (threadIdx.x == 0) {
     s.lo_bin = kSorts;
     s.hi_bin = -1;
@@ -745,8 +727,8 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
   // one of the sample stands for `each` of the row
   const float each = static_cast<float>(row.vocab) / (kSampleSize * pieces);
   const float width = fminf(high - low, 32.0f / row.inv_t);
-  // (of the weight of the largest sampled token, a power of 2 of the row's scale)
-  const float unit = kWeights ? fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -60.0f)) : 1.0f;
+  // the weight of the largest sampled token
+  const float unit = kWeights ? fast_exp2(fmaxf(fminf((__fmul_rn(high, row.inv_t) - scale.ref) * kLog2e - static_cast<float>(scale.k), 2.0f), -100.0f)) : 1.0f;
   if (!(width > 0.0f)) {                   // equal logits: their indices lie evenly, for all that is known
     const uint32_t key = order_key(high);
     const float i0 = in.hi >> 32 == key ? static_cast<float>(min(~static_cast<uint32_t>(in.hi), static_cast<uint32_t>(row.vocab))) : 0.0f;
@@ -764,7 +746,6 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
     return;
   }
   const float per = kSorts / width;
-  const float to_y = row.inv_t * kLog2e;
   for (int piece = 0; piece < pieces; ++piece) {
     if (piece > 0) on = fetch(piece, x);
 #pragma unroll
@@ -772,56 +753,70 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
       if (!(on >> e & 1)) continue;
       const int j = fabsf(x[e]) < kInf ? max(0, min(static_cast<int>((high - x[e]) * per), kSorts - 1)) : 0;
       atomicAdd(&counts[j], 1u);
-      // a weight relative to the largest of the sample's, in steps of 2^-16
-      if (kWeights) atomicAdd(&weights[j], __float2uint_rn(fminf(fast_exp2((x[e] - high) * to_y), 1.0f) * 0x1p16f));
     }
   }
   __syncthreads();
-  uint32_t n[kEach], w[kEach], up_n = 0, up_w = 0;
+  uint32_t n[kEach], up_n = 0;
 #pragma unroll
-  for (int u = 0; u < kEach; ++u) {
-    n[u] = counts[threadIdx.x * kEach + u];
-    w[u] = kWeights ? weights[threadIdx.x * kEach + u] : 0u;
-    up_n += n[u];
-    up_w += w[u];
+  for (int u = 0; u < kEach; ++u) up_n += n[u] = counts[threadIdx.x * kEach + u];
+  const uint32_t own_n = up_n;
+  // weights in the middle of their bins, relative to the largest sampled one; sums from
+  // the lowest bin up, added in an order of their own
+  const float step = row.inv_t * kLog2e / per;
+  float own_w = 0.0f, up_w;
+  if (kWeights) {
+#pragma unroll
+    for (int u = kEach - 1; u >= 0; --u)
+      own_w += n[u] * fast_exp2(-step * (static_cast<float>(threadIdx.x * kEach + u) + 0.5f));
   }
-  const uint32_t own_n = up_n, own_w = up_w;
+  up_w = own_w;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t a = __shfl_up_sync(0xffffffffu, up_n, o), b = kWeights ? __shfl_up_sync(0xffffffffu, up_w, o) : 0u;
-    if (lane >= o) {
-      up_n += a;
-      up_w += b;
-    }
+    const uint32_t a = __shfl_up_sync(0xffffffffu, up_n, o);
+    const float b = kWeights ? __shfl_down_sync(0xffffffffu, up_w, o) : 0.0f;
+    if (lane >= o) up_n += a;
+    if (lane < 32 - o) up_w += b;
   }
-  if (lane == 31) s.red[0][warp] = static_cast<uint64_t>(up_w) << 32 | up_n;
+  if (lane == 31) s.red[0][warp] = up_n;
+  if (lane == 0) s.red[1][warp] = __float_as_uint(up_w);
   __syncthreads();
-  uint32_t at_n = up_n - own_n, at_w = up_w - own_w, all_n = 0;
+  uint32_t at_n = up_n - own_n, all_n = 0;
+  float after_w = 0.0f;                    // of the warps behind
 #pragma unroll
   for (int q = 0; q < kFiltWarps; ++q) {
-    const uint64_t v = s.red[0][q];
-    if (q < warp) {
-      at_n += static_cast<uint32_t>(v);
-      at_w += static_cast<uint32_t>(v >> 32);
-    }
-    all_n += static_cast<uint32_t>(v);
+    if (q < warp) at_n += static_cast<uint32_t>(s.red[0][q]);
+    all_n += static_cast<uint32_t>(s.red[0][q]);
   }
-  float rank;
+  float rank, margin;
   if (kWeights) {
-    const uint32_t target = max(1u, __float2uint_rn(fminf(missing / (each * unit) * 0x1p16f, 4e9f)));
-    uint32_t a_n = at_n, a_w = at_w;
 #pragma unroll
-    for (int u = 0; u < kEach; ++u) {
-      if (a_w < target && target <= a_w + w[u]) s.rank = static_cast<int>(a_n + n[u] / 2);
-      a_n += n[u];
-      a_w += w[u];
+    for (int q = kFiltWarps - 1; q >= 0; --q)
+      if (q > warp) after_w += __uint_as_float(static_cast<uint32_t>(s.red[1][q]));
+    float all_w = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFiltWarps; ++q) all_w += __uint_as_float(static_cast<uint32_t>(s.red[1][q]));
+    const float want = beneath < 0.0f ? (1.0f + beneath) * all_w : beneath / (each * unit);
+    float a_w = after_w + (up_w - own_w);
+    uint32_t a_n = at_n + own_n;
+#pragma unroll
+    for (int u = kEach - 1; u >= 0; --u) {
+      const int j = threadIdx.x * kEach + u;
+      const float next = a_w + n[u] * fast_exp2(-step * (static_cast<float>(j) + 0.5f));
+      a_n -= n[u];
+      // (roundings may let two threads say so)
+      if (a_w <= want && want < next) atomicMax(&s.rank, j << 16 | static_cast<int>(a_n + n[u] / 2));
+      a_w = next;
     }
     __syncthreads();
-    rank = static_cast<float>(s.rank >= 0 ? s.rank : static_cast<int>(all_n));
+    const int found = max(s.rank, 0);      // nothing: all lies beneath
+    rank = static_cast<float>(found & 0xffff);
+    // the deviation of the weight beneath, in tokens of the place's own weight: none beneath is heavier
+    margin = sigmas * sqrtf(want / fast_exp2(fmaxf(-step * (static_cast<float>(found >> 16) + 0.5f), -100.0f))) + 6.0f;
   } else {
     rank = missing / each;
+    margin = sigmas * sqrtf(rank) + 8.0f;
   }
-  const float margin = fminf(sigmas * sqrtf(rank) + slack, most / each);
+  margin = fminf(margin, most / each);
   const int down = static_cast<int>(fminf(rank + margin, 1e9f)) + 1, up = static_cast<int>(rank - margin);
   uint32_t a_n = at_n;
 #pragma unroll
@@ -845,14 +840,13 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
 // The next bracket within the bounds: four times around what a sample says, then
 // half of the bounds.
 template <bool kWeights, typename T>
-__device__ __forceinline__ void next_bracket(const Row<T>& row, const Bounds& in, float missing, int turn,
+__device__ __forceinline__ void next_bracket(const Row<T>& row, const Bounds& in, float missing, float beneath, int turn,
                                              const WeightScale& scale, FiltSmem& s, uint64_t& lo, uint64_t& hi) {
   lo = in.lo;
   hi = in.hi;
   if (row.vocab <= kListCap) return;       // (one CTA, and all of the row on the list)
   if (turn <= kSampledTurns) {
-    // 2.5 deviations of a rank; a sum's error is that of fewer, heavier tokens
-    sample_bracket<kWeights>(row, in, missing, turn, kWeights ? 6.0f : 2.5f, 6.0f, 0.4f * kListCap, scale, s, lo, hi);
+    sample_bracket<kWeights>(row, in, missing, beneath, turn, kSamplePieces, 3.0f, 0.4f * kListCap, scale, s, lo, hi);
   } else {
     lo = in.lo + (in.hi - in.lo) / 2 + 1;
     if (lo > in.hi) lo = in.hi;
@@ -866,7 +860,7 @@ __device__ __noinline__ uint64_t locate_rank(const Row<T>& row, Bounds in, int k
   const WeightScale none = weight_scale(0.0f, row.bits);
   for (int turn = 1; turn <= kTurns; ++turn) {
     uint64_t lo, hi;
-    next_bracket<false>(row, in, static_cast<float>(k - in.n), turn, none, s, lo, hi);
+    next_bracket<false>(row, in, static_cast<float>(k - in.n), 0.0f, turn, none, s, lo, hi);
     view = pass<Weigh::kNone>(row, lo, hi, none, s);
     const int with = view.n_above + view.n_in;
     if (view.n_above >= k) {
@@ -878,7 +872,7 @@ __device__ __noinline__ uint64_t locate_rank(const Row<T>& row, Bounds in, int k
     } else if (view.whole) {
       return select_rank(view, k - view.n_above, row, s);
     } else {
-      in = {lo, hi, view.n_above, 0};
+      in = {lo, hi, view.n_above, 0, 0};
     }
   }
   return in.lo;                            // (not reached: 64 halvings leave one place)
@@ -897,8 +891,10 @@ __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Tar
   uint64_t lo = from, hi = in.hi;
   for (int turn = 1; turn <= kTurns; ++turn) {
     if (!again) {
-      const float missing = static_cast<float>(target.most - min(target.most, in.m)) * exp2f(static_cast<float>(-row.bits));
-      next_bracket<true>(row, in, missing, turn, scale, s, lo, hi);
+      const uint64_t missing = target.most > in.m ? target.most - in.m : 0, beneath = in.w > missing ? in.w - missing : 0;
+      const float unit = exp2f(static_cast<float>(-row.bits));
+      next_bracket<true>(row, in, static_cast<float>(missing) * unit, in.w ? static_cast<float>(beneath) * unit : -target.share, turn,
+                         scale, s, lo, hi);
     }
     again = false;
     view = exact ? pass<Weigh::kExact>(row, lo, hi, scale, s) : pass<Weigh::kClose>(row, lo, hi, scale, s);
@@ -921,13 +917,15 @@ __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Tar
     const uint64_t above_least = view.m_above > off ? view.m_above - off : 0, above_most = view.m_above + off;
     if (above_least >= most) {             // above the bracket
       in.lo = hi + 1;
+      in.w = view.m_above > in.m ? view.m_above - in.m : 0;
     } else if (above_most + sum + off < least) {                       // below it
       if (lo == in.lo) return in.lo;       // all that there is
       in.hi = lo - 1;
       in.n = view.n_above + view.n_in;
       in.m = view.m_above + sum;
+      in.w = view.below;
     } else if (exact ? !view.whole : !view.whole && above_most < least && most + off <= above_least + sum) {
-      in = {lo, hi, view.n_above, view.m_above};                       // in it, and more than the list holds
+      in = {lo, hi, view.n_above, view.m_above, sum};                  // in it, and more than the list holds
     } else {
       Target inner = {least > above_most ? least - above_most : 0, most - above_least, 0.0f, 0, 0};
       const uint64_t at = view.whole && inner.least > 0 && inner.most <= sum ? select_weight(view, lo, inner, sum, scale, row, s) : 0;
@@ -977,8 +975,10 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
   // 1. where the list begins (and ends, for a top-k set that no list holds)
   if (vocab > kListCap) {
     const float wanted = static_cast<float>(by_k ? k : kFirstList);
-    sample_bracket<false>(row, Bounds{kLowest, kHighest, 0, 0}, wanted, 0, 3.0f, 8.0f, 0.4f * kListCap, none, s, lo, hi);
-    if (wanted < 0.5f * kListCap) hi = kHighest;
+    const bool large = wanted >= 0.5f * kListCap;
+    sample_bracket<false>(row, Bounds{kLowest, kHighest, 0, 0, 0}, wanted, 0.0f, 0, large ? kSamplePieces : 1, 3.0f,
+                          0.4f * kListCap, none, s, lo, hi);
+    if (!large) hi = kHighest;
   }
   // 2. the list; weights below it relative to its first place, a power of two
   // from the row's (not where the reduction differs)
@@ -997,13 +997,13 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
   if (by_k) {
     const int with = view.n_above + view.n_in;
     if (view.n_above >= k) {
-      cut = locate_rank(row, Bounds{view.hi + 1, kHighest, 0, 0}, k, s, view);
+      cut = locate_rank(row, Bounds{view.hi + 1, kHighest, 0, 0, 0}, k, s, view);
     } else if (with < k) {                 // (from the lowest place on fewer than k: all stay)
-      if (view.lo > kLowest) cut = locate_rank(row, Bounds{kLowest, view.lo - 1, with, 0}, k, s, view);
+      if (view.lo > kLowest) cut = locate_rank(row, Bounds{kLowest, view.lo - 1, with, 0, 0}, k, s, view);
     } else if (view.whole) {
       cut = select_rank(view, k - view.n_above, row, s);
     } else {
-      cut = locate_rank(row, Bounds{view.lo, view.hi, view.n_above, 0}, k, s, view);
+      cut = locate_rank(row, Bounds{view.lo, view.hi, view.n_above, 0, 0}, k, s, view);
     }
   }
   // 4. top-p of what top-k leaves
@@ -1023,11 +1023,11 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
           at = select_weight(view, cut, target, sum, scale, row, s);
           mass = s.before + s.weight;
         } else {
-          at = locate_weight(row, Bounds{cut, kHighest, 0, 0}, target, 0, scale, s, view, mass);
+          at = locate_weight(row, Bounds{cut, kHighest, 0, 0, view.m_in}, target, 0, scale, s, view, mass);
         }
       }
     } else {
-      Bounds in = {kLowest, kHighest, 0, 0};
+      Bounds in = {kLowest, kHighest, 0, 0, 0};
       uint64_t from = 0;
       if (listed && low_fits && scale.ref == 0.0f && !scale.tie) {
         // The total lies within target.off. A weight's exponent y is off by less than |y| 2^-22.8 (the rounded
@@ -1041,7 +1041,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
         at = select_weight(view, view.lo, target, sum, scale, row, s);
         if (at != 0 && s.before < target.least) mass = s.before + s.weight;      // all targets fall on one token
         else if (sum >= target.least) { at = 0; from = view.lo; }                 // on the list, or close to its end
-        else if (view.lo > kLowest) { at = 0; in = {kLowest, view.lo - 1, view.n_in, sum}; }
+        else if (view.lo > kLowest) { at = 0; in = {kLowest, view.lo - 1, view.n_in, sum, target.below}; }
         else at = 0;
         target.below = target.off = 0;
       }
@@ -1066,7 +1066,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
 // ------------------------------------------------------------------- endings
 
 // ln of the kept share of a token: its weight over the sum of all kept ones.
-__device__ __forceinline__ float log_share(float s_tok, uint64_t sum, const WeightScale& w, const unsigned long long* table) {
+__device__ __forceinline__ float log_share(float s_tok, uint64_t sum, const WeightScale& w, const WeightTable& table) {
   const uint64_t mine = weight_of(s_tok, w, table);
   if (mine > sum / 2) return log1pf(-(static_cast<float>(sum - mine) / static_cast<float>(sum)));
   const float total = static_cast<float>(sum) * exp2f(static_cast<float>(-w.bits));
@@ -1141,9 +1141,11 @@ struct DrawBody {
   float cut_value;
   bool weigh;
   WeightScale scale;
-  const unsigned long long* table;
+  const WeightTable& table;
   Draw draw;
-  uint64_t sum;
+  uint64_t sum;            // of weights: exact for few tokens,
+  CloseSum close;          // within 2^-27 for many (no decision hangs on it)
+  float unit;
 
   __device__ __forceinline__ bool keeps(float x, int i) const {
     return !(x < cut_value) && (x > cut_value || pack_best(order_key(x), i) >= cut);
@@ -1164,12 +1166,15 @@ struct DrawBody {
   __device__ __forceinline__ void many(const float* x, const float* g, int i0) {
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
-      const float sx = __fmul_rn(x[e], row.inv_t), v = __fadd_rn(sx, g[e]);
-      if (weigh) {
-        if (keeps(x[e], i0 + e)) take(x[e], g[e], i0 + e);
-      } else if (draw.passes(v) && keeps(x[e], i0 + e)) {
-        draw.offer(v, i0 + e);
-      }
+      const float v = __fadd_rn(__fmul_rn(x[e], row.inv_t), g[e]);
+      if (draw.passes(v) && keeps(x[e], i0 + e)) draw.offer(v, i0 + e);
+    }
+    if (weigh) {
+      ClosePart part = {0.0f, 0.0f};
+#pragma unroll
+      for (int e = 0; e < kLen; ++e)
+        if (keeps(x[e], i0 + e)) part.add(close_weight(__fmul_rn(x[e], row.inv_t), scale, table));
+      close.add(part, unit);
     }
   }
 };
@@ -1239,12 +1244,7 @@ template <typename T, bool kSampling>
 __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
   FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
-  if (threadIdx.x < kWeightTable) {
-    const unsigned long long t = c_weight_table[threadIdx.x];
-    const float f = __ull2float_rn(t);
-    s.table[threadIdx.x] = t;
-    s.close[threadIdx.x] = make_float2(f * 0x1p-44f, static_cast<float>(static_cast<long long>(t) - static_cast<long long>(f)) / f);
-  }
+  if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
   grid_dependency_wait();
   grid_launch_dependents();
   const int csize = p.csize, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
@@ -1356,14 +1356,16 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
       finish();
       return;
     }
-    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table, no_draw(), 0};
+    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table,
+                        no_draw(), 0, {}, exp2f(static_cast<float>(p.bits))};
     if (res.listed) {
       for (int i = rank * kFiltThreads + threadIdx.x; i < res.n_list; i += csize * kFiltThreads) {
         const uint64_t c = s.list[i];
         if (c >= res.cut) body.take(place_value(c), noise[best_index(c)], best_index(c));
       }
-    } else if (res.n_list + res.n_above > p.vocab / 32) {
+    } else if (res.n_list + res.n_above > p.vocab / 32 && !res.scale.tie) {
       for_slice_noise(row, noise, body);
+      body.sum = body.close.steps(body.unit);
     } else {
       for_slice(row, body);
     }

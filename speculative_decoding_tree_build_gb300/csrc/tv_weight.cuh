@@ -70,7 +70,22 @@ inline int weight_bits(int n) {
 
 // Integers come out of floats by adding a number whose last bit stands for the
 // unit wanted: conversion instructions run at a fraction of that rate.
-__device__ __forceinline__ uint64_t weight_of(float s, const WeightScale& w, const unsigned long long* table) {
+// The table in shared memory: 32 entries of 4 bytes lie in 32 banks, so any
+// lookup of a warp is one access (of 8 bytes, three to four).
+struct WeightTable {
+  uint32_t low[kWeightTable], high[kWeightTable];        // of 2^(j / 32) times 2^44
+  float near[kWeightTable], rest[kWeightTable];          // the same in float32, and its rounding's share
+};
+__device__ __forceinline__ void fill_weight_table(WeightTable& table, int j) {
+  const unsigned long long t = c_weight_table[j];
+  const float f = __ull2float_rn(t);
+  table.low[j] = static_cast<uint32_t>(t);
+  table.high[j] = static_cast<uint32_t>(t >> 32);
+  table.near[j] = f * 0x1p-44f;
+  table.rest[j] = static_cast<float>(static_cast<long long>(t) - static_cast<long long>(f)) / f;
+}
+
+__device__ __forceinline__ uint64_t weight_of(float s, const WeightScale& w, const WeightTable& table) {
   if (w.tie) return (s == w.s_max || (s != s && w.s_max != w.s_max)) ? 1ull << w.bits : 0ull;
   s -= w.ref;
   const float yh = __fmul_rn(s, kLog2e);
@@ -87,11 +102,29 @@ __device__ __forceinline__ uint64_t weight_of(float s, const WeightScale& w, con
   const float upper = zh + kUpper;                       // zh in steps of 2^-22, what is left beside q
   const float lower = (q + (zh - (upper - kUpper))) + kLower;
   const int e = ((__float_as_int(upper) - __float_as_int(kUpper)) << 13) + (__float_as_int(lower) - __float_as_int(kLower));
-  const unsigned long long t = table[n & 31];
+  const uint64_t t = static_cast<uint64_t>(table.high[n & 31]) << 32 | table.low[n & 31];
   const int g = static_cast<int>(static_cast<uint32_t>(t >> 12) ^ 0x80000000u);   // T - 3/2 in steps of 2^-32
   const uint64_t m = t + static_cast<uint64_t>(768ll * e + ((static_cast<long long>(g) * e) >> 23));
   const int shift = w.k - (n >> 5) + 44 - w.bits;
   return shift <= 0 ? m : shift > 63 ? 0ull : ((m >> (shift - 1)) + 1) >> 1;
+}
+
+// The same in float32, for a scale without tie: w (1 + q), w = 2^(y - k) to a
+// multiple of 1 / 32 in y and to its rounding, whose share is in q. Off by 2^-30 of
+// it (z's and q's roundings, 2^-24 of |z| < 2^-6.5; z^5 / 120 left out).
+struct CloseWeight {
+  float w, q;
+};
+__device__ __forceinline__ CloseWeight close_weight(float s, const WeightScale& w, const WeightTable& table) {
+  const float k = static_cast<float>(w.k);
+  const float sx = fmaxf(s - w.ref, (k - 100.0f) * kLn2);                // (-inf: 2^-100)
+  const float yh = __fmul_rn(sx, kLog2e);
+  const float steps = yh + (kSteps - k);                 // 32 (y - k) in the last bits
+  const float yl = __fmaf_rn(sx, kLog2eLow, __fmaf_rn(sx, kLog2e, -yh));
+  const float z = __fmaf_rn(yh - (steps - (kSteps - k)), kLn2, yl * kLn2);
+  const int n = __float_as_int(steps);
+  const float q = __fmaf_rn(z * z, __fmaf_rn(z, __fmaf_rn(z, 1.0f / 24, 1.0f / 6), 0.5f), z) + table.rest[n & 31];
+  return {__int_as_float(__float_as_int(table.near[n & 31]) + ((n & ~31) << 18)), q};
 }
 
 // The smallest integer >= p * z for 0 <= p < 1, and 1 at least: a prefix whose
