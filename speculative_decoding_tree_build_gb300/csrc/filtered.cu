@@ -39,7 +39,7 @@ constexpr int kFiltThreads = 256;
 constexpr int kFiltWarps = kFiltThreads / 32;
 constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
-constexpr int kListCap = 5120;
+constexpr int kListCap = 4864;               // (four CTAs' shared memory fits an SM)
 constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
@@ -248,7 +248,7 @@ enum class Weigh { kNone, kBelow, kClose, kExact };
 struct Bracket {
   uint64_t lo, hi;
   int n_in, n_above;
-  uint64_t m_in, m_above, below;     // (kBelow: below alone)
+  uint64_t m_above, below, total;    // (kBelow: below alone, kClose: not below)
   bool whole;                        // the list holds all places in [lo, hi]
   float top;                         // the largest logit from lo on
   bool any;                          // there is one
@@ -308,7 +308,7 @@ struct PassBody {
   int n_above;
   uint64_t m_in, m_above, below;
   FloatSum f_below;                  // kBelow
-  CloseSum c_all, c_below, c_above;  // kClose
+  CloseSum c_all, c_above;           // kClose: of all tokens, of those above the bracket
 
   // 2^(y - k), y = x to_y: the factor's rounding makes the exponent good to |y| 2^-22.8.
   __device__ __forceinline__ float cheap(float x) const { return fast_exp2(__fmaf_rn(x, to_y, y_off)); }
@@ -329,11 +329,10 @@ struct PassBody {
         ++n_above;
         if (kWeigh == Weigh::kExact) m_above += exact(x);
       }
-      if (kWeigh == Weigh::kClose) {
+      if (kWeigh == Weigh::kClose && c > hi) {
         ClosePart part = {0.0f, 0.0f};
         part.add(close(x));
-        if (c < lo) c_below.add(part, unit);
-        else c_above.add(part, unit);
+        c_above.add(part, unit);
       }
       return;
     }
@@ -347,7 +346,7 @@ struct PassBody {
   __device__ __forceinline__ void many(const float* x, int i0) {
     uint32_t in = 0;
     float low = 0.0f, top = -kInf;
-    ClosePart all = {0.0f, 0.0f}, under_part = {0.0f, 0.0f}, over_part = {0.0f, 0.0f};
+    ClosePart all = {0.0f, 0.0f}, part = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
       const bool under = x[e] < lo_value, over = kWeigh != Weigh::kBelow && x[e] > hi_value;      // (a NaN is neither)
@@ -356,8 +355,7 @@ struct PassBody {
       if (kWeigh == Weigh::kClose) {
         const CloseWeight c = close(x[e]);
         all.add(c);
-        if (under) under_part.add(c);
-        if (over) over_part.add(c);
+        if (over) part.add(c);
       }
       if (kWeigh == Weigh::kExact) {
         const uint64_t w = exact(x[e]);
@@ -372,8 +370,7 @@ struct PassBody {
     if (kWeigh == Weigh::kBelow) f_below.add(low);
     if (kWeigh == Weigh::kClose) {
       c_all.add(all, unit);
-      c_below.add(under_part, unit);
-      c_above.add(over_part, unit);
+      c_above.add(part, unit);
     }
     if (kWeigh != Weigh::kBelow && top > -kInf) best = max(best, order_key(top));
     while (in) {
@@ -396,7 +393,7 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
   const float unit = exp2f(static_cast<float>(row.bits));
   PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
                               row.inv_t * kLog2e, -static_cast<float>(scale.k), unit, scale,
-                              0u, 0, 0, 0, 0, {}, {}, {}, {}};
+                              0u, 0, 0, 0, 0, {}, {}, {}};
   for_slice(row, body);
   Bracket out;
   out.lo = lo;
@@ -404,9 +401,8 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
   uint64_t v[5] = {static_cast<uint64_t>(body.n_above), body.m_in, body.m_above, body.below, body.best};
   if (kWeigh == Weigh::kBelow) v[3] = body.f_below.steps(unit);
   if (kWeigh == Weigh::kClose) {
+    v[1] = body.c_all.steps(unit);
     v[2] = body.c_above.steps(unit);
-    v[3] = body.c_below.steps(unit);
-    v[1] = body.c_all.steps(unit) - v[2] - v[3];           // (may be off by the others' roundings, below 0 too)
   }
   block_reduce<5, 4>(v, s);                // (its barriers close the list too)
   const int listed = s.n_list;
@@ -470,7 +466,7 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
     out.whole = listed <= kListCap;
   }
   out.n_above = static_cast<int>(v[0]);
-  out.m_in = v[1];
+  out.total = kWeigh == Weigh::kExact ? v[1] + v[2] + v[3] : v[1];
   out.m_above = v[2];
   out.below = v[3];
   out.any = v[4] != 0;
@@ -886,7 +882,6 @@ __device__ __noinline__ uint64_t locate_rank(const Row<T>& row, Bounds in, int k
 template <typename T>
 __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Target target, uint64_t from,
                                                const WeightScale& scale, FiltSmem& s, Bracket& view, uint64_t& mass) {
-  const uint64_t vocab_steps = static_cast<uint64_t>(row.vocab);       // exact weights are rounded to a step each
   bool exact = scale.tie, again = from != 0;
   uint64_t lo = from, hi = in.hi;
   for (int turn = 1; turn <= kTurns; ++turn) {
@@ -898,37 +893,47 @@ __device__ __noinline__ uint64_t locate_weight(const Row<T>& row, Bounds in, Tar
     }
     again = false;
     view = exact ? pass<Weigh::kExact>(row, lo, hi, scale, s) : pass<Weigh::kClose>(row, lo, hi, scale, s);
-    uint64_t sum = static_cast<int64_t>(view.m_in) < 0 ? 0 : view.m_in;
-    if (!exact && view.whole) {            // listed weights are exact
-      uint64_t own = 0;
-      for (int i = threadIdx.x; i < view.n_in; i += kFiltThreads) own += weight_of(__fmul_rn(place_value(s.list[i]), row.inv_t), scale, s.table);
-      sum = block_sum(own, s);
+    uint64_t sum = 0;                      // of the bracket
+    if (view.whole) {                      // listed weights are exact
+      for (int i = threadIdx.x; i < view.n_in; i += kFiltThreads) sum += weight_of(__fmul_rn(place_value(s.list[i]), row.inv_t), scale, s.table);
+      sum = block_sum(sum, s);
+    } else {
+      const uint64_t out = view.m_above + view.below;
+      sum = exact && view.total > out ? view.total - out : 0;
     }
-    // the others' sums are within `off` of what the pass gave: 2^-29.5 of a weight, 2^-28.5 of a vector's sum
-    const uint64_t others = view.below + view.m_above + (view.whole ? 0 : sum);
-    const uint64_t off = exact ? 0 : static_cast<uint64_t>(static_cast<float>(others) * 0x1p-27f) + vocab_steps;
+    // sums of close weights are within `off`: 2^-29.5 of a weight, 2^-28.5 of a vector's sum; exact weights are
+    // rounded to a step each
+    const uint64_t off = exact ? 0 : static_cast<uint64_t>(static_cast<float>(view.total) * 0x1p-27f) + row.vocab;
     uint64_t least = target.most, most = target.most;
     if (target.share > 0.0f) {
-      const uint64_t z = view.below + view.m_above + sum;
-      least = share_of(target.share, z > off ? z - off : 0);
-      most = off ? share_of(target.share, z + off) : least;
+      least = share_of(target.share, view.total > off ? view.total - off : 0);
+      most = off ? share_of(target.share, view.total + off) : least;
       target.most = most;
     }
     const uint64_t above_least = view.m_above > off ? view.m_above - off : 0, above_most = view.m_above + off;
     if (above_least >= most) {             // above the bracket
       in.lo = hi + 1;
       in.w = view.m_above > in.m ? view.m_above - in.m : 0;
-    } else if (above_most + sum + off < least) {                       // below it
+    } else if (!view.whole && !exact) {
+      // the bracket's own weight is not known: another one, and the second time exact weights, which tell
+      if (above_most < least) {
+        in.hi = hi;
+        in.n = view.n_above;
+        in.m = view.m_above;
+        in.w = view.total > view.m_above ? view.total - view.m_above : 0;
+      }
+      exact = turn >= 2;
+    } else if (above_most + sum < least) { // below it
       if (lo == in.lo) return in.lo;       // all that there is
       in.hi = lo - 1;
       in.n = view.n_above + view.n_in;
       in.m = view.m_above + sum;
-      in.w = view.below;
-    } else if (exact ? !view.whole : !view.whole && above_most < least && most + off <= above_least + sum) {
-      in = {lo, hi, view.n_above, view.m_above, sum};                  // in it, and more than the list holds
+      in.w = view.total > in.m ? view.total - in.m : 0;
+    } else if (!view.whole) {              // in it, and more than the list holds
+      in = {lo, hi, view.n_above, view.m_above, sum};
     } else {
       Target inner = {least > above_most ? least - above_most : 0, most - above_least, 0.0f, 0, 0};
-      const uint64_t at = view.whole && inner.least > 0 && inner.most <= sum ? select_weight(view, lo, inner, sum, scale, row, s) : 0;
+      const uint64_t at = inner.least > 0 && inner.most <= sum ? select_weight(view, lo, inner, sum, scale, row, s) : 0;
       if (at != 0 && s.before < inner.least) {
         mass = view.m_above + s.before + s.weight;
         return at;
@@ -1017,13 +1022,13 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
         mass = s.before + s.weight;
       } else {
         view = pass<Weigh::kExact>(row, cut, kHighest, scale, s);
-        target = {0, share_of(p, view.m_in), 0.0f, 0, 0};
+        target = {0, share_of(p, view.total - view.below), 0.0f, 0, 0};
         target.least = target.most;
         if (view.whole) {
           at = select_weight(view, cut, target, sum, scale, row, s);
           mass = s.before + s.weight;
         } else {
-          at = locate_weight(row, Bounds{cut, kHighest, 0, 0, view.m_in}, target, 0, scale, s, view, mass);
+          at = locate_weight(row, Bounds{cut, kHighest, 0, 0, view.total - view.below}, target, 0, scale, s, view, mass);
         }
       }
     } else {
@@ -1068,6 +1073,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
 // ln of the kept share of a token: its weight over the sum of all kept ones.
 __device__ __forceinline__ float log_share(float s_tok, uint64_t sum, const WeightScale& w, const WeightTable& table) {
   const uint64_t mine = weight_of(s_tok, w, table);
+  if (mine >= sum && mine > 0) return 0.0f;              // (a close sum may lie below its one term)
   if (mine > sum / 2) return log1pf(-(static_cast<float>(sum - mine) / static_cast<float>(sum)));
   const float total = static_cast<float>(sum) * exp2f(static_cast<float>(-w.bits));
   if (w.tie) return mine ? -logf(total) : -kInf;
