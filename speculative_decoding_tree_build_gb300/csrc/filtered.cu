@@ -44,7 +44,7 @@ constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a 
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
-constexpr int kFirstList = 384;            // tokens that the first list is made for without top-k
+constexpr int kFirstList = 128;            // tokens that the first list is made for without top-k
 constexpr int kBins = 1024;
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
@@ -195,9 +195,13 @@ struct Row {
   int bits;
 };
 
+__device__ __forceinline__ void prefetch_line(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // f.many<n>(x, first index) for all entries of the slice, n at a time (the
-// ragged end one by one).
-template <typename T, typename F>
+// ragged end one by one). kAhead > 0: the first look at the row, lines that far ahead
+// (in steps of the loop) are fetched to L2: 64 bytes a thread in flight alone leave
+// the memory idle.
+template <int kAhead, typename T, typename F>
 __device__ __forceinline__ void for_slice(const Row<T>& row, F& f) {
   constexpr int kLen = Vec<T>::kLen;
   const uint4* vecs = reinterpret_cast<const uint4*>(row.x + row.v0);
@@ -207,6 +211,10 @@ __device__ __forceinline__ void for_slice(const Row<T>& row, F& f) {
 #pragma unroll
     for (int u = 0; u < kFiltUnroll; ++u)
       if (j0 + u * kFiltThreads < n) v[u] = vecs[j0 + u * kFiltThreads];
+    if (kAhead > 0 && threadIdx.x < kFiltUnroll * kFiltThreads / 8) {
+      const int line = (j0 - static_cast<int>(threadIdx.x)) + kAhead * kFiltUnroll * kFiltThreads + threadIdx.x * 8;
+      if (line < n) prefetch_line(vecs + line);
+    }
 #pragma unroll
     for (int u = 0; u < kFiltUnroll; ++u) {
       const int j = j0 + u * kFiltThreads;
@@ -253,6 +261,12 @@ struct Bracket {
   float top;                         // the largest logit from lo on
   bool any;                          // there is one
 };
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
 
 // A float32 sum with its roundings beside it.
 struct FloatSum {
@@ -344,13 +358,26 @@ struct PassBody {
 
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
-    uint32_t in = 0;
+    if (kWeigh == Weigh::kNone || kWeigh == Weigh::kBelow) {
+      // most vectors lie below the list as a whole (a NaN does not)
+      float high = x[0];
+#pragma unroll
+      for (int e = 1; e < kLen; ++e) high = max_or_nan(high, x[e]);
+      if (high < lo_value) {
+        if (kWeigh == Weigh::kBelow) {
+          float low = 0.0f;
+#pragma unroll
+          for (int e = 0; e < kLen; ++e) low += cheap(x[e]);
+          f_below.add(low);
+        }
+        return;
+      }
+    }
     float low = 0.0f, top = -kInf;
     ClosePart all = {0.0f, 0.0f}, part = {0.0f, 0.0f};
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
       const bool under = x[e] < lo_value, over = kWeigh != Weigh::kBelow && x[e] > hi_value;      // (a NaN is neither)
-      if (!under && !over) in |= 1u << e;
       if (kWeigh == Weigh::kBelow) low += under ? cheap(x[e]) : 0.0f;
       if (kWeigh == Weigh::kClose) {
         const CloseWeight c = close(x[e]);
@@ -366,6 +393,7 @@ struct PassBody {
         top = fmaxf(top, x[e]);
         ++n_above;
       }
+      if (!under && !over) take(x[e], i0 + e);
     }
     if (kWeigh == Weigh::kBelow) f_below.add(low);
     if (kWeigh == Weigh::kClose) {
@@ -373,11 +401,6 @@ struct PassBody {
       c_above.add(part, unit);
     }
     if (kWeigh != Weigh::kBelow && top > -kInf) best = max(best, order_key(top));
-    while (in) {
-      const int e = __ffs(in) - 1;
-      in &= in - 1;
-      take(load_one(row.x + i0 + e), i0 + e);
-    }
   }
 };
 
@@ -394,7 +417,7 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
   PassBody<kWeigh, T> body = {s, row, own, cap, lo, hi, place_value(lo), hi == kHighest ? kInf : place_value(hi),
                               row.inv_t * kLog2e, -static_cast<float>(scale.k), unit, scale,
                               0u, 0, 0, 0, 0, {}, {}, {}};
-  for_slice(row, body);
+  for_slice<kWeigh == Weigh::kNone || kWeigh == Weigh::kBelow ? 3 : 0>(row, body);
   Bracket out;
   out.lo = lo;
   out.hi = hi;
@@ -810,7 +833,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
     margin = sigmas * sqrtf(want / fast_exp2(fmaxf(-step * (static_cast<float>(found >> 16) + 0.5f), -100.0f))) + 6.0f;
   } else {
     rank = missing / each;
-    margin = sigmas * sqrtf(rank) + 8.0f;
+    margin = sigmas * sqrtf(rank) + 3.0f;
   }
   margin = fminf(margin, most / each);
   const int down = static_cast<int>(fminf(rank + margin, 1e9f)) + 1, up = static_cast<int>(rank - margin);
@@ -1302,7 +1325,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
   RowResult res = {kLowest, 0, false, false, 0, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
     TopBody body = {no_draw()};
-    for_slice(row, body);
+    for_slice<3>(row, body);
     publish(block_max(body.draw.best, s), 0, 0);
     const uint64_t best = cluster_stat<true>(s, 0, csize);
     res.empty = best < kLowest;
@@ -1373,7 +1396,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
       for_slice_noise(row, noise, body);
       body.sum = body.close.steps(body.unit);
     } else {
-      for_slice(row, body);
+      for_slice<0>(row, body);
     }
     const uint64_t own = block_max(body.draw.best, s);
     publish(own, body.weigh ? block_sum(body.sum, s) : 0, 0);
@@ -1391,7 +1414,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
     MaskBody<T> body = {static_cast<T*>(p.out) + t * p.out_ld, res.cut, place_value(res.cut), 0};
     __syncwarp();
     row_barrier(csize);
-    for_slice(row, body);
+    for_slice<0>(row, body);
     const uint64_t own = block_sum(body.kept, s);
     publish(own, 0, 0);
     const int kept = static_cast<int>(cluster_stat<false>(s, 0, csize));
