@@ -44,7 +44,7 @@ constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a 
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
-constexpr int kFirstList = 128;            // tokens that the first list is made for without top-k
+constexpr int kFirstList = 512;            // tokens that the first list is made for without top-k
 constexpr int kBins = 1024;
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
@@ -373,6 +373,7 @@ struct PassBody {
         return;
       }
     }
+    uint32_t in = 0;
     float low = 0.0f, top = -kInf;
     ClosePart all = {0.0f, 0.0f}, part = {0.0f, 0.0f};
 #pragma unroll
@@ -393,7 +394,13 @@ struct PassBody {
         top = fmaxf(top, x[e]);
         ++n_above;
       }
-      if (!under && !over) take(x[e], i0 + e);
+      if (!under && !over) in |= 1u << e;
+    }
+    // (the lanes of a warp take theirs side by side: one or two turns instead of one an entry)
+    while (in) {
+      const int e = __ffs(in) - 1;
+      in &= in - 1;
+      take(load_one(row.x + i0 + e), i0 + e);
     }
     if (kWeigh == Weigh::kBelow) f_below.add(low);
     if (kWeigh == Weigh::kClose) {
