@@ -25,9 +25,12 @@
 // Weights of listed tokens are integers (tv_weight.cuh) and their sums exact: no
 // result depends on the order of the atomics that build lists and histograms.
 //
-// One CTA has a row, or a cluster where rows are few: its CTAs pass over slices,
-// exchange lists and sums through distributed shared memory, and all of them
-// take the same decisions.
+// A cluster has a row where rows are few: its CTAs pass over slices, exchange lists
+// and sums through distributed shared memory, and all of them take the same
+// decisions. Where rows are many each CTA of a cluster has a row of its own at first,
+// and the rows that take more than one pass are gone through by the cluster
+// together: a flat row takes four times as long as the others and would hold up the
+// end of the call alone on its SM.
 #include <cuda_bf16.h>
 
 #include "tv_cluster.cuh"
@@ -39,13 +42,16 @@ constexpr int kFiltThreads = 256;
 constexpr int kFiltWarps = kFiltThreads / 32;
 constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
-constexpr int kListCap = 4864;               // (four CTAs' shared memory fits an SM)
-constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
+constexpr int kListCap = 3840;               // (with kTeamCap, four CTAs' shared memory fits an SM)
+constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster that has one row
+constexpr int kTeamCap = 1024;             // and in a team
+constexpr int kTeam = 4;
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
-constexpr int kFirstList = 512;            // tokens that the first list is made for without top-k
+constexpr int kFirstList = 256;            // tokens that the first list is made for without top-k
 constexpr int kBins = 1024;
+constexpr int kHits = 4 * kBins;           // noted vectors of a pass (where the bins lie otherwise)
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
 constexpr int kFiltUnroll = 4;             // 16-byte loads in flight a thread
@@ -70,7 +76,10 @@ struct FiltParams {
   const int32_t* top_k;
   const float* top_p;
   const float* min_p;
-  int max_nodes, vocab, bits, csize;
+  int max_nodes, vocab, bits;
+  int csize, team;             // CTAs of a cluster; 1: each has a row at first
+  int local_cap;               // a CTA's part of a cluster's list
+  int rows;                    // batch * max_nodes
   int32_t* tokens;
   float* logp;
   void* out;
@@ -86,7 +95,8 @@ struct FiltSmem {
   uint64_t small[kSmall];
   uint64_t found, before, weight;          // of select
   uint64_t stat[6];                        // of a pass: listed, above, three sums, the largest key
-  int bin, bin_count, n_small, n_list;
+  uint64_t hard;                           // the CTA's own row takes more than one pass
+  int bin, bin_count, n_small, n_list, n_hits;
   int rank, lo_bin, hi_bin;                // of a bracket
   uint64_t list[kListCap];                 // in a cluster the CTA's own part follows
 };
@@ -190,7 +200,7 @@ template <typename T>
 struct Row {
   const T* x;
   int vocab, v0, v1;
-  int rank, csize;
+  int rank, csize, local_cap;
   float inv_t;
   int bits;
 };
@@ -356,6 +366,26 @@ struct PassBody {
     if (kWeigh == Weigh::kExact) m_in += exact(x);
   }
 
+  // those of a vector (or of a single entry at the slice's end) that may
+  template <int kLen>
+  __device__ __forceinline__ void take_all(int i0) {
+    float x[kLen];
+    if constexpr (kLen > 1) Vec<T>::unpack(*reinterpret_cast<const uint4*>(row.x + i0), x);
+    else x[0] = load_one(row.x + i0);
+#pragma unroll
+    for (int e = 0; e < kLen; ++e)
+      if (!(x[e] < lo_value) && (kWeigh == Weigh::kBelow || !(x[e] > hi_value))) take(x[e], i0 + e);
+  }
+  __device__ __forceinline__ void take_hits() {
+    constexpr int kLen = Vec<T>::kLen;
+    const int n = min(s.n_hits, kHits);
+    for (int h = threadIdx.x; h < n; h += kFiltThreads) {
+      const int i0 = static_cast<int>(s.bins[0][h]);
+      if (i0 + kLen <= row.v1) take_all<kLen>(i0);
+      else take_all<1>(i0);
+    }
+  }
+
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, int i0) {
     if (kWeigh == Weigh::kNone || kWeigh == Weigh::kBelow) {
@@ -396,11 +426,12 @@ struct PassBody {
       }
       if (!under && !over) in |= 1u << e;
     }
-    // (the lanes of a warp take theirs side by side: one or two turns instead of one an entry)
-    while (in) {
-      const int e = __ffs(in) - 1;
-      in &= in - 1;
-      take(load_one(row.x + i0 + e), i0 + e);
+    // Vectors with such tokens are noted, and looked at when all threads have some: one in a
+    // hundred vectors has one, and a warp that stopped for it would stop nearly always.
+    if (in) {
+      const int at = atomicAdd(&s.n_hits, 1);
+      if (at < kHits) s.bins[0][at] = i0;
+      else take_all<kLen>(i0);
     }
     if (kWeigh == Weigh::kBelow) f_below.add(low);
     if (kWeigh == Weigh::kClose) {
@@ -414,10 +445,10 @@ struct PassBody {
 template <Weigh kWeigh, typename T>
 __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi, const WeightScale& scale, FiltSmem& s) {
   uint64_t* own = row.csize > 1 ? s.list + kListCap : s.list;
-  const int cap = row.csize > 1 ? kLocalCap : kListCap;
+  const int cap = row.csize > 1 ? row.local_cap : kListCap;
   __syncwarp();
   row_barrier(row.csize);                  // the lists and sums of the pass before are read
-  if (threadIdx.x == 0) s.n_list = 0;
+  if (threadIdx.x == 0) s.n_list = s.n_hits = 0;
   __syncthreads();
   // a weight is at most 2: sums stay below 2^31, in steps of 2^-F below 2^63
   const float unit = exp2f(static_cast<float>(row.bits));
@@ -425,6 +456,8 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
                               row.inv_t * kLog2e, -static_cast<float>(scale.k), unit, scale,
                               0u, 0, 0, 0, 0, {}, {}, {}};
   for_slice<kWeigh == Weigh::kNone || kWeigh == Weigh::kBelow ? 3 : 0>(row, body);
+  __syncthreads();
+  body.take_hits();
   Bracket out;
   out.lo = lo;
   out.hi = hi;
@@ -475,7 +508,7 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
       const int q = (i + 1) << shift;
       v[i] = __shfl_sync(0xffffffffu, q < 32 ? got[0] : got[1], q & 31);
     }
-    out.whole = out.n_in <= kListCap && longest <= kLocalCap;
+    out.whole = out.n_in <= kListCap && longest <= row.local_cap;
     if (out.whole) {
 #pragma unroll 4
       for (int i = threadIdx.x; i < out.n_in; i += kFiltThreads) {
@@ -996,17 +1029,19 @@ struct RowResult {
   uint64_t cut;            // the last place that is kept
   uint64_t mass;           // the weight of all that is kept, 0: not known
   bool empty;              // nothing above -inf
+  bool hard;               // not found: more than one pass is needed
   bool listed;             // all that is kept is on the list
   int n_list, n_above;     // on the list, and above it
   WeightScale scale;
 };
 
 template <typename T>
-__device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p, float min_p, FiltSmem& s) {
+__device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p, float min_p, bool one_pass, FiltSmem& s) {
   const bool by_k = k > 0 && k < row.vocab, by_p = p < 1.0f, by_m = min_p > 0.0f;
   const int vocab = row.vocab;
   uint64_t lo = kLowest, hi = kHighest;
   const WeightScale none = weight_scale(0.0f, row.bits);
+  const RowResult hard = {kHighest, 0, false, true, false, 0, 0, none};
   // 1. where the list begins (and ends, for a top-k set that no list holds)
   if (vocab > kListCap) {
     const float wanted = static_cast<float>(by_k ? k : kFirstList);
@@ -1025,12 +1060,13 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
                                    : pass<Weigh::kNone>(row, lo, hi, none, s);
   if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)
     view = pass<Weigh::kNone>(row, kLowest, kHighest, none, s);
-  if (!view.any) return RowResult{kHighest, 0, true, true, 0, 0, none};
+  if (!view.any) return RowResult{kHighest, 0, true, false, true, 0, 0, none};
   const WeightScale scale = weight_scale(__fmul_rn(view.top, row.inv_t), row.bits);
   uint64_t cut = kLowest, mass = 0;
   // 3. top-k
   if (by_k) {
     const int with = view.n_above + view.n_in;
+    if (one_pass && (view.n_above >= k || (with < k ? view.lo > kLowest : !view.whole))) return hard;
     if (view.n_above >= k) {
       cut = locate_rank(row, Bounds{view.hi + 1, kHighest, 0, 0, 0}, k, s, view);
     } else if (with < k) {                 // (from the lowest place on fewer than k: all stay)
@@ -1050,6 +1086,8 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
       if (listed && cut >= view.lo) {
         at = select_weight(view, cut, target, sum, scale, row, s);
         mass = s.before + s.weight;
+      } else if (one_pass) {
+        return hard;
       } else {
         view = pass<Weigh::kExact>(row, cut, kHighest, scale, s);
         target = {0, share_of(p, view.total - view.below), 0.0f, 0, 0};
@@ -1080,6 +1118,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
         else at = 0;
         target.below = target.off = 0;
       }
+      if (at == 0 && one_pass) return hard;
       if (at == 0) at = locate_weight(row, in, target, from, scale, s, view, mass);
     }
     if (at > cut) cut = at;
@@ -1095,7 +1134,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
       mass = 0;
     }
   }
-  return RowResult{cut, mass, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, view.n_above, scale};
+  return RowResult{cut, mass, false, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, view.n_above, scale};
 }
 
 // ------------------------------------------------------------------- endings
@@ -1276,41 +1315,59 @@ struct MaskBody {
   }
 };
 
-template <typename T, bool kSampling>
-__global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
-  extern __shared__ __align__(16) unsigned char s_raw[];
-  FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
-  if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int csize = p.csize, rank = csize > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const int b = blockIdx.y, node = blockIdx.x / csize;
-  const int st = p.status[b];
-  const int t0 = p.cu_nodes[b], n = p.cu_nodes[b + 1] - t0;
-  const float temp = p.temperature[b];
-  const int k = p.top_k ? p.top_k[b] : 0;
-  const float top_p = p.top_p ? p.top_p[b] : 1.0f, min_p = p.min_p ? p.min_p[b] : 0.0f;
-  // every CTA of a cluster takes the same branches (same b and node)
-  if (st != 0 || (node >= n && n >= 0)) return;
-  const float inv_t = temp > 0.0f ? __frcp_rn(temp) : 1.0f;
+// A row of the call, as a CTA meets it.
+struct Job {
+  bool on;                 // there is something to do
+  int b;
+  size_t t;
+  float temp, inv_t, top_p, min_p;
+  int k;
+};
+
+template <bool kSampling>
+__device__ __forceinline__ Job job_of(const FiltParams& p, int id) {
+  Job job;
+  job.on = false;
+  if (id >= p.rows) return job;
+  job.b = id / p.max_nodes;
+  const int node = id - job.b * p.max_nodes;
+  const int st = p.status[job.b];
+  const int t0 = p.cu_nodes[job.b], n = p.cu_nodes[job.b + 1] - t0;
+  job.temp = p.temperature[job.b];
+  job.k = p.top_k ? p.top_k[job.b] : 0;
+  job.top_p = p.top_p ? p.top_p[job.b] : 1.0f;
+  job.min_p = p.min_p ? p.min_p[job.b] : 0.0f;
+  if (st != 0 || (node >= n && n >= 0)) return job;
+  job.inv_t = job.temp > 0.0f ? __frcp_rn(job.temp) : 1.0f;
   int flag = 0;
   if (n > p.max_nodes || n < 0 || t0 < 0) flag |= TV_ST_BAD_SIZE;
-  if (!(temp >= 0.0f) || temp == kInf || inv_t == kInf || (kSampling && temp > 0.0f && !p.gumbel)) flag |= TV_ST_BAD_TEMPERATURE;
-  if (k < 0 || !(top_p >= 0.0f && top_p <= 1.0f) || !(min_p >= 0.0f && min_p <= 1.0f)) flag |= TV_ST_BAD_FILTER;
+  if (!(job.temp >= 0.0f) || job.temp == kInf || job.inv_t == kInf || (kSampling && job.temp > 0.0f && !p.gumbel))
+    flag |= TV_ST_BAD_TEMPERATURE;
+  if (job.k < 0 || !(job.top_p >= 0.0f && job.top_p <= 1.0f) || !(job.min_p >= 0.0f && job.min_p <= 1.0f)) flag |= TV_ST_BAD_FILTER;
   if (flag) {
-    if (node == 0 && rank == 0 && threadIdx.x == 0) atomicOr(&p.status[b], flag);
-    return;
+    if (node == 0 && threadIdx.x == 0) atomicOr(&p.status[job.b], flag);       // (all CTAs that meet the row say the same)
+    return job;
   }
-  const size_t t = static_cast<size_t>(t0) + node;
-  Row<T> row = {static_cast<const T*>(p.logits) + t * p.logits_ld, p.vocab, 0, p.vocab, rank, csize, inv_t, p.bits};
+  job.t = static_cast<size_t>(t0) + node;
+  job.on = true;
+  return job;
+}
+
+// One row by csize CTAs that all call this. False: it takes more than one pass, and
+// nothing is written.
+template <typename T, bool kSampling>
+__device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csize, int rank, bool one_pass, FiltSmem& s) {
+  const size_t t = job.t;
+  const float inv_t = job.inv_t, top_p = job.top_p, min_p = job.min_p;
+  const int k = job.k;
+  Row<T> row = {static_cast<const T*>(p.logits) + t * p.logits_ld, p.vocab, 0, p.vocab, rank, csize, p.local_cap, inv_t, p.bits};
   if (csize > 1) {
     const int per = ((p.vocab + csize - 1) / csize + 7) & ~7;
     row.v0 = min(p.vocab, rank * per);
     row.v1 = min(p.vocab, row.v0 + per);
   }
-  const bool greedy = temp == 0.0f;
+  const bool greedy = job.temp == 0.0f;
   const bool filtered = !greedy && ((k > 0 && k < p.vocab) || top_p < 1.0f || min_p > 0.0f);
-  __syncthreads();
 
   // Each CTA's part of an ending goes to s.stat; the first CTA combines them.
   auto publish = [&](uint64_t a, uint64_t b2, uint64_t c) {
@@ -1324,12 +1381,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
     __syncwarp();
     row_barrier(csize);
   };
-  auto finish = [&] {                      // no CTA goes while its memory may be read
-    __syncwarp();
-    if (csize > 1) cluster_sync_all();
-  };
-
-  RowResult res = {kLowest, 0, false, false, 0, 0, weight_scale(0.0f, p.bits)};
+  RowResult res = {kLowest, 0, false, false, false, 0, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
     TopBody body = {no_draw()};
     for_slice<3>(row, body);
@@ -1342,11 +1394,11 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
         p.tokens[t] = res.empty ? 0 : best_index(best);
         if (p.logp) p.logp[t] = res.empty ? -kInf : 0.0f;
       }
-      finish();
-      return;
+      return true;
     }
   } else if (filtered) {
-    res = find_cut(row, k, top_p, min_p, s);
+    res = find_cut(row, k, top_p, min_p, one_pass, s);
+    if (res.hard) return false;
   }
 
   if constexpr (kSampling) {
@@ -1381,16 +1433,14 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
           p.logp[t] = best ? out : -kInf;
         }
       }
-      finish();
-      return;
+      return true;
     }
     if (res.empty) {
       if (threadIdx.x == 0 && rank == 0) {
         p.tokens[t] = 0;
         if (p.logp) p.logp[t] = -kInf;
       }
-      finish();
-      return;
+      return true;
     }
     DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table,
                         no_draw(), 0, {}, exp2f(static_cast<float>(p.bits))};
@@ -1415,7 +1465,6 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
         p.logp[t] = log_share(__fmul_rn(load_one(row.x + token), inv_t), sum, res.scale, s.table);
       }
     }
-    finish();
   } else {
     // (in place: no CTA of the cluster writes before all have read the row)
     MaskBody<T> body = {static_cast<T*>(p.out) + t * p.out_ld, res.cut, place_value(res.cut), 0};
@@ -1426,8 +1475,39 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
     publish(own, 0, 0);
     const int kept = static_cast<int>(cluster_stat<false>(s, 0, csize));
     if (p.kept && threadIdx.x == 0 && rank == 0) p.kept[t] = kept;
-    finish();
   }
+  return true;
+}
+
+template <typename T, bool kSampling>
+__global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
+  if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int rank = p.csize > 1 ? static_cast<int>(cluster_rank()) : 0, cluster = blockIdx.x / p.csize;
+  if (!p.team) {
+    const Job job = job_of<kSampling>(p, cluster);         // (the same in all CTAs of the cluster)
+    __syncthreads();
+    if (job.on) do_row<T, kSampling>(p, job, p.csize, rank, false, s);
+  } else {
+    const int first = cluster * p.csize;
+    const Job own = job_of<kSampling>(p, first + rank);
+    __syncthreads();
+    bool hard = false;
+    if (own.on) hard = !do_row<T, kSampling>(p, own, 1, 0, true, s);
+    __syncthreads();
+    if (threadIdx.x == 0) s.hard = hard;
+    __syncwarp();
+    cluster_sync_all();
+    for (int r = 0; r < p.csize; ++r) {
+      if (ld_cluster_u64(&s.hard, r) == 0) continue;
+      do_row<T, kSampling>(p, job_of<kSampling>(p, first + r), p.csize, rank, false, s);
+    }
+  }
+  __syncwarp();
+  if (p.csize > 1) cluster_sync_all();     // no CTA goes while its memory may be read
 }
 
 // ------------------------------------------------------------------ host side
@@ -1447,13 +1527,21 @@ static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
   if (sms <= 0) return TV_ERR_CUDA;
   auto* kernel = dtype == TV_DTYPE_F32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
   const long long rows = static_cast<long long>(batch) * p.max_nodes;
+  p.rows = static_cast<int>(rows);
+  // a cluster a row where that leaves no SM more than three CTAs, teams where rows that a list
+  // holds as a whole are not all there is
   p.csize = 1;
   while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * 3 && p.vocab > kListCap) p.csize *= 2;
+  p.team = p.csize == 1 && p.vocab > kListCap && rows > 1;
+  if (p.team) p.csize = kTeam;
+  p.local_cap = p.team ? kTeamCap : kLocalCap;
   const size_t most = sizeof(FiltSmem) + kLocalCap * sizeof(uint64_t);
   if (!ensure_smem(kernel, most, smem_set[dtype], dev)) return TV_ERR_CUDA;
   p.bits = weight_bits(p.vocab);
-  const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(p.max_nodes * p.csize, batch), dim3(kFiltThreads), p.csize,
-                                                  p.csize > 1 ? most : sizeof(FiltSmem), as_stream(stream), p);
+  const long long clusters = p.team ? (rows + kTeam - 1) / kTeam : rows;
+  const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? p.local_cap * sizeof(uint64_t) : 0);
+  const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(clusters * p.csize)), dim3(kFiltThreads), p.csize,
+                                                  smem, as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
