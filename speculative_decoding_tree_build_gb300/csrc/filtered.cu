@@ -27,10 +27,12 @@
 //
 // A cluster has a row where rows are few: its CTAs pass over slices, exchange lists
 // and sums through distributed shared memory, and all of them take the same
-// decisions. Where rows are many each CTA of a cluster has a row of its own at first,
-// and the rows that take more than one pass are gone through by the cluster
-// together: a flat row takes four times as long as the others and would hold up the
-// end of the call alone on its SM.
+// decisions. Where rows are many each has one CTA, which leaves a mark in the
+// row's output where one pass does not do, and a second grid of clusters goes through
+// the marked rows: a flat row takes four times as long as the others and would hold up
+// the end of the call alone on its SM.
+#include <climits>
+
 #include <cuda_bf16.h>
 
 #include "tv_cluster.cuh"
@@ -42,10 +44,10 @@ constexpr int kFiltThreads = 256;
 constexpr int kFiltWarps = kFiltThreads / 32;
 constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
-constexpr int kListCap = 3840;               // (with kTeamCap, four CTAs' shared memory fits an SM)
-constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster that has one row
-constexpr int kTeamCap = 1024;             // and in a team
-constexpr int kTeam = 4;
+constexpr int kListCap = 4864;             // (four CTAs' shared memory fits an SM)
+constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
+constexpr int kSecondCluster = 4;          // CTAs that share a row of the second grid
+constexpr int kMark = INT_MIN;             // in tokens / kept: for the second grid
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
@@ -77,8 +79,8 @@ struct FiltParams {
   const float* top_p;
   const float* min_p;
   int max_nodes, vocab, bits;
-  int csize, team;             // CTAs of a cluster; 1: each has a row at first
-  int local_cap;               // a CTA's part of a cluster's list
+  int csize;                   // CTAs of a cluster
+  bool mark;                   // rows that take more than one pass are for the second grid
   int rows;                    // batch * max_nodes
   int32_t* tokens;
   float* logp;
@@ -95,8 +97,8 @@ struct FiltSmem {
   uint64_t small[kSmall];
   uint64_t found, before, weight;          // of select
   uint64_t stat[6];                        // of a pass: listed, above, three sums, the largest key
-  uint64_t hard;                           // the CTA's own row takes more than one pass
   int bin, bin_count, n_small, n_list, n_hits;
+  uint32_t marks[kFiltWarps];
   int rank, lo_bin, hi_bin;                // of a bracket
   uint64_t list[kListCap];                 // in a cluster the CTA's own part follows
 };
@@ -200,7 +202,7 @@ template <typename T>
 struct Row {
   const T* x;
   int vocab, v0, v1;
-  int rank, csize, local_cap;
+  int rank, csize;
   float inv_t;
   int bits;
 };
@@ -445,7 +447,7 @@ struct PassBody {
 template <Weigh kWeigh, typename T>
 __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi, const WeightScale& scale, FiltSmem& s) {
   uint64_t* own = row.csize > 1 ? s.list + kListCap : s.list;
-  const int cap = row.csize > 1 ? row.local_cap : kListCap;
+  const int cap = row.csize > 1 ? kLocalCap : kListCap;
   __syncwarp();
   row_barrier(row.csize);                  // the lists and sums of the pass before are read
   if (threadIdx.x == 0) s.n_list = s.n_hits = 0;
@@ -508,7 +510,7 @@ __device__ __noinline__ Bracket pass(const Row<T>& row, uint64_t lo, uint64_t hi
       const int q = (i + 1) << shift;
       v[i] = __shfl_sync(0xffffffffu, q < 32 ? got[0] : got[1], q & 31);
     }
-    out.whole = out.n_in <= kListCap && longest <= row.local_cap;
+    out.whole = out.n_in <= kListCap && longest <= kLocalCap;
     if (out.whole) {
 #pragma unroll 4
       for (int i = threadIdx.x; i < out.n_in; i += kFiltThreads) {
@@ -1315,6 +1317,62 @@ struct MaskBody {
   }
 };
 
+// Each look at a row is a function of its own, with registers of its own.
+template <typename T>
+__device__ __noinline__ uint64_t top_row(const Row<T>& row, FiltSmem& s) {
+  TopBody body = {no_draw()};
+  for_slice<3>(row, body);
+  return block_max(body.draw.best, s);
+}
+
+template <typename T>
+__device__ __noinline__ uint64_t mask_row(const Row<T>& row, T* out, uint64_t cut, FiltSmem& s) {
+  MaskBody<T> body = {out, cut, place_value(cut), 0};
+  for_slice<0>(row, body);
+  return block_sum(body.kept, s);
+}
+
+struct FreeResult {
+  uint64_t best;
+  float top, sum, nans;
+};
+template <typename T>
+__device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* noise, FiltSmem& s) {
+  FreeBody body = {row.inv_t, no_draw(), -kInf, 0.0f, 0.0f};
+  for_slice_noise(row, noise, body);
+  FreeResult out;
+  out.best = block_max(body.draw.best, s);
+  out.top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
+  out.sum = block_sum(body.top == out.top ? body.sum : body.sum * fast_exp2((body.top - out.top) * kLog2e), s);
+  out.nans = block_sum(body.nans, s);
+  return out;
+}
+
+struct DrawResult {
+  uint64_t best, sum;
+};
+// `dense`: so many are kept that all of the noise is read.
+template <typename T>
+__device__ __noinline__ DrawResult draw_row(const Row<T>& row, const float* noise, const RowResult& res, bool weigh, bool dense, FiltSmem& s) {
+  DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), weigh, res.scale, s.table,
+                      no_draw(), 0, {}, exp2f(static_cast<float>(row.bits))};
+  if (res.listed) {
+    for (int i = row.rank * kFiltThreads + threadIdx.x; i < res.n_list; i += row.csize * kFiltThreads) {
+      const uint64_t c = s.list[i];
+      if (c >= res.cut) body.take(place_value(c), noise[best_index(c)], best_index(c));
+    }
+  } else if (dense) {
+    for_slice_noise(row, noise, body);
+    body.sum = body.close.steps(body.unit);
+  } else {
+    for_slice<0>(row, body);
+  }
+  DrawResult out;
+  out.best = block_max(body.draw.best, s);
+  out.sum = weigh ? block_sum(body.sum, s) : 0;
+  return out;
+}
+
 // A row of the call, as a CTA meets it.
 struct Job {
   bool on;                 // there is something to do
@@ -1356,11 +1414,11 @@ __device__ __forceinline__ Job job_of(const FiltParams& p, int id) {
 // One row by csize CTAs that all call this. False: it takes more than one pass, and
 // nothing is written.
 template <typename T, bool kSampling>
-__device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csize, int rank, bool one_pass, FiltSmem& s) {
+__device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int csize, int rank, bool one_pass, FiltSmem& s) {
   const size_t t = job.t;
   const float inv_t = job.inv_t, top_p = job.top_p, min_p = job.min_p;
   const int k = job.k;
-  Row<T> row = {static_cast<const T*>(p.logits) + t * p.logits_ld, p.vocab, 0, p.vocab, rank, csize, p.local_cap, inv_t, p.bits};
+  Row<T> row = {static_cast<const T*>(p.logits) + t * p.logits_ld, p.vocab, 0, p.vocab, rank, csize, inv_t, p.bits};
   if (csize > 1) {
     const int per = ((p.vocab + csize - 1) / csize + 7) & ~7;
     row.v0 = min(p.vocab, rank * per);
@@ -1383,9 +1441,7 @@ __device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csi
   };
   RowResult res = {kLowest, 0, false, false, false, 0, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
-    TopBody body = {no_draw()};
-    for_slice<3>(row, body);
-    publish(block_max(body.draw.best, s), 0, 0);
+    publish(top_row(row, s), 0, 0);
     const uint64_t best = cluster_stat<true>(s, 0, csize);
     res.empty = best < kLowest;
     res.cut = res.empty ? kHighest : best;
@@ -1404,13 +1460,8 @@ __device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csi
   if constexpr (kSampling) {
     const float* noise = p.gumbel + t * p.gumbel_ld;
     if (!filtered) {
-      FreeBody body = {inv_t, no_draw(), -kInf, 0.0f, 0.0f};
-      for_slice_noise(row, noise, body);
-      const uint64_t own = block_max(body.draw.best, s);
-      const float own_top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
-      const float own_sum = block_sum(body.top == own_top ? body.sum : body.sum * fast_exp2((body.top - own_top) * kLog2e), s);
-      const float own_nans = block_sum(body.nans, s);
-      publish(own, static_cast<uint64_t>(__float_as_uint(own_sum)) << 32 | order_key(own_top), __float_as_uint(own_nans));
+      const FreeResult own = free_row(row, noise, s);
+      publish(own.best, static_cast<uint64_t>(__float_as_uint(own.sum)) << 32 | order_key(own.top), __float_as_uint(own.nans));
       const uint64_t best = cluster_stat<true>(s, 0, csize);
       if (threadIdx.x == 0 && rank == 0) {
         const int token = best ? best_index(best) : 0;
@@ -1442,23 +1493,11 @@ __device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csi
       }
       return true;
     }
-    DrawBody<T> body = {row, noise, res.cut, place_value(res.cut), p.logp != nullptr && res.mass == 0, res.scale, s.table,
-                        no_draw(), 0, {}, exp2f(static_cast<float>(p.bits))};
-    if (res.listed) {
-      for (int i = rank * kFiltThreads + threadIdx.x; i < res.n_list; i += csize * kFiltThreads) {
-        const uint64_t c = s.list[i];
-        if (c >= res.cut) body.take(place_value(c), noise[best_index(c)], best_index(c));
-      }
-    } else if (res.n_list + res.n_above > p.vocab / 32 && !res.scale.tie) {
-      for_slice_noise(row, noise, body);
-      body.sum = body.close.steps(body.unit);
-    } else {
-      for_slice<0>(row, body);
-    }
-    const uint64_t own = block_max(body.draw.best, s);
-    publish(own, body.weigh ? block_sum(body.sum, s) : 0, 0);
+    const bool weigh = p.logp != nullptr && res.mass == 0;
+    const DrawResult own = draw_row(row, noise, res, weigh, res.n_list + res.n_above > p.vocab / 32 && !res.scale.tie, s);
+    publish(own.best, own.sum, 0);
     const int token = best_index(cluster_stat<true>(s, 0, csize));
-    const uint64_t sum = body.weigh ? cluster_stat<false>(s, 1, csize) : res.mass;
+    const uint64_t sum = weigh ? cluster_stat<false>(s, 1, csize) : res.mass;
     if (threadIdx.x == 0 && rank == 0) {
       p.tokens[t] = token;
       if (p.logp) {
@@ -1467,12 +1506,9 @@ __device__ __noinline__ bool do_row(const FiltParams& p, const Job& job, int csi
     }
   } else {
     // (in place: no CTA of the cluster writes before all have read the row)
-    MaskBody<T> body = {static_cast<T*>(p.out) + t * p.out_ld, res.cut, place_value(res.cut), 0};
     __syncwarp();
     row_barrier(csize);
-    for_slice<0>(row, body);
-    const uint64_t own = block_sum(body.kept, s);
-    publish(own, 0, 0);
+    publish(mask_row(row, static_cast<T*>(p.out) + t * p.out_ld, res.cut, s), 0, 0);
     const int kept = static_cast<int>(cluster_stat<false>(s, 0, csize));
     if (p.kept && threadIdx.x == 0 && rank == 0) p.kept[t] = kept;
   }
@@ -1486,28 +1522,50 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
   if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
   grid_dependency_wait();
   grid_launch_dependents();
-  const int rank = p.csize > 1 ? static_cast<int>(cluster_rank()) : 0, cluster = blockIdx.x / p.csize;
-  if (!p.team) {
-    const Job job = job_of<kSampling>(p, cluster);         // (the same in all CTAs of the cluster)
+  const int place = p.csize > 1 ? static_cast<int>(cluster_rank()) : 0;
+  const Job job = job_of<kSampling>(p, blockIdx.x / p.csize);
+  if (!job.on) return;                     // (the same in all CTAs of a cluster)
+  __syncthreads();
+  if (!do_row<T, kSampling>(p, job, p.csize, place, p.mark, s) && threadIdx.x == 0)
+    (kSampling ? p.tokens : p.kept)[job.t] = kMark;
+  __syncwarp();
+  if (p.csize > 1) cluster_sync_all();     // no CTA goes while its memory may be read
+}
+
+// The marked rows: each cluster looks through every so many rows.
+template <typename T, bool kSampling>
+__global__ void __launch_bounds__(kFiltThreads, kFiltPerSm - 1) marked_kernel(const __grid_constant__ FiltParams p) {
+  extern __shared__ __align__(16) unsigned char s_raw[];
+  FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
+  if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
+  const int place = static_cast<int>(cluster_rank()), cluster = blockIdx.x / kSecondCluster, clusters = gridDim.x / kSecondCluster;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  for (long long first = cluster; first < p.rows; first += static_cast<long long>(clusters) * kFiltThreads) {
+    const long long id = first + static_cast<long long>(threadIdx.x) * clusters;
+    bool marked = false;
+    if (id < p.rows) {
+      const Job job = job_of<kSampling>(p, static_cast<int>(id));
+      marked = job.on && (kSampling ? p.tokens : p.kept)[job.t] == kMark;
+    }
+    // all CTAs of the cluster have looked before one of them overwrites a mark
     __syncthreads();
-    if (job.on) do_row<T, kSampling>(p, job, p.csize, rank, false, s);
-  } else {
-    const int first = cluster * p.csize;
-    const Job own = job_of<kSampling>(p, first + rank);
-    __syncthreads();
-    bool hard = false;
-    if (own.on) hard = !do_row<T, kSampling>(p, own, 1, 0, true, s);
-    __syncthreads();
-    if (threadIdx.x == 0) s.hard = hard;
+    const uint32_t who = __ballot_sync(0xffffffffu, marked);
+    if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = who;
     __syncwarp();
     cluster_sync_all();
-    for (int r = 0; r < p.csize; ++r) {
-      if (ld_cluster_u64(&s.hard, r) == 0) continue;
-      do_row<T, kSampling>(p, job_of<kSampling>(p, first + r), p.csize, rank, false, s);
+#pragma unroll 1
+    for (int w = 0; w < kFiltWarps; ++w) {
+#pragma unroll 1
+      for (uint32_t left = s.marks[w]; left; left &= left - 1) {
+        const int i = w * 32 + __ffs(left) - 1;
+        do_row<T, kSampling>(p, job_of<kSampling>(p, static_cast<int>(first + static_cast<long long>(i) * clusters)),
+                             kSecondCluster, place, false, s);
+      }
     }
   }
   __syncwarp();
-  if (p.csize > 1) cluster_sync_all();     // no CTA goes while its memory may be read
+  cluster_sync_all();                      // no CTA goes while its memory may be read
 }
 
 // ------------------------------------------------------------------ host side
@@ -1521,27 +1579,31 @@ static int check_filter(int dtype, const void* logits, long long ld, int batch, 
 
 template <bool kSampling>
 static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
-  static size_t smem_set[2][kMaxDevices] = {};
+  static size_t smem_set[4][kMaxDevices] = {};
   const int dev = current_device();
   const int sms = dev < 0 ? -1 : device_sm_count(dev);
   if (sms <= 0) return TV_ERR_CUDA;
-  auto* kernel = dtype == TV_DTYPE_F32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
+  const bool f32 = dtype == TV_DTYPE_F32;
+  auto* kernel = f32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
+  auto* second = f32 ? marked_kernel<float, kSampling> : marked_kernel<__nv_bfloat16, kSampling>;
   const long long rows = static_cast<long long>(batch) * p.max_nodes;
   p.rows = static_cast<int>(rows);
-  // a cluster a row where that leaves no SM more than three CTAs, teams where rows that a list
-  // holds as a whole are not all there is
+  p.bits = weight_bits(p.vocab);
+  // a cluster a row where that leaves no SM more than three CTAs
   p.csize = 1;
   while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * 3 && p.vocab > kListCap) p.csize *= 2;
-  p.team = p.csize == 1 && p.vocab > kListCap && rows > 1;
-  if (p.team) p.csize = kTeam;
-  p.local_cap = p.team ? kTeamCap : kLocalCap;
-  const size_t most = sizeof(FiltSmem) + kLocalCap * sizeof(uint64_t);
-  if (!ensure_smem(kernel, most, smem_set[dtype], dev)) return TV_ERR_CUDA;
-  p.bits = weight_bits(p.vocab);
-  const long long clusters = p.team ? (rows + kTeam - 1) / kTeam : rows;
-  const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? p.local_cap * sizeof(uint64_t) : 0);
-  const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(clusters * p.csize)), dim3(kFiltThreads), p.csize,
-                                                  smem, as_stream(stream), p);
+  // one CTA a row: what one pass does not settle goes to the second grid, where there is a place for the mark
+  p.mark = p.csize == 1 && p.vocab > kListCap && (kSampling || p.kept);
+  const size_t alone = sizeof(FiltSmem), shared = alone + kLocalCap * sizeof(uint64_t);
+  if (!ensure_smem(kernel, shared, smem_set[f32], dev)) return TV_ERR_CUDA;
+  cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
+                                            p.csize > 1 ? shared : alone, as_stream(stream), p);
+  if (err != cudaSuccess || !p.mark) return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
+  if (!ensure_smem(second, shared, smem_set[2 + f32], dev)) return TV_ERR_CUDA;
+  const long long most = sms * 3 / kSecondCluster, clusters = rows < most ? rows : most;
+  p.csize = kSecondCluster;
+  err = launch_cluster_smem_pdl(second, dim3(static_cast<unsigned>(clusters * kSecondCluster)), dim3(kFiltThreads), kSecondCluster,
+                                shared, as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
