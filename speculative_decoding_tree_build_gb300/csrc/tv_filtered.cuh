@@ -25,13 +25,10 @@
 // Weights of listed tokens are integers (tv_weight.cuh) and their sums exact: no
 // result depends on the order of the atomics that build lists and histograms.
 //
-// A cluster has a row where rows are few: its CTAs pass over slices, exchange lists
-// and sums through distributed shared memory, and all of them take the same
-// decisions. Where rows are many each has one CTA, which leaves a mark in the
-// row's output where one pass does not do, and a second grid of clusters goes through
-// the marked rows: a flat row takes four times as long as the others and would hold up
-// the end of the call alone on its SM.
-#include <climits>
+// One CTA has a row, or a cluster where rows are few: its CTAs pass over slices,
+// exchange lists and sums through distributed shared memory, and all of them take
+// the same decisions.
+#pragma once
 
 #include <cuda_bf16.h>
 
@@ -46,8 +43,6 @@ constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
 constexpr int kListCap = 4864;             // (four CTAs' shared memory fits an SM)
 constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
-constexpr int kSecondCluster = 4;          // CTAs that share a row of the second grid
-constexpr int kMark = INT_MIN;             // in tokens / kept: for the second grid
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
@@ -80,7 +75,6 @@ struct FiltParams {
   const float* min_p;
   int max_nodes, vocab, bits;
   int csize;                   // CTAs of a cluster
-  bool mark;                   // rows that take more than one pass are for the second grid
   int rows;                    // batch * max_nodes
   int32_t* tokens;
   float* logp;
@@ -98,7 +92,6 @@ struct FiltSmem {
   uint64_t found, before, weight;          // of select
   uint64_t stat[6];                        // of a pass: listed, above, three sums, the largest key
   int bin, bin_count, n_small, n_list, n_hits;
-  uint32_t marks[kFiltWarps];
   int rank, lo_bin, hi_bin;                // of a bracket
   uint64_t list[kListCap];                 // in a cluster the CTA's own part follows
 };
@@ -1031,19 +1024,17 @@ struct RowResult {
   uint64_t cut;            // the last place that is kept
   uint64_t mass;           // the weight of all that is kept, 0: not known
   bool empty;              // nothing above -inf
-  bool hard;               // not found: more than one pass is needed
   bool listed;             // all that is kept is on the list
   int n_list, n_above;     // on the list, and above it
   WeightScale scale;
 };
 
 template <typename T>
-__device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p, float min_p, bool one_pass, FiltSmem& s) {
+__device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p, float min_p, FiltSmem& s) {
   const bool by_k = k > 0 && k < row.vocab, by_p = p < 1.0f, by_m = min_p > 0.0f;
   const int vocab = row.vocab;
   uint64_t lo = kLowest, hi = kHighest;
   const WeightScale none = weight_scale(0.0f, row.bits);
-  const RowResult hard = {kHighest, 0, false, true, false, 0, 0, none};
   // 1. where the list begins (and ends, for a top-k set that no list holds)
   if (vocab > kListCap) {
     const float wanted = static_cast<float>(by_k ? k : kFirstList);
@@ -1062,13 +1053,12 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
                                    : pass<Weigh::kNone>(row, lo, hi, none, s);
   if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)
     view = pass<Weigh::kNone>(row, kLowest, kHighest, none, s);
-  if (!view.any) return RowResult{kHighest, 0, true, false, true, 0, 0, none};
+  if (!view.any) return RowResult{kHighest, 0, true, true, 0, 0, none};
   const WeightScale scale = weight_scale(__fmul_rn(view.top, row.inv_t), row.bits);
   uint64_t cut = kLowest, mass = 0;
   // 3. top-k
   if (by_k) {
     const int with = view.n_above + view.n_in;
-    if (one_pass && (view.n_above >= k || (with < k ? view.lo > kLowest : !view.whole))) return hard;
     if (view.n_above >= k) {
       cut = locate_rank(row, Bounds{view.hi + 1, kHighest, 0, 0, 0}, k, s, view);
     } else if (with < k) {                 // (from the lowest place on fewer than k: all stay)
@@ -1088,8 +1078,6 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
       if (listed && cut >= view.lo) {
         at = select_weight(view, cut, target, sum, scale, row, s);
         mass = s.before + s.weight;
-      } else if (one_pass) {
-        return hard;
       } else {
         view = pass<Weigh::kExact>(row, cut, kHighest, scale, s);
         target = {0, share_of(p, view.total - view.below), 0.0f, 0, 0};
@@ -1120,7 +1108,6 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
         else at = 0;
         target.below = target.off = 0;
       }
-      if (at == 0 && one_pass) return hard;
       if (at == 0) at = locate_weight(row, in, target, from, scale, s, view, mass);
     }
     if (at > cut) cut = at;
@@ -1136,7 +1123,7 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
       mass = 0;
     }
   }
-  return RowResult{cut, mass, false, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, view.n_above, scale};
+  return RowResult{cut, mass, false, view.hi == kHighest && view.whole && cut >= view.lo, view.n_in, view.n_above, scale};
 }
 
 // ------------------------------------------------------------------- endings
@@ -1411,10 +1398,9 @@ __device__ __forceinline__ Job job_of(const FiltParams& p, int id) {
   return job;
 }
 
-// One row by csize CTAs that all call this. False: it takes more than one pass, and
-// nothing is written.
+// One row, by the csize CTAs of a cluster together.
 template <typename T, bool kSampling>
-__device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int csize, int rank, bool one_pass, FiltSmem& s) {
+__device__ __forceinline__ void do_row(const FiltParams& p, const Job& job, int csize, int rank, FiltSmem& s) {
   const size_t t = job.t;
   const float inv_t = job.inv_t, top_p = job.top_p, min_p = job.min_p;
   const int k = job.k;
@@ -1439,7 +1425,7 @@ __device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int 
     __syncwarp();
     row_barrier(csize);
   };
-  RowResult res = {kLowest, 0, false, false, false, 0, 0, weight_scale(0.0f, p.bits)};
+  RowResult res = {kLowest, 0, false, false, 0, 0, weight_scale(0.0f, p.bits)};
   if (greedy) {
     publish(top_row(row, s), 0, 0);
     const uint64_t best = cluster_stat<true>(s, 0, csize);
@@ -1450,11 +1436,10 @@ __device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int 
         p.tokens[t] = res.empty ? 0 : best_index(best);
         if (p.logp) p.logp[t] = res.empty ? -kInf : 0.0f;
       }
-      return true;
+      return;
     }
   } else if (filtered) {
-    res = find_cut(row, k, top_p, min_p, one_pass, s);
-    if (res.hard) return false;
+    res = find_cut(row, k, top_p, min_p, s);
   }
 
   if constexpr (kSampling) {
@@ -1484,14 +1469,14 @@ __device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int 
           p.logp[t] = best ? out : -kInf;
         }
       }
-      return true;
+      return;
     }
     if (res.empty) {
       if (threadIdx.x == 0 && rank == 0) {
         p.tokens[t] = 0;
         if (p.logp) p.logp[t] = -kInf;
       }
-      return true;
+      return;
     }
     const bool weigh = p.logp != nullptr && res.mass == 0;
     const DrawResult own = draw_row(row, noise, res, weigh, res.n_list + res.n_above > p.vocab / 32 && !res.scale.tie, s);
@@ -1512,7 +1497,6 @@ __device__ __forceinline__ bool do_row(const FiltParams& p, const Job& job, int 
     const int kept = static_cast<int>(cluster_stat<false>(s, 0, csize));
     if (p.kept && threadIdx.x == 0 && rank == 0) p.kept[t] = kept;
   }
-  return true;
 }
 
 template <typename T, bool kSampling>
@@ -1526,51 +1510,14 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
   const Job job = job_of<kSampling>(p, blockIdx.x / p.csize);
   if (!job.on) return;                     // (the same in all CTAs of a cluster)
   __syncthreads();
-  if (!do_row<T, kSampling>(p, job, p.csize, place, p.mark, s) && threadIdx.x == 0)
-    (kSampling ? p.tokens : p.kept)[job.t] = kMark;
+  do_row<T, kSampling>(p, job, p.csize, place, s);
   __syncwarp();
   if (p.csize > 1) cluster_sync_all();     // no CTA goes while its memory may be read
 }
 
-// The marked rows: each cluster looks through every so many rows.
-template <typename T, bool kSampling>
-__global__ void __launch_bounds__(kFiltThreads, kFiltPerSm - 1) marked_kernel(const __grid_constant__ FiltParams p) {
-  extern __shared__ __align__(16) unsigned char s_raw[];
-  FiltSmem& s = *reinterpret_cast<FiltSmem*>(s_raw);
-  if (threadIdx.x < kWeightTable) fill_weight_table(s.table, threadIdx.x);
-  const int place = static_cast<int>(cluster_rank()), cluster = blockIdx.x / kSecondCluster, clusters = gridDim.x / kSecondCluster;
-  grid_dependency_wait();
-  grid_launch_dependents();
-  for (long long first = cluster; first < p.rows; first += static_cast<long long>(clusters) * kFiltThreads) {
-    const long long id = first + static_cast<long long>(threadIdx.x) * clusters;
-    bool marked = false;
-    if (id < p.rows) {
-      const Job job = job_of<kSampling>(p, static_cast<int>(id));
-      marked = job.on && (kSampling ? p.tokens : p.kept)[job.t] == kMark;
-    }
-    // all CTAs of the cluster have looked before one of them overwrites a mark
-    __syncthreads();
-    const uint32_t who = __ballot_sync(0xffffffffu, marked);
-    if ((threadIdx.x & 31) == 0) s.marks[threadIdx.x >> 5] = who;
-    __syncwarp();
-    cluster_sync_all();
-#pragma unroll 1
-    for (int w = 0; w < kFiltWarps; ++w) {
-#pragma unroll 1
-      for (uint32_t left = s.marks[w]; left; left &= left - 1) {
-        const int i = w * 32 + __ffs(left) - 1;
-        do_row<T, kSampling>(p, job_of<kSampling>(p, static_cast<int>(first + static_cast<long long>(i) * clusters)),
-                             kSecondCluster, place, false, s);
-      }
-    }
-  }
-  __syncwarp();
-  cluster_sync_all();                      // no CTA goes while its memory may be read
-}
-
 // ------------------------------------------------------------------ host side
 
-static int check_filter(int dtype, const void* logits, long long ld, int batch, int max_nodes, int vocab) {
+inline int check_filter(int dtype, const void* logits, long long ld, int batch, int max_nodes, int vocab) {
   if (dtype != TV_DTYPE_BF16 && dtype != TV_DTYPE_F32) return TV_ERR_BAD_GEOMETRY;
   if (batch < 0 || batch > 65535 || max_nodes < 1 || max_nodes > TV_MAX_NODES || vocab < 1 || vocab > (1 << 30) || ld < vocab)
     return TV_ERR_BAD_SIZE;
@@ -1578,71 +1525,24 @@ static int check_filter(int dtype, const void* logits, long long ld, int batch, 
 }
 
 template <bool kSampling>
-static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
-  static size_t smem_set[4][kMaxDevices] = {};
+inline int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
+  static size_t smem_set[2][kMaxDevices] = {};
   const int dev = current_device();
   const int sms = dev < 0 ? -1 : device_sm_count(dev);
   if (sms <= 0) return TV_ERR_CUDA;
   const bool f32 = dtype == TV_DTYPE_F32;
   auto* kernel = f32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
-  auto* second = f32 ? marked_kernel<float, kSampling> : marked_kernel<__nv_bfloat16, kSampling>;
   const long long rows = static_cast<long long>(batch) * p.max_nodes;
   p.rows = static_cast<int>(rows);
   p.bits = weight_bits(p.vocab);
   // a cluster a row where that leaves no SM more than three CTAs
   p.csize = 1;
   while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * 3 && p.vocab > kListCap) p.csize *= 2;
-  // one CTA a row: what one pass does not settle goes to the second grid, where there is a place for the mark
-  p.mark = p.csize == 1 && p.vocab > kListCap && (kSampling || p.kept);
-  const size_t alone = sizeof(FiltSmem), shared = alone + kLocalCap * sizeof(uint64_t);
-  if (!ensure_smem(kernel, shared, smem_set[f32], dev)) return TV_ERR_CUDA;
-  cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
-                                            p.csize > 1 ? shared : alone, as_stream(stream), p);
-  if (err != cudaSuccess || !p.mark) return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
-  if (!ensure_smem(second, shared, smem_set[2 + f32], dev)) return TV_ERR_CUDA;
-  const long long most = sms * 3 / kSecondCluster, clusters = rows < most ? rows : most;
-  p.csize = kSecondCluster;
-  err = launch_cluster_smem_pdl(second, dim3(static_cast<unsigned>(clusters * kSecondCluster)), dim3(kFiltThreads), kSecondCluster,
-                                shared, as_stream(stream), p);
+  const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? kLocalCap * sizeof(uint64_t) : 0);
+  if (!ensure_smem(kernel, smem, smem_set[f32], dev)) return TV_ERR_CUDA;
+  const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
+                                                  smem, as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
 }  // namespace tv
-
-extern "C" int tv_sample_filtered(int32_t dtype, const void* logits, int64_t logits_ld, const float* gumbel,
-                                  int64_t gumbel_ld, const int32_t* cu_nodes, const float* temperature,
-                                  const int32_t* top_k, const float* top_p, const float* min_p, int32_t batch,
-                                  int32_t max_nodes, int32_t vocab, int32_t* tokens, float* logp, int32_t* status,
-                                  void* stream) {
-  int rc = tv::check_filter(dtype, logits, logits_ld, batch, max_nodes, vocab);
-  if (rc != TV_OK) return rc;
-  if (gumbel && gumbel_ld < vocab) return TV_ERR_BAD_SIZE;
-  if (batch == 0) return TV_OK;
-  if (!logits || !cu_nodes || !temperature || !tokens || !status) return TV_ERR_NULL_POINTER;
-  const int per = dtype == TV_DTYPE_F32 ? 4 : 8;
-  if (!tv::aligned(logits, 16) || logits_ld % per || (gumbel && (!tv::aligned(gumbel, 16) || gumbel_ld % 4)))
-    return TV_ERR_MISALIGNED;
-  tv::FiltParams p = {};
-  p.logits = logits; p.logits_ld = logits_ld; p.gumbel = gumbel; p.gumbel_ld = gumbel_ld;
-  p.cu_nodes = cu_nodes; p.temperature = temperature; p.top_k = top_k; p.top_p = top_p; p.min_p = min_p;
-  p.max_nodes = max_nodes; p.vocab = vocab; p.tokens = tokens; p.logp = logp; p.status = status;
-  return tv::launch_filtered<true>(dtype, p, batch, stream);
-}
-
-extern "C" int tv_filter_logits(int32_t dtype, const void* logits, int64_t logits_ld, const int32_t* cu_nodes,
-                                const float* temperature, const int32_t* top_k, const float* top_p,
-                                const float* min_p, int32_t batch, int32_t max_nodes, int32_t vocab, void* out,
-                                int64_t out_ld, int32_t* kept, int32_t* status, void* stream) {
-  int rc = tv::check_filter(dtype, logits, logits_ld, batch, max_nodes, vocab);
-  if (rc != TV_OK) return rc;
-  if (out_ld < vocab) return TV_ERR_BAD_SIZE;
-  if (batch == 0) return TV_OK;
-  if (!logits || !cu_nodes || !temperature || !out || !status) return TV_ERR_NULL_POINTER;
-  const int per = dtype == TV_DTYPE_F32 ? 4 : 8;
-  if (!tv::aligned(logits, 16) || logits_ld % per || !tv::aligned(out, 16) || out_ld % per) return TV_ERR_MISALIGNED;
-  tv::FiltParams p = {};
-  p.logits = logits; p.logits_ld = logits_ld;
-  p.cu_nodes = cu_nodes; p.temperature = temperature; p.top_k = top_k; p.top_p = top_p; p.min_p = min_p;
-  p.max_nodes = max_nodes; p.vocab = vocab; p.out = out; p.out_ld = out_ld; p.kept = kept; p.status = status;
-  return tv::launch_filtered<false>(dtype, p, batch, stream);
-}
