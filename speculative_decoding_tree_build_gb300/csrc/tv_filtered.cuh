@@ -1517,7 +1517,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
 
 // ------------------------------------------------------------------ host side
 
-inline int check_filter(int dtype, const void* logits, long long ld, int batch, int max_nodes, int vocab) {
+static int check_filter(int dtype, const void* logits, long long ld, int batch, int max_nodes, int vocab) {
   if (dtype != TV_DTYPE_BF16 && dtype != TV_DTYPE_F32) return TV_ERR_BAD_GEOMETRY;
   if (batch < 0 || batch > 65535 || max_nodes < 1 || max_nodes > TV_MAX_NODES || vocab < 1 || vocab > (1 << 30) || ld < vocab)
     return TV_ERR_BAD_SIZE;
@@ -1525,7 +1525,7 @@ inline int check_filter(int dtype, const void* logits, long long ld, int batch, 
 }
 
 template <bool kSampling>
-inline int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
+static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
   static size_t smem_set[2][kMaxDevices] = {};
   const int dev = current_device();
   const int sms = dev < 0 ? -1 : device_sm_count(dev);
