@@ -41,8 +41,8 @@ constexpr int kFiltThreads = 256;
 constexpr int kFiltWarps = kFiltThreads / 32;
 constexpr int kFiltPerSm = 4;              // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
-constexpr int kListCap = 4864;             // (four CTAs' shared memory fits an SM)
-constexpr int kLocalCap = 2048;            // a CTA's own part of the list in a cluster
+constexpr int kListCap = 3840;             // (with kLocalCap, four CTAs' shared memory fits an SM)
+constexpr int kLocalCap = 1024;            // a CTA's own part of the list in a cluster
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
@@ -75,7 +75,8 @@ struct FiltParams {
   const float* min_p;
   int max_nodes, vocab, bits;
   int csize;                   // CTAs of a cluster
-  int rows;                    // batch * max_nodes
+  int rows, batch;             // rows = batch * max_nodes
+  bool reorder;
   int32_t* tokens;
   float* logp;
   void* out;
@@ -703,7 +704,7 @@ __device__ __noinline__ void sample_bracket(const Row<T>& row, const Bounds& in,
                                             int pieces, float sigmas, float most, const WeightScale& scale, FiltSmem& s,
                                             uint64_t& lo, uint64_t& hi) {
   constexpr int kLen = Vec<T>::kLen, kVecs = kSampleEach / kLen, kLines = kSampleSize / kLen / 8;
-  constexpr int kSorts = 2 * kBins, kEach = kSorts / kFiltThreads;
+  constexpr int kSorts = kWeights ? 2 * kBins : kBins, kEach = kSorts / kFiltThreads;
   uint32_t* counts = s.bins[0];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   lo = in.lo;
@@ -1499,6 +1500,34 @@ __device__ __forceinline__ void do_row(const FiltParams& p, const Job& job, int 
   }
 }
 
+// The row of a CTA (of a cluster). Where there are more rows than fit at once, the
+// requests with top-p alone come first: their flat rows take four times as long as
+// others, and one that started last would be waited for alone.
+__device__ __forceinline__ int row_of(const FiltParams& p, FiltSmem& s) {
+  const int id = blockIdx.x / p.csize;
+  if (!p.reorder) return id;
+  const int place = id / p.max_nodes, b = threadIdx.x, lane = b & 31, warp = b >> 5;
+  bool slow = false;
+  if (b < p.batch) {
+    const int k = p.top_k ? p.top_k[b] : 0;
+    slow = p.top_p && p.top_p[b] < 1.0f && (k == 0 || k >= p.vocab);
+  }
+  const uint32_t who = __ballot_sync(0xffffffffu, slow);
+  if (lane == 0) s.red[0][warp] = who;
+  __syncthreads();
+  int all = 0, before = 0;
+#pragma unroll
+  for (int w = 0; w < kFiltWarps; ++w) {
+    const int n = __popc(static_cast<uint32_t>(s.red[0][w]));
+    if (w < warp) before += n;
+    all += n;
+  }
+  before += __popc(who & ((1u << lane) - 1));              // slow requests in front of b
+  if (b < p.batch && place == (slow ? before : all + (b - before))) s.bin = b;
+  __syncthreads();
+  return s.bin * p.max_nodes + (id - place * p.max_nodes);
+}
+
 template <typename T, bool kSampling>
 __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(const __grid_constant__ FiltParams p) {
   extern __shared__ __align__(16) unsigned char s_raw[];
@@ -1507,7 +1536,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
   grid_dependency_wait();
   grid_launch_dependents();
   const int place = p.csize > 1 ? static_cast<int>(cluster_rank()) : 0;
-  const Job job = job_of<kSampling>(p, blockIdx.x / p.csize);
+  const Job job = job_of<kSampling>(p, row_of(p, s));
   if (!job.on) return;                     // (the same in all CTAs of a cluster)
   __syncthreads();
   do_row<T, kSampling>(p, job, p.csize, place, s);
@@ -1535,9 +1564,11 @@ static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
   const long long rows = static_cast<long long>(batch) * p.max_nodes;
   p.rows = static_cast<int>(rows);
   p.bits = weight_bits(p.vocab);
-  // a cluster a row where that leaves no SM more than three CTAs
+  p.batch = batch;
+  // a cluster a row where all of them are resident at once
   p.csize = 1;
-  while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * 3 && p.vocab > kListCap) p.csize *= 2;
+  while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * kFiltPerSm && p.vocab > kListCap) p.csize *= 2;
+  p.reorder = p.top_p && batch > 1 && batch <= kFiltThreads && rows * p.csize > sms * kFiltPerSm;
   const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? kLocalCap * sizeof(uint64_t) : 0);
   if (!ensure_smem(kernel, smem, smem_set[f32], dev)) return TV_ERR_CUDA;
   const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
