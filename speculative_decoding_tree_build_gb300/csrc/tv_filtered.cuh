@@ -35,23 +35,29 @@
 #include "tv_cluster.cuh"
 #include "tv_weight.cuh"
 
+// A unit names its space and its CTA's size before it includes this: 256 threads
+// (four CTAs an SM) hide a sampled row's many short steps best, 512 (two) keep the rows
+// that are in flight small enough for L2, where the masks' second look finds them
+// (4112 rows of 151936 sampled: 595 us, with 512 threads 758; 1345 rows masked in bf16:
+// 380 us, with 256 threads 529).
 namespace tv {
+namespace TV_FILT_SPACE {
 
-constexpr int kFiltThreads = 256;
+constexpr int kFiltThreads = TV_FILT_THREADS;
 constexpr int kFiltWarps = kFiltThreads / 32;
-constexpr int kFiltPerSm = 4;              // CTAs an SM
+constexpr int kFiltPerSm = 1024 / kFiltThreads;    // CTAs an SM
 constexpr int kFiltMaxCluster = 8;
-constexpr int kListCap = 3840;             // (with kLocalCap, four CTAs' shared memory fits an SM)
-constexpr int kLocalCap = 1024;            // a CTA's own part of the list in a cluster
+constexpr int kListCap = kFiltThreads == 256 ? 3840 : 4864;   // (with kLocalCap, what shared memory holds)
+constexpr int kLocalCap = 4 * kFiltThreads;        // a CTA's own part of the list in a cluster
 constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
 constexpr int kFirstList = 256;            // tokens that the first list is made for without top-k
-constexpr int kBins = 1024;
+constexpr int kBins = 4 * kFiltThreads;
 constexpr int kHits = 4 * kBins;           // noted vectors of a pass (where the bins lie otherwise)
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
-constexpr int kFiltUnroll = 4;             // 16-byte loads in flight a thread
+constexpr int kFiltUnroll = 2;             // 16-byte loads in flight a thread
 constexpr float kInf = __builtin_huge_valf();
 
 // Places: (order key, ~index). -inf has no place: it is never kept.
@@ -1301,7 +1307,7 @@ struct MaskBody {
       kept += keep;
     }
     if constexpr (kLen == 1) store_one(out + i0, y[0]);
-    else *reinterpret_cast<uint4*>(out + i0) = Vec<T>::pack(y);
+    else __stcs(reinterpret_cast<uint4*>(out + i0), Vec<T>::pack(y));      // (the logits stay in L2 for other rows)
   }
 };
 
@@ -1576,4 +1582,5 @@ static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
 
+}  // namespace TV_FILT_SPACE
 }  // namespace tv
