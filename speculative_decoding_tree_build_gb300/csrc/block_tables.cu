@@ -16,9 +16,11 @@
 
 namespace tv {
 
-constexpr int kTableThreads = 1024;
+constexpr int kTableThreads = 512;
 constexpr int kTableMaxBatch = 4096;
 constexpr int kTablePer = kTableMaxBatch / kTableThreads;   // requests a thread looks at
+constexpr int kTableCluster = 8;
+constexpr int kTableAhead = 4;                              // moves of a thread in flight
 
 struct TableParams {
   const int32_t* want_len;
@@ -75,7 +77,7 @@ __device__ __forceinline__ int last_at_most(const int32_t* sums, int n, int p) {
 }
 
 // A cluster makes the call: every CTA works the sums out for itself (4096
-// requests are 4 a thread), then all moves are spread over the cluster's
+// requests are 8 a thread), then all moves are spread over the cluster's
 // threads, each looking its request up in the sums. Latency binds it: a round
 // trip for the requests, one for the ids, a barrier before anything is
 // overwritten, and one between pushes and pops where both occur.
@@ -119,7 +121,15 @@ __global__ void __launch_bounds__(kTableThreads, 1) block_tables_kernel(const __
                         rel[u] > p.max_blocks
                     ? TV_ST_BAD_SIZE : 0;
   }
-  TableSums total, at;
+  TableSums total = {0, 0, 0}, at;
+  // where the i-th id that comes back stands, and whose it is
+  auto back = [&](int i, int& b) -> const int32_t* {
+    const bool is_rel = i < total.rel;
+    const int q = is_rel ? i : i - static_cast<int>(total.rel);
+    b = last_at_most(is_rel ? s_rel : s_drop, p.batch, q);
+    const size_t row = static_cast<size_t>(b) * p.max_blocks;
+    return is_rel ? p.released + row + (q - s_rel[b]) : p.table + row + s_need[b] + (q - s_drop[b]);
+  };
   bool fail, checked = false;
   while (true) {
     TableSums mine = {0, 0, 0};
@@ -147,14 +157,18 @@ __global__ void __launch_bounds__(kTableThreads, 1) block_tables_kernel(const __
     if (checked || pushes == 0) break;
     // every id that comes back has to be one of the pool's
     checked = true;
-    for (int i = first; i < pushes; i += step) {
-      const bool is_rel = i < total.rel;
-      const int q = is_rel ? i : i - static_cast<int>(total.rel);
-      const int b = last_at_most(is_rel ? s_rel : s_drop, p.batch, q);
-      const size_t row = static_cast<size_t>(b) * p.max_blocks;
-      const int id = is_rel ? p.released[row + (q - s_rel[b])] : p.table[row + s_need[b] + (q - s_drop[b])];
-      if (id < 0 || id >= p.num_blocks) {
-        atomicOr(reinterpret_cast<uint32_t*>(s_faulty) + b / 32, 1u << (b % 32));
+    for (long long i0 = first; i0 < pushes; i0 += kTableAhead * step) {
+      int b[kTableAhead], id[kTableAhead];
+#pragma unroll
+      for (int u = 0; u < kTableAhead; ++u) {
+        const long long i = i0 + u * step;
+        id[u] = 0;
+        if (i < pushes) id[u] = *back(static_cast<int>(i), b[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < kTableAhead; ++u) {
+        if (id[u] >= 0 && id[u] < p.num_blocks) continue;
+        atomicOr(reinterpret_cast<uint32_t*>(s_faulty) + b[u] / 32, 1u << (b[u] % 32));
         s_any = 1;
       }
     }
@@ -179,28 +193,50 @@ __global__ void __launch_bounds__(kTableThreads, 1) block_tables_kernel(const __
   row_barrier(p.csize);                   // every CTA has read what is overwritten from here on
   const int pushes = fail ? 0 : static_cast<int>(total.rel + total.drop);
   const int top = count + pushes;
-  for (int i = first; i < pushes; i += step) {
-    const bool is_rel = i < total.rel;
-    const int q = is_rel ? i : i - static_cast<int>(total.rel);
-    const int b = last_at_most(is_rel ? s_rel : s_drop, p.batch, q);
-    const size_t row = static_cast<size_t>(b) * p.max_blocks;
-    if (is_rel) {
-      p.free_blocks[count + static_cast<int>(total.rel) - 1 - q] = p.released[row + (q - s_rel[b])];
-    } else {
-      int32_t* entry = p.table + row + s_need[b] + (q - s_drop[b]);
-      p.free_blocks[top - 1 - q] = *entry;
-      *entry = -1;
+  for (long long i0 = first; i0 < pushes; i0 += kTableAhead * step) {
+    const int32_t* from[kTableAhead];
+    int id[kTableAhead];
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u) {
+      const long long i = i0 + u * step;
+      from[u] = nullptr;
+      if (i >= pushes) continue;
+      int b;
+      from[u] = back(static_cast<int>(i), b);
+      id[u] = *from[u];
+    }
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u) {
+      if (!from[u]) continue;
+      const int i = static_cast<int>(i0) + u * step;
+      if (i < total.rel) {
+        p.free_blocks[count + static_cast<int>(total.rel) - 1 - i] = id[u];
+      } else {
+        p.free_blocks[top - 1 - (i - static_cast<int>(total.rel))] = id[u];
+        *const_cast<int32_t*>(from[u]) = -1;
+      }
     }
   }
   // First come, first served: a request whose blocks end past the list gets
   // none, nor does any growing one behind it.
   const int pops = fail ? 0 : static_cast<int>(min(total.add, static_cast<long long>(top)));
   if (pushes > 0 && pops > 0) row_barrier(p.csize);
-  for (int i = first; i < pops; i += step) {
-    const int b = last_at_most(s_add, p.batch, i);
-    const int held_b = s_held[b];
-    if (s_add[b] > top - (s_need[b] - held_b)) continue;
-    p.table[static_cast<size_t>(b) * p.max_blocks + held_b + (i - s_add[b])] = __ldcg(&p.free_blocks[top - 1 - i]);
+  for (long long i0 = first; i0 < pops; i0 += kTableAhead * step) {
+    int id[kTableAhead];
+    int32_t* to[kTableAhead];
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u) {
+      to[u] = nullptr;
+      if (i0 + u * step >= pops) continue;
+      const int i = static_cast<int>(i0) + u * step;
+      id[u] = __ldcg(&p.free_blocks[top - 1 - i]);
+      const int b = last_at_most(s_add, p.batch, i);
+      const int held_b = s_held[b];
+      if (s_add[b] <= top - (s_need[b] - held_b)) to[u] = p.table + static_cast<size_t>(b) * p.max_blocks + held_b + (i - s_add[b]);
+    }
+#pragma unroll
+    for (int u = 0; u < kTableAhead; ++u)
+      if (to[u]) *to[u] = id[u];
   }
   if (rank != 0) return;
   long long sum = at.add;
@@ -226,7 +262,7 @@ __global__ void __launch_bounds__(kTableThreads, 1) block_tables_kernel(const __
 // --------------------------------------------------------------------- slots
 
 constexpr int kSlotThreads = 512;
-constexpr int kSlotRows = 4;               // rows a thread at most
+constexpr int kSlotRows = 4;               // rows a thread in large calls
 
 struct SlotParams {
   const int32_t* cu_rows;
@@ -236,12 +272,16 @@ struct SlotParams {
   long long* slots;
   int32_t* status;
   int batch, rows, max_blocks, num_blocks, cta_rows;
+  bool wide;               // slots lie on 16 bytes
 };
 
-// A CTA has a contiguous range of rows. It takes the running maximum of all
-// offsets (4 a thread for 2048 requests), in which a row finds its request and
-// offsets that run backwards show; the requests at the two ends of its range
-// are checked in full, the ones between are checked by their rows.
+// A CTA has a contiguous range of rows, kRows of them side by side a thread (they
+// lie in one or two pages: one search, one or two table entries, one wide store). It
+// takes the running maximum of all offsets (4 a thread for 2048 requests), in
+// which a row finds its request and offsets that run backwards show; the requests at
+// the two ends of its range are checked in full, the ones between are checked by their
+// rows.
+template <int kRows>
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_constant__ SlotParams p) {
   extern __shared__ int32_t s_off[];       // running maximum of the offsets, then a request's fault
   int32_t* s_bad = s_off + p.batch;
@@ -288,18 +328,25 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   }
   __syncthreads();
 
-  int req[kSlotRows], slot[kSlotRows], id[kSlotRows];
+  int req[kRows], slot[kRows], id[kRows];
+  const int mine = t0 + static_cast<int>(threadIdx.x) * kRows;
+  int b = 0, c0 = 0, c1 = INT_MIN, start = 0;            // the request of the row before
 #pragma unroll
-  for (int u = 0; u < kSlotRows; ++u) {
-    const int t = t0 + u * kSlotThreads + threadIdx.x;
+  for (int u = 0; u < kRows; ++u) {
+    const int t = mine + u;
     req[u] = -1;
     if (t >= t1 || p.batch == 0 || s_off[0] > t) continue;
-    const int b = last_at_most(s_off, p.batch, t);
-    const int c0 = p.cu_rows[b];
-    if (s_bad[b] != 0 || t < c0 || t >= p.cu_rows[b + 1]) continue;
+    if (u == 0 || t >= c1 || t < c0) {
+      b = last_at_most(s_off, p.batch, t);
+      c0 = p.cu_rows[b];
+      c1 = p.cu_rows[b + 1];
+      start = p.start_len[b];
+    }
+    if (s_bad[b] != 0 || t < c0 || t >= c1) continue;
     req[u] = b;
-    slot[u] = p.start_len[b] + (t - c0);
-    id[u] = p.table[static_cast<size_t>(b) * p.max_blocks + slot[u] / TV_BLOCK_SIZE];
+    slot[u] = start + (t - c0);
+    if (u > 0 && req[u - 1] == b && slot[u] % TV_BLOCK_SIZE != 0) id[u] = id[u - 1];
+    else id[u] = p.table[static_cast<size_t>(b) * p.max_blocks + slot[u] / TV_BLOCK_SIZE];
   }
   // the two requests that may have rows elsewhere
   int fault[2] = {-1, -1};
@@ -319,22 +366,27 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   }
   __syncthreads();                         // s_bad is read above and written below
 #pragma unroll
-  for (int u = 0; u < kSlotRows; ++u)
+  for (int u = 0; u < kRows; ++u)
     if (req[u] >= 0 && (id[u] < 0 || id[u] >= p.num_blocks)) s_bad[req[u]] = TV_ST_BAD_BLOCK;
 #pragma unroll
   for (int e = 0; e < 2; ++e)
     if (fault[e] >= 0) s_bad[fault[e]] = TV_ST_BAD_BLOCK;
   __syncthreads();
+  long long out[kRows];
 #pragma unroll
-  for (int u = 0; u < kSlotRows; ++u) {
-    const int t = t0 + u * kSlotThreads + threadIdx.x;
-    if (t >= t1) continue;
-    long long out = -1;
-    if (req[u] >= 0) {
-      if (s_bad[req[u]] == 0) out = static_cast<long long>(id[u]) * TV_BLOCK_SIZE + slot[u] % TV_BLOCK_SIZE;
-      else if (t == max(t0, p.cu_rows[req[u]])) atomicOr(&p.status[req[u]], TV_ST_BAD_BLOCK);
-    }
-    p.slots[t] = out;
+  for (int u = 0; u < kRows; ++u) {
+    out[u] = -1;
+    if (mine + u >= t1 || req[u] < 0) continue;
+    if (s_bad[req[u]] == 0) out[u] = static_cast<long long>(id[u]) * TV_BLOCK_SIZE + slot[u] % TV_BLOCK_SIZE;
+    else if (mine + u == max(t0, p.cu_rows[req[u]])) atomicOr(&p.status[req[u]], TV_ST_BAD_BLOCK);
+  }
+  if (kRows % 2 == 0 && p.wide && mine + kRows <= t1) {
+#pragma unroll
+    for (int u = 0; u < kRows; u += 2) *reinterpret_cast<longlong2*>(p.slots + mine + u) = make_longlong2(out[u], out[u + 1 < kRows ? u + 1 : u]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+      if (mine + u < t1) p.slots[mine + u] = out[u];
   }
 }
 
@@ -358,7 +410,7 @@ extern "C" int tv_block_tables(int32_t batch, const int32_t* want_len, int32_t* 
   p.free_blocks = free_blocks; p.free_count = free_count;
   p.released = released; p.released_count = released_count; p.status = status;
   p.batch = batch; p.max_blocks = max_blocks_per_req; p.num_blocks = num_blocks;
-  p.csize = 8;
+  p.csize = tv::kTableCluster;
   const cudaError_t err = tv::launch_cluster_smem_pdl(tv::block_tables_kernel, dim3(p.csize), dim3(tv::kTableThreads),
                                                       p.csize, smem, tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
@@ -382,12 +434,13 @@ extern "C" int tv_slot_map(int32_t batch, int32_t rows, const int32_t* cu_rows,
   p.slots = reinterpret_cast<long long*>(slots); p.status = status;
   p.batch = batch; p.rows = rows; p.max_blocks = max_blocks_per_req; p.num_blocks = num_blocks;
   // a row a thread while that leaves SMs with less than two CTAs
-  const long long wave = static_cast<long long>(sms) * tv::kSlotThreads * 2;
-  const long long each = (rows + wave - 1) / wave;
-  p.cta_rows = tv::kSlotThreads * static_cast<int>(each < tv::kSlotRows ? each : tv::kSlotRows);
+  const bool large = rows > static_cast<long long>(sms) * tv::kSlotThreads * 2;
+  p.cta_rows = tv::kSlotThreads * (large ? tv::kSlotRows : 1);
+  p.wide = tv::aligned(slots, 16);
+  auto* kernel = large ? tv::slot_map_kernel<tv::kSlotRows> : tv::slot_map_kernel<1>;
   const size_t smem = static_cast<size_t>(batch) * 2 * sizeof(int32_t);
   const int ctas = static_cast<int>((rows + static_cast<long long>(p.cta_rows) - 1) / p.cta_rows);
-  const cudaError_t err = tv::launch_pdl(tv::slot_map_kernel, dim3(ctas), dim3(tv::kSlotThreads), smem,
+  const cudaError_t err = tv::launch_pdl(kernel, dim3(ctas), dim3(tv::kSlotThreads), smem,
                                          tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
