@@ -53,7 +53,8 @@ constexpr int kSampleEach = 8;             // sampled tokens a thread
 constexpr int kSampleSize = kSampleEach * kFiltThreads;
 constexpr int kSamplePieces = 4;           // samples that a second look takes
 constexpr int kFirstList = 256;            // tokens that the first list is made for without top-k
-constexpr int kBins = 4 * kFiltThreads;
+constexpr int kBinBits = kFiltThreads == 512 ? 11 : kFiltThreads == 256 ? 10 : 9, kBins = 1 << kBinBits;
+static_assert(kBins == 4 * kFiltThreads, "a thread clears 16 bytes of them and sums four");
 constexpr int kHits = 4 * kBins;           // noted vectors of a pass (where the bins lie otherwise)
 constexpr int kSmall = 32;                 // tokens that a warp ranks
 constexpr int kSampledTurns = 4, kTurns = kSampledTurns + 64;
@@ -563,7 +564,7 @@ __device__ __noinline__ uint64_t select(int n, uint64_t a, uint64_t b, Target& t
   uint64_t base = 0;
   for (bool first = true;; first = false) {
     // bins of 2^sh places, counted from b down
-    const int sh = b > a ? max(0, 54 - __clzll(b - a)) : 0;
+    const int sh = b > a ? max(0, 64 - kBinBits - __clzll(b - a)) : 0;
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < (kWeights ? 4 : 1); ++u) reinterpret_cast<uint4*>(s.bins[u])[threadIdx.x] = make_uint4(0u, 0u, 0u, 0u);
