@@ -758,7 +758,8 @@ int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32_t batch, c
  *  free_blocks    int32 [num_blocks] in/out, distinct ids in [0, num_blocks)
  *  free_count     int32 [1] in/out
  *  released       int32 [batch][max_blocks_per_req] and
- *  released_count int32 [batch] in/out, or both NULL
+ *  released_count int32 [batch] in/out (0 before tv_kv_commit's first call, which
+ *                 leaves a flagged request's count as it is), or both NULL
  *  status         in/out: requests with non-zero status are skipped;
  *                 TV_ST_NO_BLOCKS, TV_ST_BAD_SIZE (want_len < 0 or past the table,
  *                 n_blocks or released_count outside [0, max_blocks_per_req]) and
@@ -768,7 +769,8 @@ int tv_decode_attention(const tv_geom* geom, int32_t kv_format, int32_t batch, c
  *                 list could not hold all that comes back (some of it is there
  *                 already) or free_count is outside [0, num_blocks], every request
  *                 gets TV_ST_BAD_SIZE and nothing changes.
- * tv_tree_build overwrites status, so it comes before this call in a step.
+ * tv_tree_build overwrites status, so it comes before this call in a step. Calls on
+ * one list follow one another: two that overlap on the GPU race on it.
  */
 int tv_block_tables(int32_t batch, const int32_t* want_len, int32_t* block_table,
                     int32_t* n_blocks, int32_t max_blocks_per_req, int32_t num_blocks,
@@ -842,9 +844,11 @@ int tv_kv_rows_read(const tv_geom* geom, int32_t rows, const int64_t* slots, con
  * logp = s_token - s_max - ln(sum of kept w). T == 0 keeps the first argmax of the
  * logits alone (logp 0). Without filters tokens equal tv_sample_tokens' (for
  * finite noise).
- * Which tokens are kept is decided on weights that are within 2^-35 of exp and
- * added exactly, so a decision can differ from an exact evaluation only where a
- * border's sum is within about 2^-35 of it; results do not depend on timing. Where
+ * Which tokens are kept is decided on weights that are within 2^-35 of exp, rounded
+ * to steps of 2^-44 of the largest (2^-(62 - log2 vocab) from 2^18 tokens on) and added
+ * exactly; equal logits have equal weights. So a decision can differ from an exact
+ * evaluation only where a border's sum is that close to its target, and results do
+ * not depend on timing. logp is within a few roundings of float32. Where
  * s_max is infinite or NaN, tokens equal to it weigh 1, others 0. A row without a
  * logit above -inf (a mask that leaves nothing) gets token 0 and logp -inf.
  *

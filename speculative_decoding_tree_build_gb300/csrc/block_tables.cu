@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * p.cta_rows, t1 = min(p.rows, t0 + p.cta_rows);
+  const int t0 = blockIdx.x * p.cta_rows;                  // below rows, whose end may lie at 2^31 - 1
+  const int t1 = static_cast<int>(min(static_cast<long long>(p.rows), static_cast<long long>(t0) + p.cta_rows));
 
   const int per = (p.batch + kSlotThreads - 1) / kSlotThreads;
   const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
@@ -329,13 +330,14 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   __syncthreads();
 
   int req[kRows], slot[kRows], id[kRows];
-  const int mine = t0 + static_cast<int>(threadIdx.x) * kRows;
+  const long long mine = static_cast<long long>(t0) + threadIdx.x * kRows;
   int b = 0, c0 = 0, c1 = INT_MIN, start = 0;            // the request of the row before
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
-    const int t = mine + u;
     req[u] = -1;
-    if (t >= t1 || p.batch == 0 || s_off[0] > t) continue;
+    if (mine + u >= t1) continue;
+    const int t = static_cast<int>(mine) + u;
+    if (p.batch == 0 || s_off[0] > t) continue;
     if (u == 0 || t >= c1 || t < c0) {
       b = last_at_most(s_off, p.batch, t);
       c0 = p.cu_rows[b];
