@@ -791,7 +791,8 @@ int tv_block_tables(int32_t batch, const int32_t* want_len, int32_t* block_table
  *                 end before they begin, or have rows and begin before an earlier
  *                 offset or end behind `rows`, are flagged
  *  start_len, block_table, n_blocks, max_blocks_per_req, num_blocks
- *                 as for tv_kv_quant_append; the blocks of all slots must be held
+ *                 as for tv_kv_quant_append (max_blocks_per_req <= 2^27); the blocks
+ *                 of all slots must be held
  *  slots          int64 [rows] out
  *  status         in/out: requests with non-zero status get -1; TV_ST_BAD_SIZE and
  *                 TV_ST_BAD_BLOCK are OR-ed in (all of the request's rows get -1)

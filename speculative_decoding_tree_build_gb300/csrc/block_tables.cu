@@ -330,12 +330,12 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   __syncthreads();
 
   int req[kRows], slot[kRows], id[kRows];
-  const long long mine = static_cast<long long>(t0) + threadIdx.x * kRows;
+  const uint32_t mine = t0 + threadIdx.x * kRows, end = t1;      // (may pass 2^31 - 1)
   int b = 0, c0 = 0, c1 = INT_MIN, start = 0;            // the request of the row before
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     req[u] = -1;
-    if (mine + u >= t1) continue;
+    if (mine + u >= end) continue;
     const int t = static_cast<int>(mine) + u;
     if (p.batch == 0 || s_off[0] > t) continue;
     if (u == 0 || t >= c1 || t < c0) {
@@ -378,17 +378,17 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
 #pragma unroll
   for (int u = 0; u < kRows; ++u) {
     out[u] = -1;
-    if (mine + u >= t1 || req[u] < 0) continue;
+    if (mine + u >= end || req[u] < 0) continue;
     if (s_bad[req[u]] == 0) out[u] = static_cast<long long>(id[u]) * TV_BLOCK_SIZE + slot[u] % TV_BLOCK_SIZE;
-    else if (mine + u == max(t0, p.cu_rows[req[u]])) atomicOr(&p.status[req[u]], TV_ST_BAD_BLOCK);
+    else if (mine + u == static_cast<uint32_t>(max(t0, p.cu_rows[req[u]]))) atomicOr(&p.status[req[u]], TV_ST_BAD_BLOCK);
   }
-  if (kRows % 2 == 0 && p.wide && mine + kRows <= t1) {
+  if (kRows % 2 == 0 && p.wide && mine + kRows <= end) {
 #pragma unroll
     for (int u = 0; u < kRows; u += 2) *reinterpret_cast<longlong2*>(p.slots + mine + u) = make_longlong2(out[u], out[u + 1 < kRows ? u + 1 : u]);
   } else {
 #pragma unroll
     for (int u = 0; u < kRows; ++u)
-      if (mine + u < t1) p.slots[mine + u] = out[u];
+      if (mine + u < end) p.slots[mine + u] = out[u];
   }
 }
 
@@ -422,7 +422,8 @@ extern "C" int tv_slot_map(int32_t batch, int32_t rows, const int32_t* cu_rows,
                            const int32_t* start_len, const int32_t* block_table,
                            const int32_t* n_blocks, int32_t max_blocks_per_req, int32_t num_blocks,
                            int64_t* slots, int32_t* status, void* stream) {
-  if (batch < 0 || batch > tv::kTableMaxBatch || rows < 0 || max_blocks_per_req < 1 || num_blocks < 1)
+  if (batch < 0 || batch > tv::kTableMaxBatch || rows < 0 || max_blocks_per_req < 1 || num_blocks < 1 ||
+      max_blocks_per_req > (1 << 27))      // (token positions stay below 2^31)
     return TV_ERR_BAD_SIZE;
   if (rows == 0) return TV_OK;
   if (!slots || (batch > 0 && (!cu_rows || !start_len || !block_table || !n_blocks || !status)))

@@ -57,6 +57,13 @@ def test_slot_map_refusals(lib):
     assert call(swap(args, _8=P + 4)) == MIS
 
 
+def test_slot_map_refuses_tables_past_31_bits(lib):
+    """A table of more than 2^27 pages has token positions that 32 bits do not hold."""
+    args = [2, 5, P, P, P, P, (1 << 27) + 1, 9, P, P, None]
+    assert lib.tv_slot_map(*args) == SIZE
+    assert lib.tv_slot_map(*swap(args, _6=1 << 27, _1=0)) == OK
+
+
 def test_kv_rows_refusals(lib):
     g, d96, many = tv.geom(32, 8, 128), tv.geom(32, 8, 96), tv.geom(4097, 4097, 64)
     # geom, rows, k, k_ld, v, v_ld, slots, k_cache, v_cache, num_blocks, stream
