@@ -33,13 +33,10 @@
 #include <cuda_bf16.h>
 
 #include "tv_cluster.cuh"
+#include "tv_filter_params.h"
 #include "tv_weight.cuh"
 
-// A unit names its space and its CTA's size before it includes this: 256 threads
-// (four CTAs an SM) hide a sampled row's many short steps best, 512 (two) keep the rows
-// that are in flight small enough for L2, where the masks' second look finds them
-// (4112 rows of 151936 sampled: 595 us, with 512 threads 758; 1345 rows masked in bf16:
-// 380 us, with 256 threads 529).
+// A unit names its space and its CTA's size before it includes this; filtered.cu chooses.
 namespace tv {
 namespace TV_FILT_SPACE {
 
@@ -69,28 +66,6 @@ __device__ __forceinline__ float key_value(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
 }
 __device__ __forceinline__ float place_value(uint64_t c) { return key_value(static_cast<uint32_t>(c >> 32)); }
-
-struct FiltParams {
-  const void* logits;
-  long long logits_ld;
-  const float* gumbel;
-  long long gumbel_ld;
-  const int32_t* cu_nodes;
-  const float* temperature;
-  const int32_t* top_k;
-  const float* top_p;
-  const float* min_p;
-  int max_nodes, vocab, bits;
-  int csize;                   // CTAs of a cluster
-  int rows, batch;             // rows = batch * max_nodes
-  bool reorder;
-  int32_t* tokens;
-  float* logp;
-  void* out;
-  long long out_ld;
-  int32_t* kept;
-  int32_t* status;
-};
 
 struct FiltSmem {
   uint32_t bins[4][kBins];                 // counts; weights in three parts
@@ -1256,11 +1231,12 @@ struct DrawBody {
 struct FreeBody {
   float inv_t;
   Draw draw;
-  float top, sum, nans;
+  float top, nans;
+  FloatSum sum;            // (beside one heavy token hundreds of light ones would each lose up to 2^-25 of it)
 
   template <int kLen>
   __device__ __forceinline__ void many(const float* x, const float* g, int i0) {
-    float s[kLen], high = top;
+    float s[kLen], high = top, part = 0.0f;
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {
       s[e] = __fmul_rn(x[e], inv_t);
@@ -1269,14 +1245,17 @@ struct FreeBody {
       if (draw.passes(v) && x[e] != -kInf) draw.offer(v, i0 + e);
     }
     if (high > top) {
-      sum *= fast_exp2((top - high) * kLog2e);
+      const float less = fast_exp2((top - high) * kLog2e);
+      sum.sum *= less;
+      sum.low *= less;
       top = high;
     }
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {       // equal infinities weigh 1
       if (s[e] != s[e]) nans += 1.0f;
-      else sum += s[e] == top ? 1.0f : fast_exp2((s[e] - top) * kLog2e);
+      else part += s[e] == top ? 1.0f : fast_exp2((s[e] - top) * kLog2e);
     }
+    sum.add(part);
   }
 };
 
@@ -1333,12 +1312,13 @@ struct FreeResult {
 };
 template <typename T>
 __device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* noise, FiltSmem& s) {
-  FreeBody body = {row.inv_t, no_draw(), -kInf, 0.0f, 0.0f};
+  FreeBody body = {row.inv_t, no_draw(), -kInf, 0.0f, {0.0f, 0.0f}};
   for_slice_noise(row, noise, body);
   FreeResult out;
+  const float sum = body.sum.sum + body.sum.low;
   out.best = block_max(body.draw.best, s);
   out.top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
-  out.sum = block_sum(body.top == out.top ? body.sum : body.sum * fast_exp2((body.top - out.top) * kLog2e), s);
+  out.sum = block_sum(body.top == out.top ? sum : sum * fast_exp2((body.top - out.top) * kLog2e), s);
   out.nans = block_sum(body.nans, s);
   return out;
 }
@@ -1553,29 +1533,21 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
 
 // ------------------------------------------------------------------ host side
 
-static int check_filter(int dtype, const void* logits, long long ld, int batch, int max_nodes, int vocab) {
-  if (dtype != TV_DTYPE_BF16 && dtype != TV_DTYPE_F32) return TV_ERR_BAD_GEOMETRY;
-  if (batch < 0 || batch > 65535 || max_nodes < 1 || max_nodes > TV_MAX_NODES || vocab < 1 || vocab > (1 << 30) || ld < vocab)
-    return TV_ERR_BAD_SIZE;
-  return TV_OK;
-}
-
 template <bool kSampling>
-static int launch_filtered(int dtype, FiltParams& p, int batch, void* stream) {
+static int launch_filtered(int dtype, FiltParams& p, void* stream) {
   static size_t smem_set[2][kMaxDevices] = {};
   const int dev = current_device();
   const int sms = dev < 0 ? -1 : device_sm_count(dev);
   if (sms <= 0) return TV_ERR_CUDA;
   const bool f32 = dtype == TV_DTYPE_F32;
   auto* kernel = f32 ? filtered_kernel<float, kSampling> : filtered_kernel<__nv_bfloat16, kSampling>;
-  const long long rows = static_cast<long long>(batch) * p.max_nodes;
+  const long long rows = static_cast<long long>(p.batch) * p.max_nodes;
   p.rows = static_cast<int>(rows);
   p.bits = weight_bits(p.vocab);
-  p.batch = batch;
   // a cluster a row where all of them are resident at once
   p.csize = 1;
   while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * kFiltPerSm && p.vocab > kListCap) p.csize *= 2;
-  p.reorder = p.top_p && batch > 1 && batch <= kFiltThreads && rows * p.csize > sms * kFiltPerSm;
+  p.reorder = p.top_p && p.batch > 1 && p.batch <= kFiltThreads && rows * p.csize > sms * kFiltPerSm;
   const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? kLocalCap * sizeof(uint64_t) : 0);
   if (!ensure_smem(kernel, smem, smem_set[f32], dev)) return TV_ERR_CUDA;
   const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
