@@ -330,7 +330,10 @@ struct PassBody {
   __device__ __forceinline__ float cheap(float x) const { return fast_exp2(__fmaf_rn(x, to_y, y_off)); }
 
   __device__ __forceinline__ CloseWeight close(float x) const { return close_weight(__fmul_rn(x, row.inv_t), scale, s.table); }
-  __device__ __forceinline__ uint64_t exact(float x) const { return weight_of(__fmul_rn(x, row.inv_t), scale, s.table); }
+  // (a logit of -inf weighs nothing, also where all others are scaled to -inf and weigh 1)
+  __device__ __forceinline__ uint64_t exact(float x) const {
+    return x == -kInf ? 0ull : weight_of(__fmul_rn(x, row.inv_t), scale, s.table);
+  }
 
   // a token that may lie in the bracket
   __device__ __forceinline__ void take(float x, int i) {
@@ -1271,6 +1274,10 @@ struct FreeBody {
     for (int e = 0; e < kLen; ++e) {       // equal infinities weigh 1
       if (s[e] != s[e]) nans += 1.0f;
       else part += s[e] == top ? 1.0f : fast_exp2((s[e] - top) * kLog2e);
+    }
+    if (top == -kInf) {                    // logits scaled to -inf weigh 1, those that are -inf nothing
+#pragma unroll
+      for (int e = 0; e < kLen; ++e) part -= x[e] == -kInf ? 1.0f : 0.0f;
     }
     sum.add(part);
   }
