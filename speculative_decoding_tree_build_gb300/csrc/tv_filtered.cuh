@@ -1047,11 +1047,12 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
     if (!large) hi = kHighest;
   }
   // 2. the list; weights below it relative to its first place, a power of two
-  // from the row's (not where the reduction differs)
+  // from the row's (not where the reduction differs, nor where 1 / T is finite and
+  // its product with log2 e is not: T below 4.24e-39)
   const bool total = by_p && !by_k;
   const float s_lo = __fmul_rn(place_value(lo), row.inv_t);
   const WeightScale low_scale = weight_scale(s_lo, row.bits);
-  const bool low_fits = fabsf(s_lo) < kWeightSpan;
+  const bool low_fits = fabsf(s_lo) < kWeightSpan && row.inv_t * kLog2e < kInf;
   Bracket view = total && low_fits ? pass<Weigh::kBelow>(row, lo, hi, low_scale, s)
                                    : pass<Weigh::kNone>(row, lo, hi, none, s);
   if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)

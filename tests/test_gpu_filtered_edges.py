@@ -7,6 +7,7 @@ import pytest
 import torch
 
 import speculative_decoding_tree_build_gb300 as tv
+from oracle import draw_ref, filter_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -68,3 +69,38 @@ def test_masked_logits_beside_the_lowest_value(v, dtype, k, p, m):
         assert torch.equal((out[r] > -INF).nonzero().flatten().cpu(), torch.from_numpy(places[r][:want]))
         assert tok[r] == places[r][0]
         assert abs(lp[r] + math.log(want)) <= 2.0 ** -23 * math.log(want)
+
+
+# ------------------------------------------------------------------- the smallest temperatures
+
+
+@pytest.mark.parametrize("t", [3e-39, 4e-39, 5e-39])
+@pytest.mark.parametrize("v", [300, 9000, 40001])
+@pytest.mark.parametrize("value", [0.0, 1e-37, -1e-37])
+def test_equal_logits_at_the_smallest_temperatures(v, t, value):
+    """1 / T is finite from 2.94e-39 on, times log2 e it is not below 4.24e-39."""
+    x = torch.full((2, v), value)
+    for p in (0.5, 0.25):
+        _, lp, out, kept = both(x, t, None, p, None)
+        want = math.ceil(p * v)
+        assert kept == [want] * 2
+        assert bool((out[:, :want] == x[0, 0].item()).all()) and bool((out[:, want:] == -INF).all())
+        assert max(abs(a + math.log(want)) for a in lp) <= 2.0 ** -22 * math.log(want)
+
+
+@pytest.mark.parametrize("t", [3e-39, 4e-39])
+@pytest.mark.parametrize("v", [300, 9000])
+@pytest.mark.parametrize("k,p,m", [(None, 0.9, None), (50, 0.9, None), (None, None, 0.1), (0, 0.5, 0.01)])
+def test_small_logits_at_the_smallest_temperatures(v, t, k, p, m):
+    """Logits of 1e-38: scaled, they are a row like any other."""
+    rng = np.random.default_rng(v)
+    x = (rng.normal(0, 1, (3, v)) * 1e-38).astype(np.float32)
+    g = (-np.log(-np.log(rng.uniform(1e-7, 1 - 1e-7, (3, v))))).astype(np.float32)
+    tok, lp, out, kept = both(torch.from_numpy(x), t, k, p, m, torch.from_numpy(g))
+    for r in range(3):
+        keep, s, w, margin = filter_ref(x[r], t, k or 0, 1.0 if p is None else p, m or 0.0)
+        assert margin > 2.0 ** -33
+        token, logp = draw_ref(keep, s, w, g[r])
+        assert kept[r] == int(keep.sum()) and tok[r] == token
+        assert np.array_equal(out[r].cpu().numpy() > -np.inf, keep)
+        assert abs(lp[r] - logp) <= 2.0 ** -24 * (8 * abs(logp) + 8 * math.log(v) + 8)
