@@ -849,9 +849,11 @@ int tv_kv_rows_read(const tv_geom* geom, int32_t rows, const int64_t* slots, con
  * to steps of 2^-44 of the largest (2^-(62 - log2 vocab) from 2^18 tokens on) and added
  * exactly; equal logits have equal weights. So a decision can differ from an exact
  * evaluation only where a border's sum is that close to its target, and results do
- * not depend on timing. logp is within a few roundings of float32. Where
- * s_max is infinite or NaN, tokens equal to it weigh 1, others 0. A row without a
- * logit above -inf (a mask that leaves nothing) gets token 0 and logp -inf.
+ * not depend on timing. logp is within a few roundings of float32; without a filter
+ * its terms are float32 too, and their errors and those of their sum add up to 2^-17
+ * at most. Where s_max is infinite or NaN, tokens equal to it weigh 1, others (and
+ * logits of -inf) 0. A row without a logit above -inf (a mask that leaves nothing)
+ * gets token 0 and logp -inf.
  *
  *  dtype          TV_DTYPE_* of logits
  *  logits         [T][logits_ld], 16-byte aligned, rows a multiple of 16 bytes apart

@@ -30,6 +30,7 @@
 // the same decisions.
 #pragma once
 
+#include <cfloat>
 #include <cuda_bf16.h>
 
 #include "tv_cluster.cuh"
@@ -276,6 +277,11 @@ struct FloatSum {
   __device__ __forceinline__ void add(float part) {
     const float all = sum + part, back = all - sum;
     low += (sum - (all - back)) + (part - back);
+    sum = all;
+  }
+  __device__ __forceinline__ void scale(float factor) {
+    const float all = sum * factor;
+    low = __fmaf_rn(low, factor, __fmaf_rn(sum, factor, -all));
     sum = all;
   }
   __device__ __forceinline__ uint64_t steps(float unit) const {
@@ -1248,7 +1254,12 @@ struct DrawBody {
 };
 
 // No filter: all of the noise is read beside the logits, the sum of weights is
-// float32 relative to a running maximum (nothing is decided by it).
+// float32 relative to a running maximum (nothing is decided by it). The reference
+// moves where a value lies more than 1 above it: a row in ascending order would
+// move it at every vector otherwise, and the factors' errors would add up (3.7e-5 of the
+// sum in 2^20 entries that rise by 0.012). Sums fall by e at least with every move, so those
+// of n entries of a thread count ln n + 2 moves at most before they are a small part
+// of what comes; each is off by 2^-22.4 (expf, the difference).
 struct FreeBody {
   float inv_t;
   Draw draw;
@@ -1265,20 +1276,14 @@ struct FreeBody {
       const float v = __fadd_rn(s[e], g[e]);
       if (draw.passes(v) && x[e] != -kInf) draw.offer(v, i0 + e);
     }
-    if (high > top) {
-      const float less = fast_exp2((top - high) * kLog2e);
-      sum.sum *= less;
-      sum.low *= less;
+    if (high > top + 1.0f) {
+      sum.scale(expf(top - high));
       top = high;
     }
 #pragma unroll
     for (int e = 0; e < kLen; ++e) {       // equal infinities weigh 1
       if (s[e] != s[e]) nans += 1.0f;
       else part += s[e] == top ? 1.0f : fast_exp2((s[e] - top) * kLog2e);
-    }
-    if (top == -kInf) {                    // logits scaled to -inf weigh 1, those that are -inf nothing
-#pragma unroll
-      for (int e = 0; e < kLen; ++e) part -= x[e] == -kInf ? 1.0f : 0.0f;
     }
     sum.add(part);
   }
@@ -1335,9 +1340,25 @@ struct FreeResult {
   uint64_t best;
   float top, sum, nans;
 };
+// How many logits are not -inf.
+struct CountBody {
+  float n;
+  template <int kLen>
+  __device__ __forceinline__ void many(const float* x, int) {
+#pragma unroll
+    for (int e = 0; e < kLen; ++e) n += x[e] == -kInf ? 0.0f : 1.0f;
+  }
+};
+template <typename T>
+__device__ __noinline__ float count_row(const Row<T>& row, FiltSmem& s) {
+  CountBody body = {0.0f};
+  for_slice<0>(row, body);
+  return block_sum(body.n, s);
+}
+
 template <typename T>
 __device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* noise, FiltSmem& s) {
-  FreeBody body = {row.inv_t, no_draw(), -kInf, 0.0f, {0.0f, 0.0f}};
+  FreeBody body = {row.inv_t, no_draw(), -FLT_MAX, 0.0f, {0.0f, 0.0f}};
   for_slice_noise(row, noise, body);
   FreeResult out;
   const float sum = body.sum.sum + body.sum.low;
@@ -1345,6 +1366,10 @@ __device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* nois
   out.top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
   out.sum = block_sum(body.top == out.top ? sum : sum * fast_exp2((body.top - out.top) * kLog2e), s);
   out.nans = block_sum(body.nans, s);
+  if (out.sum == 0.0f && out.nans == 0.0f) {             // all are scaled to -inf: what is not -inf itself weighs 1
+    out.top = -kInf;
+    out.sum = count_row(row, s);
+  }
   return out;
 }
 

@@ -104,3 +104,73 @@ def test_small_logits_at_the_smallest_temperatures(v, t, k, p, m):
         assert kept[r] == int(keep.sum()) and tok[r] == token
         assert np.array_equal(out[r].cpu().numpy() > -np.inf, keep)
         assert abs(lp[r] - logp) <= 2.0 ** -24 * (8 * abs(logp) + 8 * math.log(v) + 8)
+
+
+# ------------------------------------------------------- log-probabilities of unfiltered rows
+
+
+def unfiltered_bound(scaled, logp, entries):
+    """Of the log-probability of a row without a filter, `entries` of it a thread. A
+    term: the difference from the reference and its product with log2 e are rounded
+    (a (2^-24 + 2^-24 + 2^-26) for an exponent of a, 1 for the reference's place), ex2 is
+    good to 2^-22. Moves of the reference: ln n + 2 of them count, each expf's 2^-23 and
+    the difference's 2^-24. A thread's sum brought to the CTA's reference, a CTA's to the
+    cluster's: ex2 and the exponent again. Additions of a warp's lanes, a CTA's warps and a
+    cluster's CTAs: 5 + 8 + 8. ln of the sum: 2^-23 of it; the difference and the last
+    subtraction 2^-24 each."""
+    s = scaled.astype(np.float64)
+    top = s.max()
+    w = np.exp(s - top)
+    far = float((w * (top - s)).sum() / w.sum()) + 1
+    total = float(np.log(w.sum())) + 1
+    return (far * 2.25 * 2.0 ** -24 + 2.0 ** -22 + (math.log(entries) + 2) * 1.5 * 2.0 ** -23 +
+            2 * (2.0 ** -22 + 2.0 ** -23) + 21 * 2.0 ** -24 + total * 2.0 ** -23 + (abs(logp) + 1) * 2.0 ** -24)
+
+
+@pytest.mark.parametrize("v,rows", [(32000, 3), (151936, 5), (1 << 20, 2), (32000, 400), (151936, 320), (1 << 20, 310)])
+@pytest.mark.parametrize("order", ["up", "down", "stairs", "any"])
+def test_unfiltered_logp_of_ordered_rows(v, rows, order):
+    """Rows that rise, fall or rise in steps from end to end, by 0.01 to 60; few rows have a
+    cluster each, many a CTA."""
+    at = torch.linspace(0, 1, v, device="cuda", dtype=torch.float64)
+    if order == "down":
+        at = at.flip(0)
+    elif order == "stairs":
+        at = (at * 40).floor() / 40
+    elif order == "any":
+        g = torch.Generator(device="cuda")
+        g.manual_seed(v)
+        at = at[torch.randperm(v, generator=g, device="cuda")]
+    x = torch.empty(rows, v, device="cuda")
+    for r, rise in enumerate(np.logspace(-2, 1.778, rows)):
+        x[r] = (at * rise).float()
+    noise = torch.zeros(rows, v, device="cuda")
+    tok, lp, st = i32([0] * rows), f32([0.0] * rows), i32([0])
+    tv.sample_filtered(x, noise, i32([0, rows]), f32([1.0]), None, None, None, rows, tok, lp, st)
+    assert not st.any()
+    assert torch.equal(tok.long(), x.argmax(-1))
+    for r in range(0, rows, max(1, rows // 12)):
+        logp = float(x[r, tok[r]].double() - torch.logsumexp(x[r].double(), 0))
+        host = x[r].cpu().numpy()
+        assert abs(float(lp[r]) - logp) <= unfiltered_bound(host, logp, v // (8 * 256) if rows < 10 else v // 256), r
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("t", [0.3, 1.0, 1.7])
+@pytest.mark.parametrize("v,rows", [(7, 3), (1000, 5), (32000, 7), (151936, 6), (50000, 400)])
+def test_unfiltered_logp_of_drawn_tokens(v, rows, t, dtype):
+    rng = np.random.default_rng(v)
+    x = torch.from_numpy((rng.normal(0, 2, (rows, v))).astype(np.float32)).to(dtype)
+    g = torch.from_numpy((-np.log(-np.log(rng.uniform(1e-7, 1 - 1e-7, (rows, v))))).astype(np.float32))
+    ld = -(-v // 8) * 8
+    lg, gumbel = torch.zeros(rows, ld, dtype=dtype, device="cuda")[:, :v], torch.zeros(rows, ld, device="cuda")[:, :v]
+    lg.copy_(x)
+    gumbel.copy_(g)
+    tok, lp, st = i32([0] * rows), f32([0.0] * rows), i32([0])
+    tv.sample_filtered(lg, gumbel, i32([0, rows]), f32([t]), None, None, None, rows, tok, lp, st)
+    assert not st.any()
+    for r in range(0, rows, max(1, rows // 12)):
+        keep, s, w, _ = filter_ref(x[r].float().numpy(), t)
+        token, logp = draw_ref(keep, s, w, g[r].numpy())
+        assert int(tok[r]) == token
+        assert abs(float(lp[r]) - logp) <= unfiltered_bound(s, logp, max(1, v // 256)), r
