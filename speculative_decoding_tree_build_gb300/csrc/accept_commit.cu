@@ -87,10 +87,10 @@ extern "C" int tv_accept_commit(const tv_geom* geom, const int32_t* target_ids,
       !new_len || !released || !released_count || !status)
     return TV_ERR_NULL_POINTER;
   if (!tv::aligned(k_cache, 16) || !tv::aligned(v_cache, 16)) return TV_ERR_MISALIGNED;
-  static size_t smem_set[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  if (!tv::ensure_smem(tv::accept_commit_kernel, tv::kFusedStage, smem_set, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::accept_commit_kernel, tv::kFusedStage, smem_limit, dev)) return TV_ERR_CUDA;
   const cudaError_t err = tv::launch_pdl(
       tv::accept_commit_kernel, dim3(batch), dim3(tv::kFusedThreads), tv::kFusedStage,
       tv::as_stream(stream), target_ids, draft_tokens, cu_nodes, next_token, next_sibling,

@@ -1391,7 +1391,7 @@ int launch_attention_tc(const tv_geom* geom, int batch, int max_nodes, const voi
   mp.ntask = grid;
 
   const dim3 rgrid(batch, (max_nodes + kRopeNodes - 1) / kRopeNodes);
-  static size_t smem_set128[kMaxDevices] = {0}, smem_set64[kMaxDevices] = {0};
+  static SmemLimit smem_limit128, smem_limit64;
   const int dev = current_device();
   if (dev < 0) return TV_ERR_CUDA;
   const size_t smem_fixed = (D == 128 ? TcCfg<128>::kSmem : TcCfg<64>::kSmem) + 1024;
@@ -1432,13 +1432,13 @@ int launch_attention_tc(const tv_geom* geom, int batch, int max_nodes, const voi
   mcfg.dynamicSmemBytes = 0;
   cudaError_t err;
   if (D == 128) {
-    if (!ensure_smem(attn_tc_kernel<128>, smem, smem_set128, dev)) return TV_ERR_CUDA;
+    if (!ensure_smem(attn_tc_kernel<128>, smem, smem_limit128, dev)) return TV_ERR_CUDA;
     err = rp.rope_style == 0 ? launch_pdl(rope_append_kernel<128, true>, rgrid, dim3(kRopeThreads), 0, stream, rp)
                              : launch_pdl(rope_append_kernel<128, false>, rgrid, dim3(kRopeThreads), 0, stream, rp);
     if (err == cudaSuccess) err = cudaLaunchKernelEx(&acfg, attn_tc_kernel<128>, tp);
     if (err == cudaSuccess) err = cudaLaunchKernelEx(&mcfg, attn_merge_kernel<128>, mp);
   } else {
-    if (!ensure_smem(attn_tc_kernel<64>, smem, smem_set64, dev)) return TV_ERR_CUDA;
+    if (!ensure_smem(attn_tc_kernel<64>, smem, smem_limit64, dev)) return TV_ERR_CUDA;
     err = rp.rope_style == 0 ? launch_pdl(rope_append_kernel<64, true>, rgrid, dim3(kRopeThreads), 0, stream, rp)
                              : launch_pdl(rope_append_kernel<64, false>, rgrid, dim3(kRopeThreads), 0, stream, rp);
     if (err == cudaSuccess) err = cudaLaunchKernelEx(&acfg, attn_tc_kernel<64>, tp);

@@ -402,11 +402,11 @@ extern "C" int tv_block_tables(int32_t batch, const int32_t* want_len, int32_t* 
   if (batch == 0) return TV_OK;
   if (!want_len || !block_table || !n_blocks || !free_blocks || !free_count || !status || !released != !released_count)
     return TV_ERR_NULL_POINTER;
-  static size_t smem_set[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
   const size_t smem = static_cast<size_t>(batch) * 5 * sizeof(int32_t);
-  if (!tv::ensure_smem(tv::block_tables_kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::block_tables_kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   tv::TableParams p = {};
   p.want_len = want_len; p.table = block_table; p.n_blocks = n_blocks;
   p.free_blocks = free_blocks; p.free_count = free_count;

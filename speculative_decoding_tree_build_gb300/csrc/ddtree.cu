@@ -551,10 +551,10 @@ extern "C" int tv_ddtree_topk(const float* logits, int64_t logits_ld, int32_t ro
   if (!tv::aligned(logits, 16) || (logits_ld & 3)) return TV_ERR_MISALIGNED;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  static size_t done[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const size_t smem = static_cast<size_t>(tv::kTopkCap + tv::kTopkBucketCap) * sizeof(uint64_t) +
                       2 * tv::kTopkBins * sizeof(uint32_t);
-  if (!tv::ensure_smem(tv::ddtree_topk_kernel, smem, done, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::ddtree_topk_kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   const cudaError_t err = tv::launch_pdl(tv::ddtree_topk_kernel, dim3(rows), dim3(tv::kTopkThreads),
                                          smem, tv::as_stream(stream), logits,
                                          static_cast<long long>(logits_ld), static_cast<int>(vocab),
@@ -574,8 +574,8 @@ extern "C" int tv_ddtree_build(const float* top_logq, const int32_t* top_tokens,
   if (!top_logq || !top_tokens || !parents || !tokens || !cu_nodes) return TV_ERR_NULL_POINTER;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  static size_t done[tv::kMaxDevices] = {0};
-  if (!tv::ensure_smem(tv::ddtree_heap_kernel, smem, done, dev)) return TV_ERR_CUDA;
+  static tv::SmemLimit smem_limit;
+  if (!tv::ensure_smem(tv::ddtree_heap_kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   const cudaError_t err = tv::launch_pdl(tv::ddtree_heap_kernel, dim3(batch), dim3(tv::kHeapThreads),
                                          smem, tv::as_stream(stream), top_logq, top_tokens,
                                          static_cast<int>(depth_L), static_cast<int>(k), n,

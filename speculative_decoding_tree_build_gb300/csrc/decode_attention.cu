@@ -881,9 +881,9 @@ __global__ void __launch_bounds__(32 * kMergeMaxParts) decode_merge_kernel(const
 template <int kFmt, int D, int kQ, int kWarps>
 static int launch_decode_one(const DecodeParams& p, int dev, cudaStream_t stream) {
   constexpr size_t smem = sizeof(float) * 8 * DecTraits<kFmt, D, kQ>::NT * (kWarps * (D + 4) + D);
-  static size_t smem_set[kMaxDevices] = {0};
+  static SmemLimit smem_limit;
   auto* kernel = decode_kernel<kFmt, D, kQ, true, kWarps>;
-  if (!ensure_smem(kernel, smem, smem_set, dev)) return TV_ERR_CUDA;
+  if (!ensure_smem(kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -940,9 +940,9 @@ static int launch_decode(DecodeParams p, int sms, int dev, cudaStream_t stream) 
     }
     return launch_decode_one<kFmt, D, kQ, kDecWarps>(p, dev, stream);
   }
-  static size_t smem_set[kMaxDevices] = {0};
+  static SmemLimit smem_limit;
   auto* kernel = decode_kernel<kFmt, D, kQ, false, kDecWarps>;
-  if (!ensure_smem(kernel, sums, smem_set, dev)) return TV_ERR_CUDA;
+  if (!ensure_smem(kernel, sums, smem_limit, dev)) return TV_ERR_CUDA;
   p.by_unit = units <= grid ? 1 : 0;
   p.parts = 1;
   if (launch_pdl(kernel, dim3(grid), dim3(kDecThreads), sums, stream, p) != cudaSuccess) return TV_ERR_CUDA;

@@ -277,9 +277,9 @@ extern "C" int tv_eagle_expand_select(const float* logp, const int32_t* parent,
   if (!logp || !parent || !cand_count || !selected || !status) return TV_ERR_NULL_POINTER;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  static size_t done[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const size_t smem = tv::expand_smem_bytes();
-  if (!tv::ensure_smem(tv::eagle_expand_select_kernel, smem, done, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::eagle_expand_select_kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   const cudaError_t err = tv::launch_pdl(tv::eagle_expand_select_kernel, dim3(batch),
                                          dim3(tv::kEagleThreads), smem, tv::as_stream(stream),
                                          logp, parent, cand_count, static_cast<int>(max_cands),
@@ -301,9 +301,9 @@ extern "C" int tv_eagle_rerank(const float* logp, const int32_t* parent, const i
     return TV_ERR_NULL_POINTER;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  static size_t done[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const size_t smem = tv::rerank_smem_bytes();
-  if (!tv::ensure_smem(tv::eagle_rerank_kernel, smem, done, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::eagle_rerank_kernel, smem, smem_limit, dev)) return TV_ERR_CUDA;
   const cudaError_t err = tv::launch_pdl(tv::eagle_rerank_kernel, dim3(batch),
                                          dim3(tv::kEagleThreads), smem, tv::as_stream(stream),
                                          logp, parent, token, cand_count,

@@ -77,10 +77,10 @@ extern "C" int tv_kv_commit(const tv_geom* geom, int32_t batch, const int32_t* a
       !v_cache || !new_len || !released || !released_count || !status)
     return TV_ERR_NULL_POINTER;
   if (!tv::aligned(k_cache, 16) || !tv::aligned(v_cache, 16)) return TV_ERR_MISALIGNED;
-  static size_t smem_set[tv::kMaxDevices] = {0};
+  static tv::SmemLimit smem_limit;
   const int dev = tv::current_device();
   if (dev < 0) return TV_ERR_CUDA;
-  if (!tv::ensure_smem(tv::kv_commit_kernel, tv::kCommitSmem, smem_set, dev)) return TV_ERR_CUDA;
+  if (!tv::ensure_smem(tv::kv_commit_kernel, tv::kCommitSmem, smem_limit, dev)) return TV_ERR_CUDA;
   const int head_vecs = geom->head_dim / 8;
   const cudaError_t err = tv::launch_pdl(
       tv::kv_commit_kernel, dim3(batch), dim3(tv::kCommitThreads), tv::kCommitSmem, tv::as_stream(stream),

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+#include <mutex>
 #include <utility>
 
 #include "../../include/treeverify.h"
@@ -58,15 +60,25 @@ inline int device_is_sm103(int dev) {
 // integer (from d = 256 on the product stays below 65536).
 inline uint32_t thread_divisor(int d) { return 65536u / d + 1u; }
 
-// Raise a kernel's dynamic shared-memory limit once per device (and again
-// only if a larger size is needed).
+// The dynamic shared-memory limit that a kernel has been given, per device. One
+// static object for each kernel.
+struct SmemLimit {
+  std::atomic<size_t> bytes[kMaxDevices] = {};
+  std::mutex lock;
+};
+
+// Raise a kernel's limit once per device (and again only if a larger size is
+// needed). Host threads whose calls need different sizes take turns: a smaller
+// limit set after a larger one would stand below what is noted here.
 template <typename Kernel>
-inline bool ensure_smem(Kernel k, size_t bytes, size_t* done_per_device, int dev) {
-  if (done_per_device[dev] >= bytes) return true;
+inline bool ensure_smem(Kernel k, size_t bytes, SmemLimit& limit, int dev) {
+  if (limit.bytes[dev].load(std::memory_order_acquire) >= bytes) return true;
+  const std::lock_guard<std::mutex> held(limit.lock);
+  if (limit.bytes[dev].load(std::memory_order_relaxed) >= bytes) return true;
   if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            static_cast<int>(bytes)) != cudaSuccess)
     return false;
-  done_per_device[dev] = bytes;
+  limit.bytes[dev].store(bytes, std::memory_order_release);
   return true;
 }
 

@@ -1585,7 +1585,7 @@ __global__ void __launch_bounds__(kFiltThreads, kFiltPerSm) filtered_kernel(cons
 
 template <bool kSampling>
 static int launch_filtered(int dtype, FiltParams& p, void* stream) {
-  static size_t smem_set[2][kMaxDevices] = {};
+  static SmemLimit smem_limit[2];
   const int dev = current_device();
   const int sms = dev < 0 ? -1 : device_sm_count(dev);
   if (sms <= 0) return TV_ERR_CUDA;
@@ -1599,7 +1599,7 @@ static int launch_filtered(int dtype, FiltParams& p, void* stream) {
   while (p.csize < kFiltMaxCluster && rows * p.csize * 2 <= sms * kFiltPerSm && p.vocab > kListCap) p.csize *= 2;
   p.reorder = p.top_p && p.batch > 1 && p.batch <= kFiltThreads && rows * p.csize > sms * kFiltPerSm;
   const size_t smem = sizeof(FiltSmem) + (p.csize > 1 ? kLocalCap * sizeof(uint64_t) : 0);
-  if (!ensure_smem(kernel, smem, smem_set[f32], dev)) return TV_ERR_CUDA;
+  if (!ensure_smem(kernel, smem, smem_limit[f32], dev)) return TV_ERR_CUDA;
   const cudaError_t err = launch_cluster_smem_pdl(kernel, dim3(static_cast<unsigned>(rows * p.csize)), dim3(kFiltThreads), p.csize,
                                                   smem, as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
