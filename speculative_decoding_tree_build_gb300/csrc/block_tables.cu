@@ -10,6 +10,7 @@
 // restores list and tables exactly. The numbers are prefix sums of the
 // requests' counts: no atomics on the list, the result depends on the
 // arguments alone.
+#include <algorithm>
 #include <climits>
 
 #include "tv_cluster.cuh"
@@ -275,25 +276,13 @@ struct SlotParams {
   bool wide;               // slots lie on 16 bytes
 };
 
-// A CTA has a contiguous range of rows, kRows of them side by side a thread (they
-// lie in one or two pages: one search, one or two table entries, one wide store). It
-// takes the running maximum of all offsets (4 a thread for 2048 requests), in
-// which a row finds its request and offsets that run backwards show; the requests at
-// the two ends of its range are checked in full, the ones between are checked by their
-// rows.
-template <int kRows>
-__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_constant__ SlotParams p) {
-  extern __shared__ int32_t s_off[];       // running maximum of the offsets, then a request's fault
-  int32_t* s_bad = s_off + p.batch;
-  __shared__ int s_warp[kSlotThreads / 32];
-  grid_dependency_wait();
-  grid_launch_dependents();
+// s_off[b] = the largest offset of a thread's requests [b0, b1) up to b, and the largest
+// of all requests before b0, which is returned.
+__device__ __forceinline__ int scan_offsets(const SlotParams& p, int32_t* s_off, int* s_warp, int& b0, int& b1) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int t0 = blockIdx.x * p.cta_rows;                  // below rows, whose end may lie at 2^31 - 1
-  const int t1 = static_cast<int>(min(static_cast<long long>(p.rows), static_cast<long long>(t0) + p.cta_rows));
-
   const int per = (p.batch + kSlotThreads - 1) / kSlotThreads;
-  const int b0 = min(p.batch, static_cast<int>(threadIdx.x) * per), b1 = min(p.batch, b0 + per);
+  b0 = min(p.batch, static_cast<int>(threadIdx.x) * per);
+  b1 = min(p.batch, b0 + per);
   int most = INT_MIN;
   for (int b = b0; b < b1; ++b) {
     most = max(most, p.cu_rows[b]);
@@ -310,6 +299,31 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   __syncthreads();
   int before = lane > 0 ? up : INT_MIN;
   for (int w = 0; w < warp; ++w) before = max(before, s_warp[w]);
+  return before;
+}
+
+// A CTA has a contiguous range of rows, kRows of them side by side a thread (they
+// lie in one or two pages: one search, one or two table entries, one wide store). It
+// takes the running maximum of all offsets (4 a thread for 2048 requests), in
+// which a row finds its request and offsets that run backwards show. Requests that lie
+// within the range are checked by their rows. In small calls (a row a thread) the ones
+// at its two ends, which may have rows elsewhere, are checked in full by each CTA that has
+// some of them. In large ones that would be quadratic in a request's length: a CTA checks
+// its own rows alone, and slot_clear_kernel takes back what others wrote for a request
+// that one of them flagged. One launch against two, us: 64 trees, 4591 rows 4.1 / 4.2;
+// one prompt of 65536 4.1 / 4.2, of 262144 7.2 / 5.2, of 8.4M 1391 / 31; 64 prompts, 1.3M
+// rows 13.4 / 10.4; 1000 requests of 1000 rows 13.0 / 10.7.
+template <int kRows>
+__global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_constant__ SlotParams p) {
+  extern __shared__ int32_t s_off[];       // running maximum of the offsets, then a request's fault
+  int32_t* s_bad = s_off + p.batch;
+  __shared__ int s_warp[kSlotThreads / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int t0 = blockIdx.x * p.cta_rows;                  // below rows, whose end may lie at 2^31 - 1
+  const int t1 = static_cast<int>(min(static_cast<long long>(p.rows), static_cast<long long>(t0) + p.cta_rows));
+  int b0, b1;
+  const int before = scan_offsets(p, s_off, s_warp, b0, b1);
   // A request with rows begins where no earlier offset lies behind. Requests
   // that end before they begin have no rows: the first CTA reports them.
   for (int b = b0; b < b1; ++b) {
@@ -353,7 +367,7 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
   // the two requests that may have rows elsewhere
   int fault[2] = {-1, -1};
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < (kRows == 1 ? 2 : 0); ++e) {
     const int t = e ? t1 - 1 : t0;
     if (p.batch == 0 || s_off[0] > t) continue;
     const int b = last_at_most(s_off, p.batch, t);
@@ -389,6 +403,33 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const __grid_con
 #pragma unroll
     for (int u = 0; u < kRows; ++u)
       if (mine + u < end) p.slots[mine + u] = out[u];
+  }
+}
+
+// -1 for all rows of requests whose blocks the grid before found wanting. Where none
+// is flagged so, a CTA has read the status and is done.
+__global__ void __launch_bounds__(kSlotThreads) slot_clear_kernel(const __grid_constant__ SlotParams p) {
+  extern __shared__ int32_t s_off[];       // as above, then whether a request's rows go
+  int32_t* s_bad = s_off + p.batch;
+  __shared__ int s_warp[kSlotThreads / 32];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  bool any = false;
+  for (int b = threadIdx.x; b < p.batch; b += kSlotThreads) any |= (p.status[b] & TV_ST_BAD_BLOCK) != 0;
+  if (!__syncthreads_or(any)) return;
+  int b0, b1;
+  const int before = scan_offsets(p, s_off, s_warp, b0, b1);
+  for (int b = b0; b < b1; ++b) {          // (rows that two requests claim are not the flagged one's)
+    const int c0 = p.cu_rows[b], c1 = p.cu_rows[b + 1];
+    s_bad[b] = (p.status[b] & TV_ST_BAD_BLOCK) && c0 >= max(0, max(before, s_off[b])) && c1 <= p.rows;
+  }
+  __syncthreads();
+  for (int b = 0; b < p.batch; ++b) {
+    if (!s_bad[b]) continue;
+    const int c1 = p.cu_rows[b + 1];
+    for (long long t = p.cu_rows[b] + static_cast<long long>(blockIdx.x) * kSlotThreads + threadIdx.x; t < c1;
+         t += static_cast<long long>(gridDim.x) * kSlotThreads)
+      p.slots[t] = -1;
   }
 }
 
@@ -440,10 +481,12 @@ extern "C" int tv_slot_map(int32_t batch, int32_t rows, const int32_t* cu_rows,
   const bool large = rows > static_cast<long long>(sms) * tv::kSlotThreads * 2;
   p.cta_rows = tv::kSlotThreads * (large ? tv::kSlotRows : 1);
   p.wide = tv::aligned(slots, 16);
-  auto* kernel = large ? tv::slot_map_kernel<tv::kSlotRows> : tv::slot_map_kernel<1>;
   const size_t smem = static_cast<size_t>(batch) * 2 * sizeof(int32_t);
   const int ctas = static_cast<int>((rows + static_cast<long long>(p.cta_rows) - 1) / p.cta_rows);
-  const cudaError_t err = tv::launch_pdl(kernel, dim3(ctas), dim3(tv::kSlotThreads), smem,
-                                         tv::as_stream(stream), p);
+  auto* kernel = large ? tv::slot_map_kernel<tv::kSlotRows> : tv::slot_map_kernel<1>;
+  cudaError_t err = tv::launch_pdl(kernel, dim3(ctas), dim3(tv::kSlotThreads), smem, tv::as_stream(stream), p);
+  if (err == cudaSuccess && large && batch > 0)
+    err = tv::launch_pdl(tv::slot_clear_kernel, dim3(std::min(ctas, 2 * sms)), dim3(tv::kSlotThreads), smem,
+                         tv::as_stream(stream), p);
   return err == cudaSuccess ? TV_OK : TV_ERR_CUDA;
 }
