@@ -174,3 +174,45 @@ def test_unfiltered_logp_of_drawn_tokens(v, rows, t, dtype):
         token, logp = draw_ref(keep, s, w, g[r].numpy())
         assert int(tok[r]) == token
         assert abs(float(lp[r]) - logp) <= unfiltered_bound(s, logp, max(1, v // 256)), r
+
+
+# ------------------------------------------------------------------------ calls that overlap
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("rows,nodes,v", [(24, 1, 50000), (64, 1, 50000), (330, 66, 20000)])
+def test_two_streams_at_once(rows, nodes, v, dtype):
+    """Calls issued in turn to two streams with no wait between them, other logits on each:
+    few rows leave SMs to the other stream's call. Every output equals the one of a call
+    alone."""
+    batch = rows // nodes
+    settings = [(0.9, 0, 0.95, 0.0), (0.7, 100, 0.9, 0.01), (1.0, 0, 1.0, 0.02), (1.1, 15000, 0.99, 0.0), (1.0, 0, 1.0, 0.0)]
+    t, k, p, m = zip(*[settings[b % 5] for b in range(batch)])
+    args = (i32([b * nodes for b in range(batch + 1)]), f32(list(t)), i32(list(k)), f32(list(p)), f32(list(m)), nodes)
+    sides = []
+    for seed in (1, 2):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        x = (torch.randn(rows, v, generator=g, device="cuda") * 3).to(dtype)
+        u = torch.rand(rows, v, generator=g, device="cuda").clamp(1e-7, 1 - 1e-7)
+        turns = [{"tok": i32([-5] * rows), "lp": f32([9.0] * rows), "out": torch.zeros_like(x), "kept": i32([-5] * rows),
+                  "st": i32([0] * batch)} for _ in range(6)]
+        sides.append({"x": x, "g": -torch.log(-torch.log(u)), "turns": turns, "stream": torch.cuda.Stream()})
+
+    def make(side, o, stream=None):
+        tv.sample_filtered(side["x"], side["g"], *args, o["tok"], o["lp"], o["st"], stream)
+        tv.filter_logits(side["x"], *args, o["out"], o["kept"], o["st"], stream)
+
+    for side in sides:                       # the first turn alone, and over before the others begin
+        make(side, side["turns"][0])
+    torch.cuda.synchronize()
+    for turn in range(1, 6):
+        for side in sides:
+            make(side, side["turns"][turn], side["stream"])
+    torch.cuda.synchronize()
+    for side in sides:
+        first = side["turns"][0]
+        assert not first["st"].any() and bool((first["tok"] >= 0).all())
+        for o in side["turns"][1:]:
+            assert all(torch.equal(o[n], first[n]) for n in first)
+    assert not torch.equal(sides[0]["turns"][0]["tok"], sides[1]["turns"][0]["tok"])
