@@ -1053,12 +1053,12 @@ __device__ __forceinline__ RowResult find_cut(const Row<T>& row, int k, float p,
     if (!large) hi = kHighest;
   }
   // 2. the list; weights below it relative to its first place, a power of two
-  // from the row's (not where the reduction differs, nor where 1 / T is finite and
-  // its product with log2 e is not: T below 4.24e-39)
+  // from the row's (not where the reduction differs, nor where 1 / T times log2 e
+  // would be infinite, from 2.36e38 on)
   const bool total = by_p && !by_k;
   const float s_lo = __fmul_rn(place_value(lo), row.inv_t);
   const WeightScale low_scale = weight_scale(s_lo, row.bits);
-  const bool low_fits = fabsf(s_lo) < kWeightSpan && row.inv_t * kLog2e < kInf;
+  const bool low_fits = fabsf(s_lo) < (row.inv_t < 2.3e38f ? kWeightSpan : 0.0f);
   Bracket view = total && low_fits ? pass<Weigh::kBelow>(row, lo, hi, low_scale, s)
                                    : pass<Weigh::kNone>(row, lo, hi, none, s);
   if (!view.any && lo > kLowest)           // (a bracket's end need not be a token's place)
@@ -1340,22 +1340,6 @@ struct FreeResult {
   uint64_t best;
   float top, sum, nans;
 };
-// How many logits are not -inf.
-struct CountBody {
-  float n;
-  template <int kLen>
-  __device__ __forceinline__ void many(const float* x, int) {
-#pragma unroll
-    for (int e = 0; e < kLen; ++e) n += x[e] == -kInf ? 0.0f : 1.0f;
-  }
-};
-template <typename T>
-__device__ __noinline__ float count_row(const Row<T>& row, FiltSmem& s) {
-  CountBody body = {0.0f};
-  for_slice<0>(row, body);
-  return block_sum(body.n, s);
-}
-
 template <typename T>
 __device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* noise, FiltSmem& s) {
   FreeBody body = {row.inv_t, no_draw(), -FLT_MAX, 0.0f, {0.0f, 0.0f}};
@@ -1366,9 +1350,11 @@ __device__ __noinline__ FreeResult free_row(const Row<T>& row, const float* nois
   out.top = key_value(static_cast<uint32_t>(block_max(order_key(body.top), s)));
   out.sum = block_sum(body.top == out.top ? sum : sum * fast_exp2((body.top - out.top) * kLog2e), s);
   out.nans = block_sum(body.nans, s);
-  if (out.sum == 0.0f && out.nans == 0.0f) {             // all are scaled to -inf: what is not -inf itself weighs 1
+  if (out.sum == 0.0f && out.nans == 0.0f) {             // all are scaled to -inf: those that are not -inf weigh 1
+    float n = 0.0f;
+    for (int i = row.v0 + threadIdx.x; i < row.v1; i += kFiltThreads) n += load_one(row.x + i) == -kInf ? 0.0f : 1.0f;
     out.top = -kInf;
-    out.sum = count_row(row, s);
+    out.sum = block_sum(n, s);
   }
   return out;
 }
